@@ -317,6 +317,102 @@ int cc_cache_seen(const KveCcCache *c);
 
 void cc_cache_destroy(KveCcCache *c);
 
+/* ---- shared-prompt decoding ------------------------------------------------------------------ */
+
+/* Decoding several requests behind one cached prompt: the M lookahead trajectories of LORE-KV
+ * (project page, Method, Monte Carlo lookahead, Eq. 1: every trajectory continues the same prompt)
+ * and the answers decoded from one compressed cache (Eq. 8). The prompt's K/V are read where they
+ * are (the arrays of lorekv_score, or the compacted K_out/V_out of lorekv_select_compact), once for
+ * all requests behind them; the rows that a request adds lie in pages of its own.
+ *
+ * n_prompts prompts are each continued by `fan` requests; request r (0 <= r < n_prompts * fan)
+ * continues prompt r / fan. A request that has nothing to do in a step adds 0 rows, so prompts with
+ * fewer requests leave some idle. A step's new rows are packed in request order into arrays of
+ * n_rows rows (a row: one new token of one request); rows behind the last one belong to nobody.
+ *   n_prefix   rows held per (prompt, KV head); 0: no prompt (K_prefix and V_prefix may be NULL)
+ *   page_size  rows per page: a power of two, 1 to 256
+ *   n_pages    pages in the pool; max_pages: entries per request in the block table
+ *   max_new    the most rows a request adds in one step
+ *   dtype      KVE_F32, KVE_BF16 or KVE_F16: queries, K, V and outputs
+ * d_head is 32, 64 or 128; query head h reads KV head h / (n_q_heads/n_kv_heads), at most 128 query
+ * heads per KV head. n_prompts * fan at most 16384; n_rows, n_pages * page_size, max_pages *
+ * page_size and n_prefix at most 2^30; n_rows * n_q_heads and n_pages * n_kv_heads * page_size below
+ * 2^31; n_prompts * n_kv_heads at most 65535 (KVE_EINVAL otherwise; KVE_EDTYPE
+ * for another dtype).
+ *
+ * The arrays of a step, all int32 on the device:
+ *   block_table [n_prompts * fan][max_pages]  the pages of each request, in order
+ *   free_pages  [n_pages]  a ring of free page ids, and pool [4]: {the ring's first free entry, the
+ *               number of free pages, rows packed in the last step, requests refused in it}. A new
+ *               pool is free_pages = 0 .. n_pages - 1 and pool = {0, n_pages, 0, 0}.
+ *   len         [n_prompts * fan]  rows each request has in its pages
+ *   q_start     [n_prompts * fan + 1]  the first packed row of each request
+ *   row_req, row_pos, slot_map [n_rows]  of each packed row: its request, its index among the
+ *               request's own rows, and page * page_size + offset; -1 for rows of nobody */
+typedef struct {
+    int n_prompts, fan, n_q_heads, n_kv_heads, d_head, n_prefix;
+    int page_size, n_pages, max_pages, n_rows, max_new, dtype;
+} KvePgShape;
+
+/* Block tables and slot maps of one step, from the requests' lengths. new_len[r] > 0: the request
+ * adds that many rows; 0: it adds none; < 0: it has finished, its pages go back to the ring (for
+ * later steps: this step's rows only take pages that were free before it) and its length to 0.
+ * A request takes ceil((len + new_len) / page_size) - ceil(len / page_size) pages from the ring, in
+ * request order, and writes their ids behind its own in block_table; other entries stay as they
+ * are. A request is refused whole (length, table and pool as they were, its rows -1, counted in
+ * pool_out[3]) when new_len > max_new, when it would not fit its table, when its rows would pass
+ * n_rows, when its length is not in [0, max_pages * page_size], or when the ring has run out; q_start
+ * still counts its rows, since the caller packed them.
+ * len_out may be len_in and pool_out may be pool_in (the step in place); no other arrays may
+ * overlap. One launch, no workspace; the head sizes, n_prefix and dtype play no part. */
+int pg_plan(const KvePgShape *shape, const int32_t *new_len, const int32_t *len_in,
+            const int32_t *pool_in, int32_t *free_pages, int32_t *block_table, int32_t *len_out,
+            int32_t *pool_out, int32_t *q_start, int32_t *row_req, int32_t *row_pos,
+            int32_t *slot_map, void *stream);
+
+/* Stores a step's new K/V rows into the pages that slot_map names; rows with a negative slot are
+ * skipped. A slot of n_pages * page_size or more is skipped and reported by kve_check_device as
+ * KVE_EINVAL.
+ *   K_new, V_new [n_rows][n_kv_heads][d_head] with K_row_stride and V_row_stride elements from one
+ *       row to the next (n_kv_heads * d_head when packed; the fused projection's row when they are
+ *       slices of its output). Addresses and strides are multiples of 16 bytes.
+ *   K_pages, V_pages [n_pages][n_kv_heads][page_size][d_head], 16-byte aligned
+ * Two rows with the same slot race; pg_plan makes none. */
+int pg_append(const KvePgShape *shape, const void *K_new, const void *V_new,
+              long long K_row_stride, long long V_row_stride, const int32_t *slot_map,
+              void *K_pages, void *V_pages, void *stream);
+
+/* Bytes of workspace pg_attention() needs. 0 on invalid input. */
+size_t pg_workspace_size(const KvePgShape *shape);
+
+/* Attention of a step's rows over their prompt and their requests' own rows, the step's own rows
+ * (stored before by pg_append) included. Row i of request r, query head h:
+ *   out = sum_j a_j v_j, a = softmax_j(q.k_j / sqrt(d_head)) over the first prefix_len[r / fan] rows
+ *   of the prompt and the own rows 0 .. len[r] - (q_start[r + 1] - q_start[r]) + i of the request.
+ * Every prompt's K/V are read once for all its rows. Nothing to see: out 0 and lse -inf. Rows with
+ * row_req < 0, or whose row_req is not the request that q_start gives, are left as they were.
+ *   q        [n_rows][n_q_heads][d_head], q_row_stride elements from one row to the next
+ *   K_prefix, V_prefix [n_prompts][n_kv_heads][n_prefix][d_head] with the strides (elements) of
+ *            prompt, head and row given: a layer's slice of a larger cache, or rows of several
+ *            heads, are read in place
+ *   prefix_len [n_prompts] int32 or NULL (every prompt has n_prefix rows)
+ *   K_pages, V_pages, block_table, len, q_start, row_req: the arrays above, after this step
+ *   out      [n_rows][n_q_heads][d_head]; lse_out [n_rows][n_q_heads] fp32 or NULL: the natural-log
+ *            log-sum-exp of the scores
+ * Addresses and strides of q, K, V and out are multiples of 16 bytes, the workspace is 256-byte
+ * aligned. K/V rows that no row of the request can see (behind prefix_len, behind len, in other
+ * pages) may hold anything, infinities and NaN included; rows that one of them sees are finite.
+ * Page ids outside the pool are read as page 0 and reported by kve_check_device as KVE_EINVAL.
+ * Results do not depend on the order in which blocks run. Calls that overlap on the GPU need a
+ * workspace each. */
+int pg_attention(const KvePgShape *shape, const void *q, long long q_row_stride,
+                 const void *K_prefix, const void *V_prefix, long long prefix_prompt_stride,
+                 long long prefix_head_stride, long long prefix_row_stride,
+                 const int32_t *prefix_len, const void *K_pages, const void *V_pages,
+                 const int32_t *block_table, const int32_t *len, const int32_t *q_start,
+                 const int32_t *row_req, void *out, float *lse_out, void *workspace,
+                 size_t ws_bytes, void *stream);
+
 /* ---- diagnostics ---------------------------------------------------------------------------- */
 
 /* Message of the last failing call on this thread ("" if none). Valid until the next call. */
@@ -324,7 +420,8 @@ const char *kve_last_error(void);
 
 /* Synchronises `stream`, then reads and clears the device error word that bounded on-device
  * waits and device-side index checks set. Returns KVE_OK, KVE_ETIMEOUT (a wait gave up),
- * KVE_EINVAL (cc_surprise met a token id outside [0, vocab)) or KVE_ECUDA. */
+ * KVE_EINVAL (cc_surprise met a token id outside [0, vocab), or pg_append or pg_attention a slot or
+ * page id outside the pool) or KVE_ECUDA. */
 int kve_check_device(void *stream);
 
 /* Self-test of the bounded on-device waits: launches one CTA whose thread waits, through the same

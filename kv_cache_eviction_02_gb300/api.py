@@ -29,7 +29,8 @@ EXPORTED = ("lorekv_prepare_wo", "lorekv_workspace_size", "lorekv_score",
             "kve_selftest_wait_timeout", "lorekv_score_noalloc",
             "cc_workspace_size", "cc_surprise", "cc_select_compact", "cc_cache_create",
             "cc_cache_append", "cc_cache_refresh", "cc_cache_step", "cc_cache_export",
-            "cc_cache_length", "cc_cache_seen", "cc_cache_destroy")
+            "cc_cache_length", "cc_cache_seen", "cc_cache_destroy",
+            "pg_plan", "pg_append", "pg_workspace_size", "pg_attention")
 
 
 class KveError(RuntimeError):
@@ -53,6 +54,12 @@ class KveCcShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("n_seq", "n_q_heads", "n_kv_heads", "d_head",
                                              "d_model", "n_tokens", "vocab", "dtype", "sink",
                                              "keep_J")]
+
+
+class KvePgShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("n_prompts", "fan", "n_q_heads", "n_kv_heads", "d_head",
+                                             "n_prefix", "page_size", "n_pages", "max_pages",
+                                             "n_rows", "max_new", "dtype")]
 
 
 _lib = None
@@ -105,6 +112,12 @@ def lib():
         L.cc_cache_seen.argtypes = [P]
         L.cc_cache_destroy.argtypes = [P]
         L.cc_cache_destroy.restype = None
+        GS, LL = ctypes.POINTER(KvePgShape), ctypes.c_longlong
+        L.pg_plan.argtypes = [GS, P, P, P, P, P, P, P, P, P, P, P, P]
+        L.pg_append.argtypes = [GS, P, P, LL, LL, P, P, P, P]
+        L.pg_workspace_size.argtypes = [GS]
+        L.pg_workspace_size.restype = Z
+        L.pg_attention.argtypes = [GS, P, LL, P, P, LL, LL, LL, P, P, P, P, P, P, P, P, P, P, Z, P]
         _lib = L
     return _lib
 
@@ -417,6 +430,216 @@ class CcCache:
             self.close()
         except Exception:
             pass
+
+
+# ---- shared-prompt decoding ------------------------------------------------------------------------
+@dataclass(frozen=True)
+class PgProblem:
+    """Shape of shared-prompt decoding (the C struct KvePgShape): n_prompts cached prompts, each
+    continued by `fan` requests whose own rows lie in pages. n_rows: rows of a step's packed arrays;
+    max_new: the most rows a request adds in a step."""
+    n_prompts: int
+    fan: int
+    n_q_heads: int
+    n_kv_heads: int
+    d_head: int
+    n_prefix: int
+    page_size: int
+    n_pages: int
+    max_pages: int
+    n_rows: int
+    max_new: int
+    dtype: int
+
+    def shape(self) -> KvePgShape:
+        return KvePgShape(self.n_prompts, self.fan, self.n_q_heads, self.n_kv_heads, self.d_head,
+                          self.n_prefix, self.page_size, self.n_pages, self.max_pages, self.n_rows,
+                          self.max_new, self.dtype)
+
+    @property
+    def requests(self) -> int:
+        return self.n_prompts * self.fan
+
+    @property
+    def pool_elements(self) -> int:
+        """Elements of K_pages (and of V_pages): [n_pages][n_kv_heads][page_size][d_head]."""
+        return self.n_pages * self.n_kv_heads * self.page_size * self.d_head
+
+
+def _here(t, device):
+    """t's address; t must be on `device` (the stream's)."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.device != device:
+        raise ValueError(f"tensor on {t.device}; the call's CUDA device is {device}")
+    return t.data_ptr()
+
+
+def _device_of(stream):
+    """The device the call launches on: the current one, which must be the stream's."""
+    dev = torch.cuda.current_device()
+    if getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"stream on cuda:{stream.device_index}; the current device is cuda:{dev}")
+    return torch.device("cuda", dev)
+
+
+def _pg(t, name, dtype, numel):
+    """_sized without the address: the checks come first, the device last."""
+    if t is None or isinstance(t, int):
+        return t
+    if isinstance(dtype, int):
+        dtype = _TORCH_DTYPE[dtype]
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, the shape declares {dtype}")
+    if t.numel() < numel:
+        raise ValueError(f"{name}: {t.numel()} elements, the shape needs {numel}")
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must be CUDA tensors")
+    if not t.is_contiguous():
+        raise ValueError("tensor arguments must be contiguous")
+    return t
+
+
+def _pg_rows(t, name, dtype, rows, heads, d):
+    """Row stride (elements) of packed rows [rows][heads][d] whose rows may lie apart (slices of a
+    wider projection); a tensor of another shape has to be contiguous."""
+    if t is None or isinstance(t, int):
+        return heads * d
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, d):
+        _pg(t, name, dtype, rows * heads * d)
+        return heads * d
+    if t.dtype != _TORCH_DTYPE[dtype]:
+        raise ValueError(f"{name}: dtype {t.dtype}, the shape declares {_TORCH_DTYPE[dtype]}")
+    if t.shape[0] < rows:
+        raise ValueError(f"{name}: {t.shape[0]} rows of elements, the shape needs {rows}")
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must be CUDA tensors")
+    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * d
+
+
+def _pg_prefix(t, name, pb):
+    """(prompt, head, row) strides of a prompt cache [n_prompts][n_kv_heads][>= n_prefix][d_head];
+    a tensor of another shape has to be contiguous with exactly n_prefix rows."""
+    if t is None or isinstance(t, int) or t.dim() != 4:
+        _pg(t, name, pb.dtype, pb.n_prompts * pb.n_kv_heads * pb.n_prefix * pb.d_head)
+        row = pb.n_prefix * pb.d_head
+        return pb.n_kv_heads * row, row, pb.d_head
+    if t.dtype != _TORCH_DTYPE[pb.dtype]:
+        raise ValueError(f"{name}: dtype {t.dtype}, the shape declares {_TORCH_DTYPE[pb.dtype]}")
+    if (tuple(t.shape[:2]) != (pb.n_prompts, pb.n_kv_heads) or t.shape[2] < pb.n_prefix or
+            t.shape[3] != pb.d_head):
+        raise ValueError(f"{name}: {tuple(t.shape)} elements, the shape needs "
+                         f"{(pb.n_prompts, pb.n_kv_heads, pb.n_prefix, pb.d_head)}")
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must be CUDA tensors")
+    if pb.d_head > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name}: a head's row must be contiguous")
+    return t.stride()[:3]
+
+
+def pg_plan(pb: PgProblem, new_len, len_in, pool_in, free_pages, block_table, len_out, pool_out,
+            q_start, row_req, row_pos, slot_map, stream=None):
+    """Block tables and slot maps of one step from the requests' lengths. len_out may be len_in and
+    pool_out may be pool_in."""
+    sh, R, n, i32 = pb.shape(), pb.requests, pb.n_rows, torch.int32
+    args = (_pg(new_len, "new_len", i32, R), _pg(len_in, "len_in", i32, R),
+            _pg(pool_in, "pool_in", i32, 4), _pg(free_pages, "free_pages", i32, pb.n_pages),
+            _pg(block_table, "block_table", i32, R * pb.max_pages),
+            _pg(len_out, "len_out", i32, R), _pg(pool_out, "pool_out", i32, 4),
+            _pg(q_start, "q_start", i32, R + 1), _pg(row_req, "row_req", i32, n),
+            _pg(row_pos, "row_pos", i32, n), _pg(slot_map, "slot_map", i32, n))
+    dev = _device_of(stream)
+    _check(lib().pg_plan(ctypes.byref(sh), *(_here(t, dev) for t in args), _stream(stream)))
+
+
+def pg_append(pb: PgProblem, K_new, V_new, slot_map, K_pages, V_pages, stream=None):
+    """Stores a step's K/V rows [n_rows][n_kv_heads][d_head] into the pages slot_map names. The rows
+    may be slices of a wider projection's output."""
+    sh = pb.shape()
+    kr = _pg_rows(K_new, "K_new", pb.dtype, pb.n_rows, pb.n_kv_heads, pb.d_head)
+    vr = _pg_rows(V_new, "V_new", pb.dtype, pb.n_rows, pb.n_kv_heads, pb.d_head)
+    args = (_pg(slot_map, "slot_map", torch.int32, pb.n_rows),
+            _pg(K_pages, "K_pages", pb.dtype, pb.pool_elements),
+            _pg(V_pages, "V_pages", pb.dtype, pb.pool_elements))
+    dev = _device_of(stream)
+    _check(lib().pg_append(ctypes.byref(sh), _here(K_new, dev), _here(V_new, dev), kr, vr,
+                           *(_here(t, dev) for t in args), _stream(stream)))
+
+
+def pg_workspace_size(pb: PgProblem) -> int:
+    sh = pb.shape()
+    return int(lib().pg_workspace_size(ctypes.byref(sh)))
+
+
+def pg_attention(pb: PgProblem, q, K_prefix, V_prefix, prefix_len, K_pages, V_pages, block_table,
+                 lens, q_start, row_req, out, lse_out, workspace, stream=None):
+    """Attention of a step's rows over their prompt and their requests' own rows. q [n_rows]
+    [n_q_heads][d_head] may be a slice of a wider projection's output; K_prefix and V_prefix
+    [n_prompts][n_kv_heads][>= n_prefix][d_head] may be a layer's slice of a larger cache (the same
+    strides for both). prefix_len and lse_out may be None."""
+    sh, R, i32 = pb.shape(), pb.requests, torch.int32
+    qr = _pg_rows(q, "q", pb.dtype, pb.n_rows, pb.n_q_heads, pb.d_head)
+    ps = _pg_prefix(K_prefix, "K_prefix", pb)
+    if _pg_prefix(V_prefix, "V_prefix", pb) != ps:
+        raise ValueError("V_prefix: the strides differ from K_prefix's")
+    pages = (_pg(prefix_len, "prefix_len", i32, pb.n_prompts),
+             _pg(K_pages, "K_pages", pb.dtype, pb.pool_elements),
+             _pg(V_pages, "V_pages", pb.dtype, pb.pool_elements),
+             _pg(block_table, "block_table", i32, R * pb.max_pages), _pg(lens, "lens", i32, R),
+             _pg(q_start, "q_start", i32, R + 1), _pg(row_req, "row_req", i32, pb.n_rows),
+             _pg(out, "out", pb.dtype, pb.n_rows * pb.n_q_heads * pb.d_head),
+             _pg(lse_out, "lse_out", torch.float32, pb.n_rows * pb.n_q_heads))
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    dev = _device_of(stream)
+    _check(lib().pg_attention(ctypes.byref(sh), _here(q, dev), qr, _here(K_prefix, dev),
+                              _here(V_prefix, dev), *ps, *(_here(t, dev) for t in pages),
+                              _here(workspace, dev), ws_bytes, _stream(stream)))
+
+
+class PgCache:
+    """Owns what shared-prompt decoding keeps between steps: the page pools of n_layers layers, the
+    block table, lengths and free pages (one set for all layers: a token takes the same slot in
+    every layer), the row arrays of the current step and the attention workspace. A step is
+    ``plan`` once, then per layer ``append`` and ``attend``; every call only enqueues work, so a
+    step can be captured into a CUDA graph and replayed (new_len and the tensors in place)."""
+
+    def __init__(self, pb: PgProblem, n_layers: int = 1, device="cuda"):
+        size = pg_workspace_size(pb)
+        if size == 0:
+            raise KveError(KVE_EINVAL, "PgCache: invalid shape")
+        dev, dt, i32 = torch.device(device), _TORCH_DTYPE[pb.dtype], torch.int32
+        R = pb.requests
+        self.pb = pb
+        self.K_pages = torch.zeros(n_layers, pb.n_pages, pb.n_kv_heads, pb.page_size, pb.d_head,
+                                   dtype=dt, device=dev)
+        self.V_pages = torch.zeros_like(self.K_pages)
+        self.block_table = torch.full((R, pb.max_pages), -1, dtype=i32, device=dev)
+        self.free_pages = torch.arange(pb.n_pages, dtype=i32, device=dev)
+        self.pool = torch.tensor([0, pb.n_pages, 0, 0], dtype=i32, device=dev)
+        self.lens = torch.zeros(R, dtype=i32, device=dev)
+        self.q_start = torch.zeros(R + 1, dtype=i32, device=dev)
+        self.row_req = torch.full((pb.n_rows,), -1, dtype=i32, device=dev)
+        self.row_pos = torch.full_like(self.row_req, -1)
+        self.slot_map = torch.full_like(self.row_req, -1)
+        self.workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+
+    def plan(self, new_len, stream=None):
+        """Takes (or returns) pages for a step in which request r adds new_len[r] rows (int32)."""
+        pg_plan(self.pb, new_len, self.lens, self.pool, self.free_pages, self.block_table,
+                self.lens, self.pool, self.q_start, self.row_req, self.row_pos, self.slot_map,
+                stream)
+
+    def append(self, layer, K_new, V_new, stream=None):
+        pg_append(self.pb, K_new, V_new, self.slot_map, self.K_pages[layer], self.V_pages[layer],
+                  stream)
+
+    def attend(self, layer, q, K_prefix, V_prefix, out, lse_out=None, prefix_len=None,
+               stream=None):
+        pg_attention(self.pb, q, K_prefix, V_prefix, prefix_len, self.K_pages[layer],
+                     self.V_pages[layer], self.block_table, self.lens, self.q_start, self.row_req,
+                     out, lse_out, self.workspace, stream)
 
 
 def kve_check_device(stream=None):

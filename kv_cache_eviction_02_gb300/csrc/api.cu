@@ -9,7 +9,7 @@
 #include <string>
 #include <vector>
 
-#include "kve_internal.cuh"
+#include "pages.cuh"
 
 namespace kve {
 
@@ -369,6 +369,11 @@ int kve_check_device(void *stream) {
             return fail(KVE_ETIMEOUT, "a bounded on-device wait gave up (error word 0x%x)", word);
         if (word & KVE_DEVERR_BADINDEX)
             return fail(KVE_EINVAL, "a token id outside [0, vocab) reached cc_surprise (error word 0x%x)",
+                        word);
+        if (word & KVE_DEVERR_BADPAGE)
+            return fail(KVE_EINVAL,
+                        "a slot or page id outside the pool reached pg_append or pg_attention "
+                        "(error word 0x%x)",
                         word);
         return fail(KVE_ECUDA, "device error word 0x%x", word);
     }
@@ -955,6 +960,140 @@ void h2o_state_destroy(KveH2O *h) {
     cudaFree(s.hole);
     cudaFree(s.prefill_part);
     delete h;
+}
+
+// ---- shared-prompt decoding ------------------------------------------------------------------------
+static bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+static int pg_common(const char *fn, const KvePgShape *shape, PgDims *D) {
+    if (int s = injected()) return s;
+    const char *why;
+    if (!shape) return fail(KVE_EINVAL, "%s: null shape", fn);
+    if (shape->dtype != KVE_F32 && shape->dtype != KVE_BF16 && shape->dtype != KVE_F16)
+        return fail(KVE_EDTYPE, "%s: dtype must be KVE_F32, KVE_BF16 or KVE_F16", fn);
+    if (!pg_dims(shape, D, &why)) return fail(KVE_EINVAL, "%s: %s", fn, why);
+    return KVE_OK;
+}
+
+int pg_plan(const KvePgShape *shape, const int32_t *new_len, const int32_t *len_in,
+            const int32_t *pool_in, int32_t *free_pages, int32_t *block_table, int32_t *len_out,
+            int32_t *pool_out, int32_t *q_start, int32_t *row_req, int32_t *row_pos,
+            int32_t *slot_map, void *stream) {
+    PgDims D;
+    if (int s = pg_common("pg_plan", shape, &D)) return s;
+    if (!new_len || !len_in || !pool_in || !free_pages || !block_table || !len_out || !pool_out ||
+        !q_start || !row_req || !row_pos || !slot_map)
+        return fail(KVE_EINVAL, "pg_plan: null argument");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const PgPlanArgs A{new_len, len_in,   pool_in, free_pages, block_table, len_out,
+                       pool_out, q_start, row_req, row_pos,    slot_map};
+    cudaError_t e;
+    {
+        ProfScope ps("pg_plan", 1, st);
+        e = launch_pg_plan(D, A, st);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "pg_plan: launch");
+    return KVE_OK;
+}
+
+int pg_append(const KvePgShape *shape, const void *K_new, const void *V_new,
+              long long K_row_stride, long long V_row_stride, const int32_t *slot_map,
+              void *K_pages, void *V_pages, void *stream) {
+    PgDims D;
+    if (int s = pg_common("pg_append", shape, &D)) return s;
+    if (!K_new || !V_new || !slot_map || !K_pages || !V_pages)
+        return fail(KVE_EINVAL, "pg_append: null argument");
+    const long long es = (long long)dtype_size(D.dtype), row = (long long)D.Hkv * D.d;
+    if (K_row_stride < row || V_row_stride < row || K_row_stride * es % 16 != 0 ||
+        V_row_stride * es % 16 != 0)
+        return fail(KVE_EINVAL, "pg_append: row strides must hold a row and be multiples of 16 bytes");
+    if (!aligned16(K_new) || !aligned16(V_new) || !aligned16(K_pages) || !aligned16(V_pages))
+        return fail(KVE_EINVAL, "pg_append: K and V must be 16-byte aligned");
+    unsigned *err = device_error_word();
+    if (!err) return fail(KVE_ECUDA, "pg_append: no device error word");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    {
+        ProfScope ps("pg_append", 1, st);
+        e = launch_pg_append(D, K_new, V_new, K_row_stride, V_row_stride, slot_map, K_pages,
+                             V_pages, err, st);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "pg_append: launch");
+    return KVE_OK;
+}
+
+size_t pg_workspace_size(const KvePgShape *shape) {
+    PgDims D;
+    const char *why;
+    if (!pg_dims(shape, &D, &why)) return 0;
+    return pg_ws_layout(D).total;
+}
+
+int pg_attention(const KvePgShape *shape, const void *q, long long q_row_stride,
+                 const void *K_prefix, const void *V_prefix, long long prefix_prompt_stride,
+                 long long prefix_head_stride, long long prefix_row_stride,
+                 const int32_t *prefix_len, const void *K_pages, const void *V_pages,
+                 const int32_t *block_table, const int32_t *len, const int32_t *q_start,
+                 const int32_t *row_req, void *out, float *lse_out, void *workspace,
+                 size_t ws_bytes, void *stream) {
+    PgDims D;
+    if (int s = pg_common("pg_attention", shape, &D)) return s;
+    if (!q || !K_pages || !V_pages || !block_table || !len || !q_start || !row_req || !out ||
+        (D.n > 0 && (!K_prefix || !V_prefix)))
+        return fail(KVE_EINVAL, "pg_attention: null argument");
+    const long long es = (long long)dtype_size(D.dtype);
+    if (q_row_stride < (long long)D.Hq * D.d || q_row_stride * es % 16 != 0)
+        return fail(KVE_EINVAL, "pg_attention: q_row_stride must hold a row and be a multiple of 16 bytes");
+    if (D.n > 0) {
+        // the stride of a dimension of one entry is never used
+        if (D.S == 1) prefix_prompt_stride = (long long)D.Hkv * D.n * D.d;
+        if (D.Hkv == 1) prefix_head_stride = (long long)D.n * D.d;
+        if (D.n == 1) prefix_row_stride = D.d;
+        for (long long s : {prefix_prompt_stride, prefix_head_stride, prefix_row_stride})
+            if (s < D.d || s * es % 16 != 0 || s >= (1LL << 36))
+                return fail(KVE_EINVAL, "pg_attention: the prompt's strides must hold a head row and "
+                                        "be multiples of 16 bytes");
+    }
+    if (!aligned16(q) || !aligned16(K_pages) || !aligned16(V_pages) || !aligned16(out) ||
+        (D.n > 0 && (!aligned16(K_prefix) || !aligned16(V_prefix))))
+        return fail(KVE_EINVAL, "pg_attention: q, K, V and out must be 16-byte aligned");
+    const PgWorkspace W = pg_ws_layout(D);
+    if (!workspace || ws_bytes < W.total)
+        return fail(KVE_EWORKSPACE, "pg_attention: workspace of %zu bytes needed, %zu given", W.total,
+                    workspace ? ws_bytes : (size_t)0);
+    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+        return fail(KVE_EINVAL, "pg_attention: workspace must be 256-byte aligned");
+    unsigned *err = device_error_word();
+    if (!err) return fail(KVE_ECUDA, "pg_attention: no device error word");
+    PgAttn A{};
+    A.q = q;
+    A.q_row = q_row_stride;
+    A.Kp = K_prefix;
+    A.Vp = V_prefix;
+    A.p_prompt = prefix_prompt_stride;
+    A.p_head = prefix_head_stride;
+    A.p_tok = prefix_row_stride;
+    A.plen = D.n > 0 ? prefix_len : nullptr;
+    A.K = K_pages;
+    A.V = V_pages;
+    A.table = block_table;
+    A.len = len;
+    A.q_start = q_start;
+    A.row_req = row_req;
+    A.out = out;
+    A.lse = lse_out;
+    char *ws = static_cast<char *>(workspace);
+    A.part_ml = reinterpret_cast<float2 *>(ws + W.part_ml);
+    A.part_o = reinterpret_cast<float *>(ws + W.part_o);
+    A.err = err;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    {
+        ProfScope ps("pg_attention", 2, st);
+        e = launch_pg_attention(D, A, st);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "pg_attention: launch");
+    return KVE_OK;
 }
 
 }  // extern "C"

@@ -31,7 +31,8 @@ inline size_t dtype_size(int dt) { return dt == KVE_F32 ? 4 : 2; }
 // ---- device error word -------------------------------------------------------------------------
 // Bit 0: a bounded wait on an mbarrier gave up. The host reads and clears it in kve_check_device.
 // Bit 1: a token id outside [0, vocab) reached the counter-causal logit kernel.
-enum : unsigned { KVE_DEVERR_TIMEOUT = 1u, KVE_DEVERR_BADINDEX = 2u };
+// Bit 2: a page id or slot outside the pool reached pg_attention or pg_append.
+enum : unsigned { KVE_DEVERR_TIMEOUT = 1u, KVE_DEVERR_BADINDEX = 2u, KVE_DEVERR_BADPAGE = 4u };
 unsigned *device_error_word();  // device address of the word in the current context
 
 // Device address of a __device__ variable (its host-side stand-in `symbol`) in the calling
