@@ -4,16 +4,18 @@
 
 namespace kve {
 
-// Splits of the prompt and of the requests' own rows: enough CTAs to fill the GPU, each with some
-// hundred tokens at least. Own rows are split by the table's width, since lengths are known on the
-// device only; the CTAs of splits that a request does not reach return at once.
+// Splits of the prompt and of the requests' own rows.
+//   Prompt on tcgen05: one CTA per SM, so the split count that minimises
+//     ceil(items * splits / 152) * (tiles per split + 4): a CTA's set-up and the partial result that
+//     it writes and the join reads cost about four tiles.
+//   Elsewhere: enough CTAs to fill the GPU a few times, at least 128 tokens each.
+// Own rows are split by the table's width, since lengths are known on the device only; the CTAs of
+// splits that a request does not reach return at once.
 static void pg_split(PgDims *D) {
-    const long long rows = (long long)D->F * D->max_new < D->rows ? (long long)D->F * D->max_new
-                                                                 : D->rows;
-    const long long pitems = (long long)D->S * D->Hkv * ((rows * D->g + 15) / 16);
-    const long long sitems = (long long)D->R * D->Hkv * (((long long)D->max_new * D->g + 15) / 16);
-    auto split = [](long long items, long long n, int *count, int *len) {
-        long long want = (152 * 8 + items - 1) / items, most = (n + 127) / 128;
+    auto split = [](long long items, long long n, long long ctas, long long least, int *count,
+                    int *len) {
+        long long want = (ctas + items - 1) / items;
+        const long long most = (n + least - 1) / least;
         if (want > most) want = most;
         if (want > 64) want = 64;
         if (want < 1) want = 1;
@@ -21,10 +23,30 @@ static void pg_split(PgDims *D) {
         *len = (int)per;
         *count = (int)((n + per - 1) / per);
     };
+    const long long prow = D->group_rows() * D->g, orow = (long long)D->max_new * D->g;
     D->np = 0;
     D->psplit = 128;
-    if (D->n > 0) split(pitems, D->n, &D->np, &D->psplit);
-    split(sitems, D->cap(), &D->ns, &D->ssplit);
+    if (D->n > 0 && pg_prompt_tc(*D)) {
+        const long long per = (long long)pg_tile_rows(*D) * pg_prompt_pairs(*D);
+        const long long items = (long long)D->S * D->Hkv * ((D->group_rows() + per - 1) / per);
+        const long long tiles = (D->n + 127LL) / 128;
+        long long best = -1, len = 1;
+        for (long long p = 1; p <= 64 && p <= tiles; ++p) {
+            const long long waves = (items * p + 151) / 152, t = (tiles + p - 1) / p;
+            const long long cost = waves * (t + 4);
+            if (best < 0 || cost < best) {
+                best = cost;
+                len = t;
+            }
+        }
+        D->psplit = (int)(len * 128);
+        D->np = (int)((tiles + len - 1) / len);
+    } else if (D->n > 0) {
+        split((long long)D->S * D->Hkv * ((prow + 15) / 16), D->n, 152 * 8, 128, &D->np,
+              &D->psplit);
+    }
+    split((long long)D->R * D->Hkv * ((orow + 15) / 16), D->cap(), 152 * 8, 256, &D->ns,
+          &D->ssplit);
 }
 
 // ---- sizes ---------------------------------------------------------------------------------------
@@ -307,10 +329,10 @@ constexpr int kSimtRows = 16, kSimtTok = 32, kSimtThreads = 128;
 // own rows. Eight threads share a row: each scores 4 of a tile's 32 tokens and holds D/8 of the
 // row's output columns; fp32 throughout, running maximum and sum in the log2 domain.
 // Blocks 0 .. prompt_ctas - 1 take the prompt's part, the others the requests'.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kSimtThreads)
     pg_attn_simt_kernel(PgDims D_, PgAttn A, int prompt_ctas, int prompt_blocks, int own_blocks) {
-    constexpr int LD = D + 4, VEC = 16 / sizeof(T), WPR = D / VEC, NC = D / 32;
+    constexpr int LD = D + 4, WPR = D / 4, NC = D / 32;
     __shared__ __align__(16) float qs[kSimtRows][LD], ks[kSimtTok][LD], vs[kSimtTok][LD];
     __shared__ float ps[kSimtRows][kSimtTok + 1];
     const bool own = (int)blockIdx.x >= prompt_ctas;
@@ -340,8 +362,8 @@ __global__ void __launch_bounds__(kSimtThreads)
 
     const int row = threadIdx.x >> 3, sub = threadIdx.x & 7;
     const float k1 = kLog2e * rsqrtf((float)D);
-    const T *Kb = static_cast<const T *>(own ? A.K : A.Kp);
-    const T *Vb = static_cast<const T *>(own ? A.V : A.Vp);
+    const float *Kb = static_cast<const float *>(own ? A.K : A.Kp);
+    const float *Vb = static_cast<const float *>(own ? A.V : A.Vp);
     // the launch has blocks for max_new rows a request; a request refused for packing more leaves
     // more rows to go through
     for (int rb = rb0; rb * kSimtRows < nrow; rb += nblk) {
@@ -354,8 +376,8 @@ __global__ void __launch_bounds__(kSimtThreads)
             const int i = e / D, c = e % D, ri = rb * kSimtRows + i;
             float v = 0.f;
             if (ri < nrow)
-                v = to_f(static_cast<const T *>(A.q)[(tok0 + ri / D_.g) * A.q_row +
-                                                     (size_t)(kh * D_.g + ri % D_.g) * D + c]);
+                v = static_cast<const float *>(A.q)[(tok0 + ri / D_.g) * A.q_row +
+                                                    (size_t)(kh * D_.g + ri % D_.g) * D + c];
             qs[i][c] = v;
         }
         float m = kPgNoMax, l = 0.f, acc[NC * 4];
@@ -364,26 +386,22 @@ __global__ void __launch_bounds__(kSimtThreads)
         for (int t = t0; t < t1; t += kSimtTok) {
             __syncthreads();
             for (int e = threadIdx.x; e < kSimtTok * WPR; e += kSimtThreads) {
-                const int i = e / WPR, c = (e % WPR) * VEC, j = t + i;
-                uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
+                const int i = e / WPR, c = (e % WPR) * 4, j = t + i;
+                float4 kw = make_float4(0.f, 0.f, 0.f, 0.f), vw = kw;
                 if (j < t1) {
                     size_t at;
                     if (own) {
-                        const int page = pg_page(A.table + (size_t)u * D_.maxp, j, D_.lgP, D_.npages,
-                                                 A.err);
+                        const int page = pg_page(A.table + (size_t)u * D_.maxp, j, D_.lgP,
+                                                 D_.npages, A.err);
                         at = ((((size_t)page * D_.Hkv + kh) << D_.lgP) + (j & (D_.P - 1))) * D;
                     } else {
                         at = u * A.p_prompt + kh * A.p_head + j * A.p_tok;
                     }
-                    kw = __ldg(reinterpret_cast<const uint4 *>(Kb + at + c));
-                    vw = __ldg(reinterpret_cast<const uint4 *>(Vb + at + c));
+                    kw = __ldg(reinterpret_cast<const float4 *>(Kb + at + c));
+                    vw = __ldg(reinterpret_cast<const float4 *>(Vb + at + c));
                 }
-                const T *kt = reinterpret_cast<const T *>(&kw), *vt = reinterpret_cast<const T *>(&vw);
-#pragma unroll
-                for (int x = 0; x < VEC; ++x) {
-                    ks[i][c + x] = to_f(kt[x]);
-                    vs[i][c + x] = to_f(vt[x]);
-                }
+                *reinterpret_cast<float4 *>(&ks[i][c]) = kw;
+                *reinterpret_cast<float4 *>(&vs[i][c]) = vw;
             }
             __syncthreads();
             float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -497,34 +515,26 @@ __global__ void __launch_bounds__(256) pg_join_kernel(PgDims D_, PgAttn A) {
     if (A.lse && lane == 0) A.lse[w] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t attn_simt(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
-    const long long prow = (long long)(D_.rows < (long long)D_.F * D_.max_new
-                                           ? D_.rows
-                                           : (long long)D_.F * D_.max_new) * D_.g;
-    const int pb = (int)((prow + kSimtRows - 1) / kSimtRows);
-    const int ob = (int)(((long long)D_.max_new * D_.g + kSimtRows - 1) / kSimtRows);
+    const long long pb = (D_.group_rows() * D_.g + kSimtRows - 1) / kSimtRows;
+    const long long ob = ((long long)D_.max_new * D_.g + kSimtRows - 1) / kSimtRows;
     const long long pc = (long long)D_.S * D_.Hkv * pb * D_.np;
     const long long oc = (long long)D_.R * D_.Hkv * ob * D_.ns;
     if (pc + oc > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    pg_attn_simt_kernel<T, D><<<(unsigned)(pc + oc), kSimtThreads, 0, st>>>(D_, A, (int)pc, pb, ob);
-    return cudaGetLastError();
-}
-
-template <typename T, int D>
-cudaError_t join(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
-    const long long warps = (long long)D_.rows * D_.Hq;
-    pg_join_kernel<T, D><<<(unsigned)((warps + 7) / 8), 256, 0, st>>>(D_, A);
+    pg_attn_simt_kernel<D><<<(unsigned)(pc + oc), kSimtThreads, 0, st>>>(D_, A, (int)pc, (int)pb,
+                                                                         (int)ob);
     return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t attention(const PgDims &D, const PgAttn &A, cudaStream_t st) {
-    cudaError_t e = D.d == 128 ? attn_simt<T, 128>(D, A, st)
-                               : (D.d == 64 ? attn_simt<T, 64>(D, A, st) : attn_simt<T, 32>(D, A, st));
-    if (e != cudaSuccess) return e;
-    return D.d == 128 ? join<T, 128>(D, A, st)
-                      : (D.d == 64 ? join<T, 64>(D, A, st) : join<T, 32>(D, A, st));
+cudaError_t join(const PgDims &D, const PgAttn &A, cudaStream_t st) {
+    const long long warps = (long long)D.rows * D.Hq;
+    const unsigned ctas = (unsigned)((warps + 7) / 8);
+    if (D.d == 128) pg_join_kernel<T, 128><<<ctas, 256, 0, st>>>(D, A);
+    else if (D.d == 64) pg_join_kernel<T, 64><<<ctas, 256, 0, st>>>(D, A);
+    else pg_join_kernel<T, 32><<<ctas, 256, 0, st>>>(D, A);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -574,9 +584,16 @@ cudaError_t launch_pg_append(const PgDims &D, const void *K_new, const void *V_n
 }
 
 cudaError_t launch_pg_attention(const PgDims &D, const PgAttn &A, cudaStream_t st) {
-    if (D.dtype == KVE_F32) return attention<float>(D, A, st);
-    if (D.dtype == KVE_BF16) return attention<__nv_bfloat16>(D, A, st);
-    return attention<__half>(D, A, st);
+    if (D.dtype == KVE_F32) {
+        cudaError_t e = D.d == 128 ? attn_simt<128>(D, A, st)
+                                   : (D.d == 64 ? attn_simt<64>(D, A, st) : attn_simt<32>(D, A, st));
+        return e != cudaSuccess ? e : join<float>(D, A, st);
+    }
+    cudaError_t e = cudaSuccess;
+    if (D.n > 0) e = pg_prompt_tc(D) ? launch_pg_prompt_tc(D, A, st) : launch_pg_prompt_mma(D, A, st);
+    if (e == cudaSuccess) e = launch_pg_own_mma(D, A, st);
+    if (e != cudaSuccess) return e;
+    return D.dtype == KVE_BF16 ? join<__nv_bfloat16>(D, A, st) : join<__half>(D, A, st);
 }
 
 }  // namespace kve

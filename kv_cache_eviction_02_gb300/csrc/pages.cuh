@@ -15,6 +15,10 @@ struct PgDims {
     int rows, max_new, dtype;
     int np, psplit;            // prompt splits and their tokens (0 without a prompt)
     int ns, ssplit;            // splits of a request's own rows and their tokens
+    // rows behind one prompt, when no request packs more than max_new
+    __host__ __device__ long long group_rows() const {
+        return (long long)F * max_new < rows ? (long long)F * max_new : rows;
+    }
     __host__ __device__ int cap() const { return maxp * P; }
 };
 
@@ -25,6 +29,17 @@ struct PgWorkspace {
 
 bool pg_dims(const KvePgShape *sh, PgDims *D, const char **why);
 PgWorkspace pg_ws_layout(const PgDims &D);
+
+// The prompt's kernel on tcgen05 takes 16-bit types and d_head 64 or 128: new rows per 128-row tile
+// (whole groups of query heads), and row tiles per CTA. Two tiles share one K/V stream and take turns
+// on the tensor pipe; an odd small number of tiles runs one per CTA, since a half-empty pair would
+// leave the pipe idle in its turn.
+inline bool pg_prompt_tc(const PgDims &D) { return D.dtype != KVE_F32 && D.d >= 64; }
+inline int pg_tile_rows(const PgDims &D) { return 128 / D.g; }
+inline int pg_prompt_pairs(const PgDims &D) {
+    const long long tiles = (D.group_rows() + pg_tile_rows(D) - 1) / pg_tile_rows(D);
+    return tiles % 2 == 0 || tiles >= 9 ? 2 : 1;
+}
 
 // Device pointers of one attention call. Strides in elements.
 struct PgAttn {
@@ -51,6 +66,9 @@ cudaError_t launch_pg_plan(const PgDims &D, const PgPlanArgs &A, cudaStream_t st
 cudaError_t launch_pg_append(const PgDims &D, const void *K_new, const void *V_new,
                              long long k_row, long long v_row, const int32_t *slots, void *K,
                              void *V, unsigned *err, cudaStream_t st);
+cudaError_t launch_pg_prompt_tc(const PgDims &D, const PgAttn &A, cudaStream_t st);
+cudaError_t launch_pg_prompt_mma(const PgDims &D, const PgAttn &A, cudaStream_t st);
+cudaError_t launch_pg_own_mma(const PgDims &D, const PgAttn &A, cudaStream_t st);
 cudaError_t launch_pg_attention(const PgDims &D, const PgAttn &A, cudaStream_t st);
 
 constexpr float kPgNoMax = -3e38f;  // running maximum before any visible token
