@@ -390,7 +390,8 @@ size_t pg_workspace_size(const KvePgShape *shape);
  *   out = sum_j a_j v_j, a = softmax_j(q.k_j / sqrt(d_head)) over the first prefix_len[r / fan] rows
  *   of the prompt and the own rows 0 .. len[r] - (q_start[r + 1] - q_start[r]) + i of the request.
  * Every prompt's K/V are read once for all its rows. Nothing to see: out 0 and lse -inf. Rows with
- * row_req < 0, or whose row_req is not the request that q_start gives, are left as they were.
+ * row_req < 0, whose row_req is not the request that q_start gives, or behind a request's first
+ * max_new rows are left as they were.
  *   q        [n_rows][n_q_heads][d_head], q_row_stride elements from one row to the next
  *   K_prefix, V_prefix [n_prompts][n_kv_heads][n_prefix][d_head] with the strides (elements) of
  *            prompt, head and row given: a layer's slice of a larger cache, or rows of several

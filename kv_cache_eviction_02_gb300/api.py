@@ -8,6 +8,7 @@ device, the call fails.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -456,121 +457,132 @@ class PgProblem:
                           self.n_prefix, self.page_size, self.n_pages, self.max_pages, self.n_rows,
                           self.max_new, self.dtype)
 
-    @property
+    @functools.cached_property
+    def c_shape(self):
+        """A pointer to shape(), made once."""
+        return ctypes.pointer(self.shape())
+
+    @functools.cached_property
+    def torch_dtype(self):
+        return _TORCH_DTYPE.get(self.dtype)
+
+    @functools.cached_property
     def requests(self) -> int:
         return self.n_prompts * self.fan
 
-    @property
+    @functools.cached_property
     def pool_elements(self) -> int:
         """Elements of K_pages (and of V_pages): [n_pages][n_kv_heads][page_size][d_head]."""
         return self.n_pages * self.n_kv_heads * self.page_size * self.d_head
 
 
-def _here(t, device):
-    """t's address; t must be on `device` (the stream's)."""
-    if t is None or isinstance(t, int):
-        return t
-    if t.device != device:
-        raise ValueError(f"tensor on {t.device}; the call's CUDA device is {device}")
-    return t.data_ptr()
+# These calls are made once per layer and decoded token, so their checks are kept to one pass over a
+# tensor's attributes; what fails is found out only when something did.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _device_of(stream):
-    """The device the call launches on: the current one, which must be the stream's."""
+def _pg_device(stream):
+    """Index of the device the call launches on: the current one, which must be the stream's."""
+    if not torch.cuda.is_initialized() and not torch.cuda.is_available():
+        return -2
     dev = torch.cuda.current_device()
-    if getattr(stream, "device_index", dev) != dev:
+    if stream is not None and getattr(stream, "device_index", dev) != dev:
         raise ValueError(f"stream on cuda:{stream.device_index}; the current device is cuda:{dev}")
-    return torch.device("cuda", dev)
+    return dev
 
 
-def _pg(t, name, dtype, numel):
-    """_sized without the address: the checks come first, the device last."""
-    if t is None or isinstance(t, int):
-        return t
-    if isinstance(dtype, int):
-        dtype = _TORCH_DTYPE[dtype]
+def _pg_stream(stream, dev):
+    if stream is None and _raw_stream is not None and dev >= 0:
+        return _raw_stream(dev)
+    return _stream(stream)
+
+
+def _pg_refuse(t, name, dtype, numel, dev):
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, the shape declares {dtype}")
     if t.numel() < numel:
         raise ValueError(f"{name}: {t.numel()} elements, the shape needs {numel}")
     if not t.is_cuda:
         raise ValueError("tensor arguments must be CUDA tensors")
-    if not t.is_contiguous():
-        raise ValueError("tensor arguments must be contiguous")
-    return t
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensor on {t.device}; the current CUDA device is cuda:{dev}")
+    raise ValueError("tensor arguments must be contiguous")
 
 
-def _pg_rows(t, name, dtype, rows, heads, d):
-    """Row stride (elements) of packed rows [rows][heads][d] whose rows may lie apart (slices of a
-    wider projection); a tensor of another shape has to be contiguous."""
-    if t is None or isinstance(t, int):
-        return heads * d
-    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, d):
-        _pg(t, name, dtype, rows * heads * d)
-        return heads * d
-    if t.dtype != _TORCH_DTYPE[dtype]:
-        raise ValueError(f"{name}: dtype {t.dtype}, the shape declares {_TORCH_DTYPE[dtype]}")
-    if t.shape[0] < rows:
-        raise ValueError(f"{name}: {t.shape[0]} rows of elements, the shape needs {rows}")
-    if not t.is_cuda:
-        raise ValueError("tensor arguments must be CUDA tensors")
-    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+def _pg(t, name, dtype, numel, dev):
+    """_sized, and on the call's device."""
+    if t is None or t.__class__ is int:
+        return t
+    if (t.dtype is not dtype or t.numel() < numel or t.get_device() != dev or
+            not t.is_contiguous()):
+        _pg_refuse(t, name, dtype, numel, dev)
+    return t.data_ptr()
+
+
+def _pg_rows(t, name, dtype, rows, heads, d, dev):
+    """Address and row stride (elements) of packed rows [rows][heads][d] whose rows may lie apart
+    (slices of a wider projection); a tensor of another shape has to be contiguous."""
+    if t is None or t.__class__ is int:
+        return t, heads * d
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
+        return _pg(t, name, dtype, rows * heads * d, dev), heads * d
+    if t.dtype is not dtype or shape[0] < rows or t.get_device() != dev:
+        _pg_refuse(t, name, dtype, rows * heads * d, dev)
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (heads > 1 and s1 != d):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * d
+    return t.data_ptr(), s0 if rows > 1 else heads * d
 
 
-def _pg_prefix(t, name, pb):
-    """(prompt, head, row) strides of a prompt cache [n_prompts][n_kv_heads][>= n_prefix][d_head];
-    a tensor of another shape has to be contiguous with exactly n_prefix rows."""
-    if t is None or isinstance(t, int) or t.dim() != 4:
-        _pg(t, name, pb.dtype, pb.n_prompts * pb.n_kv_heads * pb.n_prefix * pb.d_head)
-        row = pb.n_prefix * pb.d_head
-        return pb.n_kv_heads * row, row, pb.d_head
-    if t.dtype != _TORCH_DTYPE[pb.dtype]:
-        raise ValueError(f"{name}: dtype {t.dtype}, the shape declares {_TORCH_DTYPE[pb.dtype]}")
-    if (tuple(t.shape[:2]) != (pb.n_prompts, pb.n_kv_heads) or t.shape[2] < pb.n_prefix or
-            t.shape[3] != pb.d_head):
+def _pg_prefix(t, name, pb, dev):
+    """Address and (prompt, head, row) strides of a prompt cache [n_prompts][n_kv_heads]
+    [>= n_prefix][d_head]; a tensor of another shape has to be contiguous with n_prefix rows."""
+    row = pb.n_prefix * pb.d_head
+    numel = pb.n_prompts * pb.n_kv_heads * row
+    if t is None or t.__class__ is int or t.dim() != 4:
+        return _pg(t, name, pb.torch_dtype, numel, dev), pb.n_kv_heads * row, row, pb.d_head
+    S, H, n, d = t.shape
+    if S != pb.n_prompts or H != pb.n_kv_heads or n < pb.n_prefix or d != pb.d_head:
         raise ValueError(f"{name}: {tuple(t.shape)} elements, the shape needs "
                          f"{(pb.n_prompts, pb.n_kv_heads, pb.n_prefix, pb.d_head)}")
-    if not t.is_cuda:
-        raise ValueError("tensor arguments must be CUDA tensors")
-    if pb.d_head > 1 and t.stride(3) != 1:
+    if t.dtype is not pb.torch_dtype or t.get_device() != dev:
+        _pg_refuse(t, name, pb.torch_dtype, numel, dev)
+    s0, s1, s2, s3 = t.stride()
+    if d > 1 and s3 != 1:
         raise ValueError(f"{name}: a head's row must be contiguous")
-    return t.stride()[:3]
+    return t.data_ptr(), s0, s1, s2
 
 
 def pg_plan(pb: PgProblem, new_len, len_in, pool_in, free_pages, block_table, len_out, pool_out,
             q_start, row_req, row_pos, slot_map, stream=None):
     """Block tables and slot maps of one step from the requests' lengths. len_out may be len_in and
     pool_out may be pool_in."""
-    sh, R, n, i32 = pb.shape(), pb.requests, pb.n_rows, torch.int32
-    args = (_pg(new_len, "new_len", i32, R), _pg(len_in, "len_in", i32, R),
-            _pg(pool_in, "pool_in", i32, 4), _pg(free_pages, "free_pages", i32, pb.n_pages),
-            _pg(block_table, "block_table", i32, R * pb.max_pages),
-            _pg(len_out, "len_out", i32, R), _pg(pool_out, "pool_out", i32, 4),
-            _pg(q_start, "q_start", i32, R + 1), _pg(row_req, "row_req", i32, n),
-            _pg(row_pos, "row_pos", i32, n), _pg(slot_map, "slot_map", i32, n))
-    dev = _device_of(stream)
-    _check(lib().pg_plan(ctypes.byref(sh), *(_here(t, dev) for t in args), _stream(stream)))
+    R, n, i32, dev = pb.requests, pb.n_rows, torch.int32, _pg_device(stream)
+    _check(lib().pg_plan(
+        pb.c_shape, _pg(new_len, "new_len", i32, R, dev), _pg(len_in, "len_in", i32, R, dev),
+        _pg(pool_in, "pool_in", i32, 4, dev), _pg(free_pages, "free_pages", i32, pb.n_pages, dev),
+        _pg(block_table, "block_table", i32, R * pb.max_pages, dev),
+        _pg(len_out, "len_out", i32, R, dev), _pg(pool_out, "pool_out", i32, 4, dev),
+        _pg(q_start, "q_start", i32, R + 1, dev), _pg(row_req, "row_req", i32, n, dev),
+        _pg(row_pos, "row_pos", i32, n, dev), _pg(slot_map, "slot_map", i32, n, dev),
+        _pg_stream(stream, dev)))
 
 
 def pg_append(pb: PgProblem, K_new, V_new, slot_map, K_pages, V_pages, stream=None):
     """Stores a step's K/V rows [n_rows][n_kv_heads][d_head] into the pages slot_map names. The rows
     may be slices of a wider projection's output."""
-    sh = pb.shape()
-    kr = _pg_rows(K_new, "K_new", pb.dtype, pb.n_rows, pb.n_kv_heads, pb.d_head)
-    vr = _pg_rows(V_new, "V_new", pb.dtype, pb.n_rows, pb.n_kv_heads, pb.d_head)
-    args = (_pg(slot_map, "slot_map", torch.int32, pb.n_rows),
-            _pg(K_pages, "K_pages", pb.dtype, pb.pool_elements),
-            _pg(V_pages, "V_pages", pb.dtype, pb.pool_elements))
-    dev = _device_of(stream)
-    _check(lib().pg_append(ctypes.byref(sh), _here(K_new, dev), _here(V_new, dev), kr, vr,
-                           *(_here(t, dev) for t in args), _stream(stream)))
+    dt, n, dev = pb.torch_dtype, pb.n_rows, _pg_device(stream)
+    k, kr = _pg_rows(K_new, "K_new", dt, n, pb.n_kv_heads, pb.d_head, dev)
+    v, vr = _pg_rows(V_new, "V_new", dt, n, pb.n_kv_heads, pb.d_head, dev)
+    _check(lib().pg_append(
+        pb.c_shape, k, v, kr, vr, _pg(slot_map, "slot_map", torch.int32, n, dev),
+        _pg(K_pages, "K_pages", dt, pb.pool_elements, dev),
+        _pg(V_pages, "V_pages", dt, pb.pool_elements, dev), _pg_stream(stream, dev)))
 
 
 def pg_workspace_size(pb: PgProblem) -> int:
-    sh = pb.shape()
-    return int(lib().pg_workspace_size(ctypes.byref(sh)))
+    return int(lib().pg_workspace_size(pb.c_shape))
 
 
 def pg_attention(pb: PgProblem, q, K_prefix, V_prefix, prefix_len, K_pages, V_pages, block_table,
@@ -579,23 +591,26 @@ def pg_attention(pb: PgProblem, q, K_prefix, V_prefix, prefix_len, K_pages, V_pa
     [n_q_heads][d_head] may be a slice of a wider projection's output; K_prefix and V_prefix
     [n_prompts][n_kv_heads][>= n_prefix][d_head] may be a layer's slice of a larger cache (the same
     strides for both). prefix_len and lse_out may be None."""
-    sh, R, i32 = pb.shape(), pb.requests, torch.int32
-    qr = _pg_rows(q, "q", pb.dtype, pb.n_rows, pb.n_q_heads, pb.d_head)
-    ps = _pg_prefix(K_prefix, "K_prefix", pb)
-    if _pg_prefix(V_prefix, "V_prefix", pb) != ps:
+    dt, R, n, i32, dev = pb.torch_dtype, pb.requests, pb.n_rows, torch.int32, _pg_device(stream)
+    qp, qr = _pg_rows(q, "q", dt, n, pb.n_q_heads, pb.d_head, dev)
+    kp, *ks = _pg_prefix(K_prefix, "K_prefix", pb, dev)
+    vp, *vs = _pg_prefix(V_prefix, "V_prefix", pb, dev)
+    if ks != vs:
         raise ValueError("V_prefix: the strides differ from K_prefix's")
-    pages = (_pg(prefix_len, "prefix_len", i32, pb.n_prompts),
-             _pg(K_pages, "K_pages", pb.dtype, pb.pool_elements),
-             _pg(V_pages, "V_pages", pb.dtype, pb.pool_elements),
-             _pg(block_table, "block_table", i32, R * pb.max_pages), _pg(lens, "lens", i32, R),
-             _pg(q_start, "q_start", i32, R + 1), _pg(row_req, "row_req", i32, pb.n_rows),
-             _pg(out, "out", pb.dtype, pb.n_rows * pb.n_q_heads * pb.d_head),
-             _pg(lse_out, "lse_out", torch.float32, pb.n_rows * pb.n_q_heads))
+    heads = n * pb.n_q_heads
+    args = (_pg(prefix_len, "prefix_len", i32, pb.n_prompts, dev),
+            _pg(K_pages, "K_pages", dt, pb.pool_elements, dev),
+            _pg(V_pages, "V_pages", dt, pb.pool_elements, dev),
+            _pg(block_table, "block_table", i32, R * pb.max_pages, dev),
+            _pg(lens, "lens", i32, R, dev), _pg(q_start, "q_start", i32, R + 1, dev),
+            _pg(row_req, "row_req", i32, n, dev), _pg(out, "out", dt, heads * pb.d_head, dev),
+            _pg(lse_out, "lse_out", torch.float32, heads, dev))
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    dev = _device_of(stream)
-    _check(lib().pg_attention(ctypes.byref(sh), _here(q, dev), qr, _here(K_prefix, dev),
-                              _here(V_prefix, dev), *ps, *(_here(t, dev) for t in pages),
-                              _here(workspace, dev), ws_bytes, _stream(stream)))
+    if ws_bytes and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        _pg_refuse(workspace, "workspace", workspace.dtype, 0, dev)
+    _check(lib().pg_attention(pb.c_shape, qp, qr, kp, vp, *ks, *args,
+                              workspace.data_ptr() if ws_bytes else None, ws_bytes,
+                              _pg_stream(stream, dev)))
 
 
 class PgCache:

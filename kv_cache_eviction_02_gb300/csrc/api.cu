@@ -1085,12 +1085,27 @@ int pg_attention(const KvePgShape *shape, const void *q, long long q_row_stride,
     char *ws = static_cast<char *>(workspace);
     A.part_ml = reinterpret_cast<float2 *>(ws + W.part_ml);
     A.part_o = reinterpret_cast<float *>(ws + W.part_o);
+    A.own.ml = reinterpret_cast<float2 *>(ws + W.own_ml);
+    A.own.o = reinterpret_cast<float *>(ws + W.own_o);
+    A.own.base = reinterpret_cast<long long *>(ws + W.own_base);
+    A.own.unit = reinterpret_cast<int *>(ws + W.own_unit);
+    A.own.cpw = reinterpret_cast<long long *>(ws + W.own_cpw);
+    A.own.segs = D.dtype == KVE_F32 ? 0 : pg_own_segs(D);
+    A.own.seg_rows = pg_seg_rows(D);
     A.err = err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    {
-        ProfScope ps("pg_attention", 2, st);
-        e = launch_pg_attention(D, A, st);
+    cudaError_t e = cudaSuccess;
+    if (D.n > 0) {
+        ProfScope ps("pg_prompt", 1, st);
+        e = launch_pg_prompt(D, A, st);
+    }
+    if (e == cudaSuccess) {
+        ProfScope ps("pg_own", 1, st);
+        e = launch_pg_own(D, A, st);
+    }
+    if (e == cudaSuccess) {
+        ProfScope ps("pg_join", 1, st);
+        e = launch_pg_join(D, A, st);
     }
     if (e != cudaSuccess) return cuda_fail(e, "pg_attention: launch");
     return KVE_OK;

@@ -1,0 +1,473 @@
+// Shared-prompt decoding, 16-bit types: attention of the requests' own rows with warp-level matrix
+// products.
+//
+// Own rows are read by g query heads of one or a few new rows, so a request and KV head have 1 to a
+// few dozen query rows over its K/V: bound by HBM, with 2 g flops per byte at one new row. The products
+// run transposed, S^T = K Q^T and O^T += V^T P^T, as m16n8k16 fragments in registers: 16 tokens (or 16
+// output columns) on the wide side and 8 query rows on the narrow one, which fits a decode step's 4 to
+// 8 query heads where a 128-row tcgen05 tile would be almost empty. The weights go from the accumulator
+// of S^T to the B operand of V^T P^T by an 8 x 8 transpose in registers.
+//
+// Work is dealt to warps, not blocks. A unit is (request, KV head, block of 8 or 16 query rows), a chunk
+// 16 of its tokens; the chunks of all units stand in one line (request, then KV head, then row block)
+// and every warp takes the same number of consecutive ones, however the lengths lie. A warp's ring of
+// chunks (TMA boxes of the pages, swizzled for ldmatrix) runs on across the units it passes, so HBM sees
+// no pause at a unit's end, and no warp waits for another. Each piece of a unit that a warp has seen
+// becomes one partial result at place (unit index + warp index), which no other piece has; the join finds
+// a unit's pieces from the same arithmetic, in order.
+#include <cudaTypedefs.h>
+
+#include <type_traits>
+
+#include "pages_ptx.cuh"
+
+namespace kve {
+namespace {
+
+constexpr int kMmThreads = 32 * kPgOwnWarps, kMmTok = kPgChunk;  // tokens per chunk
+
+template <int D> constexpr int mm_stages() { return D == 128 ? 3 : 4; }
+template <int D> constexpr int mm_stage_bytes() { return kMmTok * D * 2 * 2; }  // K and V
+template <int D> constexpr int mm_smem() {
+    return kPgOwnWarps * mm_stages<D>() * mm_stage_bytes<D>() + 1024;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4],
+                                                        uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                 uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two weights as a 16-bit pair. A weight is at most 2^8 (see kMmRescale) and rounds to half a step
+// of the type, as V's own entries did; their sum l is taken in fp32 before the rounding.
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Where TMA puts 16-byte word c of a chunk's row: column blocks of 64 values one after the other, in
+// each 128-byte (D = 32: 64-byte) rows swizzled so that 8 rows of a word fall into different banks.
+template <int D> __device__ __forceinline__ uint32_t mm_off(int row, int c) {
+    if (D == 32) return (uint32_t)(row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+    return (uint32_t)((c >> 3) * (kMmTok * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+}
+
+constexpr float kMmRescale = 8.f;  // O is rescaled when a row's maximum grew by more than 2^8
+
+// Where a warp stands in the line of chunks.
+struct Cursor {
+    int r, len, first, nq;  // request, its rows in pages, its first packed row and their number
+    int cr, nb;             // chunks per unit, row blocks
+    int kh, rb, c;          // KV head, row block, chunk of the unit
+    __device__ __forceinline__ void enter(const PgDims &D, const PgAttn &A, int req) {
+        r = req;
+        pg_own_request(D, A, r, &len, &first, &nq, &cr, &nb);
+        kh = rb = c = 0;
+    }
+    // to the next chunk; only called when there is one
+    __device__ __forceinline__ void next(const PgDims &D, const PgAttn &A) {
+        if (++c < cr) return;
+        c = 0;
+        if (++rb < nb) return;
+        rb = 0;
+        if (++kh < D.Hkv) return;
+        do enter(D, A, r + 1);
+        while ((cr == 0 || nb == 0) && r + 1 < D.R);
+    }
+};
+
+// NT: blocks of 8 query rows per unit. RB = 8 NT is the unit's rows.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kMmThreads, 2)
+    pg_own_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  PgDims D_, PgAttn A, PgOwn W) {
+    constexpr int NST = mm_stages<D>(), SB = mm_stage_bytes<D>(), RB = 8 * NT;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~uintptr_t(1023));
+    __shared__ long long csum[kMmThreads + 1];  // chunks before each thread's requests
+    __shared__ int usum[kMmThreads + 1];        // units before them
+    __shared__ uint64_t bars[kPgOwnWarps][NST];
+    __shared__ int s_abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane < NST) tc::mbar_init(&bars[warp][lane], 1);
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        tc::tma_prefetch_desc(&tm_k);
+        tc::tma_prefetch_desc(&tm_v);
+    }
+    tc::mbar_fence_init();
+    if (D_.n == 0) pg_wait_prior();  // first kernel of its call (else the prompt's has waited)
+    pg_launch_dependents();
+
+    // ---- chunks and units of all requests: thread t sums q consecutive ones ----
+    const int q = (D_.R + kMmThreads - 1) / kMmThreads;
+    const int ra = min(D_.R, (int)threadIdx.x * q), rz = min(D_.R, ra + q);
+    long long cs = 0;
+    int us = 0;
+    for (int r = ra; r < rz; ++r) {
+        int len, first, nq, cr, nb;
+        pg_own_request(D_, A, r, &len, &first, &nq, &cr, &nb);
+        cs += (long long)cr * nb * D_.Hkv;
+        us += nb * D_.Hkv;
+    }
+    csum[threadIdx.x + 1] = cs;
+    usum[threadIdx.x + 1] = us;
+    if (threadIdx.x == 0) {
+        csum[0] = 0;
+        usum[0] = 0;
+    }
+    __syncthreads();
+    if (warp == 0) {  // lane l scans entries 4 l + 1 .. 4 l + 4
+        long long c4[4];
+        int u4[4];
+        long long ct = 0;
+        int ut = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c4[i] = ct += csum[4 * lane + 1 + i];
+            u4[i] = ut += usum[4 * lane + 1 + i];
+        }
+        long long cb = ct;
+        int ub = ut;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, cb, o);
+            const int y = __shfl_up_sync(0xffffffffu, ub, o);
+            if (lane >= o) {
+                cb += x;
+                ub += y;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            csum[4 * lane + 1 + i] = cb - ct + c4[i];
+            usum[4 * lane + 1 + i] = ub - ut + u4[i];
+        }
+    }
+    __syncthreads();
+    const long long total = csum[kMmThreads];
+    const int nw = gridDim.x * kPgOwnWarps;
+    long long cpw = (total + nw - 1) / nw;
+    if (cpw < 1) cpw = 1;
+    if (blockIdx.x == 0) {  // what the join needs to find the pieces again
+        cs = csum[threadIdx.x];
+        us = usum[threadIdx.x];
+        for (int r = ra; r < rz; ++r) {
+            int len, first, nq, cr, nb;
+            pg_own_request(D_, A, r, &len, &first, &nq, &cr, &nb);
+            W.base[r] = cs;
+            W.unit[r] = us;
+            cs += (long long)cr * nb * D_.Hkv;
+            us += nb * D_.Hkv;
+        }
+        if (threadIdx.x == 0) *W.cpw = cpw;
+    }
+    const int w = blockIdx.x * kPgOwnWarps + warp;
+    const long long X0 = w * cpw;
+    const int n = (int)(total - X0 < cpw ? total - X0 : cpw);  // chunks of this warp
+    if (n > 0) {
+        // ---- the request, unit and chunk of X0 ----
+        int grp = 0;  // the group of requests that holds X0: the last with csum <= X0
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            grp += __popc(__ballot_sync(0xffffffffu, csum[4 * lane + 1 + i] <= X0));
+        Cursor cc;
+        long long x = X0 - csum[grp];
+        int unit = usum[grp];
+        cc.enter(D_, A, grp * q);
+        while (x >= (long long)cc.cr * cc.nb * D_.Hkv) {
+            x -= (long long)cc.cr * cc.nb * D_.Hkv;
+            unit += cc.nb * D_.Hkv;
+            cc.enter(D_, A, cc.r + 1);
+        }
+        const int u = (unsigned long long)x >> 31 ? (int)(x / cc.cr) : (int)x / cc.cr;
+        cc.c = (int)(x - (long long)u * cc.cr);
+        cc.kh = u / cc.nb;
+        cc.rb = u - cc.kh * cc.nb;
+        unit += u;
+        Cursor ca = cc;  // runs ahead: the addresses of the chunks to load
+
+        uint8_t *ring = smem + warp * NST * SB;
+        uint64_t *bar = bars[warp];
+        volatile int *abort_flag = &s_abort;
+        const float k1 = kLog2e * rsqrtf((float)D);
+        uint32_t qf[NT][D / 16][2];  // B operand of S^T: query row lane / 4 of each block
+        float o[NT][D / 16][4], m[NT][2], l[NT][2];  // this lane's query rows 2 (lane % 4), + 1
+        int see[NT][2], rows, row0;  // tokens they see; query rows of the request, the unit's first
+        auto begin = [&]() {         // of a unit, or of this warp's part of one
+            rows = min(cc.nq, D_.max_new) * D_.g;
+            row0 = cc.rb * RB;
+#pragma unroll
+            for (int b = 0; b < NT; ++b) {
+                const int rr = row0 + 8 * b + (lane >> 2), t = rr < rows ? rr / D_.g : 0;
+                const T *qp = static_cast<const T *>(A.q) + (cc.first + t) * A.q_row +
+                              (size_t)(cc.kh * D_.g + (rr < rows ? rr - t * D_.g : 0)) * D +
+                              (lane & 3) * 2;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    qf[b][k][0] =
+                        rr < rows ? __ldg(reinterpret_cast<const uint32_t *>(qp + 16 * k)) : 0u;
+                    qf[b][k][1] =
+                        rr < rows ? __ldg(reinterpret_cast<const uint32_t *>(qp + 16 * k + 8)) : 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int qr = row0 + 8 * b + (lane & 3) * 2 + e;
+                    see[b][e] = qr < rows ? cc.len - cc.nq + 1 + qr / D_.g : 0;
+                    m[b][e] = kPgNoMax;
+                    l[b][e] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[b][j][e] = 0.f;
+            }
+        };
+        // A chunk is 16 / box boxes of box = min(page, 16) rows, one per lane. Where a chunk's pages lie
+        // is asked two chunks before they are loaded: the answer of the table (a trip to L2) is not
+        // waited for. at: the box's row within its page and head, -1 behind the request's last page.
+        const int lgB = D_.lgP < 4 ? D_.lgP : 4, boxes = kMmTok >> lgB;
+        const int page_rows = D_.Hkv << D_.lgP;
+        const uint32_t box_bytes = (uint32_t)(D * 2 * 2) << lgB;
+        // a box of 16 rows brings all column blocks, [block][row][64 values]; smaller ones one block
+        const int zs = lgB < 4 && D > 64 ? D / 64 : 1;
+        struct Where {
+            int page, at;
+        };
+        auto where = [&]() -> Where {
+            const int j = ca.c * kMmTok + (lane << lgB);
+            if (lane >= boxes || j >= ca.len) return Where{0, -1};
+            return Where{__ldg(A.table + (size_t)ca.r * D_.maxp + (j >> D_.lgP)),
+                         (ca.kh << D_.lgP) + (j & (D_.P - 1))};
+        };
+        auto load = [&](int place, Where x) {
+            int row = -1;
+            if (x.at >= 0) row = pg_page_id(x.page, D_.npages, A.err) * page_rows + x.at;
+            const int used = __popc(__ballot_sync(0xffffffffu, row >= 0));
+            uint8_t *k = ring + place * SB;
+            if (tc::elect_one()) tc::mbar_expect_tx(&bar[place], used * box_bytes);
+            for (int b = 0; b < used; ++b) {  // one lane issues: TMA takes uniform operands
+                const int y = __shfl_sync(0xffffffffu, row, b);
+                if (tc::elect_one()) {
+                    for (int z = 0; z < zs; ++z) {
+                        tc::tma_load_3d(k + z * (kMmTok * 128), &tm_k, 0, y, z, &bar[place]);
+                        tc::tma_load_3d(k + SB / 2 + z * (kMmTok * 128), &tm_v, 0, y, z, &bar[place]);
+                    }
+                }
+                k += (D == 32 ? 64 : 128) << lgB;
+            }
+        };
+        int asked = 1, ahead = 0;  // chunks asked for, chunks issued
+        Where x0 = where(), x1{0, -1};
+        begin();  // its loads of Q run beside the table's
+        auto ask = [&]() {
+            if (asked < n) {
+                ca.next(D_, A);
+                x1 = where();
+                ++asked;
+            }
+        };
+        ask();
+#pragma unroll 1
+        for (int i = 0; i < NST - 1 && ahead < n; ++i) {
+            load(ahead++, x0);
+            x0 = x1;
+            ask();
+        }
+
+        int slot = 0, fill = NST - 1;  // ring places of this chunk and of the one to issue
+        uint32_t phase = 0;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            if (ahead < n) {
+                load(fill, x0);
+                ++ahead;
+                x0 = x1;
+                ask();
+            }
+            if (++fill == NST) fill = 0;
+            if (i > 0 && cc.c == 0) begin();
+            if (!tc::mbar_wait_warp(&bar[slot], phase, abort_flag, A.err)) break;
+            const int tb = cc.c * kMmTok;
+            const uint32_t ks = tc::smem_u32(ring + slot * SB), vs = ks + SB / 2;
+            if (tb + kMmTok > cc.len) {
+                // V rows behind the last token hold anything (their weights are 0): zeros instead
+                for (int e = (cc.len - tb) * (D / 8) + lane; e < kMmTok * (D / 8); e += 32)
+                    *reinterpret_cast<uint4 *>(ring + slot * SB + SB / 2 +
+                                               mm_off<D>(e / (D / 8), e % (D / 8))) =
+                        make_uint4(0, 0, 0, 0);
+                tc::fence_proxy_async_smem();  // before TMA writes there again
+                __syncwarp();
+            }
+            if (++slot == NST) {
+                slot = 0;
+                phase ^= 1;
+            }
+            // S^T: 16 tokens x 8 query rows per block
+            float s[NT][4];
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[b][e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t kf[4];
+                ldsm4(ks + mm_off<D>(lane & 15, 2 * k + (lane >> 4)), kf);
+#pragma unroll
+                for (int b = 0; b < NT; ++b) mma16816<T>(s[b], kf, qf[b][k][0], qf[b][k][1]);
+            }
+            uint32_t pf[NT][2];
+            const int tok = tb + (lane >> 2);
+            bool grow = false;
+            float mt[NT][2];
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {  // scores in the log2 domain, maximum over the tokens
+                    s[b][e] = tok < see[b][e] ? s[b][e] * k1 : -INFINITY;
+                    s[b][e + 2] = tok + 8 < see[b][e] ? s[b][e + 2] * k1 : -INFINITY;
+                    float x = fmaxf(s[b][e], s[b][e + 2]);
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    mt[b][e] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                    grow = grow || mt[b][e] > m[b][e] + kMmRescale;
+                }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int b = 0; b < NT; ++b)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float mn = fmaxf(m[b][e], mt[b][e]), f = tc::ex2_approx(m[b][e] - mn);
+                        m[b][e] = mn;
+                        l[b][e] *= f;
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            o[b][j][e] *= f;
+                            o[b][j][e + 2] *= f;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {  // tokens 0-7, 8-15
+                    const float p0 = tc::ex2_approx(s[b][2 * x] - m[b][0]);
+                    const float p1 = tc::ex2_approx(s[b][2 * x + 1] - m[b][1]);
+                    l[b][0] += p0;
+                    l[b][1] += p1;
+                    pf[b][x] = transpose8(pack2<T>(p0, p1));
+                }
+            // O^T: 16 output columns x 8 query rows per block
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+                uint32_t vf[4];
+                ldsm4t(vs + mm_off<D>((lane & 7) + ((lane >> 4) << 3), 2 * j + ((lane >> 3) & 1)), vf);
+#pragma unroll
+                for (int b = 0; b < NT; ++b) mma16816<T>(o[b][j], vf, pf[b][0], pf[b][1]);
+            }
+            if (i == n - 1 || cc.c == cc.cr - 1) {  // the piece ends
+                const long long seg = (long long)unit + w;
+#pragma unroll
+                for (int b = 0; b < NT; ++b)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = l[b][e];
+                        x += __shfl_xor_sync(0xffffffffu, x, 4);
+                        x += __shfl_xor_sync(0xffffffffu, x, 8);
+                        x += __shfl_xor_sync(0xffffffffu, x, 16);
+                        const int qr = 8 * b + (lane & 3) * 2 + e;
+                        // (row starts that are no sums of lengths can ask for more places than there are)
+                        if (row0 + qr >= rows || seg >= W.segs) continue;
+                        const size_t row = (size_t)seg * W.seg_rows + qr;
+                        if (lane < 4) W.ml[row] = make_float2(m[b][e], x);
+                        float *dst = W.o + row * D + (lane >> 2);
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            dst[16 * j] = o[b][j][e];
+                            dst[16 * j + 8] = o[b][j][e + 2];
+                        }
+                    }
+                ++unit;
+            }
+            if (i + 1 < n) cc.next(D_, A);
+            __syncwarp();  // the chunk's readers are done: the next issue may overwrite it
+        }
+        if (s_abort) {  // copies still in flight land before the block ends
+            for (int k = 0; k < NST; ++k) {
+                tc::mbar_drain(&bar[k], 0);
+                tc::mbar_drain(&bar[k], 1);
+            }
+        }
+    }
+    pg_wait_prior();
+}
+
+template <typename T, int D, int NT>
+cudaError_t go(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
+    const bool f16 = std::is_same<T, __half>::value;
+    CUtensorMap tk, tv;
+    // {64 columns, rows of the pool, column blocks}
+    constexpr cuuint32_t col = D == 32 ? 32 : 64;
+    const bool whole = D_.P >= kMmTok;
+    const cuuint64_t dims[3] = {col, (cuuint64_t)D_.npages * D_.Hkv * D_.P, D / col};
+    const long long stride[2] = {D, col};
+    const cuuint32_t box[3] = {col, (cuuint32_t)(whole ? kMmTok : D_.P), whole ? D / col : 1};
+    if (!pg_tmap(&tk, f16, A.K, 3, dims, stride, box, D == 32) ||
+        !pg_tmap(&tv, f16, A.V, 3, dims, stride, box, D == 32))
+        return cudaErrorInvalidValue;
+    return pg_launch(pg_own_kernel<T, D, NT>, pg_own_ctas(D_), kMmThreads, mm_smem<D>(), true, st, tk,
+                     tv, D_, A, A.own);
+}
+
+template <typename T, int D> cudaError_t by_rows(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
+    return pg_unit_rows(D_) == 8 ? go<T, D, 1>(D_, A, st) : go<T, D, 2>(D_, A, st);
+}
+
+template <typename T> cudaError_t by_head(const PgDims &D, const PgAttn &A, cudaStream_t st) {
+    return D.d == 128 ? by_rows<T, 128>(D, A, st)
+                      : (D.d == 64 ? by_rows<T, 64>(D, A, st) : by_rows<T, 32>(D, A, st));
+}
+
+}  // namespace
+
+cudaError_t launch_pg_own16(const PgDims &D, const PgAttn &A, cudaStream_t st) {
+    return D.dtype == KVE_BF16 ? by_head<__nv_bfloat16>(D, A, st) : by_head<__half>(D, A, st);
+}
+
+}  // namespace kve

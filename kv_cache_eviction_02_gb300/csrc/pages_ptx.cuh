@@ -1,0 +1,28 @@
+// sm_103a building blocks of the shared-prompt kernels next to tc_common.cuh's.
+#pragma once
+
+#include "pages.cuh"
+#include "tc_common.cuh"
+
+namespace kve {
+namespace tc {
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+// One lane of a converged warp; unlike a test of the lane's number, the compiler knows the branch to
+// be uniform and keeps descriptors in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+                 : "=r"(p));
+    return p != 0;
+}
+
+}  // namespace tc
+}  // namespace kve

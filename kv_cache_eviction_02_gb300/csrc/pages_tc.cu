@@ -1,5 +1,6 @@
 // Shared-prompt decoding on the 5th-generation tensor cores (tcgen05, sm_103a): attention of all
-// rows behind a prompt over the prompt's K/V, bf16 or fp16, d_head 64 or 128.
+// rows behind a prompt over the prompt's K/V, bf16 or fp16. d_head 32 runs as 64: the boxes reach behind
+// the arrays' rows, where TMA fills in zeros.
 //
 // The rows of a prompt's requests (new rows x g query heads of a KV head) are stacked into 128-row
 // tiles, so the prompt's K/V stream from HBM once per tile or pair of tiles, however many requests
@@ -14,20 +15,11 @@
 // Few rows (lookahead: 4 trajectories x 4 heads): bound by HBM; many (hundreds): by the tensor pipe.
 #include <cudaTypedefs.h>
 
-#include "pages.cuh"
-#include "tc_common.cuh"
+#include "pages_ptx.cuh"
 
 namespace kve {
 namespace {
 
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z,
-                                            uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(tc::smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar))
-        : "memory");
-}
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z,
                                             int w, uint64_t *bar) {
     asm volatile(
@@ -36,6 +28,17 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, i
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w),
         "r"(tc::smem_u32(bar))
         : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ void mbar_inval(uint64_t *bar) {
     asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
@@ -59,8 +62,11 @@ template <int D, int QT> struct PtLayout {
     static constexpr uint32_t TILE = KB * 16384;
     static constexpr int SLOTS = D == 128 ? (QT == 2 ? 5 : 6) : (QT == 2 ? 11 : 12);
     static constexpr uint32_t RING = QT * TILE, BAR = RING + SLOTS * TILE;
-    static constexpr int NBAR = 1 + 2 * SLOTS + 8;
+    static constexpr int NBAR = 1 + 2 * SLOTS + 9;
     static constexpr size_t SMEM = BAR + 512 + 1024;
+};
+struct PtDesc {
+    uint64_t q, k, v;  // of row tile 0 and of ring place 0 as K and as V
 };
 template <int QT> constexpr int pt_threads() { return (4 + 4 * QT) * 32; }
 constexpr float kPtRescale = 8.f;
@@ -77,64 +83,134 @@ struct PtArgs {
 
 // Barriers of a CTA, in shared memory.
 template <int D, int QT> struct PtBars {
-    uint64_t *q_full, *rfull, *rempty, *s_full, *p_full, *o_done, *drain, *o_final;
+    uint64_t *q_full, *rfull, *rempty, *s_full, *p_half, *p_full, *o_done, *drain, *o_final;
     __device__ explicit PtBars(uint64_t *b) {
         constexpr int S = PtLayout<D, QT>::SLOTS;
         q_full = b;
         rfull = b + 1;
         rempty = rfull + S;
         s_full = rempty + S;
-        p_full = s_full + 2;
+        p_half = s_full + 2;
+        p_full = p_half + 2;
         o_done = p_full + 2;
-        drain = o_done + 2;
+        drain = o_done + 1;
         o_final = drain + 1;
     }
 };
 
-// S(i) = Q_t K_i^T into S buffer `sb`. With two row tiles sb = t and K_i is released after the last;
-// with one, the buffers alternate and S(i + 1) is computed while the softmax of S(i) runs. MMAs run
-// in issue order, so the product that read P from these columns is done before they are overwritten.
+// Matrix descriptors advance by adding to the address field (16-byte units): building one per product
+// costs the issuing thread about 150 cycles, more than the product's 64 (measured: 8 products of
+// 128 x 128 x 16 took 1200 cycles with descriptors built in place, 514 with added offsets).
+//
+// S(i) = Q_t K_i^T into S buffer `sb`. With two row tiles sb = t; with one, the buffers alternate and
+// S(i + 1) is computed while the softmax of S(i) runs. A thread's MMAs run in issue order, so the
+// product that read P from these columns is done before they are overwritten.
 template <typename T, int D, int QT>
-__device__ __forceinline__ bool pt_issue_s(const PtBars<D, QT> &B, uint32_t base, uint32_t tmem,
-                                           int t, int sb, int i, bool wait, bool last,
-                                           volatile int *abort_flag, unsigned *err) {
+__device__ __forceinline__ void pt_issue_s(const PtDesc &d, uint32_t tmem, int t, int sb, int i) {
     using L = PtLayout<D, QT>;
     constexpr uint32_t id = tc::idesc_f16kind(128, 128, 0, !PtIsHalf<T>::value);
-    const int c = 2 * i, slot = c % L::SLOTS;
-    if (wait && !tc::mbar_wait(&B.rfull[slot], (c / L::SLOTS) & 1, abort_flag, err)) return false;
+    const int slot = (2 * i) % L::SLOTS;
     tc::fence_after_sync();
-    const uint32_t q = base + t * L::TILE, k = base + L::RING + slot * L::TILE;
+    const uint64_t q = d.q + (uint32_t)t * (L::TILE / 16), k = d.k + (uint32_t)slot * (L::TILE / 16);
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
-        const uint32_t o = (s >> 2) * 16384 + (s & 3) * 32;
-        tc::mma_bf16(tmem + sb * 128, tc::sdesc_sw128(q + o, 16, 1024),
-                     tc::sdesc_sw128(k + o, 16, 1024), id, s > 0);
+        const uint32_t o = ((s >> 2) * 16384 + (s & 3) * 32) / 16;
+        tc::mma_bf16(tmem + sb * 128, q + o, k + o, id, s > 0);
     }
-    tc::mma_commit(&B.s_full[sb]);
-    if (last) tc::mma_commit(&B.rempty[slot]);
+}
+
+// O_t += P(i) V_i, P from S buffer `sb`; the first half of the tokens goes as soon as its weights are
+// stored, while the softmax is still at the second. half_ready: the first half is known to be there.
+template <typename T, int D, int QT>
+__device__ __forceinline__ bool pt_issue_pv(const PtBars<D, QT> &B, const PtDesc &d, uint32_t tmem,
+                                            int t, int sb, uint32_t p_phase, int i, bool half_ready,
+                                            volatile int *abort_flag, unsigned *err) {
+    using L = PtLayout<D, QT>;
+    constexpr uint32_t id = tc::idesc_f16kind(128, D, 1, !PtIsHalf<T>::value);
+    const int slot = (2 * i + 1) % L::SLOTS;
+    const uint64_t v = d.v + (uint32_t)slot * (L::TILE / 16);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        if (!(half == 0 && half_ready) &&
+            !tc::mbar_wait(half ? &B.p_full[sb] : &B.p_half[sb], p_phase, abort_flag, err))
+            return false;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int s = 4 * half; s < 4 * half + 4; ++s)  // 16 tokens: 8 TMEM columns of P, 16 V rows
+            tc::mma_bf16_ts(tmem + 256 + t * D, tmem + sb * 128 + 8 * s, v + s * (2048 / 16), id,
+                            (i > 0 || s > 0) ? 1u : 0u);
+    }
     return true;
 }
 
-// O_t += P(i) V_i, P from S buffer `sb`.
+// Waits until item c of the ring (K_i: 2 i, V_i: 2 i + 1) has landed.
 template <typename T, int D, int QT>
-__device__ __forceinline__ bool pt_issue_pv(const PtBars<D, QT> &B, uint32_t base, uint32_t tmem,
-                                            int t, int sb, uint32_t p_phase, int i, bool wait,
-                                            bool last, bool final, volatile int *abort_flag,
-                                            unsigned *err) {
-    using L = PtLayout<D, QT>;
-    constexpr uint32_t id = tc::idesc_f16kind(128, D, 1, !PtIsHalf<T>::value);
-    const int c = 2 * i + 1, slot = c % L::SLOTS;
-    if (wait && !tc::mbar_wait(&B.rfull[slot], (c / L::SLOTS) & 1, abort_flag, err)) return false;
-    if (!tc::mbar_wait(&B.p_full[sb], p_phase, abort_flag, err)) return false;
-    tc::fence_after_sync();
-    const uint32_t v = base + L::RING + slot * L::TILE;
+__device__ __forceinline__ bool pt_landed(const PtBars<D, QT> &B, int c, volatile int *abort_flag,
+                                          unsigned *err) {
+    constexpr int S = PtLayout<D, QT>::SLOTS;
+    return tc::mbar_wait(&B.rfull[c % S], (c / S) & 1, abort_flag, err);
+}
+
+// One row tile: S is double-buffered, so a tile's scores are two ahead.
+template <typename T, int D, int QT>
+__device__ __forceinline__ bool pt_issue_one(const PtBars<D, QT> &B, const PtDesc &d, uint32_t tmem,
+                                             int ntl, volatile int *abort_flag, unsigned *err) {
+    constexpr int S = PtLayout<D, QT>::SLOTS;
+    auto scores = [&](int i) {
+        if (!pt_landed<T, D, QT>(B, 2 * i, abort_flag, err)) return false;
+        pt_issue_s<T, D, QT>(d, tmem, 0, i & 1, i);
+        tc::mma_commit(&B.s_full[i & 1]);
+        tc::mma_commit(&B.rempty[(2 * i) % S]);
+        return true;
+    };
+    bool ok = true;
+    for (int i = 0; ok && i < 2 && i < ntl; ++i) ok = scores(i);
+    for (int i = 0; ok && i < ntl; ++i) {
+        ok = pt_landed<T, D, QT>(B, 2 * i + 1, abort_flag, err) &&
+             pt_issue_pv<T, D, QT>(B, d, tmem, 0, i & 1, (i >> 1) & 1, i, false, abort_flag, err);
+        if (!ok) break;
+        tc::mma_commit(B.o_done);
+        if (i == ntl - 1) tc::mma_commit(B.o_final);
+        tc::mma_commit(&B.rempty[(2 * i + 1) % S]);
+        if (i + 2 < ntl) ok = scores(i + 2);
+    }
+    return ok;
+}
+
+// Two row tiles, in strict turn: [P_0 V, S_0 next], [P_1 V, S_1 next]. The turns keep the softmax
+// groups half a period apart, one computing weights while the other's products run (a thread per tile
+// let them fall into step and both wait: 3400 cycles a period instead of 2650). A commit holds the
+// issuing thread until the products before it are nearly done and a wait on a barrier that has
+// completed costs it 75 cycles, so there is one commit a turn, and what can be tested for the next
+// turn is tested before it. A tile's s_full then stands for everything before it: the ring places of
+// K_(i+1) and V_i (released by the softmax of tile 1) and the previous product into O.
+template <typename T, int D, int QT>
+__device__ __forceinline__ bool pt_issue_two(const PtBars<D, QT> &B, const PtDesc &d, uint32_t tmem,
+                                             int ntl, volatile int *abort_flag, unsigned *err) {
+    constexpr int S = PtLayout<D, QT>::SLOTS;
+    if (!pt_landed<T, D, QT>(B, 0, abort_flag, err)) return false;
+    for (int t = 0; t < 2; ++t) {
+        pt_issue_s<T, D, QT>(d, tmem, t, t, 0);
+        tc::mma_commit(&B.s_full[t]);
+    }
+    bool v_ready = false, p_ready = false;
+    for (int i = 0; i < ntl; ++i) {
+        const bool more = i + 1 < ntl;
 #pragma unroll
-    for (int s = 0; s < 8; ++s)  // 16 tokens per step: 8 TMEM columns of P, 16 rows of V
-        tc::mma_bf16_ts(tmem + 256 + t * D, tmem + sb * 128 + 8 * s,
-                        tc::sdesc_sw128(v + s * 2048, 16384, 1024), id, (i > 0 || s > 0) ? 1u : 0u);
-    tc::mma_commit(&B.o_done[t]);
-    if (final) tc::mma_commit(B.o_final);
-    if (last) tc::mma_commit(&B.rempty[slot]);
+        for (int t = 0; t < 2; ++t) {
+            if (t == 0 && !v_ready && !pt_landed<T, D, QT>(B, 2 * i + 1, abort_flag, err))
+                return false;
+            if (!pt_issue_pv<T, D, QT>(B, d, tmem, t, t, i & 1, i, p_ready, abort_flag, err))
+                return false;
+            if (t == 0 && more && !pt_landed<T, D, QT>(B, 2 * i + 2, abort_flag, err)) return false;
+            if (more) pt_issue_s<T, D, QT>(d, tmem, t, t, i + 1);
+            p_ready = t == 0 ? mbar_test(&B.p_half[1], i & 1) : mbar_test(&B.p_half[0], (i + 1) & 1);
+            if (t == 1)
+                v_ready = more && mbar_test(&B.rfull[(2 * i + 3) % S], ((2 * i + 3) / S) & 1);
+            if (more) tc::mma_commit(&B.s_full[t]);
+        }
+    }
+    tc::mma_commit(B.o_final);
     return true;
 }
 
@@ -163,6 +239,10 @@ __device__ __forceinline__ void pt_softmax(const PtArgs &A, const PtBars<D, QT> 
             break;
         }
         tc::fence_after_sync();
+        if (!DB && t == 1 && r == 0) {
+            tc::mbar_arrive(&B.rempty[(2 * i) % L::SLOTS]);
+            if (i > 0) tc::mbar_arrive(&B.rempty[(2 * i - 1) % L::SLOTS]);
+        }
         float s[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc::tmem_ld32(s_col + c * 32, s[c]);
@@ -187,79 +267,111 @@ __device__ __forceinline__ void pt_softmax(const PtArgs &A, const PtBars<D, QT> 
                     *reinterpret_cast<uint4 *>(v + kb * 16384 + e * 16) = make_uint4(0, 0, 0, 0);
             tc::fence_proxy_async_smem();
         }
+        // weights of a half from its scores: p = 2^(s k1 - m), rounded to the type of V (half a step,
+        // like V's own entries); their sum takes p before the rounding
+        float pk[32], l0, l1;
+        auto half_weights = [&](const float (&x)[32], const float (&y)[32]) {
+            const uint64_t k1_2 = tc::pk2(A.k1, A.k1), negm_2 = tc::pk2(-m, -m);
+            uint64_t sum2[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const float u0 = j < 16 ? x[(2 * j) & 31] : y[(2 * j) & 31];
+                const float u1 = j < 16 ? x[(2 * j + 1) & 31] : y[(2 * j + 1) & 31];
+                float x0, x1;
+                tc::upk2(tc::fma2(tc::pk2(u0, u1), k1_2, negm_2), x0, x1);
+                const float p0 = tc::ex2_approx(x0), p1 = tc::ex2_approx(x1);
+                sum2[j & 3] = tc::add2(sum2[j & 3], tc::pk2(p0, p1));
+                pk[j] = __uint_as_float(pt_pack<T>(p0, p1));
+            }
+            float a[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tc::upk2(sum2[k], a[2 * k], a[2 * k + 1]);
+            return ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
+        };
+        // The first half goes ahead with the maximum of the tiles before, beside the search for this
+        // tile's: a weight may exceed 1 by up to 2^8 before the row is rescaled anyway, and only a
+        // larger growth (rare after the first tiles) makes the half anew from S, still in TMEM.
+        l0 = half_weights(s[0], s[1]);
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int e = 0; e < 32; e += 2) m4[c] = tc::max3(m4[c], s[c][e], s[c][e + 1]);
-        const float mt = tc::max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
-        const float mn = fmaxf(m, mt * A.k1);
+        const float mn = fmaxf(m, tc::max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * A.k1);
         // rows of the tile that hold no query carry whatever shared memory held: they never rescale
-        const bool rescale = valid && mn > m + kPtRescale;
-        const float f = (rescale && i > 0) ? tc::ex2_approx(m - mn) : 1.f;
-        if (rescale) m = mn;
-        const uint64_t k1_2 = tc::pk2(A.k1, A.k1), negm_2 = tc::pk2(-m, -m);
-        uint64_t lsum2[4] = {0, 0, 0, 0};
-        // p = 2^(s k1 - m) <= 2^8, rounded to the type of V (half a step, like V's own entries); the
-        // sum l takes p before the rounding
-        float pk[2][32];
-#pragma unroll
-        for (int j = 0; j < 64; ++j) {
-            float x0, x1;
-            tc::upk2(tc::fma2(tc::pk2(s[j >> 4][(2 * j) & 31], s[j >> 4][(2 * j + 1) & 31]), k1_2,
-                              negm_2),
-                     x0, x1);
-            const float p0 = tc::ex2_approx(x0), p1 = tc::ex2_approx(x1);
-            lsum2[j & 3] = tc::add2(lsum2[j & 3], tc::pk2(p0, p1));
-            pk[j >> 5][j & 31] = __uint_as_float(pt_pack<T>(p0, p1));
-        }
-        float a[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tc::upk2(lsum2[k], a[2 * k], a[2 * k + 1]);
-        l = fmaf(l, f, ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7])));
+        const bool grow = valid && mn > m + kPtRescale;
         // tcgen05.ld/st are warp-collective: the whole warp rescales when one of its rows does
-        if (__any_sync(0xffffffffu, f != 1.f)) {
-            if (!tc::mbar_wait_warp(&B.o_done[t], (i - 1) & 1, abort_flag, A.err)) {
-                ok = false;
-                break;
-            }
-            tc::fence_after_sync();
+        if (__any_sync(0xffffffffu, grow)) {
+            const float f = grow ? tc::ex2_approx(m - mn) : 1.f;
+            if (grow) m = mn;
+            l *= f;
+            if (i > 0) {  // O holds the product before (s_full says so with two tiles)
+                if (DB && !tc::mbar_wait_warp(B.o_done, (i - 1) & 1, abort_flag, A.err)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after_sync();
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                float o[32];
-                tc::tmem_ld32(o_col + c * 32, o);
-                tc::tmem_wait_ld();
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tc::tmem_ld32(o_col + c * 32, o);
+                    tc::tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= f;
-                tc::tmem_st32(o_col + c * 32, o);
+                    for (int e = 0; e < 32; ++e) o[e] *= f;
+                    tc::tmem_st32(o_col + c * 32, o);
+                }
             }
+            tc::tmem_ld32(s_col, s[0]);
+            tc::tmem_ld32(s_col + 32, s[1]);
+            tc::tmem_wait_ld();
+            if (nv < 64) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                    if (e >= nv) s[e >> 5][e & 31] = -INFINITY;
+            }
+            l0 = half_weights(s[0], s[1]);
         }
-        tc::tmem_st32(s_col, pk[0]);
-        tc::tmem_st32(s_col + 32, pk[1]);
+        tc::tmem_st32(s_col, pk);
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        tc::mbar_arrive(&B.p_half[sb]);
+        l1 = half_weights(s[2], s[3]);
+        tc::tmem_st32(s_col + 32, pk);
         tc::tmem_wait_st();
         tc::fence_before_sync();
         tc::mbar_arrive(&B.p_full[sb]);
+        l += l0 + l1;
     }
-    if (__all_sync(0xffffffffu,
-                   ok && (DB ? tc::mbar_wait(B.o_final, 0, abort_flag, A.err)
-                             : tc::mbar_wait(&B.o_done[t], (ntl - 1) & 1, abort_flag, A.err)))) {
+    // the last product of all: O is done and the ring is free
+    if (__all_sync(0xffffffffu, ok && tc::mbar_wait(B.o_final, 0, abort_flag, A.err))) {
         tc::fence_after_sync();
-        const size_t at =
-            ((size_t)sp * A.D.rows + tok0 + (valid ? rr / g : 0)) * A.D.Hq + kh * g +
-            (valid ? rr % g : 0);
+        // O leaves through the ring, which is free now: a thread's row into shared memory (rows 16
+        // bytes apart in the banks), then whole rows to the workspace, 16 bytes a lane. Straight from
+        // the threads, every store would touch 32 lines.
+        const int d = A.D.d, rows = min(32, min(A.tt * g, nrow - first) - lg * 32);
+        float *st = reinterpret_cast<float *>(sm + L::RING) + (warp - 4) * (32 * (D + 4));
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
             float o[32];
             tc::tmem_ld32(o_col + c * 32, o);
             tc::tmem_wait_ld();
-            if (valid) {
-                float4 *dst = reinterpret_cast<float4 *>(A.part_o + at * D + c * 32);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            }
+            for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<float4 *>(st + lane * (D + 4) + c * 32 + 4 * e) =
+                    make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
-        if (valid) A.part_ml[at] = make_float2(m, l);
+        __syncwarp();
+        const size_t place =  // of this lane's row
+            ((size_t)sp * A.D.rows + tok0 + rr / g) * A.D.Hq + kh * g + rr % g;
+        const int lpr = d / 4, col = (lane % lpr) * 4;  // lanes per row: 32, 16 or 8
+        for (int x0 = 0; x0 < rows; x0 += 32 / lpr) {
+            const int x = x0 + lane / lpr;
+            const size_t to = __shfl_sync(0xffffffffu, place, x & 31);
+            if (x < rows)
+                *reinterpret_cast<float4 *>(A.part_o + to * d + col) =
+                    *reinterpret_cast<const float4 *>(st + x * (D + 4) + col);
+        }
+        if (valid) A.part_ml[place] = make_float2(m, l);
     }
 }
 
@@ -274,6 +386,22 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // what needs no input first: under programmatic launch it overlaps the end of the kernel before
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
+    const PtBars<D, QT> B(bars);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::NBAR);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + L::NBAR + 1);
+    if (warp == 1) {
+        tc::tmem_alloc(tmem_slot, 512);
+        tc::fence_before_sync();
+    } else if (warp == 0 && lane == 0) {
+        tc::tma_prefetch_desc(&tm_k);
+        tc::tma_prefetch_desc(&tm_v);
+        tc::tma_prefetch_desc(&tm_q);
+        *abort_flag = 0;
+    }
+    pg_wait_prior();
+    pg_launch_dependents();
     // the row tiles of a (prompt, KV head, split) are adjacent: they meet in L2 on its K/V
     int b = blockIdx.x;
     const int rt0 = b % A.nrt;
@@ -283,25 +411,14 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
     const int kh = b % A.D.Hkv, s = b / A.D.Hkv;
     const int tok0 = pg_start(A.q_start, s * A.D.F, A.D.rows);
     const int tok1 = pg_start(A.q_start, (s + 1) * A.D.F, A.D.rows);
-    const int nrow = (tok1 - tok0) * A.D.g, per = A.tt * A.D.g;
     const int end = A.plen ? pg_clamp(__ldg(A.plen + s), 0, A.D.n) : A.D.n;
+    const int nrow = (tok1 - tok0) * A.D.g, per = A.tt * A.D.g;
     const int t0 = sp * A.D.psplit, t1 = min(end, t0 + A.D.psplit);
     const int ntl = (t1 - t0 + 127) / 128;
-    if (ntl <= 0 || rt0 * QT * per >= nrow) return;
-
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::BAR);
-    const PtBars<D, QT> B(bars);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::NBAR);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + L::NBAR + 1);
-    if (warp == 1) {
-        tc::tmem_alloc(tmem_slot, 512);
-        tc::fence_before_sync();
-    }
-    if (threadIdx.x == 0) *abort_flag = 0;
 
     // the launch has tiles for max_new rows a request; a request refused for packing more leaves
     // more rows to go through
-    for (int rt = rt0; rt * QT * per < nrow; rt += A.nrt) {
+    for (int rt = rt0; ntl > 0 && rt * QT * per < nrow; rt += A.nrt) {
         const int row0 = rt * QT * per;
         const int nqt = QT == 2 && row0 + per < nrow ? 2 : 1;
         // softmax warps with a valid row, per tile
@@ -314,9 +431,10 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
             }
             for (int t = 0; t < 2; ++t) {
                 tc::mbar_init(&B.s_full[t], 1);
+                tc::mbar_init(&B.p_half[t], 32 * warps_of(nqt == 2 ? t : 0));
                 tc::mbar_init(&B.p_full[t], 32 * warps_of(nqt == 2 ? t : 0));
-                tc::mbar_init(&B.o_done[t], 1);
             }
+            tc::mbar_init(B.o_done, 1);
             tc::mbar_init(B.drain, 1);
             tc::mbar_init(B.o_final, 1);
             tc::mbar_fence_init();
@@ -330,7 +448,7 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
                 tc::mbar_expect_tx(B.q_full, (uint32_t)(nqt * L::KB * per * 128));
                 for (int t = 0; t < nqt; ++t)
                     for (int kb = 0; kb < L::KB; ++kb)
-                        tma_load_3d(sm + t * L::TILE + kb * 16384, &tm_q, 64 * kb, kh * A.D.g,
+                        tc::tma_load_3d(sm + t * L::TILE + kb * 16384, &tm_q, 64 * kb, kh * A.D.g,
                                     tok0 + (rt * QT + t) * A.tt, B.q_full);
                 int issued = 0;
                 for (int c = 0; c < 2 * ntl; ++c) {
@@ -351,32 +469,16 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
                     tc::mbar_drain(&B.rfull[c % L::SLOTS], (c / L::SLOTS) & 1);
             }
         } else if (warp == 1) {
-            if (lane == 0) {  // ---- MMA issuer ----
+            if (tc::elect_one()) {  // ---- MMA issuer ----
                 const uint32_t base = tc::smem_u32(sm);
-                bool ok = tc::mbar_wait(B.q_full, 0, abort_flag, A.err);
-                if (nqt == 1) {
-                    for (int i = 0; ok && i < 2 && i < ntl; ++i)
-                        ok = pt_issue_s<T, D, QT>(B, base, tmem, 0, i & 1, i, true, true,
-                                                  abort_flag, A.err);
-                    for (int i = 0; ok && i < ntl; ++i) {
-                        ok = pt_issue_pv<T, D, QT>(B, base, tmem, 0, i & 1, (i >> 1) & 1, i, true,
-                                                   true, i == ntl - 1, abort_flag, A.err);
-                        if (ok && i + 2 < ntl)
-                            ok = pt_issue_s<T, D, QT>(B, base, tmem, 0, i & 1, i + 2, true, true,
-                                                      abort_flag, A.err);
-                    }
-                } else {
-                    for (int t = 0; ok && t < 2; ++t)
-                        ok = pt_issue_s<T, D, QT>(B, base, tmem, t, t, 0, t == 0, t == 1,
-                                                  abort_flag, A.err);
-                    for (int i = 0; ok && i < ntl; ++i)
-                        for (int t = 0; ok && t < 2; ++t) {
-                            ok = pt_issue_pv<T, D, QT>(B, base, tmem, t, t, i & 1, i, t == 0, t == 1,
-                                                       false, abort_flag, A.err);
-                            if (ok && i + 1 < ntl)
-                                ok = pt_issue_s<T, D, QT>(B, base, tmem, t, t, i + 1, t == 0, t == 1,
-                                                          abort_flag, A.err);
-                        }
+                const PtDesc d{tc::sdesc_sw128(base, 16, 1024),
+                               tc::sdesc_sw128(base + L::RING, 16, 1024),
+                               tc::sdesc_sw128(base + L::RING, 16384, 1024)};
+                if (tc::mbar_wait(B.q_full, 0, abort_flag, A.err)) {
+                    if (QT == 2 && nqt == 2)
+                        pt_issue_two<T, D, QT>(B, d, tmem, ntl, abort_flag, A.err);
+                    else
+                        pt_issue_one<T, D, QT>(B, d, tmem, ntl, abort_flag, A.err);
                 }
                 // every product issued has completed before the tiles or the TMEM are reused
                 tc::mma_commit(B.drain);
@@ -394,18 +496,60 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
             }
         }
         tc::fence_before_sync();
+        tc::fence_proxy_async_smem();  // the ring's plain reads and writes before the next TMA loads
         __syncthreads();
         tc::fence_after_sync();
         if (*abort_flag) break;
         if (threadIdx.x == 0)
             for (int i = 0; i < L::NBAR; ++i) mbar_inval(bars + i);
     }
+    __syncthreads();
     if (warp == 1) tc::tmem_dealloc(*tmem_slot, 512);
 }
 
 // ---- host ------------------------------------------------------------------------------------------
-bool tmap(CUtensorMap *map, bool f16, const void *base, int rank, const cuuint64_t *dims,
-          const long long *strides, const cuuint32_t *box) {
+template <typename T, int D, int QT>
+cudaError_t go(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
+    using L = PtLayout<D, QT>;
+    constexpr bool f16 = PtIsHalf<T>::value;
+    const int tt = pg_tile_rows(D_);
+    CUtensorMap tq, tk, tv;
+    const cuuint64_t qd[3] = {(cuuint64_t)D_.d, (cuuint64_t)D_.Hq, (cuuint64_t)D_.rows};
+    const long long qs[2] = {D_.d, A.q_row};
+    const cuuint32_t qb[3] = {64, (cuuint32_t)D_.g, (cuuint32_t)tt};
+    const cuuint64_t kd[4] = {(cuuint64_t)D_.d, (cuuint64_t)D_.n, (cuuint64_t)D_.Hkv,
+                              (cuuint64_t)D_.S};
+    const long long ks[3] = {A.p_tok, A.p_head, A.p_prompt};
+    const cuuint32_t kb[4] = {64, 128, 1, 1};
+    if (!pg_tmap(&tq, f16, A.q, 3, qd, qs, qb, false) || !pg_tmap(&tk, f16, A.Kp, 4, kd, ks, kb, false) ||
+        !pg_tmap(&tv, f16, A.Vp, 4, kd, ks, kb, false))
+        return cudaErrorInvalidValue;
+    PtArgs P{};
+    P.D = D_;
+    P.tt = tt;
+    P.nrt = (int)((D_.group_rows() + (long long)tt * QT - 1) / ((long long)tt * QT));
+    P.k1 = kLog2e / sqrtf((float)D_.d);
+    P.plen = A.plen;
+    P.q_start = A.q_start;
+    P.part_ml = A.part_ml;
+    P.part_o = A.part_o;
+    P.err = A.err;
+    const long long ctas = (long long)D_.S * D_.Hkv * D_.np * P.nrt;
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return pg_launch(pg_prompt_tc_kernel<T, D, QT>, (unsigned)ctas, pt_threads<QT>(), L::SMEM, true, st, tq, tk, tv, P);
+}
+
+template <typename T>
+cudaError_t by_shape(const PgDims &D, const PgAttn &A, cudaStream_t st) {
+    const int qt = pg_prompt_pairs(D);
+    if (D.d == 128) return qt == 2 ? go<T, 128, 2>(D, A, st) : go<T, 128, 1>(D, A, st);
+    return qt == 2 ? go<T, 64, 2>(D, A, st) : go<T, 64, 1>(D, A, st);
+}
+
+}  // namespace
+
+bool pg_tmap(CUtensorMap *map, bool f16, const void *base, int rank, const cuuint64_t *dims,
+             const long long *strides, const cuuint32_t *box, bool swizzle64) {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -421,54 +565,9 @@ bool tmap(CUtensorMap *map, bool f16, const void *base, int rank, const cuuint64
     const cuuint32_t one[4] = {1, 1, 1, 1};
     return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
               const_cast<void *>(base), dims, bytes, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              swizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-template <typename T, int D, int QT>
-cudaError_t go(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
-    using L = PtLayout<D, QT>;
-    constexpr bool f16 = PtIsHalf<T>::value;
-    const int tt = pg_tile_rows(D_);
-    CUtensorMap tq, tk, tv;
-    const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)D_.Hq, (cuuint64_t)D_.rows};
-    const long long qs[2] = {D, A.q_row};
-    const cuuint32_t qb[3] = {64, (cuuint32_t)D_.g, (cuuint32_t)tt};
-    const cuuint64_t kd[4] = {(cuuint64_t)D, (cuuint64_t)D_.n, (cuuint64_t)D_.Hkv,
-                              (cuuint64_t)D_.S};
-    const long long ks[3] = {A.p_tok, A.p_head, A.p_prompt};
-    const cuuint32_t kb[4] = {64, 128, 1, 1};
-    if (!tmap(&tq, f16, A.q, 3, qd, qs, qb) || !tmap(&tk, f16, A.Kp, 4, kd, ks, kb) ||
-        !tmap(&tv, f16, A.Vp, 4, kd, ks, kb))
-        return cudaErrorInvalidValue;
-    PtArgs P{};
-    P.D = D_;
-    P.tt = tt;
-    P.nrt = (int)((D_.group_rows() + (long long)tt * QT - 1) / ((long long)tt * QT));
-    P.k1 = kLog2e / sqrtf((float)D);
-    P.plen = A.plen;
-    P.q_start = A.q_start;
-    P.part_ml = A.part_ml;
-    P.part_o = A.part_o;
-    P.err = A.err;
-    const long long ctas = (long long)D_.S * D_.Hkv * D_.np * P.nrt;
-    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    auto kern = pg_prompt_tc_kernel<T, D, QT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)L::SMEM);
-    if (e != cudaSuccess) return e;
-    kern<<<(unsigned)ctas, pt_threads<QT>(), L::SMEM, st>>>(tq, tk, tv, P);
-    return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t by_shape(const PgDims &D, const PgAttn &A, cudaStream_t st) {
-    const int qt = pg_prompt_pairs(D);
-    if (D.d == 128) return qt == 2 ? go<T, 128, 2>(D, A, st) : go<T, 128, 1>(D, A, st);
-    return qt == 2 ? go<T, 64, 2>(D, A, st) : go<T, 64, 1>(D, A, st);
-}
-
-}  // namespace
 
 cudaError_t launch_pg_prompt_tc(const PgDims &D, const PgAttn &A, cudaStream_t st) {
     return D.dtype == KVE_BF16 ? by_shape<__nv_bfloat16>(D, A, st) : by_shape<__half>(D, A, st);

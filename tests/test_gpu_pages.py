@@ -312,6 +312,27 @@ def test_ragged_prompts_idle_requests_and_strided_inputs(case):
         Case(*case, seed=seed, ragged=True, idle=0.3, stride=True).check()
 
 
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 128), ("f16", 64), ("bf16", 32)])
+def test_a_prompt_stored_row_by_row_with_all_heads(dtype, d):
+    """K and V as [prompt][row][head][d]: the head stride is smaller than the row's."""
+    c = Case(dtype, 2, 3, 6, 3, d, 333, 16, 20, 2, seed=14, ragged=True)
+    ref = c.run()
+    c.Kp, c.Vp = (x.transpose(1, 2).contiguous().transpose(1, 2) for x in (c.Kp, c.Vp))
+    assert c.Kp.stride(1) < c.Kp.stride(2)
+    got = c.check()
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_many_requests_of_very_different_lengths(dtype):
+    """700 requests, most without rows or nearly so, a few long: the same rows whichever requests
+    stand around them."""
+    c = Case(dtype, 1, 700, 4, 2, 64, 40, 16, 12, 2, seed=15, idle=0.5)
+    c.check(set(range(0, c.rows, 37)))
+    c = Case(dtype, 7, 20, 4, 2, 64, 40, 16, 3000, 1, seed=16, idle=0.8, ragged=True)
+    c.check(set(range(0, c.rows, 5)) | {c.rows - 1})
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 def test_rows_that_see_nothing_are_zero(dtype):
     c = Case(dtype, 2, 6, 4, 2, 64, 0, 8, 5, 4, seed=5, nothing=True)
@@ -411,7 +432,7 @@ def test_another_stream_and_the_wrong_device(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     with pytest.raises(ValueError, match="current"):
         c.run(stream=s)
-    with pytest.raises(ValueError, match="CUDA device is cuda:1"):
+    with pytest.raises(ValueError, match="current CUDA device is cuda:1"):
         api.pg_append(c.pb, c.Kp, c.Kp, c.args()[0].int(), c.K, c.V, stream=0)
 
 
