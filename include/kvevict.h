@@ -337,8 +337,8 @@ void cc_cache_destroy(KveCcCache *c);
  * d_head is 32, 64 or 128; query head h reads KV head h / (n_q_heads/n_kv_heads), at most 128 query
  * heads per KV head. n_prompts * fan at most 16384; n_rows, n_pages * page_size, max_pages *
  * page_size and n_prefix at most 2^30; n_rows * n_q_heads and n_pages * n_kv_heads * page_size below
- * 2^31; n_prompts * n_kv_heads at most 65535 (KVE_EINVAL otherwise; KVE_EDTYPE
- * for another dtype).
+ * 2^31; n_prompts * n_kv_heads and n_q_heads at most 65535 (KVE_EINVAL otherwise;
+ * KVE_EDTYPE for another dtype).
  *
  * The arrays of a step, all int32 on the device:
  *   block_table [n_prompts * fan][max_pages]  the pages of each request, in order
@@ -364,7 +364,7 @@ typedef struct {
  * n_rows, when its length is not in [0, max_pages * page_size], or when the ring has run out; q_start
  * still counts its rows, since the caller packed them.
  * len_out may be len_in and pool_out may be pool_in (the step in place); no other arrays may
- * overlap. One launch, no workspace; the head sizes, n_prefix and dtype play no part. */
+ * overlap. One or two launches, no workspace; the head sizes, n_prefix and dtype play no part. */
 int pg_plan(const KvePgShape *shape, const int32_t *new_len, const int32_t *len_in,
             const int32_t *pool_in, int32_t *free_pages, int32_t *block_table, int32_t *len_out,
             int32_t *pool_out, int32_t *q_start, int32_t *row_req, int32_t *row_pos,

@@ -989,7 +989,7 @@ int pg_plan(const KvePgShape *shape, const int32_t *new_len, const int32_t *len_
                        pool_out, q_start, row_req, row_pos,    slot_map};
     cudaError_t e;
     {
-        ProfScope ps("pg_plan", 1, st);
+        ProfScope ps("pg_plan", D.rows > 4096 ? 2 : 1, st);
         e = launch_pg_plan(D, A, st);
     }
     if (e != cudaSuccess) return cuda_fail(e, "pg_plan: launch");
@@ -1090,17 +1090,17 @@ int pg_attention(const KvePgShape *shape, const void *q, long long q_row_stride,
     A.own.base = reinterpret_cast<long long *>(ws + W.own_base);
     A.own.unit = reinterpret_cast<int *>(ws + W.own_unit);
     A.own.cpw = reinterpret_cast<long long *>(ws + W.own_cpw);
-    A.own.segs = D.dtype == KVE_F32 ? 0 : pg_own_segs(D);
+    A.own.segs = pg_own_segs(D);
     A.own.seg_rows = pg_seg_rows(D);
     A.err = err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    if (D.n > 0) {
+    if (D.n > 0 && D.dtype != KVE_F32) {
         ProfScope ps("pg_prompt", 1, st);
-        e = launch_pg_prompt(D, A, st);
+        e = launch_pg_prompt_tc(D, A, st);
     }
     if (e == cudaSuccess) {
-        ProfScope ps("pg_own", 1, st);
+        ProfScope ps("pg_own", pg_many_new(D) ? 2 : 1, st);
         e = launch_pg_own(D, A, st);
     }
     if (e == cudaSuccess) {

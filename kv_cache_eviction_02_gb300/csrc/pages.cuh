@@ -15,9 +15,9 @@ struct PgDims {
     int n;                     // prompt rows held per (prompt, KV head)
     int P, lgP, npages, maxp;  // page size (a power of two), pages in the pool, table width
     int rows, max_new, dtype;
-    int np, psplit;            // prompt splits and their tokens (0 without a prompt)
-    int ns, ssplit;            // fp32: splits of a request's own rows and their tokens
-    int own_sms;               // 16-bit types: SMs for the own rows' kernel
+    int np, psplit;            // 16-bit types: prompt splits and their tokens (0 without a prompt)
+    int ns, ssplit;            // pg_many_new: splits of a request's own rows and their tokens
+    int own_sms;               // SMs for the kernel that deals out units
     // rows behind one prompt, when no request packs more than max_new
     __host__ __device__ long long group_rows() const {
         return (long long)F * max_new < rows ? (long long)F * max_new : rows;
@@ -30,10 +30,12 @@ constexpr int kPgShare = 100;  // most SMs the prompt's kernel takes beside the 
 
 // Own rows of 16-bit types: units of 8 or 16 query rows, chunks of 16 tokens (pages_own.cu).
 constexpr int kPgChunk = 16, kPgOwnWarps = 4;
+// fp32: units of 16 query rows, chunks of 8 tokens, prompts and own rows alike (pages_f32.cu).
+constexpr int kPgF32Chunk = 8, kPgF32Rows = 16;
 
 // Workspace carve-up (byte offsets, 256-aligned): partial results [splits][rows][Hq] (m in log2 and l;
-// o [d] fp32) over the prompt and, fp32 only, over the own rows' splits; 16-bit types: the pieces of
-// own rows [segs][seg_rows], with what the join needs to find them.
+// o [d] fp32) over the prompt and over the own rows of requests with many new rows; the pieces of units
+// [segs][seg_rows], with what the join needs to find them.
 struct PgWorkspace {
     size_t part_ml, part_o;
     size_t own_ml, own_o, own_base, own_unit, own_cpw;
@@ -43,42 +45,58 @@ struct PgWorkspace {
 bool pg_dims(const KvePgShape *sh, PgDims *D, const char **why);
 PgWorkspace pg_ws_layout(const PgDims &D);
 
-// The prompt's kernel on tcgen05 (16-bit types): new rows per 128-row tile (whole groups of query
-// heads), and row tiles per CTA. Two tiles share one K/V stream and take turns on the tensor pipe; an
+// The kernel on tcgen05 (16-bit types): new rows per 128-row tile (whole groups of query heads), and row
+// tiles per CTA for `rows` new rows. Two tiles share one K/V stream and take turns on the tensor pipe; an
 // odd small number of tiles runs one per CTA, since a half-empty pair would leave the pipe idle in its
 // turn.
 inline int pg_tile_rows(const PgDims &D) { return 128 / D.g; }
-inline int pg_prompt_pairs(const PgDims &D) {
-    const long long tiles = (D.group_rows() + pg_tile_rows(D) - 1) / pg_tile_rows(D);
+inline int pg_pairs(const PgDims &D, long long rows) {
+    const long long tiles = (rows + pg_tile_rows(D) - 1) / pg_tile_rows(D);
     return tiles % 2 == 0 || tiles >= 9 ? 2 : 1;
 }
+// A request with more query rows per KV head than this has its own rows done on tcgen05 (the warps of
+// pages_own.cu would read its K/V more than twice), the others go to pages_own.cu; the choice is made per
+// request on the device, so a batch of both runs both kernels.
+constexpr int kPgFewRows = 32;
+__host__ __device__ inline bool pg_many_new(const PgDims &D) {
+    return D.dtype != KVE_F32 && (long long)D.max_new * D.g > kPgFewRows;
+}
+
 // Query rows of a unit of own rows: 8 when no request has more, else 16 (the rows of a unit share its
 // K/V loads; more than 16 would not leave registers for two blocks per SM).
 __host__ __device__ inline int pg_unit_rows(const PgDims &D) {
-    return (long long)D.max_new * D.g <= 8 ? 8 : 16;
+    return D.dtype != KVE_F32 && (long long)D.max_new * D.g <= 8 ? 8 : 16;
 }
-// Rows of a unit that can hold a query, CTAs of the own rows' kernel (two per SM, fewer when the tables
-// cannot hold a chunk for each warp), and the places its pieces need.
+// Rows of a unit that can hold a query, CTAs of the kernel that deals out units (two per SM, fewer when
+// there cannot be a chunk for each warp), and the places its pieces need.
 inline int pg_seg_rows(const PgDims &D) {
-    const long long rows = (long long)D.max_new * D.g;
+    long long rows = (long long)D.max_new * D.g;
+    if (D.dtype == KVE_F32 && D.n > 0) rows = D.group_rows() * D.g;
     return rows < pg_unit_rows(D) ? (int)rows : pg_unit_rows(D);
 }
 inline int pg_own_ctas(const PgDims &D) {
     const int rb = pg_unit_rows(D);
-    const long long units = (long long)D.R * D.Hkv * (((long long)D.max_new * D.g + rb - 1) / rb);
-    const long long ctas = (units * ((D.cap() + kPgChunk - 1) / kPgChunk) + kPgOwnWarps - 1) /
-                           kPgOwnWarps;
+    long long rows = (long long)D.max_new * D.g;
+    if (D.dtype != KVE_F32 && rows > kPgFewRows) rows = kPgFewRows;
+    const int chunk = D.dtype == KVE_F32 ? kPgF32Chunk : kPgChunk;
+    long long chunks = (long long)D.R * D.Hkv * ((rows + rb - 1) / rb) * ((D.cap() + chunk - 1) / chunk);
+    if (D.dtype == KVE_F32)
+        chunks += (long long)D.S * D.Hkv * ((D.group_rows() * D.g + rb - 1) / rb) *
+                  ((D.n + chunk - 1) / chunk);
+    const long long ctas = (chunks + kPgOwnWarps - 1) / kPgOwnWarps;
     return (int)(ctas < 2 * D.own_sms ? ctas : 2 * D.own_sms);
 }
 inline long long pg_own_segs(const PgDims &D) {
     const long long busy = D.R < D.rows ? D.R : D.rows;
-    return D.Hkv * ((long long)D.rows * D.g / pg_unit_rows(D) + busy) +
-           (long long)pg_own_ctas(D) * kPgOwnWarps;
+    long long units = D.Hkv * ((long long)D.rows * D.g / pg_unit_rows(D) + busy);
+    if (D.dtype == KVE_F32 && D.n > 0)
+        units += D.Hkv * ((long long)D.rows * D.g / pg_unit_rows(D) + (D.S < D.rows ? D.S : D.rows));
+    return units + (long long)pg_own_ctas(D) * kPgOwnWarps;
 }
 
-// Where the own rows' pieces lie: request r's chunks start at base[r] in the line of all chunks and its
-// units at unit[r]; every warp has cpw chunks; the piece of unit u that warp w saw is at place u + w,
-// seg_rows rows each.
+// Where the pieces lie: the chunks of entity e (request e; fp32: prompt e, then request e - S) start at
+// base[e] in the line of all chunks and its units at unit[e]; every warp has cpw chunks; the piece of
+// unit u that warp w saw is at place u + w, seg_rows rows each.
 struct PgOwn {
     float2 *ml;
     float *o;
@@ -115,14 +133,15 @@ cudaError_t launch_pg_append(const PgDims &D, const void *K_new, const void *V_n
                              long long k_row, long long v_row, const int32_t *slots, void *K,
                              void *V, unsigned *err, cudaStream_t st);
 cudaError_t launch_pg_prompt_tc(const PgDims &D, const PgAttn &A, cudaStream_t st);
+cudaError_t launch_pg_own_tc(const PgDims &D, const PgAttn &A, cudaStream_t st);
+cudaError_t launch_pg_f32(const PgDims &D, const PgAttn &A, cudaStream_t st);
 cudaError_t launch_pg_own16(const PgDims &D, const PgAttn &A, cudaStream_t st);
-// Tensor map of a 16-bit array: rank dims, strides (elements) of all but the innermost, a box of at
-// most 128 bytes (swizzled by 128, or by 64 bytes) in the innermost.
+// Tensor map of a 16-bit array: rank dims, strides (elements) of all but the innermost, a box of
+// 128 bytes in the innermost, 128-byte swizzle. Boxes land on multiples of 128 bytes.
 bool pg_tmap(CUtensorMap *map, bool f16, const void *base, int rank, const cuuint64_t *dims,
-             const long long *strides, const cuuint32_t *box, bool swizzle64);
-// the three stages of pg_attention: partial results over the prompt, over the requests' own rows, and
-// their join
-cudaError_t launch_pg_prompt(const PgDims &D, const PgAttn &A, cudaStream_t st);
+             const long long *strides, const cuuint32_t *box);
+// the stages of pg_attention: partial results over the prompt (16-bit types: launch_pg_prompt_tc), over
+// the requests' own rows (fp32: and over the prompt), and their join
 cudaError_t launch_pg_own(const PgDims &D, const PgAttn &A, cudaStream_t st);
 cudaError_t launch_pg_join(const PgDims &D, const PgAttn &A, cudaStream_t st);
 
@@ -137,7 +156,7 @@ __device__ __forceinline__ int pg_start(const int32_t *q_start, int r, int rows)
     return pg_clamp(__ldg(q_start + r), 0, rows);
 }
 
-// A request's own rows: how many lie in its pages, its packed rows, and (16-bit types) its chunks per
+// A request's own rows: how many lie in its pages, its packed rows, and for pages_own.cu its chunks per
 // unit and its row blocks. Rows beyond max_new have no place.
 __device__ __forceinline__ void pg_own_request(const PgDims &D, const PgAttn &A, int r, int *len,
                                                int *first, int *nq, int *cr, int *nb) {
@@ -146,7 +165,120 @@ __device__ __forceinline__ void pg_own_request(const PgDims &D, const PgAttn &A,
     *nq = max(0, pg_start(A.q_start, r + 1, D.rows) - *first);
     *cr = (*len + kPgChunk - 1) / kPgChunk;
     const int rb = pg_unit_rows(D);
-    *nb = (min(*nq, D.max_new) * D.g + rb - 1) / rb;
+    const int rows = min(*nq, D.max_new) * D.g;
+    *nb = rows > kPgFewRows ? 0 : (rows + rb - 1) / rb;
+}
+
+// The same for fp32: entity e < S is prompt e with the rows of all its requests, S + r is request r.
+__device__ __forceinline__ void pg_f32_entity(const PgDims &D, const PgAttn &A, int e, int *len,
+                                              int *first, int *nq, int *rows, int *cr, int *nb) {
+    const bool own = e >= D.S;
+    const int r0 = own ? e - D.S : e * D.F, r1 = own ? r0 + 1 : r0 + D.F;
+    if (own) *len = pg_clamp(__ldg(A.len + r0), 0, D.cap());
+    else *len = A.plen ? pg_clamp(__ldg(A.plen + e), 0, D.n) : D.n;
+    *first = pg_start(A.q_start, r0, D.rows);
+    *nq = max(0, pg_start(A.q_start, r1, D.rows) - *first);
+    *rows = (own ? min(*nq, D.max_new) : *nq) * D.g;
+    *cr = (*len + kPgF32Chunk - 1) / kPgF32Chunk;
+    *nb = (*rows + kPgF32Rows - 1) / kPgF32Rows;
+}
+
+__device__ __forceinline__ long long pg_div(long long a, long long b) {  // of non-negative numbers
+    if (((unsigned long long)(a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+    return a / b;
+}
+
+// Equal shares of the line of chunks. All threads of the block: sums chunks and units of n entities
+// (thread t of q consecutive ones; csum[t], usum[t]: those before its), shares the chunks out evenly over
+// the launch's warps, and lets block 0 write down what the join needs. A share is at least a unit's
+// average, up to 4 chunks: less would leave more pieces to join than it saves.
+struct PgShare {
+    long long total, cpw;  // chunks in all, chunks per warp
+    int q;                 // entities per thread
+};
+template <int THREADS, typename F>
+__device__ __forceinline__ PgShare pg_share(int n, int Hkv, long long *csum, int *usum,
+                                            const PgOwn &W, F entity) {
+    const int lane = threadIdx.x & 31, q = (n + THREADS - 1) / THREADS;
+    const int a = min(n, (int)threadIdx.x * q), z = min(n, a + q);
+    long long cs = 0;
+    int us = 0;
+    for (int e = a; e < z; ++e) {
+        int cr, nb;
+        entity(e, &cr, &nb);
+        cs += (long long)cr * nb * Hkv;
+        us += nb * Hkv;
+    }
+    csum[threadIdx.x + 1] = cs;
+    usum[threadIdx.x + 1] = us;
+    if (threadIdx.x == 0) {
+        csum[0] = 0;
+        usum[0] = 0;
+    }
+    __syncthreads();
+    constexpr int K = THREADS / 32;
+    if (threadIdx.x < 32) {  // lane l scans entries K l + 1 .. K l + K
+        long long c4[K], ct = 0;
+        int u4[K], ut = 0;
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            c4[i] = ct += csum[K * lane + 1 + i];
+            u4[i] = ut += usum[K * lane + 1 + i];
+        }
+        long long cb = ct;
+        int ub = ut;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, cb, o);
+            const int y = __shfl_up_sync(0xffffffffu, ub, o);
+            if (lane >= o) {
+                cb += x;
+                ub += y;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            csum[K * lane + 1 + i] = cb - ct + c4[i];
+            usum[K * lane + 1 + i] = ub - ut + u4[i];
+        }
+    }
+    __syncthreads();
+    PgShare s;
+    s.total = csum[THREADS];
+    s.q = q;
+    const int nw = gridDim.x * (THREADS / 32), units = usum[THREADS];
+    const long long even = pg_div(s.total + nw - 1, nw);
+    const long long least = units > 0 ? min(4LL, pg_div(s.total, units)) : 1;
+    s.cpw = max(1LL, max(even, least));
+    if (blockIdx.x == 0) {
+        cs = csum[threadIdx.x];
+        us = usum[threadIdx.x];
+        for (int e = a; e < z; ++e) {
+            int cr, nb;
+            entity(e, &cr, &nb);
+            W.base[e] = cs;
+            W.unit[e] = us;
+            cs += (long long)cr * nb * Hkv;
+            us += nb * Hkv;
+        }
+        if (threadIdx.x == 0) *W.cpw = s.cpw;
+    }
+    return s;
+}
+// The first entity of the group that holds chunk X, X counted from there, and the units before it.
+template <int THREADS>
+__device__ __forceinline__ void pg_share_find(const long long *csum, const int *usum,
+                                              const PgShare &s, long long X, int *e, long long *x,
+                                              int *unit) {
+    constexpr int K = THREADS / 32;
+    const int lane = threadIdx.x & 31;
+    int grp = 0;  // the last with csum <= X
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+        grp += __popc(__ballot_sync(0xffffffffu, csum[K * lane + 1 + i] <= X));
+    *e = grp * s.q;
+    *x = X - csum[grp];
+    *unit = usum[grp];
 }
 
 // Programmatic dependent launch: a dependent kernel of the same call may start when every block of the
@@ -174,28 +306,25 @@ __device__ __forceinline__ int pg_page(const int32_t *trow, int pos, int lgP, in
     return pg_page_id(__ldg(trow + (pos >> lgP)), npages, err);
 }
 
-// Launches `kern` on `st`, as a dependent of the kernel before it if asked. All of these kernels ask for
-// the same split of the SM's memory (all of it shared memory): an SM changes its split only when it is
-// empty, so kernels that differ in it could not overlap, and with the default split the own rows' kernel
-// found room for one block on some SMs and ran in two waves (35 instead of 22 us for 64 answers).
+// Launches `kern` on `st`, as a dependent of the kernel before it if asked.
 template <typename... P, typename... Q>
-cudaError_t pg_launch(void (*kern)(P...), unsigned grid, unsigned block, size_t smem, bool dependent,
+cudaError_t pg_launch(void (*kern)(P...), dim3 grid, unsigned block, size_t smem, bool dependent,
                       cudaStream_t st, Q &&...args) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = dependent ? 1 : 0;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                         cudaSharedmemCarveoutMaxShared);
-    if (e == cudaSuccess && smem > 48 * 1024)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)smem);
+        if (e != cudaSuccess) return e;
+    }
     return cudaLaunchKernelEx(&cfg, kern, P(args)...);
 }
 

@@ -27,7 +27,10 @@ namespace {
 constexpr int kMmThreads = 32 * kPgOwnWarps, kMmTok = kPgChunk;  // tokens per chunk
 
 template <int D> constexpr int mm_stages() { return D == 128 ? 3 : 4; }
-template <int D> constexpr int mm_stage_bytes() { return kMmTok * D * 2 * 2; }  // K and V
+// A row takes at least 128 bytes: a box must start on a multiple of them, and one of page size 1 is a
+// single row. With d_head 32 the boxes reach behind the rows, where TMA fills in zeros.
+template <int D> constexpr int mm_row_bytes() { return D == 32 ? 128 : D * 2; }
+template <int D> constexpr int mm_stage_bytes() { return kMmTok * mm_row_bytes<D>() * 2; }  // K and V
 template <int D> constexpr int mm_smem() {
     return kPgOwnWarps * mm_stages<D>() * mm_stage_bytes<D>() + 1024;
 }
@@ -81,9 +84,8 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) 
 }
 
 // Where TMA puts 16-byte word c of a chunk's row: column blocks of 64 values one after the other, in
-// each 128-byte (D = 32: 64-byte) rows swizzled so that 8 rows of a word fall into different banks.
-template <int D> __device__ __forceinline__ uint32_t mm_off(int row, int c) {
-    if (D == 32) return (uint32_t)(row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+// each 128-byte rows swizzled so that 8 rows of a word fall into different banks.
+__device__ __forceinline__ uint32_t mm_off(int row, int c) {
     return (uint32_t)((c >> 3) * (kMmTok * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
 }
 
@@ -135,88 +137,26 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     if (D_.n == 0) pg_wait_prior();  // first kernel of its call (else the prompt's has waited)
     pg_launch_dependents();
 
-    // ---- chunks and units of all requests: thread t sums q consecutive ones ----
-    const int q = (D_.R + kMmThreads - 1) / kMmThreads;
-    const int ra = min(D_.R, (int)threadIdx.x * q), rz = min(D_.R, ra + q);
-    long long cs = 0;
-    int us = 0;
-    for (int r = ra; r < rz; ++r) {
-        int len, first, nq, cr, nb;
-        pg_own_request(D_, A, r, &len, &first, &nq, &cr, &nb);
-        cs += (long long)cr * nb * D_.Hkv;
-        us += nb * D_.Hkv;
-    }
-    csum[threadIdx.x + 1] = cs;
-    usum[threadIdx.x + 1] = us;
-    if (threadIdx.x == 0) {
-        csum[0] = 0;
-        usum[0] = 0;
-    }
-    __syncthreads();
-    if (warp == 0) {  // lane l scans entries 4 l + 1 .. 4 l + 4
-        long long c4[4];
-        int u4[4];
-        long long ct = 0;
-        int ut = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            c4[i] = ct += csum[4 * lane + 1 + i];
-            u4[i] = ut += usum[4 * lane + 1 + i];
-        }
-        long long cb = ct;
-        int ub = ut;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, cb, o);
-            const int y = __shfl_up_sync(0xffffffffu, ub, o);
-            if (lane >= o) {
-                cb += x;
-                ub += y;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            csum[4 * lane + 1 + i] = cb - ct + c4[i];
-            usum[4 * lane + 1 + i] = ub - ut + u4[i];
-        }
-    }
-    __syncthreads();
-    const long long total = csum[kMmThreads];
-    const int nw = gridDim.x * kPgOwnWarps;
-    long long cpw = (total + nw - 1) / nw;
-    if (cpw < 1) cpw = 1;
-    if (blockIdx.x == 0) {  // what the join needs to find the pieces again
-        cs = csum[threadIdx.x];
-        us = usum[threadIdx.x];
-        for (int r = ra; r < rz; ++r) {
-            int len, first, nq, cr, nb;
-            pg_own_request(D_, A, r, &len, &first, &nq, &cr, &nb);
-            W.base[r] = cs;
-            W.unit[r] = us;
-            cs += (long long)cr * nb * D_.Hkv;
-            us += nb * D_.Hkv;
-        }
-        if (threadIdx.x == 0) *W.cpw = cpw;
-    }
+    const PgShare sh =
+        pg_share<kMmThreads>(D_.R, D_.Hkv, csum, usum, W, [&](int r, int *cr, int *nb) {
+            int len, first, nq;
+            pg_own_request(D_, A, r, &len, &first, &nq, cr, nb);
+        });
     const int w = blockIdx.x * kPgOwnWarps + warp;
-    const long long X0 = w * cpw;
-    const int n = (int)(total - X0 < cpw ? total - X0 : cpw);  // chunks of this warp
+    const long long X0 = w * sh.cpw;
+    const int n = (int)min(sh.total - X0, sh.cpw);  // chunks of this warp
     if (n > 0) {
-        // ---- the request, unit and chunk of X0 ----
-        int grp = 0;  // the group of requests that holds X0: the last with csum <= X0
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            grp += __popc(__ballot_sync(0xffffffffu, csum[4 * lane + 1 + i] <= X0));
         Cursor cc;
-        long long x = X0 - csum[grp];
-        int unit = usum[grp];
-        cc.enter(D_, A, grp * q);
+        long long x;
+        int r, unit;
+        pg_share_find<kMmThreads>(csum, usum, sh, X0, &r, &x, &unit);
+        cc.enter(D_, A, r);
         while (x >= (long long)cc.cr * cc.nb * D_.Hkv) {
             x -= (long long)cc.cr * cc.nb * D_.Hkv;
             unit += cc.nb * D_.Hkv;
             cc.enter(D_, A, cc.r + 1);
         }
-        const int u = (unsigned long long)x >> 31 ? (int)(x / cc.cr) : (int)x / cc.cr;
+        const int u = (int)pg_div(x, cc.cr);
         cc.c = (int)(x - (long long)u * cc.cr);
         cc.kh = u / cc.nb;
         cc.rb = u - cc.kh * cc.nb;
@@ -264,7 +204,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
         // waited for. at: the box's row within its page and head, -1 behind the request's last page.
         const int lgB = D_.lgP < 4 ? D_.lgP : 4, boxes = kMmTok >> lgB;
         const int page_rows = D_.Hkv << D_.lgP;
-        const uint32_t box_bytes = (uint32_t)(D * 2 * 2) << lgB;
+        const uint32_t box_bytes = (uint32_t)(mm_row_bytes<D>() * 2) << lgB;
         // a box of 16 rows brings all column blocks, [block][row][64 values]; smaller ones one block
         const int zs = lgB < 4 && D > 64 ? D / 64 : 1;
         struct Where {
@@ -290,7 +230,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
                         tc::tma_load_3d(k + SB / 2 + z * (kMmTok * 128), &tm_v, 0, y, z, &bar[place]);
                     }
                 }
-                k += (D == 32 ? 64 : 128) << lgB;
+                k += 128 << lgB;
             }
         };
         int asked = 1, ahead = 0;  // chunks asked for, chunks issued
@@ -330,7 +270,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
                 // V rows behind the last token hold anything (their weights are 0): zeros instead
                 for (int e = (cc.len - tb) * (D / 8) + lane; e < kMmTok * (D / 8); e += 32)
                     *reinterpret_cast<uint4 *>(ring + slot * SB + SB / 2 +
-                                               mm_off<D>(e / (D / 8), e % (D / 8))) =
+                                               mm_off(e / (D / 8), e % (D / 8))) =
                         make_uint4(0, 0, 0, 0);
                 tc::fence_proxy_async_smem();  // before TMA writes there again
                 __syncwarp();
@@ -348,7 +288,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 uint32_t kf[4];
-                ldsm4(ks + mm_off<D>(lane & 15, 2 * k + (lane >> 4)), kf);
+                ldsm4(ks + mm_off(lane & 15, 2 * k + (lane >> 4)), kf);
 #pragma unroll
                 for (int b = 0; b < NT; ++b) mma16816<T>(s[b], kf, qf[b][k][0], qf[b][k][1]);
             }
@@ -397,7 +337,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
                 uint32_t vf[4];
-                ldsm4t(vs + mm_off<D>((lane & 7) + ((lane >> 4) << 3), 2 * j + ((lane >> 3) & 1)), vf);
+                ldsm4t(vs + mm_off((lane & 7) + ((lane >> 4) << 3), 2 * j + ((lane >> 3) & 1)), vf);
 #pragma unroll
                 for (int b = 0; b < NT; ++b) mma16816<T>(o[b][j], vf, pf[b][0], pf[b][1]);
             }
@@ -443,13 +383,13 @@ cudaError_t go(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
     const bool f16 = std::is_same<T, __half>::value;
     CUtensorMap tk, tv;
     // {64 columns, rows of the pool, column blocks}
-    constexpr cuuint32_t col = D == 32 ? 32 : 64;
+    constexpr int blocks = D == 128 ? 2 : 1;
     const bool whole = D_.P >= kMmTok;
-    const cuuint64_t dims[3] = {col, (cuuint64_t)D_.npages * D_.Hkv * D_.P, D / col};
-    const long long stride[2] = {D, col};
-    const cuuint32_t box[3] = {col, (cuuint32_t)(whole ? kMmTok : D_.P), whole ? D / col : 1};
-    if (!pg_tmap(&tk, f16, A.K, 3, dims, stride, box, D == 32) ||
-        !pg_tmap(&tv, f16, A.V, 3, dims, stride, box, D == 32))
+    const cuuint64_t dims[3] = {D == 32 ? 32 : 64, (cuuint64_t)D_.npages * D_.Hkv * D_.P, blocks};
+    const long long stride[2] = {D, 64};
+    const cuuint32_t box[3] = {64, (cuuint32_t)(whole ? kMmTok : D_.P), whole ? blocks : 1};
+    if (!pg_tmap(&tk, f16, A.K, 3, dims, stride, box) ||
+        !pg_tmap(&tv, f16, A.V, 3, dims, stride, box))
         return cudaErrorInvalidValue;
     return pg_launch(pg_own_kernel<T, D, NT>, pg_own_ctas(D_), kMmThreads, mm_smem<D>(), true, st, tk,
                      tv, D_, A, A.own);

@@ -13,6 +13,9 @@
 // zeros. Rows between a prompt's own length and the map's end may hold anything: their scores are
 // masked, and the softmax warps write zeros over their V rows in shared memory before they hand P on.
 // Few rows (lookahead: 4 trajectories x 4 heads): bound by HBM; many (hundreds): by the tensor pipe.
+//
+// The same kernel (OWN) takes the own rows of requests that add many rows at once: K and V as boxes of
+// the request's pages, scores masked at each row's own position.
 #include <cudaTypedefs.h>
 
 #include "pages_ptx.cuh"
@@ -75,7 +78,7 @@ struct PtArgs {
     PgDims D;
     int nrt, tt;  // row tiles (or pairs) per prompt and KV head, new rows per tile
     float k1;
-    const int32_t *plen, *q_start;
+    const int32_t *plen, *q_start, *len, *table;
     float2 *part_ml;
     float *part_o;
     unsigned *err;
@@ -216,17 +219,19 @@ __device__ __forceinline__ bool pt_issue_two(const PtBars<D, QT> &B, const PtDes
 
 // Softmax of one row tile by 4 warps (warp lg owns TMEM lanes 32 lg .. 32 lg + 31, a thread one
 // row). DB: one row tile, S(i) in buffer i % 2, whose barriers complete every second tile.
-template <typename T, int D, int QT, bool DB>
+// see0: with OWN, the tokens that the first new row sees (each later one sees one more).
+template <typename T, int D, int QT, bool OWN, bool DB>
 __device__ __forceinline__ void pt_softmax(const PtArgs &A, const PtBars<D, QT> &B, uint8_t *sm,
                                            uint32_t tmem, int warp, int lane, int row0, int nrow,
-                                           int tok0, int kh, int t0, int t1, int ntl, int sp,
-                                           volatile int *abort_flag) {
+                                           int tok0, int kh, int t0, int t1, int see0, int ntl,
+                                           int sp, volatile int *abort_flag) {
     using L = PtLayout<D, QT>;
     const int t = DB ? 0 : (warp - 4) >> 2, lg = warp & 3;
     const int r = lg * 32 + lane, g = A.D.g;
     const int first = row0 + t * A.tt * g;              // the tile's first row of the prompt
     const int rr = first + r;
     const bool valid = r < A.tt * g && rr < nrow;
+    const int see = OWN ? min(t1, see0 + rr / g) : t1;  // this row's end
     const uint32_t lane_off = (uint32_t)(lg * 32) << 16;
     const uint32_t o_col = tmem + lane_off + 256 + t * D;
     float m = kPgNoMax, l = 0.f;
@@ -247,13 +252,16 @@ __device__ __forceinline__ void pt_softmax(const PtArgs &A, const PtBars<D, QT> 
 #pragma unroll
         for (int c = 0; c < 4; ++c) tc::tmem_ld32(s_col + c * 32, s[c]);
         tc::tmem_wait_ld();
-        const int nv = t1 - (t0 + i * 128);  // tokens of this tile
-        if (nv < 128) {
+        const int nv = t1 - (t0 + i * 128);         // tokens of this tile
+        const int nvr = OWN ? see - (t0 + i * 128) : nv;  // of which the row sees
+        if (nvr < 128) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
-                    if (c * 32 + e >= nv) s[c][e] = -INFINITY;
+                    if (c * 32 + e >= nvr) s[c][e] = -INFINITY;
+        }
+        if (nv < 128) {
             // V rows behind the last token: zeros, whatever the array holds there
             const int vc = 2 * i + 1, slot = vc % L::SLOTS;
             if (!tc::mbar_wait_warp(&B.rfull[slot], (vc / L::SLOTS) & 1, abort_flag, A.err)) {
@@ -324,10 +332,10 @@ __device__ __forceinline__ void pt_softmax(const PtArgs &A, const PtBars<D, QT> 
             tc::tmem_ld32(s_col, s[0]);
             tc::tmem_ld32(s_col + 32, s[1]);
             tc::tmem_wait_ld();
-            if (nv < 64) {
+            if (nvr < 64) {
 #pragma unroll
                 for (int e = 0; e < 64; ++e)
-                    if (e >= nv) s[e >> 5][e & 31] = -INFINITY;
+                    if (e >= nvr) s[e >> 5][e & 31] = -INFINITY;
             }
             l0 = half_weights(s[0], s[1]);
         }
@@ -362,7 +370,7 @@ __device__ __forceinline__ void pt_softmax(const PtArgs &A, const PtBars<D, QT> 
         }
         __syncwarp();
         const size_t place =  // of this lane's row
-            ((size_t)sp * A.D.rows + tok0 + rr / g) * A.D.Hq + kh * g + rr % g;
+            ((size_t)(OWN ? A.D.np + sp : sp) * A.D.rows + tok0 + rr / g) * A.D.Hq + kh * g + rr % g;
         const int lpr = d / 4, col = (lane % lpr) * 4;  // lanes per row: 32, 16 or 8
         for (int x0 = 0; x0 < rows; x0 += 32 / lpr) {
             const int x = x0 + lane / lpr;
@@ -376,7 +384,7 @@ __device__ __forceinline__ void pt_softmax(const PtArgs &A, const PtBars<D, QT> 
 }
 
 // Warps: 0 TMA, 1 MMA, 2-3 idle, then 4 softmax warps per row tile.
-template <typename T, int D, int QT>
+template <typename T, int D, int QT, bool OWN>
 __global__ void __launch_bounds__(pt_threads<QT>(), 1)
     pg_prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_k,
@@ -400,27 +408,44 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
         tc::tma_prefetch_desc(&tm_q);
         *abort_flag = 0;
     }
-    pg_wait_prior();
+    if (!OWN) pg_wait_prior();  // (with OWN the call's first kernel has waited)
     pg_launch_dependents();
-    // the row tiles of a (prompt, KV head, split) are adjacent: they meet in L2 on its K/V
+    // the row tiles of a (prompt or request, KV head, split) are adjacent: they meet in L2 on its K/V
     int b = blockIdx.x;
     const int rt0 = b % A.nrt;
     b /= A.nrt;
-    const int sp = b % A.D.np;
-    b /= A.D.np;
-    const int kh = b % A.D.Hkv, s = b / A.D.Hkv;
-    const int tok0 = pg_start(A.q_start, s * A.D.F, A.D.rows);
-    const int tok1 = pg_start(A.q_start, (s + 1) * A.D.F, A.D.rows);
-    const int end = A.plen ? pg_clamp(__ldg(A.plen + s), 0, A.D.n) : A.D.n;
-    const int nrow = (tok1 - tok0) * A.D.g, per = A.tt * A.D.g;
-    const int t0 = sp * A.D.psplit, t1 = min(end, t0 + A.D.psplit);
-    const int ntl = (t1 - t0 + 127) / 128;
+    const int nsplit = OWN ? A.D.ns : A.D.np;
+    const int sp = b % nsplit;
+    b /= nsplit;
+    const int kh = b % A.D.Hkv, s = b / A.D.Hkv;  // prompt or request
+    const int tok0 = pg_start(A.q_start, OWN ? s : s * A.D.F, A.D.rows);
+    const int tok1 = pg_start(A.q_start, OWN ? s + 1 : (s + 1) * A.D.F, A.D.rows);
+    int end;
+    if (OWN) end = pg_clamp(__ldg(A.len + s), 0, A.D.cap());
+    else end = A.plen ? pg_clamp(__ldg(A.plen + s), 0, A.D.n) : A.D.n;
+    const int per = A.tt * A.D.g, see0 = end - (tok1 - tok0) + 1;
+    int nrow = (tok1 - tok0) * A.D.g;
+    if (OWN) {
+        nrow = min(tok1 - tok0, A.D.max_new) * A.D.g;
+        if (nrow <= kPgFewRows) nrow = 0;  // pages_own.cu's
+    }
+    const int step = OWN ? A.D.ssplit : A.D.psplit;
+    const int t0 = sp * step, t_end = min(end, t0 + step);
+    if (t_end <= t0) nrow = 0;
 
     // the launch has tiles for max_new rows a request; a request refused for packing more leaves
     // more rows to go through
-    for (int rt = rt0; ntl > 0 && rt * QT * per < nrow; rt += A.nrt) {
+    for (int rt = rt0; rt * QT * per < nrow; rt += A.nrt) {
         const int row0 = rt * QT * per;
         const int nqt = QT == 2 && row0 + per < nrow ? 2 : 1;
+        // with OWN, no further than its last row sees (one token at least: every split that the join
+        // counts has a result)
+        int t1 = t_end;
+        if (OWN) {
+            const int last = (min(nrow, row0 + QT * per) - 1) / A.D.g;
+            t1 = max(t0 + 1, min(t_end, see0 + last));
+        }
+        const int ntl = (t1 - t0 + 127) / 128;
         // softmax warps with a valid row, per tile
         auto warps_of = [&](int t) { return (min(per, nrow - row0 - t * per) + 31) / 32; };
         if (threadIdx.x == 0) {
@@ -444,13 +469,47 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
         const uint32_t tmem = *tmem_slot;
 
         if (warp == 0) {
-            if (lane == 0) {  // ---- TMA producer ----
+            // ---- TMA producer ----
+            if (lane == 0) {
                 tc::mbar_expect_tx(B.q_full, (uint32_t)(nqt * L::KB * per * 128));
                 for (int t = 0; t < nqt; ++t)
                     for (int kb = 0; kb < L::KB; ++kb)
                         tc::tma_load_3d(sm + t * L::TILE + kb * 16384, &tm_q, 64 * kb, kh * A.D.g,
                                     tok0 + (rt * QT + t) * A.tt, B.q_full);
-                int issued = 0;
+            }
+            int issued = 0;
+            if (OWN) {
+                // a tile is up to 128 / box boxes of box = min(page, 128) rows; the lanes look up 32
+                // at a time, one lane issues (TMA takes uniform operands)
+                const int lgB = A.D.lgP < 7 ? A.D.lgP : 7;
+                for (int c = 0; c < 2 * ntl; ++c) {
+                    const int slot = c % L::SLOTS, tb = t0 + (c >> 1) * 128;
+                    if (!tc::mbar_wait_warp(&B.rempty[slot], ((c / L::SLOTS) & 1) ^ 1, abort_flag,
+                                            A.err))
+                        break;
+                    const int boxes = (min(128, t1 - tb) + (1 << lgB) - 1) >> lgB;
+                    if (lane == 0)
+                        tc::mbar_expect_tx(&B.rfull[slot], (uint32_t)(boxes * L::KB * 128) << lgB);
+                    __syncwarp();
+                    for (int b0 = 0; b0 < boxes; b0 += 32) {
+                        const int j = tb + ((b0 + lane) << lgB);
+                        int row = 0;
+                        if (b0 + lane < boxes)
+                            row = ((pg_page(A.table + (size_t)s * A.D.maxp, j, A.D.lgP, A.D.npages,
+                                            A.err) * A.D.Hkv + kh) << A.D.lgP) + (j & (A.D.P - 1));
+                        for (int x = 0; x < min(32, boxes - b0); ++x) {
+                            const int y = __shfl_sync(0xffffffffu, row, x);
+                            if (tc::elect_one())
+                                for (int kb = 0; kb < L::KB; ++kb)
+                                    tc::tma_load_2d(sm + L::RING + slot * L::TILE + kb * 16384 +
+                                                        ((b0 + x) << lgB) * 128,
+                                                    (c & 1) ? &tm_v : &tm_k, 64 * kb, y,
+                                                    &B.rfull[slot]);
+                        }
+                    }
+                    issued = c + 1;
+                }
+            } else if (lane == 0) {
                 for (int c = 0; c < 2 * ntl; ++c) {
                     const int slot = c % L::SLOTS;
                     if (!tc::mbar_wait(&B.rempty[slot], ((c / L::SLOTS) & 1) ^ 1, abort_flag,
@@ -463,6 +522,8 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
                                     &B.rfull[slot]);
                     issued = c + 1;
                 }
+            }
+            if (lane == 0) {
                 // copies still in flight land before the CTA goes on (at once on the normal path)
                 tc::mbar_drain(B.q_full, 0);
                 for (int c = issued - L::SLOTS < 0 ? 0 : issued - L::SLOTS; c < issued; ++c)
@@ -488,11 +549,11 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
             const int t = (warp - 4) >> 2;
             if (t < nqt && (warp & 3) < warps_of(t)) {
                 if (nqt == 1)
-                    pt_softmax<T, D, QT, true>(A, B, sm, tmem, warp, lane, row0, nrow, tok0, kh, t0,
-                                               t1, ntl, sp, abort_flag);
+                    pt_softmax<T, D, QT, OWN, true>(A, B, sm, tmem, warp, lane, row0, nrow, tok0, kh,
+                                                    t0, t1, see0, ntl, sp, abort_flag);
                 else if (QT == 2)
-                    pt_softmax<T, D, QT, false>(A, B, sm, tmem, warp, lane, row0, nrow, tok0, kh, t0,
-                                                t1, ntl, sp, abort_flag);
+                    pt_softmax<T, D, QT, OWN, false>(A, B, sm, tmem, warp, lane, row0, nrow, tok0,
+                                                     kh, t0, t1, see0, ntl, sp, abort_flag);
             }
         }
         tc::fence_before_sync();
@@ -505,51 +566,60 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
     }
     __syncthreads();
     if (warp == 1) tc::tmem_dealloc(*tmem_slot, 512);
+    if (OWN) pg_wait_prior();
 }
 
 // ---- host ------------------------------------------------------------------------------------------
-template <typename T, int D, int QT>
+template <typename T, int D, int QT, bool OWN>
 cudaError_t go(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
     using L = PtLayout<D, QT>;
     constexpr bool f16 = PtIsHalf<T>::value;
     const int tt = pg_tile_rows(D_);
+    const cuuint64_t d = D_.d, one = 1;
     CUtensorMap tq, tk, tv;
-    const cuuint64_t qd[3] = {(cuuint64_t)D_.d, (cuuint64_t)D_.Hq, (cuuint64_t)D_.rows};
+    const cuuint64_t qd[3] = {d, (cuuint64_t)D_.Hq, (cuuint64_t)D_.rows};
     const long long qs[2] = {D_.d, A.q_row};
     const cuuint32_t qb[3] = {64, (cuuint32_t)D_.g, (cuuint32_t)tt};
-    const cuuint64_t kd[4] = {(cuuint64_t)D_.d, (cuuint64_t)D_.n, (cuuint64_t)D_.Hkv,
-                              (cuuint64_t)D_.S};
-    const long long ks[3] = {A.p_tok, A.p_head, A.p_prompt};
-    const cuuint32_t kb[4] = {64, 128, 1, 1};
-    if (!pg_tmap(&tq, f16, A.q, 3, qd, qs, qb, false) || !pg_tmap(&tk, f16, A.Kp, 4, kd, ks, kb, false) ||
-        !pg_tmap(&tv, f16, A.Vp, 4, kd, ks, kb, false))
+    // the prompt's {columns, tokens, heads, prompts}, or the pool's {columns, rows}
+    const cuuint64_t kd[4] = {d, OWN ? (cuuint64_t)D_.npages * D_.Hkv * D_.P : (cuuint64_t)D_.n,
+                              OWN ? one : (cuuint64_t)D_.Hkv, OWN ? one : (cuuint64_t)D_.S};
+    const long long ks[3] = {OWN ? D_.d : A.p_tok, A.p_head, A.p_prompt};
+    const cuuint32_t kb[4] = {64, OWN && D_.P < 128 ? (cuuint32_t)D_.P : 128u, 1, 1};
+    const int rank = OWN ? 2 : 4;
+    if (!pg_tmap(&tq, f16, A.q, 3, qd, qs, qb) ||
+        !pg_tmap(&tk, f16, OWN ? A.K : A.Kp, rank, kd, ks, kb) ||
+        !pg_tmap(&tv, f16, OWN ? A.V : A.Vp, rank, kd, ks, kb))
         return cudaErrorInvalidValue;
     PtArgs P{};
     P.D = D_;
     P.tt = tt;
-    P.nrt = (int)((D_.group_rows() + (long long)tt * QT - 1) / ((long long)tt * QT));
+    const long long most = OWN ? D_.max_new : D_.group_rows();
+    P.nrt = (int)((most + (long long)tt * QT - 1) / ((long long)tt * QT));
     P.k1 = kLog2e / sqrtf((float)D_.d);
     P.plen = A.plen;
     P.q_start = A.q_start;
+    P.len = A.len;
+    P.table = A.table;
     P.part_ml = A.part_ml;
     P.part_o = A.part_o;
     P.err = A.err;
-    const long long ctas = (long long)D_.S * D_.Hkv * D_.np * P.nrt;
+    const long long ctas = (long long)(OWN ? D_.R : D_.S) * D_.Hkv * (OWN ? D_.ns : D_.np) * P.nrt;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    return pg_launch(pg_prompt_tc_kernel<T, D, QT>, (unsigned)ctas, pt_threads<QT>(), L::SMEM, true, st, tq, tk, tv, P);
+    return pg_launch(pg_prompt_tc_kernel<T, D, QT, OWN>, (unsigned)ctas, pt_threads<QT>(), L::SMEM,
+                     true, st, tq, tk, tv, P);
 }
 
-template <typename T>
+template <typename T, bool OWN>
 cudaError_t by_shape(const PgDims &D, const PgAttn &A, cudaStream_t st) {
-    const int qt = pg_prompt_pairs(D);
-    if (D.d == 128) return qt == 2 ? go<T, 128, 2>(D, A, st) : go<T, 128, 1>(D, A, st);
-    return qt == 2 ? go<T, 64, 2>(D, A, st) : go<T, 64, 1>(D, A, st);
+    const int qt = pg_pairs(D, OWN ? D.max_new : D.group_rows());
+    if (D.d == 128) return qt == 2 ? go<T, 128, 2, OWN>(D, A, st) : go<T, 128, 1, OWN>(D, A, st);
+    return qt == 2 ? go<T, 64, 2, OWN>(D, A, st) : go<T, 64, 1, OWN>(D, A, st);
 }
 
 }  // namespace
 
 bool pg_tmap(CUtensorMap *map, bool f16, const void *base, int rank, const cuuint64_t *dims,
-             const long long *strides, const cuuint32_t *box, bool swizzle64) {
+             const long long *strides, const cuuint32_t *box) {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -565,12 +635,18 @@ bool pg_tmap(CUtensorMap *map, bool f16, const void *base, int rank, const cuuin
     const cuuint32_t one[4] = {1, 1, 1, 1};
     return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
               const_cast<void *>(base), dims, bytes, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_pg_prompt_tc(const PgDims &D, const PgAttn &A, cudaStream_t st) {
-    return D.dtype == KVE_BF16 ? by_shape<__nv_bfloat16>(D, A, st) : by_shape<__half>(D, A, st);
+    return D.dtype == KVE_BF16 ? by_shape<__nv_bfloat16, false>(D, A, st)
+                               : by_shape<__half, false>(D, A, st);
+}
+
+cudaError_t launch_pg_own_tc(const PgDims &D, const PgAttn &A, cudaStream_t st) {
+    return D.dtype == KVE_BF16 ? by_shape<__nv_bfloat16, true>(D, A, st)
+                               : by_shape<__half, true>(D, A, st);
 }
 
 }  // namespace kve

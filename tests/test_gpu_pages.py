@@ -348,6 +348,22 @@ def test_peaked_scores(dtype):
     Case(dtype, 1, 6, 8, 2, 128, 700, 16, 300, 2, seed=8, scale=12.0).check()
 
 
+# requests of one new row beside requests of many: both ways of the own rows in one batch
+MANY_NEW = [
+    ("bf16", 1, 5, 10, 2, 128, 200, 16, 300, 64), ("f16", 2, 3, 8, 1, 64, 130, 4, 200, 33),
+    ("bf16", 1, 4, 4, 1, 32, 90, 1, 40, 50), ("f16", 1, 3, 6, 2, 128, 0, 256, 700, 100),
+    ("bf16", 1, 2, 128, 2, 64, 70, 32, 150, 3), ("bf16", 3, 4, 3, 3, 128, 33, 128, 257, 130),
+]
+
+
+@pytest.mark.parametrize("case", MANY_NEW, ids=ids)
+def test_many_new_rows_beside_few(case):
+    Case(*case, seed=17).check()
+    c = Case(*case, seed=18, ragged=True, idle=0.2, stride=True)
+    c.check()
+    Case(*case, seed=19, nothing=True).check()
+
+
 LONG = [("bf16", 1, 4, 32, 8, 128, 16384, 16, 7, 1), ("f16", 2, 3, 8, 2, 64, 9001, 16, 5000, 1),
         ("bf16", 1, 2, 5, 1, 128, 3, 256, 20000, 2), ("f32", 1, 2, 4, 2, 64, 4000, 16, 3000, 2),
         ("bf16", 1, 300, 8, 2, 128, 2500, 64, 700, 1), ("bf16", 2, 4, 10, 2, 128, 4100, 32, 600, 64)]

@@ -97,7 +97,8 @@ BAD = [
     dict(max_pages=1 << 27),
     dict(n_rows=1 << 28, n_q_heads=8),            # rows * heads beyond 31 bits
     dict(n_kv_heads=64, n_q_heads=64, n_pages=1 << 22),   # pool rows beyond 31 bits
-    dict(n_prompts=2048, fan=1, n_q_heads=64, n_kv_heads=64),  # launch-grid limit
+    dict(n_prompts=2048, fan=1, n_q_heads=64, n_kv_heads=64),  # launch-grid limits
+    dict(n_prompts=1, fan=1, n_rows=1, n_q_heads=1 << 17, n_kv_heads=1 << 12),
 ]
 
 
