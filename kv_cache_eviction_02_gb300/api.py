@@ -481,20 +481,16 @@ class PgProblem:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _pg_device(stream):
-    """Index of the device the call launches on: the current one, which must be the stream's."""
+def _pg_launch(stream):
+    """(device index, stream address) of a call: the current device, which must be the stream's."""
     if not torch.cuda.is_initialized() and not torch.cuda.is_available():
-        return -2
+        return -2, 0 if stream is None else _stream(stream)
     dev = torch.cuda.current_device()
-    if stream is not None and getattr(stream, "device_index", dev) != dev:
+    if stream is None:
+        return dev, _raw_stream(dev) if _raw_stream is not None else _stream(None)
+    if getattr(stream, "device_index", dev) != dev:
         raise ValueError(f"stream on cuda:{stream.device_index}; the current device is cuda:{dev}")
-    return dev
-
-
-def _pg_stream(stream, dev):
-    if stream is None and _raw_stream is not None and dev >= 0:
-        return _raw_stream(dev)
-    return _stream(stream)
+    return dev, _stream(stream)
 
 
 def _pg_refuse(t, name, dtype, numel, dev):
@@ -558,27 +554,28 @@ def pg_plan(pb: PgProblem, new_len, len_in, pool_in, free_pages, block_table, le
             q_start, row_req, row_pos, slot_map, stream=None):
     """Block tables and slot maps of one step from the requests' lengths. len_out may be len_in and
     pool_out may be pool_in."""
-    R, n, i32, dev = pb.requests, pb.n_rows, torch.int32, _pg_device(stream)
+    R, n, i32 = pb.requests, pb.n_rows, torch.int32
+    dev, st = _pg_launch(stream)
     _check(lib().pg_plan(
         pb.c_shape, _pg(new_len, "new_len", i32, R, dev), _pg(len_in, "len_in", i32, R, dev),
         _pg(pool_in, "pool_in", i32, 4, dev), _pg(free_pages, "free_pages", i32, pb.n_pages, dev),
         _pg(block_table, "block_table", i32, R * pb.max_pages, dev),
         _pg(len_out, "len_out", i32, R, dev), _pg(pool_out, "pool_out", i32, 4, dev),
         _pg(q_start, "q_start", i32, R + 1, dev), _pg(row_req, "row_req", i32, n, dev),
-        _pg(row_pos, "row_pos", i32, n, dev), _pg(slot_map, "slot_map", i32, n, dev),
-        _pg_stream(stream, dev)))
+        _pg(row_pos, "row_pos", i32, n, dev), _pg(slot_map, "slot_map", i32, n, dev), st))
 
 
 def pg_append(pb: PgProblem, K_new, V_new, slot_map, K_pages, V_pages, stream=None):
     """Stores a step's K/V rows [n_rows][n_kv_heads][d_head] into the pages slot_map names. The rows
     may be slices of a wider projection's output."""
-    dt, n, dev = pb.torch_dtype, pb.n_rows, _pg_device(stream)
+    dt, n = pb.torch_dtype, pb.n_rows
+    dev, st = _pg_launch(stream)
     k, kr = _pg_rows(K_new, "K_new", dt, n, pb.n_kv_heads, pb.d_head, dev)
     v, vr = _pg_rows(V_new, "V_new", dt, n, pb.n_kv_heads, pb.d_head, dev)
     _check(lib().pg_append(
         pb.c_shape, k, v, kr, vr, _pg(slot_map, "slot_map", torch.int32, n, dev),
         _pg(K_pages, "K_pages", dt, pb.pool_elements, dev),
-        _pg(V_pages, "V_pages", dt, pb.pool_elements, dev), _pg_stream(stream, dev)))
+        _pg(V_pages, "V_pages", dt, pb.pool_elements, dev), st))
 
 
 def pg_workspace_size(pb: PgProblem) -> int:
@@ -591,26 +588,27 @@ def pg_attention(pb: PgProblem, q, K_prefix, V_prefix, prefix_len, K_pages, V_pa
     [n_q_heads][d_head] may be a slice of a wider projection's output; K_prefix and V_prefix
     [n_prompts][n_kv_heads][>= n_prefix][d_head] may be a layer's slice of a larger cache (the same
     strides for both). prefix_len and lse_out may be None."""
-    dt, R, n, i32, dev = pb.torch_dtype, pb.requests, pb.n_rows, torch.int32, _pg_device(stream)
+    dt, R, n, i32 = pb.torch_dtype, pb.requests, pb.n_rows, torch.int32
+    dev, st = _pg_launch(stream)
     qp, qr = _pg_rows(q, "q", dt, n, pb.n_q_heads, pb.d_head, dev)
-    kp, *ks = _pg_prefix(K_prefix, "K_prefix", pb, dev)
+    kp, s0, s1, s2 = _pg_prefix(K_prefix, "K_prefix", pb, dev)
     vp, *vs = _pg_prefix(V_prefix, "V_prefix", pb, dev)
-    if ks != vs:
+    if vs != [s0, s1, s2]:
         raise ValueError("V_prefix: the strides differ from K_prefix's")
     heads = n * pb.n_q_heads
+    pool = pb.pool_elements
     args = (_pg(prefix_len, "prefix_len", i32, pb.n_prompts, dev),
-            _pg(K_pages, "K_pages", dt, pb.pool_elements, dev),
-            _pg(V_pages, "V_pages", dt, pb.pool_elements, dev),
+            _pg(K_pages, "K_pages", dt, pool, dev), _pg(V_pages, "V_pages", dt, pool, dev),
             _pg(block_table, "block_table", i32, R * pb.max_pages, dev),
             _pg(lens, "lens", i32, R, dev), _pg(q_start, "q_start", i32, R + 1, dev),
             _pg(row_req, "row_req", i32, n, dev), _pg(out, "out", dt, heads * pb.d_head, dev),
             _pg(lse_out, "lse_out", torch.float32, heads, dev))
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    if ws_bytes and (workspace.get_device() != dev or not workspace.is_contiguous()):
-        _pg_refuse(workspace, "workspace", workspace.dtype, 0, dev)
-    _check(lib().pg_attention(pb.c_shape, qp, qr, kp, vp, *ks, *args,
-                              workspace.data_ptr() if ws_bytes else None, ws_bytes,
-                              _pg_stream(stream, dev)))
+    ws = ws_bytes = None
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            _pg_refuse(workspace, "workspace", workspace.dtype, 0, dev)
+    _check(lib().pg_attention(pb.c_shape, qp, qr, kp, vp, s0, s1, s2, *args, ws, ws_bytes or 0, st))
 
 
 class PgCache:

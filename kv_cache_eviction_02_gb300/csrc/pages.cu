@@ -20,13 +20,17 @@ static void pg_split(PgDims *D) {
     auto tiles_split = [](long long items, long long n, int *count, int *len) {
         const long long tiles = (n + 127) / 128;
         long long best = -1, per = 1;
-        for (long long p = 1; p <= 64 && p <= tiles; ++p) {
-            const long long waves = (items * p + kPgSms - 1) / kPgSms, t = (tiles + p - 1) / p;
-            const long long cost = waves * (t + 4);
+        // the most splits that w rounds of the SMs hold, for the first few w
+        for (long long w = (items + kPgSms - 1) / kPgSms, last = w + 12; w <= last; ++w) {
+            long long p = w * kPgSms / items;
+            if (p > 64) p = 64;
+            if (p > tiles) p = tiles;
+            const long long t = (tiles + p - 1) / p, cost = w * (t + 4);
             if (best < 0 || cost < best) {
                 best = cost;
                 per = t;
             }
+            if (p == tiles || p == 64) break;
         }
         *len = (int)(per * 128);
         *count = (int)((tiles + per - 1) / per);
@@ -115,7 +119,7 @@ PgWorkspace pg_ws_layout(const PgDims &D) {
     const size_t rows = (size_t)D.rows * D.Hq * (D.np + D.ns);
     W.part_ml = take(sizeof(float2) * rows);
     W.part_o = take(sizeof(float) * rows * D.d);
-    const size_t segs = (size_t)pg_own_segs(D) * pg_seg_rows(D);
+    const size_t segs = pg_join_own(D) ? 0 : (size_t)pg_own_segs(D) * pg_seg_rows(D);
     W.own_ml = take(sizeof(float2) * segs);
     W.own_o = take(sizeof(float) * segs * D.d);
     W.own_base = take(sizeof(long long) * (D.S + D.R));
@@ -389,7 +393,22 @@ __global__ void __launch_bounds__(256)
 // kernels that make them have ended, and eight are on their way at a time. Many are bound by reading
 // them from L2. (A warp for all heads of a KV head, to share the search, was slower: 28 against 22 us
 // for 21K rows and heads.)
-template <typename T, int D, int U>
+template <typename T, int E> __device__ __forceinline__ void row_cols(const T *p, float (&v)[E]) {
+    if (sizeof(T) * E == 8) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
+        const T *y = reinterpret_cast<const T *>(&x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = to_f(y[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = to_f(__ldg(p + e));
+    }
+}
+
+// OWN (tables of at most kPgJoinOwn rows behind a prompt: the lookahead's trajectories): the warp works
+// out the own rows itself, 8 tokens at a time, while the prompt's kernel is still running: a launch less
+// (16K lookahead step: 23 -> ? us).
+template <typename T, int D, int U, bool OWN>
 __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
     constexpr int E = D / 32;
     constexpr bool F32 = sizeof(T) == 4;
@@ -408,6 +427,7 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
             plen = A.plen ? pg_clamp(__ldg(A.plen + p), 0, D_.n) : D_.n;
         }
     }
+    const int all = nq;
     nq = min(nq, D_.max_new);
     const bool mine = r >= 0 && tok >= first && tok - first < nq;
     const int kh = h / D_.g, hk = h - kh * D_.g;
@@ -420,6 +440,52 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
     long long prow = row, pstep = step, orow = D_.np * step + row, ostep = step;
     int np = F32 || D_.np == 0 ? 0 : (plen + D_.psplit - 1) / D_.psplit;
     int no = dense ? (len + D_.ssplit - 1) / D_.ssplit : 0;
+    float M = kPgNoMax, L = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    if (OWN && mine) {
+        float q[E];
+        row_cols<T, E>(static_cast<const T *>(A.q) + tok * A.q_row + (size_t)h * D + lane * E, q);
+        const int see = len - all + 1 + (tok - first);
+        const float k1 = kLog2e * rsqrtf((float)D);
+        for (int t0 = 0; t0 < see; t0 += 8) {
+            float k[8][E], v[8][E], s[8], Mn = M;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) k[j][e] = v[j][e] = 0.f;
+                if (t0 + j < see) {
+                    const int t = t0 + j;
+                    const int page =
+                        pg_page(A.table + (size_t)r * D_.maxp, t, D_.lgP, D_.npages, A.err);
+                    const size_t at = ((((size_t)page * D_.Hkv + kh) << D_.lgP) + (t & (D_.P - 1))) * D +
+                                      lane * E;
+                    row_cols<T, E>(static_cast<const T *>(A.K) + at, k[j]);
+                    row_cols<T, E>(static_cast<const T *>(A.V) + at, v[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float x = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) x = fmaf(q[e], k[j][e], x);
+                s[j] = t0 + j < see ? warp_sum(x) * k1 : -INFINITY;  // (the same in every lane)
+                Mn = fmaxf(Mn, s[j]);
+            }
+            const float f = exp2f(M - Mn);
+            M = Mn;
+            L *= f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] *= f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float p = exp2f(s[j] - M);
+                L += p;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(p, v[j][e], acc[e]);
+            }
+        }
+    }
     pg_wait_prior();
     pg_launch_dependents();
     if (!mine) return;
@@ -433,7 +499,7 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
         *count = (int)max(min(w1 - w0 + 1, A.own.segs - at), 0LL);
         *at_row = at * A.own.seg_rows + (rr & (rb - 1));
     };
-    if (!dense) {
+    if (!dense && !OWN) {
         pieces(F32 ? D_.S + r : r, (tok - first) * D_.g + hk, cr, nb, &orow, &no);
         ostep = A.own.seg_rows;
     }
@@ -443,9 +509,6 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
     }
     const int nsp = np + no;
     // U at a time: a running maximum over the groups, in order
-    float M = kPgNoMax, L = 0.f, acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
     for (int s0 = 0; s0 < nsp; s0 += U) {
         float v[U][E];
         float2 ml[U];
@@ -503,13 +566,18 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
     if (A.lse && lane == 0) A.lse[row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
-template <typename T> cudaError_t join(const PgDims &D, const PgAttn &A, cudaStream_t st) {
+template <typename T, int D> cudaError_t join_d(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
     // few rows: 8 partial results on their way at a time; many: fewer instructions for few results
-    const bool few = (long long)D.rows * D.Hq < kPgSms * 32;
-    auto kern = D.d == 128 ? (few ? pg_join_kernel<T, 128, 8> : pg_join_kernel<T, 128, 4>)
-                           : (D.d == 64 ? (few ? pg_join_kernel<T, 64, 8> : pg_join_kernel<T, 64, 4>)
-                                        : (few ? pg_join_kernel<T, 32, 8> : pg_join_kernel<T, 32, 4>));
-    return pg_launch(kern, dim3(D.rows, (D.Hq + 3) / 4), 128, 0, true, st, D, A);
+    const bool few = (long long)D_.rows * D_.Hq < kPgSms * 32;
+    auto kern = few ? pg_join_kernel<T, D, 8, false> : pg_join_kernel<T, D, 4, false>;
+    if constexpr (sizeof(T) == 2)
+        if (pg_join_own(D_)) kern = pg_join_kernel<T, D, 8, true>;
+    return pg_launch(kern, dim3(D_.rows, (D_.Hq + 3) / 4), 128, 0, true, st, D_, A);
+}
+
+template <typename T> cudaError_t join(const PgDims &D, const PgAttn &A, cudaStream_t st) {
+    return D.d == 128 ? join_d<T, 128>(D, A, st)
+                      : (D.d == 64 ? join_d<T, 64>(D, A, st) : join_d<T, 32>(D, A, st));
 }
 
 }  // namespace
@@ -561,6 +629,7 @@ cudaError_t launch_pg_append(const PgDims &D, const void *K_new, const void *V_n
 
 cudaError_t launch_pg_own(const PgDims &D, const PgAttn &A, cudaStream_t st) {
     if (D.dtype == KVE_F32) return launch_pg_f32(D, A, st);
+    if (pg_join_own(D)) return cudaSuccess;
     const cudaError_t e = launch_pg_own16(D, A, st);
     return e == cudaSuccess && pg_many_new(D) ? launch_pg_own_tc(D, A, st) : e;
 }

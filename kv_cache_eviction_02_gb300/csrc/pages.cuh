@@ -30,8 +30,8 @@ constexpr int kPgShare = 100;  // most SMs the prompt's kernel takes beside the 
 
 // Own rows of 16-bit types: units of 8 or 16 query rows, chunks of 16 tokens (pages_own.cu).
 constexpr int kPgChunk = 16, kPgOwnWarps = 4;
-// fp32: units of 16 query rows, chunks of 8 tokens, prompts and own rows alike (pages_f32.cu).
-constexpr int kPgF32Chunk = 8, kPgF32Rows = 16;
+// fp32: units of 16 query rows, chunks of 16 tokens, prompts and own rows alike (pages_f32.cu).
+constexpr int kPgF32Chunk = 16, kPgF32Rows = 16, kPgF32Warps = 6;
 
 // Workspace carve-up (byte offsets, 256-aligned): partial results [splits][rows][Hq] (m in log2 and l;
 // o [d] fp32) over the prompt and over the own rows of requests with many new rows; the pieces of units
@@ -62,13 +62,18 @@ __host__ __device__ inline bool pg_many_new(const PgDims &D) {
     return D.dtype != KVE_F32 && (long long)D.max_new * D.g > kPgFewRows;
 }
 
+// The join works out the own rows itself where a table holds few rows behind a prompt (16-bit types).
+constexpr int kPgJoinOwn = 32;
+inline bool pg_join_own(const PgDims &D) {
+    return D.dtype != KVE_F32 && D.n > 0 && D.cap() <= kPgJoinOwn && !pg_many_new(D);
+}
 // Query rows of a unit of own rows: 8 when no request has more, else 16 (the rows of a unit share its
 // K/V loads; more than 16 would not leave registers for two blocks per SM).
 __host__ __device__ inline int pg_unit_rows(const PgDims &D) {
     return D.dtype != KVE_F32 && (long long)D.max_new * D.g <= 8 ? 8 : 16;
 }
-// Rows of a unit that can hold a query, CTAs of the kernel that deals out units (two per SM, fewer when
-// there cannot be a chunk for each warp), and the places its pieces need.
+// Rows of a unit that can hold a query, CTAs of the kernel that deals out units (two per SM, fp32 one;
+// fewer when there cannot be a chunk for each warp), and the places its pieces need.
 inline int pg_seg_rows(const PgDims &D) {
     long long rows = (long long)D.max_new * D.g;
     if (D.dtype == KVE_F32 && D.n > 0) rows = D.group_rows() * D.g;
@@ -83,15 +88,16 @@ inline int pg_own_ctas(const PgDims &D) {
     if (D.dtype == KVE_F32)
         chunks += (long long)D.S * D.Hkv * ((D.group_rows() * D.g + rb - 1) / rb) *
                   ((D.n + chunk - 1) / chunk);
-    const long long ctas = (chunks + kPgOwnWarps - 1) / kPgOwnWarps;
-    return (int)(ctas < 2 * D.own_sms ? ctas : 2 * D.own_sms);
+    const int warps = D.dtype == KVE_F32 ? kPgF32Warps : kPgOwnWarps;
+    const long long ctas = (chunks + warps - 1) / warps, most = D.own_sms * (D.dtype == KVE_F32 ? 1 : 2);
+    return (int)(ctas < most ? ctas : most);
 }
 inline long long pg_own_segs(const PgDims &D) {
     const long long busy = D.R < D.rows ? D.R : D.rows;
     long long units = D.Hkv * ((long long)D.rows * D.g / pg_unit_rows(D) + busy);
     if (D.dtype == KVE_F32 && D.n > 0)
         units += D.Hkv * ((long long)D.rows * D.g / pg_unit_rows(D) + (D.S < D.rows ? D.S : D.rows));
-    return units + (long long)pg_own_ctas(D) * kPgOwnWarps;
+    return units + (long long)pg_own_ctas(D) * (D.dtype == KVE_F32 ? kPgF32Warps : kPgOwnWarps);
 }
 
 // Where the pieces lie: the chunks of entity e (request e; fp32: prompt e, then request e - S) start at
@@ -190,8 +196,8 @@ __device__ __forceinline__ long long pg_div(long long a, long long b) {  // of n
 
 // Equal shares of the line of chunks. All threads of the block: sums chunks and units of n entities
 // (thread t of q consecutive ones; csum[t], usum[t]: those before its), shares the chunks out evenly over
-// the launch's warps, and lets block 0 write down what the join needs. A share is at least a unit's
-// average, up to 4 chunks: less would leave more pieces to join than it saves.
+// the launch's warps, and lets block 0 write down what the join needs. A share is at least a 16th of the
+// longest unit, up to 4 chunks: smaller ones would leave more pieces to join than they save.
 struct PgShare {
     long long total, cpw;  // chunks in all, chunks per warp
     int q;                 // entities per thread
@@ -202,13 +208,16 @@ __device__ __forceinline__ PgShare pg_share(int n, int Hkv, long long *csum, int
     const int lane = threadIdx.x & 31, q = (n + THREADS - 1) / THREADS;
     const int a = min(n, (int)threadIdx.x * q), z = min(n, a + q);
     long long cs = 0;
-    int us = 0;
+    int us = 0, longest = 0;
     for (int e = a; e < z; ++e) {
         int cr, nb;
         entity(e, &cr, &nb);
         cs += (long long)cr * nb * Hkv;
         us += nb * Hkv;
+        if (nb > 0) longest = max(longest, cr);
     }
+    __shared__ int s_longest;
+    if (threadIdx.x == 0) s_longest = 0;
     csum[threadIdx.x + 1] = cs;
     usum[threadIdx.x + 1] = us;
     if (threadIdx.x == 0) {
@@ -216,6 +225,7 @@ __device__ __forceinline__ PgShare pg_share(int n, int Hkv, long long *csum, int
         usum[0] = 0;
     }
     __syncthreads();
+    atomicMax(&s_longest, longest);
     constexpr int K = THREADS / 32;
     if (threadIdx.x < 32) {  // lane l scans entries K l + 1 .. K l + K
         long long c4[K], ct = 0;
@@ -246,10 +256,8 @@ __device__ __forceinline__ PgShare pg_share(int n, int Hkv, long long *csum, int
     PgShare s;
     s.total = csum[THREADS];
     s.q = q;
-    const int nw = gridDim.x * (THREADS / 32), units = usum[THREADS];
-    const long long even = pg_div(s.total + nw - 1, nw);
-    const long long least = units > 0 ? min(4LL, pg_div(s.total, units)) : 1;
-    s.cpw = max(1LL, max(even, least));
+    const int nw = gridDim.x * (THREADS / 32);
+    s.cpw = max(max(1LL, pg_div(s.total + nw - 1, nw)), min(4LL, (s_longest + 15) / 16LL));
     if (blockIdx.x == 0) {
         cs = csum[threadIdx.x];
         us = usum[threadIdx.x];

@@ -2,31 +2,35 @@
 // in one launch.
 //
 // The work of all prompts and all requests stands in one line: entities (the prompts, then the
-// requests), of each its units (KV head, block of 16 query rows), of each its chunks of 8 tokens; every
+// requests), of each its units (KV head, block of 16 query rows), of each its chunks of 16 tokens; every
 // warp takes the same number of consecutive chunks and leaves one partial result per unit it has seen a
 // piece of, at place (unit index + warp index). (pages_own.cu deals out the own rows of 16-bit types in
 // the same way.)
 //
-// Within a warp a lane owns D/32 columns of K, V, Q and O, so a token's row is one shared-memory read
-// without bank conflicts and Q and O stay in registers. For 4 query rows and 8 tokens the lanes' 32
-// partial dot products are summed by recursive halving (31 exchanges in all), which leaves the score of
-// (row, token) in lane 8 row + token; weights go back to all lanes through 512 bytes of shared memory.
-// Sums of d products in a tree of 32, everything fp32; the factor log2 e / sqrt d is carried as two
-// floats, since its rounding would shift every score the same way. Bound by HBM up to 8 query rows per
-// KV head, by FFMA issue at 16.
+// The products run on the tensor cores as sums of three tf32 products: x = hi + lo, hi of 11 and lo of
+// the next 11 bits, x y = hi hi + hi lo + lo hi up to 2^-21 |x y| (fp32 carries 2^-24; the errors of d
+// products of either sign add up to less than the rounding of their fp32 sum). They are taken transposed,
+// S^T = K Q^T and O^T = V^T P^T in m16n8k8 fragments: 16 tokens (or output columns) on the wide side, 8
+// query rows on the narrow one. The tensor cores' own sums are kept short: the scores in three
+// accumulators, O of each chunk in fresh ones that are then added to the running O in fp32. (FFMA with a
+// lane per D/32 columns took 4 times the instructions: a lookahead step over 32K rows 143 us.)
+// Everything else is fp32; the factor log2 e / sqrt d is carried as two floats, since its rounding would
+// shift every score the same way.
 #include "pages.cuh"
 
 namespace kve {
 namespace {
 
-constexpr int kF3Threads = 32 * kPgOwnWarps, kF3Tok = kPgF32Chunk, kF3Rows = kPgF32Rows;
+constexpr int kF3Warps = kPgF32Warps, kF3Threads = 32 * kF3Warps;
+constexpr int kF3Tok = kPgF32Chunk, kF3Rows = kPgF32Rows, kF3NT = kF3Rows / 8;
 
-template <int D> constexpr int f3_stages() { return D == 128 ? 3 : 6; }
-template <int D> constexpr int f3_stage_floats() { return 2 * kF3Tok * D; }  // K and V
+// Rows in shared memory are padded so that the fragments' reads fall into 32 different banks: K's by 4
+// floats (8 tokens x 4 columns), V's by 8 (4 tokens x 8 columns).
+template <int D> constexpr int f3_stages() { return D == 128 ? 2 : (D == 64 ? 4 : 6); }
+template <int D> constexpr int f3_stage_floats() { return kF3Tok * (2 * D + 12); }
 template <int D> constexpr int f3_smem() {
-    return kPgOwnWarps * (f3_stages<D>() * f3_stage_floats<D>() + kF3Tok * kF3Rows) * 4;
+    return kF3Warps * f3_stages<D>() * f3_stage_floats<D>() * 4;
 }
-constexpr float kF3Rescale = 8.f;  // O is rescaled when a row's maximum grew by more than 2^8
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool on) {
     // src-size 0 fills the 16 bytes with zeros: rows behind the last token hold anything
@@ -39,38 +43,17 @@ template <int N> __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <int E> struct Cols { float v[E]; };
-template <int E> __device__ __forceinline__ Cols<E> cols(const float *p) {
-    Cols<E> c;
-    if (E == 4) {
-        const float4 x = *reinterpret_cast<const float4 *>(p);
-        c.v[0] = x.x;
-        c.v[1 % E] = x.y;
-        c.v[2 % E] = x.z;
-        c.v[3 % E] = x.w;
-    } else if (E == 2) {
-        const float2 x = *reinterpret_cast<const float2 *>(p);
-        c.v[0] = x.x;
-        c.v[1 % E] = x.y;
-    } else {
-        c.v[0] = *p;
-    }
-    return c;
+// x = hi + lo, hi rounded to tf32 (the tensor cores read the upper 19 bits of lo).
+__device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
 }
-
-// Sums 32 values over the 32 lanes: lane L is left with the sum of value L.
-__device__ __forceinline__ float halve(float (&v)[32]) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const bool up = lane & o;
-#pragma unroll
-        for (int i = 0; i < o; ++i) {
-            const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-        }
-    }
-    return v[0];
+__device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // Where a warp stands in the line of chunks.
@@ -96,8 +79,9 @@ struct Cursor {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kF3Threads, 2) pg_f32_kernel(PgDims D_, PgAttn A, PgOwn W) {
-    constexpr int NST = f3_stages<D>(), SF = f3_stage_floats<D>(), E = D / 32, NG = kF3Rows / 4;
+__global__ void __launch_bounds__(kF3Threads, 1) pg_f32_kernel(PgDims D_, PgAttn A, PgOwn W) {
+    constexpr int NST = f3_stages<D>(), SF = f3_stage_floats<D>(), NT = kF3NT;
+    constexpr int KP = D + 4, VP = D + 8;  // floats from one row to the next
     extern __shared__ __align__(16) float sm[];
     __shared__ long long csum[kF3Threads + 1];
     __shared__ int usum[kF3Threads + 1];
@@ -109,7 +93,7 @@ __global__ void __launch_bounds__(kF3Threads, 2) pg_f32_kernel(PgDims D_, PgAttn
             int len, first, nq, rows;
             pg_f32_entity(D_, A, e, &len, &first, &nq, &rows, cr, nb);
         });
-    const int w = blockIdx.x * kPgOwnWarps + warp;
+    const int w = blockIdx.x * kF3Warps + warp;
     const long long X0 = w * sh.cpw;
     const int n = (int)min(sh.total - X0, sh.cpw);  // chunks of this warp
     if (n <= 0) return;
@@ -133,9 +117,9 @@ __global__ void __launch_bounds__(kF3Threads, 2) pg_f32_kernel(PgDims D_, PgAttn
     }
     Cursor ca = cc;  // runs ahead: the chunks to load
 
-    float *ring = sm + warp * (NST * SF + kF3Tok * kF3Rows), *ps = ring + NST * SF;
+    float *ring = sm + warp * (NST * SF);
     const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-    // lane t (mod 8) looks after token t of a chunk: where it lies is asked two chunks before it is
+    // lane t (mod 16) looks after token t of a chunk: where it lies is asked two chunks before it is
     // loaded, so the answer of the block table is not waited for
     struct Where {
         long long base;  // prompts: the element offset of the head's first row
@@ -161,40 +145,45 @@ __global__ void __launch_bounds__(kF3Threads, 2) pg_f32_kernel(PgDims D_, PgAttn
         if (x.at >= 0)
             o = x.own ? ((long long)pg_page_id(x.page, D_.npages, A.err) * (D_.Hkv << D_.lgP) + x.at) * D
                       : x.base + x.at * A.p_tok;
-        const uint32_t dst = ring_s + (uint32_t)(place * SF * 4 + lane * 16);
+        const uint32_t dst = ring_s + (uint32_t)(place * SF * 4 + (lane % WPR) * 16);
 #pragma unroll
         for (int i = 0; i < kF3Tok / RPI; ++i) {
-            const long long r = __shfl_sync(0xffffffffu, o, i * RPI + lane / WPR);
+            const int row = i * RPI + lane / WPR;
+            const long long r = __shfl_sync(0xffffffffu, o, row);
             const long long at = (r < 0 ? 0 : r) + (lane % WPR) * 4;
-            cp16(dst + i * 512, Kb + at, r >= 0);
-            cp16(dst + i * 512 + kF3Tok * D * 4, Vb + at, r >= 0);
+            cp16(dst + row * KP * 4, Kb + at, r >= 0);
+            cp16(dst + (kF3Tok * KP + row * VP) * 4, Vb + at, r >= 0);
         }
     };
-    float q[kF3Rows][E], o[kF3Rows][E];  // this lane's columns of the unit's 16 rows
-    float m[NG], l[NG];                  // of row lane / 8 of each group of 4
-    int see[NG], live;                   // tokens the row sees; the unit's rows
-    auto begin = [&]() {                 // of a unit, or of this warp's part of one
+    float q[NT][D / 8][2];                    // B operand of S^T: query row lane / 4 of each block
+    float o[NT][D / 16][4], m[NT][2], l[NT][2];  // this lane's query rows 2 (lane % 4), + 1
+    int see[NT][2], live;                     // tokens they see; the unit's rows
+    auto begin = [&]() {                      // of a unit, or of this warp's part of one
         const int row0 = cc.rb * kF3Rows;
         live = min(kF3Rows, cc.rows - row0);
 #pragma unroll
-        for (int r = 0; r < kF3Rows; ++r) {
+        for (int b = 0; b < NT; ++b) {
+            const int rr = row0 + 8 * b + (lane >> 2), t = rr < cc.rows ? rr / D_.g : 0;
+            const float *qp = static_cast<const float *>(A.q) + (cc.first + t) * A.q_row +
+                              (size_t)(cc.kh * D_.g + (rr < cc.rows ? rr - t * D_.g : 0)) * D +
+                              (lane & 3);
 #pragma unroll
-            for (int x = 0; x < E; ++x) q[r][x] = o[r][x] = 0.f;
-            if (r < live) {
-                const int t = (row0 + r) / D_.g, h = cc.kh * D_.g + row0 + r - t * D_.g;
-                const Cols<E> c = cols<E>(static_cast<const float *>(A.q) +
-                                          (cc.first + t) * A.q_row + (size_t)h * D + lane * E);
-#pragma unroll
-                for (int x = 0; x < E; ++x) q[r][x] = c.v[x];
+            for (int k = 0; k < D / 8; ++k) {
+                q[b][k][0] = rr < cc.rows ? __ldg(qp + 8 * k) : 0.f;
+                q[b][k][1] = rr < cc.rows ? __ldg(qp + 8 * k + 4) : 0.f;
             }
-        }
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const int r = row0 + g * 4 + (lane >> 3);
-            see[g] = cc.e < D_.S ? cc.len : cc.len - cc.nq + 1 + r / D_.g;
-            if (r >= cc.rows) see[g] = 0;
-            m[g] = kPgNoMax;
-            l[g] = 0.f;
+            for (int e = 0; e < 2; ++e) {
+                const int qr = row0 + 8 * b + (lane & 3) * 2 + e;
+                see[b][e] = qr >= cc.rows ? 0
+                                          : (cc.e < D_.S ? cc.len : cc.len - cc.nq + 1 + qr / D_.g);
+                m[b][e] = kPgNoMax;
+                l[b][e] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[b][j][e] = 0.f;
         }
     };
     int asked = 1, ahead = 0;
@@ -233,85 +222,121 @@ __global__ void __launch_bounds__(kF3Threads, 2) pg_f32_kernel(PgDims D_, PgAttn
         if (i > 0 && cc.c == 0) begin();
         cp_wait<NST - 1>();
         __syncwarp();
-        const float *ks = ring + slot * SF + lane * E, *vs = ks + kF3Tok * D;
+        const float *ks = ring + slot * SF, *vs = ks + kF3Tok * KP;
         if (++slot == NST) slot = 0;
-        const int tok = cc.c * kF3Tok + (lane & 7);
+        const int nb = live > 8 ? 2 : 1;  // blocks with a row
+        // S^T, in three accumulators: hi hi of even and of odd steps, and the rest
+        float s0[NT][4], s1[NT][4], s2[NT][4];
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            if (g * 4 >= live) break;
-            float part[32];
+        for (int b = 0; b < NT; ++b)
 #pragma unroll
-            for (int t = 0; t < kF3Tok; ++t) {
-                const Cols<E> k = cols<E>(ks + t * D);
+            for (int e = 0; e < 4; ++e) s0[b][e] = s1[b][e] = s2[b][e] = 0.f;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    float a = q[g * 4 + r][0] * k.v[0];
+        for (int k = 0; k < D / 8; ++k) {
+            uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int x = 1; x < E; ++x) a = fmaf(q[g * 4 + r][x], k.v[x], a);
-                    part[r * 8 + t] = a;
-                }
+            for (int e = 0; e < 4; ++e)
+                split(ks[((lane >> 2) + 8 * (e & 1)) * KP + 8 * k + 4 * (e >> 1) + (lane & 3)], hi[e],
+                      lo[e]);
+#pragma unroll
+            for (int b = 0; b < NT; ++b) {
+                if (b >= nb) break;
+                uint32_t h0, l0, h1, l1;
+                split(q[b][k][0], h0, l0);
+                split(q[b][k][1], h1, l1);
+                mma1688(k & 1 ? s1[b] : s0[b], hi, h0, h1);
+                mma1688(s2[b], hi, l0, l1);
+                mma1688(s2[b], lo, h0, h1);
             }
-            const float dot = halve(part);  // (by all lanes)
-            const float s = tok < see[g] ? dot : -INFINITY;
-            float smax = s;
-#pragma unroll
-            for (int x = 1; x < 8; x <<= 1)
-                smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, x));
-            const float mt = fmaf(smax, k_hi, smax * k_lo);
-            const bool grow = mt > m[g] + kF3Rescale;
-            if (__any_sync(0xffffffffu, grow)) {
-                const float mn = fmaxf(m[g], mt), f = exp2f(m[g] - mn);
-                m[g] = mn;
-                l[g] *= f;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float fr = __shfl_sync(0xffffffffu, f, r * 8);
-#pragma unroll
-                    for (int x = 0; x < E; ++x) o[g * 4 + r][x] *= fr;
-                }
-            }
-            // s log2 e / sqrt d - m with one rounding near the result
-            const float p = s == -INFINITY ? 0.f : exp2f(fmaf(s, k_hi, fmaf(s, k_lo, -m[g])));
-            l[g] += p;
-            ps[(lane & 7) * kF3Rows + g * 4 + (lane >> 3)] = p;
         }
-        __syncwarp();
+        const int tok = cc.c * kF3Tok + (lane >> 2);
+        uint32_t ph[NT][2][2], pl[NT][2][2];  // B operand of O^T: tokens 8 x .. 8 x + 7
+        float f[NT][2];                       // what the rows' O and l shrink by
 #pragma unroll
-        for (int t = 0; t < kF3Tok; ++t) {
-            const Cols<E> v = cols<E>(vs + t * D);
+        for (int b = 0; b < NT; ++b) {
+            if (b >= nb) break;
+            float p[4];
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                if (g * 4 >= live) break;
-                const float4 p = *reinterpret_cast<const float4 *>(ps + t * kF3Rows + g * 4);
-                const float pr[4] = {p.x, p.y, p.z, p.w};
+            for (int e = 0; e < 2; ++e) {
+                float a = (s0[b][e] + s1[b][e]) + s2[b][e];
+                float c = (s0[b][e + 2] + s1[b][e + 2]) + s2[b][e + 2];
+                a = tok < see[b][e] ? a : -INFINITY;
+                c = tok + 8 < see[b][e] ? c : -INFINITY;
+                float x = fmaxf(a, c);
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                const float mn = x == -INFINITY ? m[b][e] : fmaxf(m[b][e], fmaf(x, k_hi, x * k_lo));
+                f[b][e] = exp2f(m[b][e] - mn);
+                m[b][e] = mn;
+                // s log2 e / sqrt d - m with one rounding near the result
+                p[e] = a == -INFINITY ? 0.f : exp2f(fmaf(a, k_hi, fmaf(a, k_lo, -mn)));
+                p[e + 2] = c == -INFINITY ? 0.f : exp2f(fmaf(c, k_hi, fmaf(c, k_lo, -mn)));
+                l[b][e] = fmaf(l[b][e], f[b][e], p[e] + p[e + 2]);
+            }
+            // from (token lane / 4, row 2 (lane % 4) + e) to (token lane % 4 + 4 h, row lane / 4)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int x = 0; x < E; ++x) o[g * 4 + r][x] = fmaf(pr[r], v.v[x], o[g * 4 + r][x]);
+                for (int h = 0; h < 2; ++h) {
+                    const int from = ((lane & 3) + 4 * h) * 4 + (lane >> 3);
+                    const float even = __shfl_sync(0xffffffffu, p[2 * x], from);
+                    const float odd = __shfl_sync(0xffffffffu, p[2 * x + 1], from);
+                    split(lane & 4 ? odd : even, ph[b][x][h], pl[b][x][h]);
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            float t[NT][4];
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) t[b][e] = 0.f;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    split(vs[(8 * x + 4 * (e >> 1) + (lane & 3)) * VP + 16 * j + 8 * (e & 1) +
+                             (lane >> 2)],
+                          hi[e], lo[e]);
+#pragma unroll
+                for (int b = 0; b < NT; ++b) {
+                    if (b >= nb) break;
+                    mma1688(t[b], lo, ph[b][x][0], ph[b][x][1]);
+                    mma1688(t[b], hi, pl[b][x][0], pl[b][x][1]);
+                    mma1688(t[b], hi, ph[b][x][0], ph[b][x][1]);
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < NT; ++b) {
+                if (b >= nb) break;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[b][j][e] = fmaf(o[b][j][e], f[b][e & 1], t[b][e]);
             }
         }
         if (i == n - 1 || cc.c == cc.cr - 1) {  // the piece ends
             const long long seg = (long long)unit + w;
-            // (row starts that are no sums of lengths can ask for more places than there are)
-            if (seg < W.segs) {
-                const size_t at = (size_t)seg * W.seg_rows;
 #pragma unroll
-                for (int r = 0; r < kF3Rows; ++r)
-                    if (r < live) {
-                        float *dst = W.o + (at + r) * D + lane * E;
+            for (int b = 0; b < NT; ++b)
 #pragma unroll
-                        for (int x = 0; x < E; ++x) dst[x] = o[r][x];
-                    }
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    float x = l[g];
-                    x += __shfl_xor_sync(0xffffffffu, x, 1);
-                    x += __shfl_xor_sync(0xffffffffu, x, 2);
+                for (int e = 0; e < 2; ++e) {
+                    float x = l[b][e];
                     x += __shfl_xor_sync(0xffffffffu, x, 4);
-                    const int r = g * 4 + (lane >> 3);
-                    if ((lane & 7) == 0 && r < live) W.ml[at + r] = make_float2(m[g], x);
+                    x += __shfl_xor_sync(0xffffffffu, x, 8);
+                    x += __shfl_xor_sync(0xffffffffu, x, 16);
+                    const int qr = 8 * b + (lane & 3) * 2 + e;
+                    // (row starts that are no sums of lengths can ask for more places than there are)
+                    if (qr >= live || seg >= W.segs) continue;
+                    const size_t row = (size_t)seg * W.seg_rows + qr;
+                    if (lane < 4) W.ml[row] = make_float2(m[b][e], x);
+                    float *dst = W.o + row * D + (lane >> 2);
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        dst[16 * j] = o[b][j][e];
+                        dst[16 * j + 8] = o[b][j][e + 2];
+                    }
                 }
-            }
             ++unit;
         }
         if (i + 1 < n) cc.next(D_, A);
