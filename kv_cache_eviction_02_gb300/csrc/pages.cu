@@ -42,8 +42,8 @@ static void pg_split(PgDims *D) {
     if (D->dtype == KVE_F32) return;
     if (D->n > 0) {
         const long long per = pg_tile_rows(*D) * pg_pairs(*D, D->group_rows());
-        const long long most = D->S * ((D->group_rows() + per - 1) / per);  // launched per KV head
-        const long long all = D->rows / per + D->S;                         // of which hold rows
+        const long long most = (long long)D->S * pg_tc_blocks(*D, false);  // launched per KV head
+        const long long all = D->rows / per + D->S;                        // of which hold rows
         const long long items = D->Hkv * (most < all ? most : all);
         tiles_split(items, D->n, &D->np, &D->psplit);
         // (the prompt's kernel starts first)
@@ -52,7 +52,7 @@ static void pg_split(PgDims *D) {
     }
     if (pg_many_new(*D)) {
         const long long per = pg_tile_rows(*D) * pg_pairs(*D, D->max_new);
-        const long long most = D->R * ((D->max_new + per - 1) / per), all = D->rows / per + D->R;
+        const long long most = (long long)D->R * pg_tc_blocks(*D, true), all = D->rows / per + D->R;
         tiles_split(D->Hkv * (most < all ? most : all), D->cap(), &D->ns, &D->ssplit);
     }
 }
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
         const long long w0 = pg_div(x, cpw), w1 = chunks > 0 ? pg_div(x + chunks - 1, cpw) : w0 - 1;
         const long long at = A.own.unit[e] + u + w0;
         // as many as there are places (all, when the row starts are sums of lengths)
-        *count = (int)max(min(w1 - w0 + 1, A.own.segs - at), 0LL);
+        *count = at < 0 ? 0 : (int)max(min(w1 - w0 + 1, (long long)A.own.segs - at), 0LL);
         *at_row = at * A.own.seg_rows + (rr & (rb - 1));
     };
     if (!dense && !OWN) {

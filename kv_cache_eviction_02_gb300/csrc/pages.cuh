@@ -54,6 +54,15 @@ inline int pg_pairs(const PgDims &D, long long rows) {
     const long long tiles = (rows + pg_tile_rows(D) - 1) / pg_tile_rows(D);
     return tiles % 2 == 0 || tiles >= 9 ? 2 : 1;
 }
+// Row blocks (one or two tiles) that the launch has places for, per prompt or request: as many as it can
+// have, and no more than four times its even share (with max_new far above what most requests add, nearly
+// all of them would come to nothing).
+inline int pg_tc_blocks(const PgDims &D, bool own) {
+    const long long rows = own ? D.max_new : D.group_rows(), of = own ? D.R : D.S;
+    const long long per = (long long)pg_tile_rows(D) * pg_pairs(D, rows);
+    const long long most = (rows + per - 1) / per, share = 4 * ((D.rows + per * of - 1) / (per * of));
+    return (int)(most < share ? most : share);
+}
 // A request with more query rows per KV head than this has its own rows done on tcgen05 (the warps of
 // pages_own.cu would read its K/V more than twice), the others go to pages_own.cu; the choice is made per
 // request on the device, so a batch of both runs both kernels.
@@ -75,8 +84,8 @@ __host__ __device__ inline int pg_unit_rows(const PgDims &D) {
 // Rows of a unit that can hold a query, CTAs of the kernel that deals out units (two per SM, fp32 one;
 // fewer when there cannot be a chunk for each warp), and the places its pieces need.
 inline int pg_seg_rows(const PgDims &D) {
-    long long rows = (long long)D.max_new * D.g;
-    if (D.dtype == KVE_F32 && D.n > 0) rows = D.group_rows() * D.g;
+    // (a prompt's rows may be all there are: a refused request can pack more than max_new)
+    const long long rows = (long long)(D.dtype == KVE_F32 && D.n > 0 ? D.rows : D.max_new) * D.g;
     return rows < pg_unit_rows(D) ? (int)rows : pg_unit_rows(D);
 }
 inline int pg_own_ctas(const PgDims &D) {
@@ -108,7 +117,7 @@ struct PgOwn {
     float *o;
     long long *base, *cpw;
     int *unit;
-    long long segs;
+    unsigned long long segs;
     int seg_rows;
 };
 
@@ -152,6 +161,12 @@ cudaError_t launch_pg_own(const PgDims &D, const PgAttn &A, cudaStream_t st);
 cudaError_t launch_pg_join(const PgDims &D, const PgAttn &A, cudaStream_t st);
 
 constexpr float kPgNoMax = -3e38f;  // running maximum before any visible token
+
+// 16-bit types: a row is rescaled when its maximum has grown by 2^kPgRescale, so weights reach that. fp16
+// weights are carried kPgHalfUp powers of two higher (its largest number is just below 2^16): a weight is
+// then off by half a step or, below 2^-21 of the largest, by 2^-32 of it, where 2^-25 would let many small
+// ones vanish together. The reference stored as m is lower by as much.
+constexpr float kPgRescale = 8.f, kPgHalfUp = 7.f;
 
 // ---- device helpers --------------------------------------------------------------------------------
 // The device arrays are the caller's: every index read from them is brought into range before it

@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kF3Threads, 1) pg_f32_kernel(PgDims D_, PgAttn
                     x += __shfl_xor_sync(0xffffffffu, x, 16);
                     const int qr = 8 * b + (lane & 3) * 2 + e;
                     // (row starts that are no sums of lengths can ask for more places than there are)
-                    if (qr >= live || seg >= W.segs) continue;
+                    if (qr >= live || (unsigned long long)seg >= W.segs) continue;
                     const size_t row = (size_t)seg * W.seg_rows + qr;
                     if (lane < 4) W.ml[row] = make_float2(m[b][e], x);
                     float *dst = W.o + row * D + (lane >> 2);

@@ -71,7 +71,7 @@ __device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two weights as a 16-bit pair. A weight is at most 2^8 (see kMmRescale) and rounds to half a step
+// Two weights as a 16-bit pair. A weight is at most 2^8 (fp16: 2^15; see kPgRescale) and rounds to half a step
 // of the type, as V's own entries did; their sum l is taken in fp32 before the rounding.
 template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
 template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
@@ -89,7 +89,6 @@ __device__ __forceinline__ uint32_t mm_off(int row, int c) {
     return (uint32_t)((c >> 3) * (kMmTok * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
 }
 
-constexpr float kMmRescale = 8.f;  // O is rescaled when a row's maximum grew by more than 2^8
 
 // Where a warp stands in the line of chunks.
 struct Cursor {
@@ -306,7 +305,8 @@ __global__ void __launch_bounds__(kMmThreads, 2)
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                     mt[b][e] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    grow = grow || mt[b][e] > m[b][e] + kMmRescale;
+                    if (std::is_same<T, __half>::value) mt[b][e] -= kPgHalfUp;
+                    grow = grow || mt[b][e] > m[b][e] + kPgRescale;
                 }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
                         x += __shfl_xor_sync(0xffffffffu, x, 16);
                         const int qr = 8 * b + (lane & 3) * 2 + e;
                         // (row starts that are no sums of lengths can ask for more places than there are)
-                        if (row0 + qr >= rows || seg >= W.segs) continue;
+                        if (row0 + qr >= rows || (unsigned long long)seg >= W.segs) continue;
                         const size_t row = (size_t)seg * W.seg_rows + qr;
                         if (lane < 4) W.ml[row] = make_float2(m[b][e], x);
                         float *dst = W.o + row * D + (lane >> 2);

@@ -72,7 +72,6 @@ struct PtDesc {
     uint64_t q, k, v;  // of row tile 0 and of ring place 0 as K and as V
 };
 template <int QT> constexpr int pt_threads() { return (4 + 4 * QT) * 32; }
-constexpr float kPtRescale = 8.f;
 
 struct PtArgs {
     PgDims D;
@@ -305,9 +304,10 @@ __device__ __forceinline__ void pt_softmax(const PtArgs &A, const PtBars<D, QT> 
         for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int e = 0; e < 32; e += 2) m4[c] = tc::max3(m4[c], s[c][e], s[c][e + 1]);
-        const float mn = fmaxf(m, tc::max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * A.k1);
+        const float mt = tc::max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * A.k1;
+        const float mn = fmaxf(m, PtIsHalf<T>::value ? mt - kPgHalfUp : mt);
         // rows of the tile that hold no query carry whatever shared memory held: they never rescale
-        const bool grow = valid && mn > m + kPtRescale;
+        const bool grow = valid && mn > m + kPgRescale;
         // tcgen05.ld/st are warp-collective: the whole warp rescales when one of its rows does
         if (__any_sync(0xffffffffu, grow)) {
             const float f = grow ? tc::ex2_approx(m - mn) : 1.f;
@@ -433,8 +433,8 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
     const int t0 = sp * step, t_end = min(end, t0 + step);
     if (t_end <= t0) nrow = 0;
 
-    // the launch has tiles for max_new rows a request; a request refused for packing more leaves
-    // more rows to go through
+    // there can be more row blocks than the launch has places for: a prompt with more than four times its
+    // even share of the rows, or with a request that was refused for packing more than max_new
     for (int rt = rt0; rt * QT * per < nrow; rt += A.nrt) {
         const int row0 = rt * QT * per;
         const int nqt = QT == 2 && row0 + per < nrow ? 2 : 1;
@@ -593,8 +593,7 @@ cudaError_t go(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
     PtArgs P{};
     P.D = D_;
     P.tt = tt;
-    const long long most = OWN ? D_.max_new : D_.group_rows();
-    P.nrt = (int)((most + (long long)tt * QT - 1) / ((long long)tt * QT));
+    P.nrt = pg_tc_blocks(D_, OWN);
     P.k1 = kLog2e / sqrtf((float)D_.d);
     P.plen = A.plen;
     P.q_start = A.q_start;

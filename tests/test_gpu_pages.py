@@ -10,6 +10,7 @@ Bound of an output component, o = sum_j a_j v_j in exact arithmetic:
     at most 2 w sum_j a_j |v_j| (numerator and denominator);
   * sums over n tokens in fp32: 8 sqrt(n) 2^-24 sum_j a_j |v_j| (roundings add like a random walk).
 lse: the same w, plus the sum's and its own rounding."""
+import dataclasses
 import math
 
 import numpy as np
@@ -176,13 +177,15 @@ class Case:
     """Inputs of one attention call: random lengths, rows and pages; NaN wherever no row may look."""
 
     def __init__(self, dtype, S, F, Hq, Hkv, d, n, page, own_hi, new_hi, ragged=False, seed=0,
-                 idle=0.0, nothing=False, stride=False, scale=1.0):
+                 idle=0.0, nothing=False, stride=False, scale=1.0, new=None):
         rng = np.random.default_rng(seed)
         gen = torch.Generator(device=DEV).manual_seed(seed)
         dt, R = DT[dtype], S * F
         self.dtype, self.F = dtype, F
         nq = rng.integers(1, new_hi + 1, R)
         nq[rng.random(R) < idle] = 0
+        if new is not None:
+            nq = np.asarray(new)
         own = rng.integers(0, own_hi + 1, R)
         lens = own + nq
         if nothing:
@@ -436,6 +439,118 @@ def test_refused_and_mismatched_rows_are_left_alone():
     assert (f64(out)[c2.row_req < 0] == 3.0).all()
     got, want = f64(out[live]), f64(ref[live[pad:]])
     assert np.abs(got - want).max() <= 2 ** -6 * np.abs(want).max()  # other splits, same rows
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("pad,g", [(7, 1), (40, 3)])
+def test_a_refused_request_with_most_of_the_rows(dtype, pad, g):
+    """Its rows stand in front of all others' in the packed arrays, more than a step may add for a
+    request and more than all others together."""
+    c = Case(dtype, 2, 2, 2 * g, 2, 64, 50, 8, 30, 1, seed=20)
+    c.q = torch.cat((torch.full_like(c.q[:1], float("nan")).expand(pad, -1, -1), c.q))
+    c.q_start = np.concatenate(([0], c.q_start[1:] + pad))
+    c.row_req = np.concatenate((np.full(pad + 1, -1), c.row_req[1:]))
+    c.lens[0] -= 1
+    c.rows, c.n_rows = c.rows + pad, c.n_rows + pad
+    c.shape = (c.n_rows, *c.shape[1:])
+    c.pb = dataclasses.replace(c.pb, n_rows=c.n_rows)
+    c.ws = torch.empty(api.pg_workspace_size(c.pb), dtype=torch.uint8, device=DEV)
+    out, lse = c.check(set(range(pad + 1, c.rows)))
+    assert (f64(out)[:pad + 1] == 3.0).all() and (f64(lse)[:pad + 1] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_one_request_with_most_of_the_rows(dtype):
+    """700 new rows of one request among 12: more than four times its even share, of which the
+    launches on the tensor cores have places for."""
+    new = np.ones(12, int)
+    new[3] = 700
+    c = Case(dtype, 6, 2, 8, 2, 64, 150, 16, 40, 700, seed=21, new=new)
+    c.check({0, 2, 3, 4, 66, 67, 260, 261, 511, 514, 701, 702, 703, 710})
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_requests_that_share_pages(dtype):
+    """A fork: both requests' block tables name the same pages, the second up to the middle of one."""
+    c = Case(dtype, 1, 4, 4, 2, 128, 60, 8, 60, 3, seed=22)
+    c.lens[0] = max(c.lens)
+    c.table[0] = c.table[np.argmax(c.lens[1:]) + 1]
+    c.table[1], c.lens[1] = c.table[0], max(1, c.lens[0] - 3)
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_most_requests(dtype):
+    c = Case(dtype, 64, 256, 4, 2, 32, 20, 4, 2, 2, seed=23, idle=0.96, ragged=True)
+    assert c.pb.requests == 16384
+    c.check(set(range(0, c.rows, 41)) | {c.rows - 1})
+
+
+def test_small_fp16_weights_do_not_vanish():
+    """One token far above the rest, which have 2^-25.5 of its weight each: rounded to fp16 as they
+    are they would all be 0. Bound: the module's, and 2^-32 of the largest weight for each of them
+    (half a step of the smallest fp16 numbers, 2^-25, with weights carried 2^7 higher)."""
+    n, own, d = 16384, 4096, 64
+    c = Case("f16", 1, 1, 1, 1, d, n, 16, own - 1, 1, seed=24)
+    c.lens[0] = int(c.lens[0])
+    for k, v in ((c.Kp, c.Vp), (c.K, c.V)):
+        k.zero_()
+        v.fill_(1.0)
+    c.q[0] = 0.0
+    c.q[0, 0, 0] = 8.0 * math.log(2)  # score: k_0 ln 2
+    tops = (c.Kp[0, 0, 0], c.K[int(c.table[0, 0]), 0, 0])
+    vals = (c.Vp[0, 0, 0], c.V[int(c.table[0, 0]), 0, 0])
+    for k, v in zip(tops, vals):
+        k[0] = 25.5
+        v.zero_()
+    out, _ = c.run()
+    ref = c.oracle()
+    w = (d + 8) * U * ref["mag"][0, 0] + 2.0 ** -21
+    h = 2.0 ** -11
+    tol = (2 * w + 8 * math.sqrt(n + own) * U + 2 * h) * ref["terms"][0, 0] * (1 + h)
+    tol = tol + 2.0 ** -25 + 2.0 ** -32 * (n + own)
+    assert ref["out"][0, 0, 0] > 20 * tol[0]
+    assert (np.abs(f64(out[0, 0]) - ref["out"][0, 0]) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_calls_that_overlap_on_two_streams(dtype):
+    """Each with its own workspace: the results are those of the calls one after the other."""
+    cs = [Case(dtype, 1, 8, 8, 2, 128, 2000, 16, 300, 1, seed=25),
+          Case(dtype, 2, 3, 8, 2, 128, 700, 16, 100, 20, seed=26)]
+    want = [c.run() for c in cs]
+    args = [c.args() for c in cs]
+    outs = [[torch.full_like(w[0], 3.0) for _ in range(10)] for w in want]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for i in range(10):
+        for c, a, o, s in zip(cs, args, outs, streams):
+            api.pg_attention(c.pb, c.q, c.Kp, c.Vp, c.plen, *a, o[i], None, c.ws, stream=s)
+    api.kve_check_device(streams[0])
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w[0], x) for x in o)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("order", ["falling", "same", "wild"])
+def test_row_starts_that_are_no_sums_of_lengths_stay_in_bounds(dtype, order):
+    """Nothing behind the arrays is written, and rows whose request is not the one that q_start
+    gives stay."""
+    c = Case(dtype, 2, 20, 8, 2, 64, 90, 8, 60, 12, seed=27)
+    rng = np.random.default_rng(0)
+    if order == "falling":
+        c.q_start = c.q_start[::-1].copy()
+    elif order == "same":  # every request claims all rows
+        c.q_start = np.where(np.arange(41) % 2, c.rows, 0)
+    else:
+        c.q_start = rng.integers(-2 ** 31, 2 ** 31, 41)
+    start = np.clip(c.q_start, 0, c.n_rows)
+    out, lse = c.run()  # (checks the guards)
+    at = np.arange(c.n_rows)
+    r = np.maximum(c.row_req, 0)
+    left = (c.row_req < 0) | (at < start[r]) | (at - start[r] >= np.minimum(start[r + 1] - start[r], 12))
+    assert (f64(out)[left] == 3.0).all() and (f64(lse)[left] == 5.0).all()
 
 
 def test_another_stream_and_the_wrong_device(monkeypatch):
