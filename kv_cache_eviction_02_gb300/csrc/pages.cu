@@ -407,12 +407,15 @@ template <typename T, int E> __device__ __forceinline__ void row_cols(const T *p
 
 // OWN (tables of at most kPgJoinOwn rows behind a prompt: the lookahead's trajectories): the warp works
 // out the own rows itself, 8 tokens at a time, while the prompt's kernel is still running: a launch less
-// (16K lookahead step: 23 -> ? us).
-template <typename T, int D, int U, bool OWN>
+// (16K lookahead step: 23.3 -> 20.5 us).
+// W: warps per row and head, 1 or all 4 of the block, which then take turns of U results and are joined in
+// shared memory, in order.
+template <typename T, int D, int U, bool OWN, int W>
 __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
     constexpr int E = D / 32;
     constexpr bool F32 = sizeof(T) == 4;
-    const int h = blockIdx.y * 4 + (threadIdx.x >> 5), tok = blockIdx.x, lane = threadIdx.x & 31;
+    const int tok = blockIdx.x, lane = threadIdx.x & 31, w = W == 1 ? 0 : threadIdx.x >> 5;
+    const int h = W == 1 ? blockIdx.y * 4 + (threadIdx.x >> 5) : blockIdx.y;
     int r = h < D_.Hq ? __ldg(A.row_req + tok) : -1;
     if (r >= D_.R) r = -1;
     // the request's own rows and its prompt: tokens, first packed row, chunks per unit, row blocks
@@ -448,7 +451,7 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
         row_cols<T, E>(static_cast<const T *>(A.q) + tok * A.q_row + (size_t)h * D + lane * E, q);
         const int see = len - all + 1 + (tok - first);
         const float k1 = kLog2e * rsqrtf((float)D);
-        for (int t0 = 0; t0 < see; t0 += 8) {
+        for (int t0 = 8 * w; t0 < see; t0 += 8 * W) {
             float k[8][E], v[8][E], s[8], Mn = M;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -509,7 +512,7 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
     }
     const int nsp = np + no;
     // U at a time: a running maximum over the groups, in order
-    for (int s0 = 0; s0 < nsp; s0 += U) {
+    for (int s0 = U * w; s0 < nsp; s0 += U * W) {
         float v[U][E];
         float2 ml[U];
 #pragma unroll
@@ -553,6 +556,25 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
             for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, v[j][e], acc[e]);
         }
     }
+    if constexpr (W > 1) {
+        __shared__ float part[W][E + 2][32];
+        if (w > 0) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) part[w][e][lane] = acc[e];
+            part[w][E][lane] = M;
+            part[w][E + 1][lane] = L;
+        }
+        __syncthreads();
+        if (w > 0) return;
+#pragma unroll
+        for (int x = 1; x < W; ++x) {
+            const float mx = part[x][E][lane], Mn = fmaxf(M, mx), f = exp2f(M - Mn), fx = exp2f(mx - Mn);
+            M = Mn;
+            L = fmaf(fx, part[x][E + 1][lane], L * f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(fx, part[x][e][lane], acc[e] * f);
+        }
+    }
     const float inv = L > 0.f ? 1.f / L : 0.f;
     alignas(16) T out[E];
 #pragma unroll
@@ -567,12 +589,18 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
 }
 
 template <typename T, int D> cudaError_t join_d(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
-    // few rows: 8 partial results on their way at a time; many: fewer instructions for few results
+    // few rows: all warps of a block for one, 8 partial results on their way in each (lookahead over 32K
+    // rows of fp32, 152 pieces a row: the join 20 -> 12 us), unless there are few results to each (4 prompts
+    // of 32K rows, 9 results a row: 91 us against 87.5 with a warp a row); many: fewer instructions
     const bool few = (long long)D_.rows * D_.Hq < kPgSms * 32;
-    auto kern = few ? pg_join_kernel<T, D, 8, false> : pg_join_kernel<T, D, 4, false>;
+    const bool alone = (long long)D_.rows * D_.Hq <= kPgSms * 8 &&
+                       !(pg_join_own(D_) && D_.np <= 16);
+    auto kern = few ? pg_join_kernel<T, D, 8, false, 1> : pg_join_kernel<T, D, 4, false, 1>;
+    if (alone) kern = pg_join_kernel<T, D, 8, false, 4>;
     if constexpr (sizeof(T) == 2)
-        if (pg_join_own(D_)) kern = pg_join_kernel<T, D, 8, true>;
-    return pg_launch(kern, dim3(D_.rows, (D_.Hq + 3) / 4), 128, 0, true, st, D_, A);
+        if (pg_join_own(D_))
+            kern = alone ? pg_join_kernel<T, D, 8, true, 4> : pg_join_kernel<T, D, 8, true, 1>;
+    return pg_launch(kern, dim3(D_.rows, alone ? D_.Hq : (D_.Hq + 3) / 4), 128, 0, true, st, D_, A);
 }
 
 template <typename T> cudaError_t join(const PgDims &D, const PgAttn &A, cudaStream_t st) {

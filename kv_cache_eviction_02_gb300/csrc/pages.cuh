@@ -31,7 +31,7 @@ constexpr int kPgShare = 100;  // most SMs the prompt's kernel takes beside the 
 // Own rows of 16-bit types: units of 8 or 16 query rows, chunks of 16 tokens (pages_own.cu).
 constexpr int kPgChunk = 16, kPgOwnWarps = 4;
 // fp32: units of 16 query rows, chunks of 16 tokens, prompts and own rows alike (pages_f32.cu).
-constexpr int kPgF32Chunk = 16, kPgF32Rows = 16, kPgF32Warps = 6;
+constexpr int kPgF32Chunk = 16, kPgF32Rows = 16, kPgF32Warps = 8;
 
 // Workspace carve-up (byte offsets, 256-aligned): partial results [splits][rows][Hq] (m in log2 and l;
 // o [d] fp32) over the prompt and over the own rows of requests with many new rows; the pieces of units

@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
             }
             uint32_t pf[NT][2];
             const int tok = tb + (lane >> 2);
+            constexpr float UP = std::is_same<T, __half>::value ? kPgHalfUp : 0.f;
             bool grow = false;
             float mt[NT][2];
 #pragma unroll
@@ -305,15 +306,14 @@ __global__ void __launch_bounds__(kMmThreads, 2)
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                     mt[b][e] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    if (std::is_same<T, __half>::value) mt[b][e] -= kPgHalfUp;
-                    grow = grow || mt[b][e] > m[b][e] + kPgRescale;
+                    grow = grow || mt[b][e] > m[b][e] + (kPgRescale + UP);
                 }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int b = 0; b < NT; ++b)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float mn = fmaxf(m[b][e], mt[b][e]), f = tc::ex2_approx(m[b][e] - mn);
+                        const float mn = fmaxf(m[b][e], mt[b][e] - UP), f = tc::ex2_approx(m[b][e] - mn);
                         m[b][e] = mn;
                         l[b][e] *= f;
 #pragma unroll
