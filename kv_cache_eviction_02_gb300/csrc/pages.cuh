@@ -305,14 +305,18 @@ __device__ __forceinline__ void pg_share_find(const long long *csum, const int *
 }
 
 // Programmatic dependent launch: a dependent kernel of the same call may start when every block of the
-// one before it has called pg_launch_dependents(), and reads its results after pg_wait_prior(). Every
-// block of a dependent kernel calls pg_wait_prior() before it ends, so its own end implies the end of
-// the kernel before it, and what follows in the stream waits for all of the call.
+// one before it has called pg_launch_dependents(), and reads its results after pg_wait_prior(). Of a
+// kernel that reads nothing of the one before it the last block waits all the same before it ends, so its
+// own end implies the end of the kernel before it, and what follows in the stream waits for all of the
+// call. (The other blocks leave their SMs to the next ones.)
 __device__ __forceinline__ void pg_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 __device__ __forceinline__ void pg_wait_prior() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void pg_end_after_prior() {
+    if (blockIdx.x == gridDim.x - 1) pg_wait_prior();
 }
 
 // A page id of the caller's table; one outside the pool is recorded and read as page 0.

@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
             }
         }
     }
-    pg_wait_prior();
+    pg_end_after_prior();
 }
 
 template <typename T, int D, int NT>

@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
     }
     __syncthreads();
     if (warp == 1) tc::tmem_dealloc(*tmem_slot, 512);
-    if (OWN) pg_wait_prior();
+    if (OWN) pg_end_after_prior();
 }
 
 // ---- host ------------------------------------------------------------------------------------------
