@@ -1,18 +1,22 @@
 """Builds libkvevict.so in-tree with nvcc for sm_103a (one -gencode, translation units compiled
-in parallel), and liboracle.so is built separately by ``oracle.build``."""
+in parallel) and the Python module _binding with g++ against the installed torch; liboracle.so is
+built separately by ``oracle.build``."""
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkvevict.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -28,6 +32,17 @@ def nvcc() -> str:
 
 def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
+
+
+def binding_command(out: str):
+    """g++ on csrc/binding.cpp."""
+    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
+    return [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"], "-I", inc,
+            "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+            os.path.join(CSRC, "binding.cpp"), "-o", out, "-L", lib, "-ltorch_python",
+            "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{lib}"]
 
 
 def _stale(target: str, deps) -> bool:
@@ -49,15 +64,22 @@ def build(verbose: bool = False, extra=()) -> str:
         if _stale(obj, [src] + headers):
             jobs.append([cc, *ARCH, *NVFLAGS, *extra, "-c", src, "-o", obj])
 
+    made = {}  # temporary output: its final name
+    if _stale(BINDING, [os.path.join(CSRC, "binding.cpp"), headers[-1]]):
+        made[BINDING + f".tmp{os.getpid()}"] = BINDING
+        jobs.insert(0, binding_command(next(iter(made))))
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if verbose or r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed: " + " ".join(cmd))
+            raise RuntimeError("compilation failed: " + " ".join(cmd))
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
         list(ex.map(run, jobs))
+    for tmp, name in made.items():
+        os.replace(tmp, name)
     if jobs or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])

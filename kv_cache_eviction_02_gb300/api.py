@@ -463,6 +463,10 @@ class PgProblem:
         return ctypes.pointer(self.shape())
 
     @functools.cached_property
+    def c_address(self) -> int:
+        return ctypes.addressof(self.c_shape.contents)
+
+    @functools.cached_property
     def torch_dtype(self):
         return _TORCH_DTYPE.get(self.dtype)
 
@@ -476,8 +480,26 @@ class PgProblem:
         return self.n_pages * self.n_kv_heads * self.page_size * self.d_head
 
 
-# These calls are made once per layer and decoded token, so their checks are kept to one pass over a
-# tensor's attributes; what fails is found out only when something did.
+# These calls are made once per layer and decoded token: the module _binding (csrc/binding.cpp) checks their
+# tensors and makes them. What it does not take, addresses and arguments that do not fit the shape, goes
+# through the checks here, which say what is wrong.
+_native, _OTHER = None, -1
+
+
+def _bind():
+    global _native
+    L = lib()
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise RuntimeError("the module _binding is missing or does not load: build it with "
+                           "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+    _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                    for f in (L.pg_plan, L.pg_append, L.pg_attention)))
+    _native = _binding
+    return _native
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -554,8 +576,13 @@ def pg_plan(pb: PgProblem, new_len, len_in, pool_in, free_pages, block_table, le
             q_start, row_req, row_pos, slot_map, stream=None):
     """Block tables and slot maps of one step from the requests' lengths. len_out may be len_in and
     pool_out may be pool_in."""
-    R, n, i32 = pb.requests, pb.n_rows, torch.int32
     dev, st = _pg_launch(stream)
+    status = (_native or _bind()).plan(pb.c_address, dev, st, new_len, len_in, pool_in, free_pages,
+                                       block_table, len_out, pool_out, q_start, row_req, row_pos,
+                                       slot_map)
+    if status != _OTHER:
+        return _check(status)
+    R, n, i32 = pb.requests, pb.n_rows, torch.int32
     _check(lib().pg_plan(
         pb.c_shape, _pg(new_len, "new_len", i32, R, dev), _pg(len_in, "len_in", i32, R, dev),
         _pg(pool_in, "pool_in", i32, 4, dev), _pg(free_pages, "free_pages", i32, pb.n_pages, dev),
@@ -568,8 +595,12 @@ def pg_plan(pb: PgProblem, new_len, len_in, pool_in, free_pages, block_table, le
 def pg_append(pb: PgProblem, K_new, V_new, slot_map, K_pages, V_pages, stream=None):
     """Stores a step's K/V rows [n_rows][n_kv_heads][d_head] into the pages slot_map names. The rows
     may be slices of a wider projection's output."""
-    dt, n = pb.torch_dtype, pb.n_rows
     dev, st = _pg_launch(stream)
+    status = (_native or _bind()).append(pb.c_address, dev, st, K_new, V_new, slot_map, K_pages,
+                                         V_pages)
+    if status != _OTHER:
+        return _check(status)
+    dt, n = pb.torch_dtype, pb.n_rows
     k, kr = _pg_rows(K_new, "K_new", dt, n, pb.n_kv_heads, pb.d_head, dev)
     v, vr = _pg_rows(V_new, "V_new", dt, n, pb.n_kv_heads, pb.d_head, dev)
     _check(lib().pg_append(
@@ -588,8 +619,13 @@ def pg_attention(pb: PgProblem, q, K_prefix, V_prefix, prefix_len, K_pages, V_pa
     [n_q_heads][d_head] may be a slice of a wider projection's output; K_prefix and V_prefix
     [n_prompts][n_kv_heads][>= n_prefix][d_head] may be a layer's slice of a larger cache (the same
     strides for both). prefix_len and lse_out may be None."""
-    dt, R, n, i32 = pb.torch_dtype, pb.requests, pb.n_rows, torch.int32
     dev, st = _pg_launch(stream)
+    status = (_native or _bind()).attention(pb.c_address, dev, st, q, K_prefix, V_prefix, prefix_len,
+                                            K_pages, V_pages, block_table, lens, q_start, row_req,
+                                            out, lse_out, workspace)
+    if status != _OTHER:
+        return _check(status)
+    dt, R, n, i32 = pb.torch_dtype, pb.requests, pb.n_rows, torch.int32
     qp, qr = _pg_rows(q, "q", dt, n, pb.n_q_heads, pb.d_head, dev)
     kp, s0, s1, s2 = _pg_prefix(K_prefix, "K_prefix", pb, dev)
     vp, *vs = _pg_prefix(V_prefix, "V_prefix", pb, dev)

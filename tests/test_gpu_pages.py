@@ -553,6 +553,42 @@ def test_row_starts_that_are_no_sums_of_lengths_stay_in_bounds(dtype, order):
     assert (f64(out)[left] == 3.0).all() and (f64(lse)[left] == 5.0).all()
 
 
+def test_addresses_and_tensors_that_do_not_fit():
+    """Addresses give what tensors give; a tensor that does not fit the shape is named, and nothing
+    is written."""
+    c = Case("bf16", 2, 3, 8, 2, 64, 120, 8, 40, 2, seed=28, stride=True)
+    ref, lse = c.run()
+    qk = (c.q, c.Kp, c.Vp, c.plen, *c.args())
+    out = torch.full(c.shape, 3.0, dtype=torch.bfloat16, device=DEV)
+    z = torch.full(c.shape[:2], 5.0, device=DEV)
+    args = [*qk, out, z, c.ws]
+    for i in (4, 5, 6, 7, 8, 9, 10, 11):
+        call = list(args)
+        call[i] = call[i].data_ptr()
+        api.pg_attention(c.pb, *call)
+        assert torch.equal(out, ref) and torch.equal(z, lse)
+        out.fill_(3.0)
+        z.fill_(5.0)
+    bad = [(0, c.q.float(), "dtype"), (0, c.q[:-1], "elements"), (0, c.q.transpose(0, 1), "contiguous"),
+           (1, c.Kp[:, :, :-1], "elements"), (1, c.Kp[..., :32], "elements"), (1, c.Kp.half(), "dtype"),
+           (2, c.Vp.contiguous(), "strides differ"), (4, c.K.view(-1)[1:], "elements"),
+           (6, args[6].view(-1)[:-1], "elements"), (7, args[7].long(), "dtype"),
+           (8, args[8][:-1], "elements"), (9, args[9].cpu(), "CUDA"),
+           (10, torch.empty(*c.shape, 2, dtype=torch.bfloat16, device=DEV)[..., 0], "contiguous"),
+           (11, z.double(), "dtype"), (11, z[:-1], "elements"), (12, c.ws.cpu(), "CUDA")]
+    for i, t, word in bad:
+        call = list(args)
+        call[i] = t
+        with pytest.raises(ValueError, match=word):
+            api.pg_attention(c.pb, *call)
+    with pytest.raises(api.KveError, match="workspace"):
+        api.pg_attention(c.pb, *args[:12], c.ws[:-256])
+    with pytest.raises(api.KveError, match="null"):
+        api.pg_attention(c.pb, *args[:10], None, *args[11:])
+    api.kve_check_device()
+    assert (f64(out) == 3.0).all() and (f64(z) == 5.0).all()
+
+
 def test_another_stream_and_the_wrong_device(monkeypatch):
     c = Case("bf16", 1, 4, 8, 2, 128, 700, 16, 60, 1, seed=13)
     a, _ = c.run()
