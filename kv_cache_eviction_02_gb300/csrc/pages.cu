@@ -405,6 +405,80 @@ template <typename T, int E> __device__ __forceinline__ void row_cols(const T *p
     }
 }
 
+// What the partial results of a row's heads have in common, read before the kernels that make them have
+// ended; `where` then says where those of a head lie: two runs, the prompt's and the own rows', each with its
+// first row, the rows from one to the next, and how many there are.
+template <bool F32> struct PgFound {
+    int r, first, all, nq, len, cr, nb, pfirst, pcr, pnb;
+    int np, nd;  // splits of its prompt and, if dense, of its own rows
+    bool mine;   // the row has a place
+    bool dense;  // own rows on tcgen05: splits of [splits][rows][Hq], like the prompt's of 16-bit types
+    struct Runs {
+        const float *po, *oo;
+        const float2 *pm, *om;
+        long long prow, pstep, orow, ostep;
+        int np, no;
+    };
+    __device__ __forceinline__ PgFound(const PgDims &D, const PgAttn &A, int tok, bool on) {
+        r = on ? __ldg(A.row_req + tok) : -1;
+        if (r >= D.R) r = -1;
+        int x0, x1;
+        int plen = 0;
+        len = first = nq = cr = nb = pfirst = pcr = pnb = 0;
+        if (r >= 0) {
+            const int p = r / D.F;
+            if (F32) {
+                pg_f32_entity(D, A, D.S + r, &len, &first, &nq, &x0, &cr, &nb);
+                pg_f32_entity(D, A, p, &plen, &pfirst, &x0, &x1, &pcr, &pnb);
+            } else {
+                pg_own_request(D, A, r, &len, &first, &nq, &cr, &nb);
+                plen = A.plen ? pg_clamp(__ldg(A.plen + p), 0, D.n) : D.n;
+            }
+        }
+        all = nq;
+        nq = min(nq, D.max_new);
+        mine = r >= 0 && tok >= first && tok - first < nq;
+        dense = !F32 && pg_on_tc((long long)nq * D.g, len);
+        np = F32 || D.np == 0 ? 0 : (plen + D.psplit - 1) / D.psplit;
+        nd = dense ? (len + D.ssplit - 1) / D.ssplit : 0;
+    }
+    // own: its own rows have results (they are not worked out by the join)
+    __device__ __forceinline__ Runs where(const PgDims &D, const PgAttn &A, int tok, int h, int kh, bool own) const {
+        const int hk = h - kh * D.g;
+        const long long row = (long long)tok * D.Hq + h, step = (long long)D.rows * D.Hq;
+        Runs x;
+        x.po = F32 ? A.own.o : A.part_o;
+        x.oo = dense ? A.part_o : A.own.o;
+        x.pm = F32 ? A.own.ml : A.part_ml;
+        x.om = dense ? A.part_ml : A.own.ml;
+        x.prow = row;
+        x.pstep = step;
+        x.orow = D.np * step + row;
+        x.ostep = step;
+        x.np = np;
+        x.no = nd;
+        // pieces of a unit: query row rr of entity e
+        auto pieces = [&](int e, int rr, int chunks, int blocks, long long *at_row, int *count) {
+            const int rb = pg_unit_rows(D), u = kh * blocks + rr / rb;
+            const long long c = A.own.base[e] + (long long)u * chunks, cpw = *A.own.cpw;
+            const long long w0 = pg_div(c, cpw), w1 = chunks > 0 ? pg_div(c + chunks - 1, cpw) : w0 - 1;
+            const long long at = A.own.unit[e] + u + w0;
+            // as many as there are places (all, when the row starts are sums of lengths)
+            *count = at < 0 ? 0 : (int)max(min(w1 - w0 + 1, (long long)A.own.segs - at), 0LL);
+            *at_row = at * A.own.seg_rows + (rr & (rb - 1));
+        };
+        if (own && !dense) {
+            pieces(F32 ? D.S + r : r, (tok - first) * D.g + hk, cr, nb, &x.orow, &x.no);
+            x.ostep = A.own.seg_rows;
+        }
+        if (F32) {
+            pieces(r / D.F, (tok - pfirst) * D.g + hk, pcr, pnb, &x.prow, &x.np);
+            x.pstep = A.own.seg_rows;
+        }
+        return x;
+    }
+};
+
 // OWN (tables of at most kPgJoinOwn rows behind a prompt: the lookahead's trajectories): the warp works
 // out the own rows itself, 8 tokens at a time, while the prompt's kernel is still running: a launch less
 // (16K lookahead step: 23.3 -> 20.5 us).
@@ -416,40 +490,17 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
     constexpr bool F32 = sizeof(T) == 4;
     const int tok = blockIdx.x, lane = threadIdx.x & 31, w = W == 1 ? 0 : threadIdx.x >> 5;
     const int h = W == 1 ? blockIdx.y * 4 + (threadIdx.x >> 5) : blockIdx.y;
-    int r = h < D_.Hq ? __ldg(A.row_req + tok) : -1;
-    if (r >= D_.R) r = -1;
-    // the request's own rows and its prompt: tokens, first packed row, chunks per unit, row blocks
-    int len = 0, first = 0, nq = 0, cr = 0, nb = 0, plen = 0, pfirst = 0, pcr = 0, pnb = 0, x0, x1;
-    if (r >= 0) {
-        const int p = r / D_.F;
-        if (F32) {
-            pg_f32_entity(D_, A, D_.S + r, &len, &first, &nq, &x0, &cr, &nb);
-            pg_f32_entity(D_, A, p, &plen, &pfirst, &x0, &x1, &pcr, &pnb);
-        } else {
-            pg_own_request(D_, A, r, &len, &first, &nq, &cr, &nb);
-            plen = A.plen ? pg_clamp(__ldg(A.plen + p), 0, D_.n) : D_.n;
-        }
-    }
-    const int all = nq;
-    nq = min(nq, D_.max_new);
-    const bool mine = r >= 0 && tok >= first && tok - first < nq;
-    const int kh = h / D_.g, hk = h - kh * D_.g;
-    const long long row = (long long)tok * D_.Hq + h, step = (long long)D_.rows * D_.Hq;
-    // two runs of partial results: the prompt's and the own rows', each with its first row, the rows from
-    // one to the next, and how many there are. Splits of [splits][rows][Hq] ...
-    const bool dense = !F32 && nq * D_.g > kPgFewRows;
-    const float *po = F32 ? A.own.o : A.part_o, *oo = dense ? A.part_o : A.own.o;
-    const float2 *pm = F32 ? A.own.ml : A.part_ml, *om = dense ? A.part_ml : A.own.ml;
-    long long prow = row, pstep = step, orow = D_.np * step + row, ostep = step;
-    int np = F32 || D_.np == 0 ? 0 : (plen + D_.psplit - 1) / D_.psplit;
-    int no = dense ? (len + D_.ssplit - 1) / D_.ssplit : 0;
+    const PgFound<F32> at(D_, A, tok, h < D_.Hq);
+    const bool mine = at.mine;
+    const int kh = h / D_.g;
+    const long long row = (long long)tok * D_.Hq + h;
     float M = kPgNoMax, L = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
     if (OWN && mine) {
         float q[E];
         row_cols<T, E>(static_cast<const T *>(A.q) + tok * A.q_row + (size_t)h * D + lane * E, q);
-        const int see = len - all + 1 + (tok - first);
+        const int see = at.len - at.all + 1 + (tok - at.first);
         const float k1 = kLog2e * rsqrtf((float)D);
         for (int t0 = 8 * w; t0 < see; t0 += 8 * W) {
             float k[8][E], v[8][E], s[8], Mn = M;
@@ -460,11 +511,11 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
                 if (t0 + j < see) {
                     const int t = t0 + j;
                     const int page =
-                        pg_page(A.table + (size_t)r * D_.maxp, t, D_.lgP, D_.npages, A.err);
-                    const size_t at = ((((size_t)page * D_.Hkv + kh) << D_.lgP) + (t & (D_.P - 1))) * D +
+                        pg_page(A.table + (size_t)at.r * D_.maxp, t, D_.lgP, D_.npages, A.err);
+                    const size_t x = ((((size_t)page * D_.Hkv + kh) << D_.lgP) + (t & (D_.P - 1))) * D +
                                       lane * E;
-                    row_cols<T, E>(static_cast<const T *>(A.K) + at, k[j]);
-                    row_cols<T, E>(static_cast<const T *>(A.V) + at, v[j]);
+                    row_cols<T, E>(static_cast<const T *>(A.K) + x, k[j]);
+                    row_cols<T, E>(static_cast<const T *>(A.V) + x, v[j]);
                 }
             }
 #pragma unroll
@@ -492,25 +543,8 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
     pg_wait_prior();
     pg_launch_dependents();
     if (!mine) return;
-    // ... or pieces of a unit: query row rr of entity e
-    auto pieces = [&](int e, int rr, int chunks, int blocks, long long *at_row, int *count) {
-        const int rb = pg_unit_rows(D_), u = kh * blocks + rr / rb;
-        const long long x = A.own.base[e] + (long long)u * chunks, cpw = *A.own.cpw;
-        const long long w0 = pg_div(x, cpw), w1 = chunks > 0 ? pg_div(x + chunks - 1, cpw) : w0 - 1;
-        const long long at = A.own.unit[e] + u + w0;
-        // as many as there are places (all, when the row starts are sums of lengths)
-        *count = at < 0 ? 0 : (int)max(min(w1 - w0 + 1, (long long)A.own.segs - at), 0LL);
-        *at_row = at * A.own.seg_rows + (rr & (rb - 1));
-    };
-    if (!dense && !OWN) {
-        pieces(F32 ? D_.S + r : r, (tok - first) * D_.g + hk, cr, nb, &orow, &no);
-        ostep = A.own.seg_rows;
-    }
-    if (F32) {
-        pieces(r / D_.F, (tok - pfirst) * D_.g + hk, pcr, pnb, &prow, &np);
-        pstep = A.own.seg_rows;
-    }
-    const int nsp = np + no;
+    const auto x = at.where(D_, A, tok, h, kh, !OWN);
+    const int np = x.np, nsp = np + x.no;
     // U at a time: a running maximum over the groups, in order
     for (int s0 = U * w; s0 < nsp; s0 += U * W) {
         float v[U][E];
@@ -522,19 +556,19 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
 #pragma unroll
             for (int e = 0; e < E; ++e) v[j][e] = 0.f;
             if (s < nsp) {
-                const long long at = s < np ? prow + s * pstep : orow + (s - np) * ostep;
-                const float *o = (s < np ? po : oo) + at * D + lane * E;
-                ml[j] = (s < np ? pm : om)[at];
+                const long long pr = s < np ? x.prow + s * x.pstep : x.orow + (s - np) * x.ostep;
+                const float *o = (s < np ? x.po : x.oo) + pr * D + lane * E;
+                ml[j] = (s < np ? x.pm : x.om)[pr];
                 if (E == 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(o);
-                    v[j][0] = x.x;
-                    v[j][1 % E] = x.y;
-                    v[j][2 % E] = x.z;
-                    v[j][3 % E] = x.w;
+                    const float4 y = *reinterpret_cast<const float4 *>(o);
+                    v[j][0] = y.x;
+                    v[j][1 % E] = y.y;
+                    v[j][2 % E] = y.z;
+                    v[j][3 % E] = y.w;
                 } else if (E == 2) {
-                    const float2 x = *reinterpret_cast<const float2 *>(o);
-                    v[j][0] = x.x;
-                    v[j][1 % E] = x.y;
+                    const float2 y = *reinterpret_cast<const float2 *>(o);
+                    v[j][0] = y.x;
+                    v[j][1 % E] = y.y;
                 } else {
                     v[j][0] = *o;
                 }
@@ -588,13 +622,102 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
     if (A.lse && lane == 0) A.lse[row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
+// The same for many rows of d_head 32 and 64: a warp joins four heads of a row (2 or 4 at a time, 4 columns a
+// lane), so that the steps to find their results, which wait for one another, are taken once for four (92K
+// rows and heads: 45 -> 22 us with d_head 32; with 128, where the four take turns, it was slower: 15 -> 17).
+template <typename T, int D>
+__global__ void __launch_bounds__(128) pg_join_many_kernel(PgDims D_, PgAttn A) {
+    constexpr bool F32 = sizeof(T) == 4;
+    static_assert(D < 128);
+    constexpr int LANES = D / 4, PAR = 32 / LANES, N = 4 / PAR;  // lanes per head, heads at a time, turns
+    constexpr int U = 8 / N;                                     // results on their way per head
+    const int lane = threadIdx.x & 31, sub = lane / LANES, col = lane % LANES * 4;
+    const int quads = (D_.Hq + 3) / 4;
+    const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int tok = (int)pg_div(w, quads), h0 = (int)(w - (long long)tok * quads) * 4;
+    const PgFound<F32> at(D_, A, tok, tok < D_.rows);
+    int kh[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)  // (heads behind the last: not stored)
+        kh[i] = min(h0 + i * PAR + sub, D_.Hq - 1) / D_.g;
+    pg_wait_prior();
+    pg_launch_dependents();
+    if (!at.mine) return;
+    typename PgFound<F32>::Runs x[N];
+    float M[N], L[N];
+    float4 acc[N];
+    int most = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] = at.where(D_, A, tok, min(h0 + i * PAR + sub, D_.Hq - 1), kh[i], true);
+        most = max(most, x[i].np + x[i].no);
+        M[i] = kPgNoMax;
+        L[i] = 0.f;
+        acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int s0 = 0; s0 < most; s0 += U) {
+        float4 v[N][U];
+        float2 ml[N][U];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int s = s0 + j, np = x[i].np;
+                v[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                ml[i][j] = make_float2(kPgNoMax, 0.f);
+                if (s < np + x[i].no) {
+                    const long long r =
+                        s < np ? x[i].prow + s * x[i].pstep : x[i].orow + (s - np) * x[i].ostep;
+                    v[i][j] = *reinterpret_cast<const float4 *>((s < np ? x[i].po : x[i].oo) + r * D + col);
+                    ml[i][j] = (s < np ? x[i].pm : x[i].om)[r];
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float Mn = M[i];
+#pragma unroll
+            for (int j = 0; j < U; ++j) Mn = fmaxf(Mn, ml[i][j].x);
+            const float f = exp2f(M[i] - Mn);
+            M[i] = Mn;
+            L[i] *= f;
+            acc[i] = make_float4(acc[i].x * f, acc[i].y * f, acc[i].z * f, acc[i].w * f);
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const float wt = exp2f(ml[i][j].x - Mn);
+                L[i] = fmaf(wt, ml[i][j].y, L[i]);
+                acc[i] = make_float4(fmaf(wt, v[i][j].x, acc[i].x), fmaf(wt, v[i][j].y, acc[i].y),
+                                     fmaf(wt, v[i][j].z, acc[i].z), fmaf(wt, v[i][j].w, acc[i].w));
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int h = h0 + i * PAR + sub;
+        if (h >= D_.Hq) continue;
+        const float inv = L[i] > 0.f ? 1.f / L[i] : 0.f;
+        alignas(16) T out[4] = {from_f<T>(acc[i].x * inv), from_f<T>(acc[i].y * inv),
+                                from_f<T>(acc[i].z * inv), from_f<T>(acc[i].w * inv)};
+        const long long row = (long long)tok * D_.Hq + h;
+        T *dst = static_cast<T *>(A.out) + row * D + col;
+        if (sizeof(out) == 16) *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<uint4 *>(out);
+        else *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<uint2 *>(out);
+        if (A.lse && col == 0) A.lse[row] = L[i] > 0.f ? (M[i] + log2f(L[i])) * kLn2 : -INFINITY;
+    }
+}
+
 template <typename T, int D> cudaError_t join_d(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
     // few rows: all warps of a block for one, 8 partial results on their way in each (lookahead over 32K
     // rows of fp32, 152 pieces a row: the join 20 -> 12 us), unless there are few results to each (4 prompts
     // of 32K rows, 9 results a row: 91 us against 87.5 with a warp a row); many: fewer instructions
-    const bool few = (long long)D_.rows * D_.Hq < kPgSms * 32;
     const bool alone = (long long)D_.rows * D_.Hq <= kPgSms * 8 &&
                        !(pg_join_own(D_) && D_.np <= 16);
+    const bool few = (long long)D_.rows * D_.Hq < kPgSms * 32;
+    if constexpr (D < 128)
+        if (!few && !pg_join_own(D_)) {
+            const long long warps = (long long)D_.rows * ((D_.Hq + 3) / 4);
+            return pg_launch(pg_join_many_kernel<T, D>, (unsigned)((warps + 3) / 4), 128, 0, true, st, D_,
+                             A);
+        }
     auto kern = few ? pg_join_kernel<T, D, 8, false, 1> : pg_join_kernel<T, D, 4, false, 1>;
     if (alone) kern = pg_join_kernel<T, D, 8, false, 4>;
     if constexpr (sizeof(T) == 2)

@@ -63,12 +63,16 @@ inline int pg_tc_blocks(const PgDims &D, bool own) {
     const long long most = (rows + per - 1) / per, share = 4 * ((D.rows + per * of - 1) / (per * of));
     return (int)(most < share ? most : share);
 }
-// A request with more query rows per KV head than this has its own rows done on tcgen05 (the warps of
-// pages_own.cu would read its K/V more than twice), the others go to pages_own.cu; the choice is made per
-// request on the device, so a batch of both runs both kernels.
-constexpr int kPgFewRows = 32;
+// A request with more query rows per KV head than kPgFewRows (the warps of pages_own.cu would read its K/V
+// more than twice) and more than kPgFewScores scores has its own rows done on tcgen05, where a CTA costs
+// several microseconds whatever it does; the others go to pages_own.cu. The choice is made per request on
+// the device, so a batch of both runs both kernels.
+constexpr int kPgFewRows = 32, kPgFewScores = 12288;
+__host__ __device__ inline bool pg_on_tc(long long rows, int len) {
+    return rows > kPgFewRows && rows * len > kPgFewScores;
+}
 __host__ __device__ inline bool pg_many_new(const PgDims &D) {
-    return D.dtype != KVE_F32 && (long long)D.max_new * D.g > kPgFewRows;
+    return D.dtype != KVE_F32 && pg_on_tc((long long)D.max_new * D.g, D.cap());
 }
 
 // The join works out the own rows itself where a table holds few rows behind a prompt (16-bit types).
@@ -91,7 +95,6 @@ inline int pg_seg_rows(const PgDims &D) {
 inline int pg_own_ctas(const PgDims &D) {
     const int rb = pg_unit_rows(D);
     long long rows = (long long)D.max_new * D.g;
-    if (D.dtype != KVE_F32 && rows > kPgFewRows) rows = kPgFewRows;
     const int chunk = D.dtype == KVE_F32 ? kPgF32Chunk : kPgChunk;
     long long chunks = (long long)D.R * D.Hkv * ((rows + rb - 1) / rb) * ((D.cap() + chunk - 1) / chunk);
     if (D.dtype == KVE_F32)
@@ -187,7 +190,7 @@ __device__ __forceinline__ void pg_own_request(const PgDims &D, const PgAttn &A,
     *cr = (*len + kPgChunk - 1) / kPgChunk;
     const int rb = pg_unit_rows(D);
     const int rows = min(*nq, D.max_new) * D.g;
-    *nb = rows > kPgFewRows ? 0 : (rows + rb - 1) / rb;
+    *nb = pg_on_tc(rows, *len) ? 0 : (rows + rb - 1) / rb;
 }
 
 // The same for fp32: entity e < S is prompt e with the rows of all its requests, S + r is request r.

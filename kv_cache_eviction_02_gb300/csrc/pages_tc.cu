@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
     int nrow = (tok1 - tok0) * A.D.g;
     if (OWN) {
         nrow = min(tok1 - tok0, A.D.max_new) * A.D.g;
-        if (nrow <= kPgFewRows) nrow = 0;  // pages_own.cu's
+        if (!pg_on_tc(nrow, end)) nrow = 0;  // pages_own.cu's
     }
     const int step = OWN ? A.D.ssplit : A.D.psplit;
     const int t0 = sp * step, t_end = min(end, t0 + step);
