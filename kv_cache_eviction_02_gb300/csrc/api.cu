@@ -1095,7 +1095,7 @@ int pg_attention(const KvePgShape *shape, const void *q, long long q_row_stride,
     A.err = err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    if (D.n > 0 && D.dtype != KVE_F32) {
+    if (D.np > 0) {
         ProfScope ps("pg_prompt", 1, st);
         e = launch_pg_prompt_tc(D, A, st);
     }

@@ -39,8 +39,10 @@ static void pg_split(PgDims *D) {
     D->psplit = 128;
     D->ssplit = 256;
     D->own_sms = kPgSms;
+    D->line = D->n > 0;
     if (D->dtype == KVE_F32) return;
-    if (D->n > 0) {
+    D->line = D->line && pg_short_prompts(*D);
+    if (D->n > 0 && !D->line) {
         const long long per = pg_tile_rows(*D) * pg_pairs(*D, D->group_rows());
         const long long most = (long long)D->S * pg_tc_blocks(*D, false);  // launched per KV head
         const long long all = D->rows / per + D->S;                        // of which hold rows
@@ -427,19 +429,15 @@ template <bool F32> struct PgFound {
         len = first = nq = cr = nb = pfirst = pcr = pnb = 0;
         if (r >= 0) {
             const int p = r / D.F;
-            if (F32) {
-                pg_f32_entity(D, A, D.S + r, &len, &first, &nq, &x0, &cr, &nb);
-                pg_f32_entity(D, A, p, &plen, &pfirst, &x0, &x1, &pcr, &pnb);
-            } else {
-                pg_own_request(D, A, r, &len, &first, &nq, &cr, &nb);
-                plen = A.plen ? pg_clamp(__ldg(A.plen + p), 0, D.n) : D.n;
-            }
+            pg_unit_entity<F32>(D, A, D.S + r, &len, &first, &nq, &x0, &cr, &nb);
+            if (D.line) pg_unit_entity<F32>(D, A, p, &plen, &pfirst, &x0, &x1, &pcr, &pnb);
+            else if (!F32) plen = A.plen ? pg_clamp(__ldg(A.plen + p), 0, D.n) : D.n;
         }
         all = nq;
         nq = min(nq, D.max_new);
         mine = r >= 0 && tok >= first && tok - first < nq;
         dense = !F32 && pg_on_tc((long long)nq * D.g, len);
-        np = F32 || D.np == 0 ? 0 : (plen + D.psplit - 1) / D.psplit;
+        np = D.np == 0 ? 0 : (plen + D.psplit - 1) / D.psplit;
         nd = dense ? (len + D.ssplit - 1) / D.ssplit : 0;
     }
     // own: its own rows have results (they are not worked out by the join)
@@ -447,9 +445,10 @@ template <bool F32> struct PgFound {
         const int hk = h - kh * D.g;
         const long long row = (long long)tok * D.Hq + h, step = (long long)D.rows * D.Hq;
         Runs x;
-        x.po = F32 ? A.own.o : A.part_o;
+        const bool line = F32 || D.line;
+        x.po = line ? A.own.o : A.part_o;
         x.oo = dense ? A.part_o : A.own.o;
-        x.pm = F32 ? A.own.ml : A.part_ml;
+        x.pm = line ? A.own.ml : A.part_ml;
         x.om = dense ? A.part_ml : A.own.ml;
         x.prow = row;
         x.pstep = step;
@@ -459,19 +458,19 @@ template <bool F32> struct PgFound {
         x.no = nd;
         // pieces of a unit: query row rr of entity e
         auto pieces = [&](int e, int rr, int chunks, int blocks, long long *at_row, int *count) {
-            const int rb = pg_unit_rows(D), u = kh * blocks + rr / rb;
+            const int lg = F32 || pg_unit_rows(D) == 16 ? 4 : 3, u = kh * blocks + (rr >> lg);
             const long long c = A.own.base[e] + (long long)u * chunks, cpw = *A.own.cpw;
             const long long w0 = pg_div(c, cpw), w1 = chunks > 0 ? pg_div(c + chunks - 1, cpw) : w0 - 1;
             const long long at = A.own.unit[e] + u + w0;
             // as many as there are places (all, when the row starts are sums of lengths)
             *count = at < 0 ? 0 : (int)max(min(w1 - w0 + 1, (long long)A.own.segs - at), 0LL);
-            *at_row = at * A.own.seg_rows + (rr & (rb - 1));
+            *at_row = at * A.own.seg_rows + (rr & ((1 << lg) - 1));
         };
         if (own && !dense) {
-            pieces(F32 ? D.S + r : r, (tok - first) * D.g + hk, cr, nb, &x.orow, &x.no);
+            pieces((line ? D.S : 0) + r, (tok - first) * D.g + hk, cr, nb, &x.orow, &x.no);
             x.ostep = A.own.seg_rows;
         }
-        if (F32) {
+        if (D.line) {
             pieces(r / D.F, (tok - pfirst) * D.g + hk, pcr, pnb, &x.prow, &x.np);
             x.pstep = A.own.seg_rows;
         }

@@ -18,6 +18,7 @@ struct PgDims {
     int np, psplit;            // 16-bit types: prompt splits and their tokens (0 without a prompt)
     int ns, ssplit;            // pg_many_new: splits of a request's own rows and their tokens
     int own_sms;               // SMs for the kernel that deals out units
+    bool line;                 // that kernel takes the prompts too (fp32; 16-bit types: short work)
     // rows behind one prompt, when no request packs more than max_new
     __host__ __device__ long long group_rows() const {
         return (long long)F * max_new < rows ? (long long)F * max_new : rows;
@@ -28,10 +29,9 @@ struct PgDims {
 constexpr int kPgSms = 152;    // GB300
 constexpr int kPgShare = 100;  // most SMs the prompt's kernel takes beside the own rows' one
 
-// Own rows of 16-bit types: units of 8 or 16 query rows, chunks of 16 tokens (pages_own.cu).
-constexpr int kPgChunk = 16, kPgOwnWarps = 4;
-// fp32: units of 16 query rows, chunks of 16 tokens, prompts and own rows alike (pages_f32.cu).
-constexpr int kPgF32Chunk = 16, kPgF32Rows = 16, kPgF32Warps = 8;
+// Units of 8 or 16 query rows (fp32: 16), chunks of 16 tokens, dealt out to the warps of pages_own.cu
+// (16-bit types) or pages_f32.cu.
+constexpr int kPgChunk = 16, kPgOwnWarps = 4, kPgF32Warps = 8, kPgF32Rows = 16;
 
 // Workspace carve-up (byte offsets, 256-aligned): partial results [splits][rows][Hq] (m in log2 and l;
 // o [d] fp32) over the prompt and over the own rows of requests with many new rows; the pieces of units
@@ -78,28 +78,40 @@ __host__ __device__ inline bool pg_many_new(const PgDims &D) {
 // The join works out the own rows itself where a table holds few rows behind a prompt (16-bit types).
 constexpr int kPgJoinOwn = 32;
 inline bool pg_join_own(const PgDims &D) {
-    return D.dtype != KVE_F32 && D.n > 0 && D.cap() <= kPgJoinOwn && !pg_many_new(D);
+    return D.np > 0 && D.cap() <= kPgJoinOwn && !pg_many_new(D);
 }
-// Query rows of a unit of own rows: 8 when no request has more, else 16 (the rows of a unit share its
-// K/V loads; more than 16 would not leave registers for two blocks per SM).
+// Query rows of a unit: 8 when no request has more, else 16 (the rows of a unit share its K/V loads; more
+// than 16 would not leave registers for two blocks per SM).
 __host__ __device__ inline int pg_unit_rows(const PgDims &D) {
     return D.dtype != KVE_F32 && (long long)D.max_new * D.g <= 8 ? 8 : 16;
+}
+// 16-bit types: the warps of pages_own.cu take the prompts too when all there is to do is short, so that a
+// call has one launch less and no tcgen05 kernel, which costs several microseconds whatever it does (a step of
+// 4 requests behind 11 rows 12.0 -> 8.7 us); not when the join takes the own rows, since there are two launches
+// either way, nor with long own rows (64 requests of up to 1875: 54 us, in one line 70).
+inline bool pg_short_prompts(const PgDims &D) {
+    const int rb = pg_unit_rows(D);
+    auto chunks = [&](long long of, long long rows, int tokens) {  // at most
+        return of * D.Hkv * ((rows * D.g + rb - 1) / rb) * ((tokens + kPgChunk - 1) / kPgChunk);
+    };
+    return D.n <= 256 && chunks(D.S, D.group_rows(), D.n) <= 2048 &&
+           chunks(D.R, D.max_new, D.cap()) <= 16384 && (D.cap() > kPgJoinOwn || pg_many_new(D));
 }
 // Rows of a unit that can hold a query, CTAs of the kernel that deals out units (two per SM, fp32 one;
 // fewer when there cannot be a chunk for each warp), and the places its pieces need.
 inline int pg_seg_rows(const PgDims &D) {
     // (a prompt's rows may be all there are: a refused request can pack more than max_new)
-    const long long rows = (long long)(D.dtype == KVE_F32 && D.n > 0 ? D.rows : D.max_new) * D.g;
+    const long long rows = (long long)(D.line ? D.rows : D.max_new) * D.g;
     return rows < pg_unit_rows(D) ? (int)rows : pg_unit_rows(D);
 }
 inline int pg_own_ctas(const PgDims &D) {
     const int rb = pg_unit_rows(D);
     long long rows = (long long)D.max_new * D.g;
-    const int chunk = D.dtype == KVE_F32 ? kPgF32Chunk : kPgChunk;
-    long long chunks = (long long)D.R * D.Hkv * ((rows + rb - 1) / rb) * ((D.cap() + chunk - 1) / chunk);
-    if (D.dtype == KVE_F32)
+    long long chunks =
+        (long long)D.R * D.Hkv * ((rows + rb - 1) / rb) * ((D.cap() + kPgChunk - 1) / kPgChunk);
+    if (D.line)
         chunks += (long long)D.S * D.Hkv * ((D.group_rows() * D.g + rb - 1) / rb) *
-                  ((D.n + chunk - 1) / chunk);
+                  ((D.n + kPgChunk - 1) / kPgChunk);
     const int warps = D.dtype == KVE_F32 ? kPgF32Warps : kPgOwnWarps;
     const long long ctas = (chunks + warps - 1) / warps, most = D.own_sms * (D.dtype == KVE_F32 ? 1 : 2);
     return (int)(ctas < most ? ctas : most);
@@ -107,7 +119,7 @@ inline int pg_own_ctas(const PgDims &D) {
 inline long long pg_own_segs(const PgDims &D) {
     const long long busy = D.R < D.rows ? D.R : D.rows;
     long long units = D.Hkv * ((long long)D.rows * D.g / pg_unit_rows(D) + busy);
-    if (D.dtype == KVE_F32 && D.n > 0)
+    if (D.line)
         units += D.Hkv * ((long long)D.rows * D.g / pg_unit_rows(D) + (D.S < D.rows ? D.S : D.rows));
     return units + (long long)pg_own_ctas(D) * (D.dtype == KVE_F32 ? kPgF32Warps : kPgOwnWarps);
 }
@@ -180,22 +192,12 @@ __device__ __forceinline__ int pg_start(const int32_t *q_start, int r, int rows)
     return pg_clamp(__ldg(q_start + r), 0, rows);
 }
 
-// A request's own rows: how many lie in its pages, its packed rows, and for pages_own.cu its chunks per
-// unit and its row blocks. Rows beyond max_new have no place.
-__device__ __forceinline__ void pg_own_request(const PgDims &D, const PgAttn &A, int r, int *len,
-                                               int *first, int *nq, int *cr, int *nb) {
-    *len = pg_clamp(__ldg(A.len + r), 0, D.cap());
-    *first = pg_start(A.q_start, r, D.rows);
-    *nq = max(0, pg_start(A.q_start, r + 1, D.rows) - *first);
-    *cr = (*len + kPgChunk - 1) / kPgChunk;
-    const int rb = pg_unit_rows(D);
-    const int rows = min(*nq, D.max_new) * D.g;
-    *nb = pg_on_tc(rows, *len) ? 0 : (rows + rb - 1) / rb;
-}
-
-// The same for fp32: entity e < S is prompt e with the rows of all its requests, S + r is request r.
-__device__ __forceinline__ void pg_f32_entity(const PgDims &D, const PgAttn &A, int e, int *len,
-                                              int *first, int *nq, int *rows, int *cr, int *nb) {
+// An entity of the line of units: prompt e < S with the rows of all its requests, or request e - S: its
+// tokens, first packed row, packed rows, query rows per KV head that have a place (a request: not those beyond
+// max_new), chunks per unit and row blocks (none for what runs on tcgen05).
+template <bool F32>
+__device__ __forceinline__ void pg_unit_entity(const PgDims &D, const PgAttn &A, int e, int *len,
+                                               int *first, int *nq, int *rows, int *cr, int *nb) {
     const bool own = e >= D.S;
     const int r0 = own ? e - D.S : e * D.F, r1 = own ? r0 + 1 : r0 + D.F;
     if (own) *len = pg_clamp(__ldg(A.len + r0), 0, D.cap());
@@ -203,8 +205,10 @@ __device__ __forceinline__ void pg_f32_entity(const PgDims &D, const PgAttn &A, 
     *first = pg_start(A.q_start, r0, D.rows);
     *nq = max(0, pg_start(A.q_start, r1, D.rows) - *first);
     *rows = (own ? min(*nq, D.max_new) : *nq) * D.g;
-    *cr = (*len + kPgF32Chunk - 1) / kPgF32Chunk;
-    *nb = (*rows + kPgF32Rows - 1) / kPgF32Rows;
+    *cr = (*len + kPgChunk - 1) / kPgChunk;
+    const int lg = F32 || pg_unit_rows(D) == 16 ? 4 : 3;
+    *nb = (*rows + (1 << lg) - 1) >> lg;
+    if (!F32 && (own ? pg_on_tc(*rows, *len) : !D.line)) *nb = 0;  // (fp32 without a prompt: cr is 0)
 }
 
 __device__ __forceinline__ long long pg_div(long long a, long long b) {  // of non-negative numbers

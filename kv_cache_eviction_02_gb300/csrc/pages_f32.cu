@@ -26,7 +26,7 @@ namespace kve {
 namespace {
 
 constexpr int kF3Warps = kPgF32Warps, kF3Threads = 32 * kF3Warps;
-constexpr int kF3Tok = kPgF32Chunk, kF3Rows = kPgF32Rows, kF3NT = kF3Rows / 8;
+constexpr int kF3Tok = kPgChunk, kF3Rows = kPgF32Rows, kF3NT = kF3Rows / 8;
 
 // A warp's ring holds K and V of a chunk as items of their own (K_0, V_0, K_1, ...): K's place is free as
 // soon as the scores are there, so 3 items keep as many bytes on their way as two whole chunks would, and
@@ -71,7 +71,7 @@ struct Cursor {
     int kh, rb, c;                // KV head, row block, chunk of the unit
     __device__ __forceinline__ void enter(const PgDims &D, const PgAttn &A, int entity) {
         e = entity;
-        pg_f32_entity(D, A, e, &len, &first, &nq, &rows, &cr, &nb);
+        pg_unit_entity<true>(D, A, e, &len, &first, &nq, &rows, &cr, &nb);
         kh = rb = c = 0;
     }
     // to the next chunk; only called when there is one
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kF3Threads, 1) pg_f32_kernel(PgDims D_, PgAttn
     const PgShare sh = pg_share<kF3Threads>(
         D_.S + D_.R, D_.Hkv, csum, usum, W, [&](int e, int *cr, int *nb) {
             int len, first, nq, rows;
-            pg_f32_entity(D_, A, e, &len, &first, &nq, &rows, cr, nb);
+            pg_unit_entity<true>(D_, A, e, &len, &first, &nq, &rows, cr, nb);
         });
     const int w = blockIdx.x * kF3Warps + warp;
     const long long X0 = w * sh.cpw;

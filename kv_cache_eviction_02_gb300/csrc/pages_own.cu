@@ -92,12 +92,12 @@ __device__ __forceinline__ uint32_t mm_off(int row, int c) {
 
 // Where a warp stands in the line of chunks.
 struct Cursor {
-    int r, len, first, nq;  // request, its rows in pages, its first packed row and their number
-    int cr, nb;             // chunks per unit, row blocks
-    int kh, rb, c;          // KV head, row block, chunk of the unit
-    __device__ __forceinline__ void enter(const PgDims &D, const PgAttn &A, int req) {
-        r = req;
-        pg_own_request(D, A, r, &len, &first, &nq, &cr, &nb);
+    int e, len, first, rows, nq;  // entity, its tokens, its first packed row, its query rows per KV head
+    int cr, nb;                   // chunks per unit, row blocks
+    int kh, rb, c;                // KV head, row block, chunk of the unit
+    __device__ __forceinline__ void enter(const PgDims &D, const PgAttn &A, int entity) {
+        e = entity;
+        pg_unit_entity<false>(D, A, e, &len, &first, &nq, &rows, &cr, &nb);
         kh = rb = c = 0;
     }
     // to the next chunk; only called when there is one
@@ -107,15 +107,16 @@ struct Cursor {
         if (++rb < nb) return;
         rb = 0;
         if (++kh < D.Hkv) return;
-        do enter(D, A, r + 1);
-        while ((cr == 0 || nb == 0) && r + 1 < D.R);
+        do enter(D, A, e + 1);
+        while ((cr == 0 || nb == 0) && e + 1 < D.S + D.R);
     }
 };
 
-// NT: blocks of 8 query rows per unit. RB = 8 NT is the unit's rows.
-template <typename T, int D, int NT>
+// NT: blocks of 8 query rows per unit. RB = 8 NT is the unit's rows. LINE: the prompts stand in the line too.
+template <typename T, int D, int NT, bool LINE>
 __global__ void __launch_bounds__(kMmThreads, 2)
     pg_own_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
                   PgDims D_, PgAttn A, PgOwn W) {
     constexpr int NST = mm_stages<D>(), SB = mm_stage_bytes<D>(), RB = 8 * NT;
     extern __shared__ uint8_t smem_raw[];
@@ -131,15 +132,19 @@ __global__ void __launch_bounds__(kMmThreads, 2)
         s_abort = 0;
         tc::tma_prefetch_desc(&tm_k);
         tc::tma_prefetch_desc(&tm_v);
+        if (LINE) {
+            tc::tma_prefetch_desc(&tm_kp);
+            tc::tma_prefetch_desc(&tm_vp);
+        }
     }
     tc::mbar_fence_init();
-    if (D_.n == 0) pg_wait_prior();  // first kernel of its call (else the prompt's has waited)
+    if (D_.np == 0) pg_wait_prior();  // first kernel of its call (else the prompt's has waited)
     pg_launch_dependents();
 
     const PgShare sh =
-        pg_share<kMmThreads>(D_.R, D_.Hkv, csum, usum, W, [&](int r, int *cr, int *nb) {
-            int len, first, nq;
-            pg_own_request(D_, A, r, &len, &first, &nq, cr, nb);
+        pg_share<kMmThreads>(D_.R + (LINE ? D_.S : 0), D_.Hkv, csum, usum, W, [&](int e, int *cr, int *nb) {
+            int len, first, nq, rows;
+            pg_unit_entity<false>(D_, A, e + (LINE ? 0 : D_.S), &len, &first, &nq, &rows, cr, nb);
         });
     const int w = blockIdx.x * kPgOwnWarps + warp;
     const long long X0 = w * sh.cpw;
@@ -147,13 +152,13 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     if (n > 0) {
         Cursor cc;
         long long x;
-        int r, unit;
-        pg_share_find<kMmThreads>(csum, usum, sh, X0, &r, &x, &unit);
-        cc.enter(D_, A, r);
+        int e, unit;
+        pg_share_find<kMmThreads>(csum, usum, sh, X0, &e, &x, &unit);
+        cc.enter(D_, A, e + (LINE ? 0 : D_.S));
         while (x >= (long long)cc.cr * cc.nb * D_.Hkv) {
             x -= (long long)cc.cr * cc.nb * D_.Hkv;
             unit += cc.nb * D_.Hkv;
-            cc.enter(D_, A, cc.r + 1);
+            cc.enter(D_, A, cc.e + 1);
         }
         const int u = (int)pg_div(x, cc.cr);
         cc.c = (int)(x - (long long)u * cc.cr);
@@ -168,9 +173,9 @@ __global__ void __launch_bounds__(kMmThreads, 2)
         const float k1 = kLog2e * rsqrtf((float)D);
         uint32_t qf[NT][D / 16][2];  // B operand of S^T: query row lane / 4 of each block
         float o[NT][D / 16][4], m[NT][2], l[NT][2];  // this lane's query rows 2 (lane % 4), + 1
-        int see[NT][2], rows, row0;  // tokens they see; query rows of the request, the unit's first
+        int see[NT][2], rows, row0;  // tokens they see; query rows of the entity, the unit's first
         auto begin = [&]() {         // of a unit, or of this warp's part of one
-            rows = min(cc.nq, D_.max_new) * D_.g;
+            rows = cc.rows;
             row0 = cc.rb * RB;
 #pragma unroll
             for (int b = 0; b < NT; ++b) {
@@ -188,7 +193,8 @@ __global__ void __launch_bounds__(kMmThreads, 2)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int qr = row0 + 8 * b + (lane & 3) * 2 + e;
-                    see[b][e] = qr < rows ? cc.len - cc.nq + 1 + qr / D_.g : 0;
+                    see[b][e] = qr >= rows ? 0
+                                           : (LINE && cc.e < D_.S ? cc.len : cc.len - cc.nq + 1 + qr / D_.g);
                     m[b][e] = kPgNoMax;
                     l[b][e] = 0.f;
                 }
@@ -200,22 +206,38 @@ __global__ void __launch_bounds__(kMmThreads, 2)
         };
         // A chunk is 16 / box boxes of box = min(page, 16) rows, one per lane. Where a chunk's pages lie
         // is asked two chunks before they are loaded: the answer of the table (a trip to L2) is not
-        // waited for. at: the box's row within its page and head, -1 behind the request's last page.
+        // waited for. at: the box's row within its page and head, -1 behind the request's last page; a
+        // prompt's chunk is one box (one of each column block): its prompt, its first token and its head.
         const int lgB = D_.lgP < 4 ? D_.lgP : 4, boxes = kMmTok >> lgB;
         const int page_rows = D_.Hkv << D_.lgP;
         const uint32_t box_bytes = (uint32_t)(mm_row_bytes<D>() * 2) << lgB;
         // a box of 16 rows brings all column blocks, [block][row][64 values]; smaller ones one block
         const int zs = lgB < 4 && D > 64 ? D / 64 : 1;
         struct Where {
-            int page, at;
+            int page, at, head;  // head: -1 for pages
         };
         auto where = [&]() -> Where {
+            if (LINE && ca.e < D_.S) return Where{ca.e, ca.c * kMmTok, ca.kh};
             const int j = ca.c * kMmTok + (lane << lgB);
-            if (lane >= boxes || j >= ca.len) return Where{0, -1};
-            return Where{__ldg(A.table + (size_t)ca.r * D_.maxp + (j >> D_.lgP)),
-                         (ca.kh << D_.lgP) + (j & (D_.P - 1))};
+            if (lane >= boxes || j >= ca.len) return Where{0, -1, -1};
+            return Where{__ldg(A.table + (size_t)(ca.e - D_.S) * D_.maxp + (j >> D_.lgP)),
+                         (ca.kh << D_.lgP) + (j & (D_.P - 1)), -1};
         };
         auto load = [&](int place, Where x) {
+            if (LINE && x.head >= 0) {
+                if (tc::elect_one()) {
+                    uint8_t *k = ring + place * SB;
+                    tc::mbar_expect_tx(&bar[place], SB);
+                    for (int z = 0; z < (D == 128 ? 2 : 1); ++z) {
+                        tc::tma_load_4d(k + z * (kMmTok * 128), &tm_kp, 64 * z, x.at, x.head, x.page,
+                                    &bar[place]);
+                        tc::tma_load_4d(k + SB / 2 + z * (kMmTok * 128), &tm_vp, 64 * z, x.at, x.head, x.page,
+                                    &bar[place]);
+                    }
+                }
+                __syncwarp();
+                return;
+            }
             int row = -1;
             if (x.at >= 0) row = pg_page_id(x.page, D_.npages, A.err) * page_rows + x.at;
             const int used = __popc(__ballot_sync(0xffffffffu, row >= 0));
@@ -233,7 +255,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
             }
         };
         int asked = 1, ahead = 0;  // chunks asked for, chunks issued
-        Where x0 = where(), x1{0, -1};
+        Where x0 = where(), x1{0, -1, -1};
         begin();  // its loads of Q run beside the table's
         auto ask = [&]() {
             if (asked < n) {
@@ -378,7 +400,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     pg_end_after_prior();
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool LINE>
 cudaError_t go(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
     const bool f16 = std::is_same<T, __half>::value;
     CUtensorMap tk, tv;
@@ -391,12 +413,21 @@ cudaError_t go(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
     if (!pg_tmap(&tk, f16, A.K, 3, dims, stride, box) ||
         !pg_tmap(&tv, f16, A.V, 3, dims, stride, box))
         return cudaErrorInvalidValue;
-    return pg_launch(pg_own_kernel<T, D, NT>, pg_own_ctas(D_), kMmThreads, mm_smem<D>(), true, st, tk,
-                     tv, D_, A, A.own);
+    CUtensorMap pk = tk, pv = tv;
+    if (LINE) {
+        const cuuint64_t pd[4] = {D, (cuuint64_t)D_.n, (cuuint64_t)D_.Hkv, (cuuint64_t)D_.S};
+        const long long ps[3] = {A.p_tok, A.p_head, A.p_prompt};
+        const cuuint32_t pb[4] = {64, kMmTok, 1, 1};
+        if (!pg_tmap(&pk, f16, A.Kp, 4, pd, ps, pb) || !pg_tmap(&pv, f16, A.Vp, 4, pd, ps, pb))
+            return cudaErrorInvalidValue;
+    }
+    return pg_launch(pg_own_kernel<T, D, NT, LINE>, pg_own_ctas(D_), kMmThreads, mm_smem<D>(), true, st, tk,
+                     tv, pk, pv, D_, A, A.own);
 }
 
 template <typename T, int D> cudaError_t by_rows(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
-    return pg_unit_rows(D_) == 8 ? go<T, D, 1>(D_, A, st) : go<T, D, 2>(D_, A, st);
+    if (D_.line) return pg_unit_rows(D_) == 8 ? go<T, D, 1, true>(D_, A, st) : go<T, D, 2, true>(D_, A, st);
+    return pg_unit_rows(D_) == 8 ? go<T, D, 1, false>(D_, A, st) : go<T, D, 2, false>(D_, A, st);
 }
 
 template <typename T> cudaError_t by_head(const PgDims &D, const PgAttn &A, cudaStream_t st) {

@@ -23,15 +23,6 @@
 namespace kve {
 namespace {
 
-__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z,
-                                            int w, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(tc::smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w),
-        "r"(tc::smem_u32(bar))
-        : "memory");
-}
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -517,7 +508,7 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
                         break;
                     tc::mbar_expect_tx(&B.rfull[slot], L::TILE);
                     for (int kb = 0; kb < L::KB; ++kb)
-                        tma_load_4d(sm + L::RING + slot * L::TILE + kb * 16384,
+                        tc::tma_load_4d(sm + L::RING + slot * L::TILE + kb * 16384,
                                     (c & 1) ? &tm_v : &tm_k, 64 * kb, t0 + (c >> 1) * 128, kh, s,
                                     &B.rfull[slot]);
                     issued = c + 1;
