@@ -97,7 +97,8 @@ inline bool pg_short_prompts(const PgDims &D) {
     return D.n <= 256 && chunks(D.S, D.group_rows(), D.n) <= 2048 &&
            chunks(D.R, D.max_new, D.cap()) <= 16384 && (D.cap() > kPgJoinOwn || pg_many_new(D));
 }
-// Rows of a unit that can hold a query, CTAs of the kernel that deals out units (two per SM, fp32 one;
+// Rows of a unit that can hold a query, CTAs of the kernel that deals out units (three per SM, two for units
+// of 16 rows, fp32 one;
 // fewer when there cannot be a chunk for each warp), and the places its pieces need.
 inline int pg_seg_rows(const PgDims &D) {
     // (a prompt's rows may be all there are: a refused request can pack more than max_new)
@@ -113,7 +114,7 @@ inline int pg_own_ctas(const PgDims &D) {
         chunks += (long long)D.S * D.Hkv * ((D.group_rows() * D.g + rb - 1) / rb) *
                   ((D.n + kPgChunk - 1) / kPgChunk);
     const int warps = D.dtype == KVE_F32 ? kPgF32Warps : kPgOwnWarps;
-    const long long ctas = (chunks + warps - 1) / warps, most = D.own_sms * (D.dtype == KVE_F32 ? 1 : 2);
+    const long long ctas = (chunks + warps - 1) / warps, most = D.own_sms * (D.dtype == KVE_F32 ? 1 : (rb == 8 ? 3 : 2));
     return (int)(ctas < most ? ctas : most);
 }
 inline long long pg_own_segs(const PgDims &D) {
@@ -124,8 +125,8 @@ inline long long pg_own_segs(const PgDims &D) {
     return units + (long long)pg_own_ctas(D) * (D.dtype == KVE_F32 ? kPgF32Warps : kPgOwnWarps);
 }
 
-// Where the pieces lie: the chunks of entity e (request e; fp32: prompt e, then request e - S) start at
-// base[e] in the line of all chunks and its units at unit[e]; every warp has cpw chunks; the piece of
+// Where the pieces lie: the chunks of entity e (request e; with the prompts in the line prompt e, then request
+// e - S; fp32 always) start at base[e] in the line of all chunks and its units at unit[e]; every warp has cpw chunks; the piece of
 // unit u that warp w saw is at place u + w, seg_rows rows each.
 struct PgOwn {
     float2 *ml;

@@ -1,5 +1,5 @@
-// Shared-prompt decoding, fp32: attention over the prompts and the requests' own rows on the CUDA cores,
-// in one launch.
+// Shared-prompt decoding, fp32: attention over the prompts and the requests' own rows in one launch,
+// with warp-level matrix products.
 //
 // The work of all prompts and all requests stands in one line: entities (the prompts, then the
 // requests), of each its units (KV head, block of 16 query rows), of each its chunks of 16 tokens; every

@@ -1,5 +1,5 @@
-// Shared-prompt decoding, 16-bit types: attention of the requests' own rows with warp-level matrix
-// products.
+// Shared-prompt decoding, 16-bit types: attention of the requests' own rows, and over short prompts, with
+// warp-level matrix products.
 //
 // Own rows are read by g query heads of one or a few new rows, so a request and KV head have 1 to a
 // few dozen query rows over its K/V: bound by HBM, with 2 g flops per byte at one new row. The products
@@ -8,13 +8,17 @@
 // 8 query heads where a 128-row tcgen05 tile would be almost empty. The weights go from the accumulator
 // of S^T to the B operand of V^T P^T by an 8 x 8 transpose in registers.
 //
-// Work is dealt to warps, not blocks. A unit is (request, KV head, block of 8 or 16 query rows), a chunk
-// 16 of its tokens; the chunks of all units stand in one line (request, then KV head, then row block)
+// Work is dealt to warps, not blocks. A unit is (request or prompt, KV head, block of 8 or 16 query rows), a
+// chunk 16 of its tokens; the chunks of all units stand in one line (request, then KV head, then row block)
 // and every warp takes the same number of consecutive ones, however the lengths lie. A warp's ring of
 // chunks (TMA boxes of the pages, swizzled for ldmatrix) runs on across the units it passes, so HBM sees
 // no pause at a unit's end, and no warp waits for another. Each piece of a unit that a warp has seen
 // becomes one partial result at place (unit index + warp index), which no other piece has; the join finds
 // a unit's pieces from the same arithmetic, in order.
+//
+// 256 requests of up to 1024 own rows (8 KV heads of d 128, 542 MB): 5.4 TB/s of DRAM, 0.8 of what a copy
+// reaches; a warp's steps from a chunk's arrival to its output take 2300 cycles, about what its share of the
+// bytes takes to arrive.
 #include <cudaTypedefs.h>
 
 #include <type_traits>
@@ -26,13 +30,15 @@ namespace {
 
 constexpr int kMmThreads = 32 * kPgOwnWarps, kMmTok = kPgChunk;  // tokens per chunk
 
-template <int D> constexpr int mm_stages() { return D == 128 ? 3 : 4; }
+// Three blocks per SM for units of 8 query rows (d_head 128: two stages; 256 requests behind 8K rows 137 us
+// with two blocks of three stages, 130 so), two for 16, whose fragments take the registers.
+template <int D, int NT> constexpr int mm_stages() { return D == 128 ? (NT == 1 ? 2 : 3) : 4; }
 // A row takes at least 128 bytes: a box must start on a multiple of them, and one of page size 1 is a
 // single row. With d_head 32 the boxes reach behind the rows, where TMA fills in zeros.
 template <int D> constexpr int mm_row_bytes() { return D == 32 ? 128 : D * 2; }
 template <int D> constexpr int mm_stage_bytes() { return kMmTok * mm_row_bytes<D>() * 2; }  // K and V
-template <int D> constexpr int mm_smem() {
-    return kPgOwnWarps * mm_stages<D>() * mm_stage_bytes<D>() + 1024;
+template <int D, int NT> constexpr int mm_smem() {
+    return kPgOwnWarps * mm_stages<D, NT>() * mm_stage_bytes<D>() + 1024;
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -114,11 +120,11 @@ struct Cursor {
 
 // NT: blocks of 8 query rows per unit. RB = 8 NT is the unit's rows. LINE: the prompts stand in the line too.
 template <typename T, int D, int NT, bool LINE>
-__global__ void __launch_bounds__(kMmThreads, 2)
+__global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
     pg_own_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
                   PgDims D_, PgAttn A, PgOwn W) {
-    constexpr int NST = mm_stages<D>(), SB = mm_stage_bytes<D>(), RB = 8 * NT;
+    constexpr int NST = mm_stages<D, NT>(), SB = mm_stage_bytes<D>(), RB = 8 * NT;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
@@ -421,7 +427,7 @@ cudaError_t go(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
         if (!pg_tmap(&pk, f16, A.Kp, 4, pd, ps, pb) || !pg_tmap(&pv, f16, A.Vp, 4, pd, ps, pb))
             return cudaErrorInvalidValue;
     }
-    return pg_launch(pg_own_kernel<T, D, NT, LINE>, pg_own_ctas(D_), kMmThreads, mm_smem<D>(), true, st, tk,
+    return pg_launch(pg_own_kernel<T, D, NT, LINE>, pg_own_ctas(D_), kMmThreads, mm_smem<D, NT>(), true, st, tk,
                      tv, pk, pv, D_, A, A.own);
 }
 
