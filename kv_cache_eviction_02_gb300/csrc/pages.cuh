@@ -120,7 +120,7 @@ inline int pg_own_ctas(const PgDims &D) {
 inline long long pg_own_segs(const PgDims &D) {
     const long long busy = D.R < D.rows ? D.R : D.rows;
     long long units = D.Hkv * ((long long)D.rows * D.g / pg_unit_rows(D) + busy);
-    if (D.line)
+    if (D.line || D.dtype == KVE_F32)  // (fp32: without a prompt they are counted all the same, with no chunks)
         units += D.Hkv * ((long long)D.rows * D.g / pg_unit_rows(D) + (D.S < D.rows ? D.S : D.rows));
     return units + (long long)pg_own_ctas(D) * (D.dtype == KVE_F32 ? kPgF32Warps : kPgOwnWarps);
 }
@@ -209,7 +209,7 @@ __device__ __forceinline__ void pg_unit_entity(const PgDims &D, const PgAttn &A,
     *cr = (*len + kPgChunk - 1) / kPgChunk;
     const int lg = F32 || pg_unit_rows(D) == 16 ? 4 : 3;
     *nb = (*rows + (1 << lg) - 1) >> lg;
-    if (!F32 && (own ? pg_on_tc(*rows, *len) : !D.line)) *nb = 0;  // (fp32 without a prompt: cr is 0)
+    if (!F32 && (own ? pg_on_tc(*rows, *len) : !D.line)) *nb = 0;
 }
 
 __device__ __forceinline__ long long pg_div(long long a, long long b) {  // of non-negative numbers

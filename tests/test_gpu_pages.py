@@ -367,6 +367,17 @@ def test_many_new_rows_beside_few(case):
     Case(*case, seed=19, nothing=True).check()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("S", [1, 40])
+def test_many_requests_with_several_blocks_of_rows_each(dtype, S):
+    """17 to 20 new rows each, without a prompt and behind a short one: every unit has its place."""
+    rng = np.random.default_rng(29)
+    new = rng.integers(17, 21, 200)
+    for n in (0, 7):
+        c = Case(dtype, S, 200 // S, 8, 8, 32, n, 16, 5, 20, seed=29, new=new)
+        c.check(set(range(0, c.rows, 61)) | {c.rows - 1})
+
+
 LONG = [("bf16", 1, 4, 32, 8, 128, 16384, 16, 7, 1), ("f16", 2, 3, 8, 2, 64, 9001, 16, 5000, 1),
         ("bf16", 1, 2, 5, 1, 128, 3, 256, 20000, 2), ("f32", 1, 2, 4, 2, 64, 4000, 16, 3000, 2),
         ("bf16", 1, 300, 8, 2, 128, 2500, 64, 700, 1), ("bf16", 2, 4, 10, 2, 128, 4100, 32, 600, 64)]
