@@ -4,6 +4,7 @@ built separately by ``oracle.build``."""
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -64,10 +65,15 @@ def build(verbose: bool = False, extra=()) -> str:
         if _stale(obj, [src] + headers):
             jobs.append([cc, *ARCH, *NVFLAGS, *extra, "-c", src, "-o", obj])
 
-    made = {}  # temporary output: its final name
-    if _stale(BINDING, [os.path.join(CSRC, "binding.cpp"), headers[-1]]):
-        made[BINDING + f".tmp{os.getpid()}"] = BINDING
-        jobs.insert(0, binding_command(next(iter(made))))
+    # the binding is built for the Python and torch that are installed
+    stamp, made = os.path.join(BUILD, "binding.txt"), BINDING + f".tmp{os.getpid()}"
+    for_ = f"python {sys.version_info[:2]} torch {importlib.metadata.version('torch')}"
+    bind = _stale(BINDING, [os.path.join(CSRC, "binding.cpp"), headers[-1]])
+    if not bind and os.path.exists(stamp):
+        with open(stamp) as f:
+            bind = f.read() != for_
+    if bind:
+        jobs.insert(0, binding_command(made))
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -78,8 +84,10 @@ def build(verbose: bool = False, extra=()) -> str:
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
         list(ex.map(run, jobs))
-    for tmp, name in made.items():
-        os.replace(tmp, name)
+    if bind:
+        os.replace(made, BINDING)
+        with open(stamp, "w") as f:
+            f.write(for_)
     if jobs or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
