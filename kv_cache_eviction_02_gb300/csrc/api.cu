@@ -1103,7 +1103,7 @@ int pg_attention(const KvePgShape *shape, const void *q, long long q_row_stride,
         ProfScope ps("pg_own", pg_many_new(D) ? 2 : 1, st);
         e = launch_pg_own(D, A, st);
     }
-    if (e == cudaSuccess) {
+    if (e == cudaSuccess && !D.direct) {
         ProfScope ps("pg_join", 1, st);
         e = launch_pg_join(D, A, st);
     }

@@ -35,12 +35,13 @@ static void pg_split(PgDims *D) {
         *len = (int)(per * 128);
         *count = (int)((tiles + per - 1) / per);
     };
+    D->own_sms = kPgSms;
     D->np = D->ns = 0;
     D->psplit = 128;
     D->ssplit = 256;
-    D->own_sms = kPgSms;
+    D->direct = pg_direct(*D);
     D->line = D->n > 0;
-    if (D->dtype == KVE_F32) return;
+    if (D->dtype == KVE_F32 || D->direct) return;
     D->line = D->line && pg_short_prompts(*D);
     if (D->n > 0 && !D->line) {
         const long long per = pg_tile_rows(*D) * pg_pairs(*D, D->group_rows());
@@ -121,7 +122,7 @@ PgWorkspace pg_ws_layout(const PgDims &D) {
     const size_t rows = (size_t)D.rows * D.Hq * (D.np + D.ns);
     W.part_ml = take(sizeof(float2) * rows);
     W.part_o = take(sizeof(float) * rows * D.d);
-    const size_t segs = pg_join_own(D) ? 0 : (size_t)pg_own_segs(D) * pg_seg_rows(D);
+    const size_t segs = pg_join_own(D) || D.direct ? 0 : (size_t)pg_own_segs(D) * pg_seg_rows(D);
     W.own_ml = take(sizeof(float2) * segs);
     W.own_o = take(sizeof(float) * segs * D.d);
     W.own_base = take(sizeof(long long) * (D.S + D.R));

@@ -19,6 +19,7 @@ struct PgDims {
     int ns, ssplit;            // pg_many_new: splits of a request's own rows and their tokens
     int own_sms;               // SMs for the kernel that deals out units
     bool line;                 // that kernel takes the prompts too (fp32; 16-bit types: short work)
+    bool direct;               // it does all, a warp per request and KV head
     // rows behind one prompt, when no request packs more than max_new
     __host__ __device__ long long group_rows() const {
         return (long long)F * max_new < rows ? (long long)F * max_new : rows;
@@ -97,6 +98,17 @@ inline bool pg_short_prompts(const PgDims &D) {
     return D.n <= 256 && chunks(D.S, D.group_rows(), D.n) <= 2048 &&
            chunks(D.R, D.max_new, D.cap()) <= 16384 && (D.cap() > kPgJoinOwn || pg_many_new(D));
 }
+// Very short work of 16-bit types: a warp takes all that one request and KV head see, prompt and own rows, and
+// writes the output, so a call is one launch (183 requests behind 11 rows, up to 16 own ones: 16.8 -> 7.3 us).
+// A lone warp takes 0.5 to 0.8 us a chunk of d_head 128, half that of 64 and 32, and two launches 9 us: 8
+// requests of up to 143 own rows 9.0 us, so 12.0. (With fp32, 1.2 us a chunk and more, it paid for next to
+// nothing.)
+inline bool pg_direct(const PgDims &D) {
+    const long long warps = kPgSms * kPgOwnWarps * (pg_unit_rows(D) == 8 ? 3 : 2);
+    return D.dtype != KVE_F32 && (long long)D.max_new * D.g <= pg_unit_rows(D) &&
+           (long long)D.R * D.Hkv <= warps &&
+           (D.n + kPgChunk - 1) / kPgChunk + (D.cap() + kPgChunk - 1) / kPgChunk <= (D.d == 128 ? 7 : 11);
+}
 // Rows of a unit that can hold a query, CTAs of the kernel that deals out units (three per SM, two for units
 // of 16 rows, fp32 one;
 // fewer when there cannot be a chunk for each warp), and the places its pieces need.
@@ -106,6 +118,7 @@ inline int pg_seg_rows(const PgDims &D) {
     return rows < pg_unit_rows(D) ? (int)rows : pg_unit_rows(D);
 }
 inline int pg_own_ctas(const PgDims &D) {
+    if (D.direct) return (D.R * D.Hkv + kPgOwnWarps - 1) / kPgOwnWarps;
     const int rb = pg_unit_rows(D);
     long long rows = (long long)D.max_new * D.g;
     long long chunks =

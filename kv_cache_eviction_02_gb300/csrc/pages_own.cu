@@ -118,13 +118,16 @@ struct Cursor {
     }
 };
 
-// NT: blocks of 8 query rows per unit. RB = 8 NT is the unit's rows. LINE: the prompts stand in the line too.
-template <typename T, int D, int NT, bool LINE>
+// NT: blocks of 8 query rows per unit. RB = 8 NT is the unit's rows. MODE: what a warp takes, its share of the
+// requests' units, of the prompts' and the requests', or all of one request and KV head.
+enum { kOwn, kLine, kDirect };
+template <typename T, int D, int NT, int MODE>
 __global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
     pg_own_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
                   PgDims D_, PgAttn A, PgOwn W) {
     constexpr int NST = mm_stages<D, NT>(), SB = mm_stage_bytes<D>(), RB = 8 * NT;
+    constexpr bool LINE = MODE == kLine, DIRECT = MODE == kDirect;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~uintptr_t(1023));
@@ -138,7 +141,7 @@ __global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
         s_abort = 0;
         tc::tma_prefetch_desc(&tm_k);
         tc::tma_prefetch_desc(&tm_v);
-        if (LINE) {
+        if (MODE != kOwn) {
             tc::tma_prefetch_desc(&tm_kp);
             tc::tma_prefetch_desc(&tm_vp);
         }
@@ -147,30 +150,48 @@ __global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
     if (D_.np == 0) pg_wait_prior();  // first kernel of its call (else the prompt's has waited)
     pg_launch_dependents();
 
-    const PgShare sh =
-        pg_share<kMmThreads>(D_.R + (LINE ? D_.S : 0), D_.Hkv, csum, usum, W, [&](int e, int *cr, int *nb) {
-            int len, first, nq, rows;
-            pg_unit_entity<false>(D_, A, e + (LINE ? 0 : D_.S), &len, &first, &nq, &rows, cr, nb);
-        });
     const int w = blockIdx.x * kPgOwnWarps + warp;
-    const long long X0 = w * sh.cpw;
-    const int n = (int)min(sh.total - X0, sh.cpw);  // chunks of this warp
-    if (n > 0) {
-        Cursor cc;
-        long long x;
-        int e, unit;
-        pg_share_find<kMmThreads>(csum, usum, sh, X0, &e, &x, &unit);
-        cc.enter(D_, A, e + (LINE ? 0 : D_.S));
-        while (x >= (long long)cc.cr * cc.nb * D_.Hkv) {
-            x -= (long long)cc.cr * cc.nb * D_.Hkv;
-            unit += cc.nb * D_.Hkv;
-            cc.enter(D_, A, cc.e + 1);
+    int n = 0, unit = 0;  // chunks of this warp; the index of its first unit
+    Cursor cc;
+    int prompt = 0, plen = 0, pchunks = 0;  // kDirect: chunks c < pchunks are the prompt's
+    if constexpr (DIRECT) {
+        __syncthreads();  // the barriers and s_abort are set
+        cc.rows = 0;
+        if (w < D_.R * D_.Hkv) {
+            const int r = w / D_.Hkv;
+            cc.enter(D_, A, D_.S + r);
+            cc.kh = w - r * D_.Hkv;
+            prompt = r / D_.F;
+            plen = A.plen ? pg_clamp(__ldg(A.plen + prompt), 0, D_.n) : D_.n;
+            pchunks = (plen + kMmTok - 1) / kMmTok;
+            n = pchunks + cc.cr;
         }
-        const int u = (int)pg_div(x, cc.cr);
-        cc.c = (int)(x - (long long)u * cc.cr);
-        cc.kh = u / cc.nb;
-        cc.rb = u - cc.kh * cc.nb;
-        unit += u;
+    } else {
+        const PgShare sh = pg_share<kMmThreads>(
+            D_.R + (LINE ? D_.S : 0), D_.Hkv, csum, usum, W, [&](int e, int *cr, int *nb) {
+                int len, first, nq, rows;
+                pg_unit_entity<false>(D_, A, e + (LINE ? 0 : D_.S), &len, &first, &nq, &rows, cr, nb);
+            });
+        const long long X0 = w * sh.cpw;
+        n = (int)min(sh.total - X0, sh.cpw);
+        if (n > 0) {
+            long long x;
+            int e;
+            pg_share_find<kMmThreads>(csum, usum, sh, X0, &e, &x, &unit);
+            cc.enter(D_, A, e + (LINE ? 0 : D_.S));
+            while (x >= (long long)cc.cr * cc.nb * D_.Hkv) {
+                x -= (long long)cc.cr * cc.nb * D_.Hkv;
+                unit += cc.nb * D_.Hkv;
+                cc.enter(D_, A, cc.e + 1);
+            }
+            const int u = (int)pg_div(x, cc.cr);
+            cc.c = (int)(x - (long long)u * cc.cr);
+            cc.kh = u / cc.nb;
+            cc.rb = u - cc.kh * cc.nb;
+            unit += u;
+        }
+    }
+    if (DIRECT ? cc.rows > 0 : n > 0) {
         Cursor ca = cc;  // runs ahead: the addresses of the chunks to load
 
         uint8_t *ring = smem + warp * NST * SB;
@@ -224,13 +245,14 @@ __global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
         };
         auto where = [&]() -> Where {
             if (LINE && ca.e < D_.S) return Where{ca.e, ca.c * kMmTok, ca.kh};
-            const int j = ca.c * kMmTok + (lane << lgB);
+            if (DIRECT && ca.c < pchunks) return Where{prompt, ca.c * kMmTok, ca.kh};
+            const int j = (ca.c - pchunks) * kMmTok + (lane << lgB);
             if (lane >= boxes || j >= ca.len) return Where{0, -1, -1};
             return Where{__ldg(A.table + (size_t)(ca.e - D_.S) * D_.maxp + (j >> D_.lgP)),
                          (ca.kh << D_.lgP) + (j & (D_.P - 1)), -1};
         };
         auto load = [&](int place, Where x) {
-            if (LINE && x.head >= 0) {
+            if (MODE != kOwn && x.head >= 0) {
                 if (tc::elect_one()) {
                     uint8_t *k = ring + place * SB;
                     tc::mbar_expect_tx(&bar[place], SB);
@@ -265,7 +287,8 @@ __global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
         begin();  // its loads of Q run beside the table's
         auto ask = [&]() {
             if (asked < n) {
-                ca.next(D_, A);
+                if (DIRECT) ++ca.c;
+                else ca.next(D_, A);
                 x1 = where();
                 ++asked;
             }
@@ -289,13 +312,14 @@ __global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
                 ask();
             }
             if (++fill == NST) fill = 0;
-            if (i > 0 && cc.c == 0) begin();
+            if (!DIRECT && i > 0 && cc.c == 0) begin();
             if (!tc::mbar_wait_warp(&bar[slot], phase, abort_flag, A.err)) break;
-            const int tb = cc.c * kMmTok;
+            const bool pre = DIRECT && cc.c < pchunks;  // a chunk of the prompt, which all rows see
+            const int tb = (cc.c - (pre ? 0 : pchunks)) * kMmTok, len = pre ? plen : cc.len;
             const uint32_t ks = tc::smem_u32(ring + slot * SB), vs = ks + SB / 2;
-            if (tb + kMmTok > cc.len) {
+            if (tb + kMmTok > len) {
                 // V rows behind the last token hold anything (their weights are 0): zeros instead
-                for (int e = (cc.len - tb) * (D / 8) + lane; e < kMmTok * (D / 8); e += 32)
+                for (int e = (len - tb) * (D / 8) + lane; e < kMmTok * (D / 8); e += 32)
                     *reinterpret_cast<uint4 *>(ring + slot * SB + SB / 2 +
                                                mm_off(e / (D / 8), e % (D / 8))) =
                         make_uint4(0, 0, 0, 0);
@@ -328,8 +352,9 @@ __global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
             for (int b = 0; b < NT; ++b)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {  // scores in the log2 domain, maximum over the tokens
-                    s[b][e] = tok < see[b][e] ? s[b][e] * k1 : -INFINITY;
-                    s[b][e + 2] = tok + 8 < see[b][e] ? s[b][e + 2] * k1 : -INFINITY;
+                    const int end = pre ? plen : see[b][e];
+                    s[b][e] = tok < end ? s[b][e] * k1 : -INFINITY;
+                    s[b][e + 2] = tok + 8 < end ? s[b][e + 2] * k1 : -INFINITY;
                     float x = fmaxf(s[b][e], s[b][e + 2]);
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
@@ -369,7 +394,7 @@ __global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
 #pragma unroll
                 for (int b = 0; b < NT; ++b) mma16816<T>(o[b][j], vf, pf[b][0], pf[b][1]);
             }
-            if (i == n - 1 || cc.c == cc.cr - 1) {  // the piece ends
+            if (!DIRECT && (i == n - 1 || cc.c == cc.cr - 1)) {  // the piece ends
                 const long long seg = (long long)unit + w;
 #pragma unroll
                 for (int b = 0; b < NT; ++b)
@@ -393,8 +418,31 @@ __global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
                     }
                 ++unit;
             }
-            if (i + 1 < n) cc.next(D_, A);
+            if (DIRECT) ++cc.c;
+            else if (i + 1 < n) cc.next(D_, A);
             __syncwarp();  // the chunk's readers are done: the next issue may overwrite it
+        }
+        if (DIRECT && !s_abort) {
+#pragma unroll
+            for (int b = 0; b < NT; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = l[b][e];
+                    x += __shfl_xor_sync(0xffffffffu, x, 4);
+                    x += __shfl_xor_sync(0xffffffffu, x, 8);
+                    x += __shfl_xor_sync(0xffffffffu, x, 16);
+                    const int qr = 8 * b + (lane & 3) * 2 + e, t = qr / D_.g, tok = cc.first + t;
+                    if (qr >= rows || __ldg(A.row_req + tok) != cc.e - D_.S) continue;
+                    const float inv = x > 0.f ? 1.f / x : 0.f;
+                    const long long row = (long long)tok * D_.Hq + cc.kh * D_.g + (qr - t * D_.g);
+                    T *dst = static_cast<T *>(A.out) + row * D + (lane >> 2);
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        dst[16 * j] = from_f<T>(o[b][j][e] * inv);
+                        dst[16 * j + 8] = from_f<T>(o[b][j][e + 2] * inv);
+                    }
+                    if (A.lse && lane < 4) A.lse[row] = x > 0.f ? (m[b][e] + log2f(x)) * kLn2 : -INFINITY;
+                }
         }
         if (s_abort) {  // copies still in flight land before the block ends
             for (int k = 0; k < NST; ++k) {
@@ -406,7 +454,7 @@ __global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
     pg_end_after_prior();
 }
 
-template <typename T, int D, int NT, bool LINE>
+template <typename T, int D, int NT, int MODE>
 cudaError_t go(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
     const bool f16 = std::is_same<T, __half>::value;
     CUtensorMap tk, tv;
@@ -420,20 +468,22 @@ cudaError_t go(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
         !pg_tmap(&tv, f16, A.V, 3, dims, stride, box))
         return cudaErrorInvalidValue;
     CUtensorMap pk = tk, pv = tv;
-    if (LINE) {
+    if (MODE != kOwn && D_.n > 0) {
         const cuuint64_t pd[4] = {D, (cuuint64_t)D_.n, (cuuint64_t)D_.Hkv, (cuuint64_t)D_.S};
         const long long ps[3] = {A.p_tok, A.p_head, A.p_prompt};
         const cuuint32_t pb[4] = {64, kMmTok, 1, 1};
         if (!pg_tmap(&pk, f16, A.Kp, 4, pd, ps, pb) || !pg_tmap(&pv, f16, A.Vp, 4, pd, ps, pb))
             return cudaErrorInvalidValue;
     }
-    return pg_launch(pg_own_kernel<T, D, NT, LINE>, pg_own_ctas(D_), kMmThreads, mm_smem<D, NT>(), true, st, tk,
+    return pg_launch(pg_own_kernel<T, D, NT, MODE>, pg_own_ctas(D_), kMmThreads, mm_smem<D, NT>(), true, st, tk,
                      tv, pk, pv, D_, A, A.own);
 }
 
 template <typename T, int D> cudaError_t by_rows(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
-    if (D_.line) return pg_unit_rows(D_) == 8 ? go<T, D, 1, true>(D_, A, st) : go<T, D, 2, true>(D_, A, st);
-    return pg_unit_rows(D_) == 8 ? go<T, D, 1, false>(D_, A, st) : go<T, D, 2, false>(D_, A, st);
+    const bool one = pg_unit_rows(D_) == 8;
+    if (D_.direct) return one ? go<T, D, 1, kDirect>(D_, A, st) : go<T, D, 2, kDirect>(D_, A, st);
+    if (D_.line) return one ? go<T, D, 1, kLine>(D_, A, st) : go<T, D, 2, kLine>(D_, A, st);
+    return one ? go<T, D, 1, kOwn>(D_, A, st) : go<T, D, 2, kOwn>(D_, A, st);
 }
 
 template <typename T> cudaError_t by_head(const PgDims &D, const PgAttn &A, cudaStream_t st) {

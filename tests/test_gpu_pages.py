@@ -378,6 +378,39 @@ def test_many_requests_with_several_blocks_of_rows_each(dtype, S):
         c.check(set(range(0, c.rows, 61)) | {c.rows - 1})
 
 
+# little enough for one warp per request and KV head, which writes the output itself
+BRIEF = [
+    # dtype, S, F, Hq, Hkv, d, n, page, own_hi, new_hi
+    ("bf16", 1, 9, 32, 8, 128, 20, 16, 15, 1), ("f16", 3, 5, 8, 1, 128, 3, 8, 40, 1),
+    ("bf16", 2, 60, 28, 4, 64, 40, 1, 30, 1), ("f16", 1, 33, 16, 16, 32, 100, 2, 20, 7),
+    ("bf16", 2, 7, 16, 1, 128, 17, 32, 9, 1),      # 16 query heads per KV head
+    ("f16", 1, 30, 10, 2, 64, 0, 4, 60, 3),        # up to 15 query rows, no prompt
+    ("bf16", 5, 4, 3, 1, 32, 16, 16, 16, 5),
+]
+
+
+@pytest.mark.parametrize("case", BRIEF, ids=ids)
+def test_brief_work(case):
+    for seed in (30, 31):
+        c = Case(*case, seed=seed, ragged=seed == 31, idle=0.2 if seed == 31 else 0.0,
+                 stride=seed == 31)
+        out, lse = c.check()
+        b, z = c.run()
+        assert torch.equal(out, b) and torch.equal(lse, z)
+        assert torch.equal(out, c.run(lse=False)[0])
+    Case(*case, seed=32, nothing=True).check()
+    # rows whose request is not the one that q_start gives, and of nobody, stay
+    c = Case(*case, seed=33)
+    ref, _ = c.run()
+    keep = c.row_req.copy()
+    c.row_req[keep == 1] = -1
+    c.row_req[keep == 2] = 0
+    out, lse = c.run()
+    hit = torch.as_tensor((keep == 1) | (keep == 2) | (keep < 0), device=DEV)
+    assert (out[hit] == 3.0).all() and (lse[hit] == 5.0).all()
+    assert torch.equal(out[~hit], ref[~hit])
+
+
 LONG = [("bf16", 1, 4, 32, 8, 128, 16384, 16, 7, 1), ("f16", 2, 3, 8, 2, 64, 9001, 16, 5000, 1),
         ("bf16", 1, 2, 5, 1, 128, 3, 256, 20000, 2), ("f32", 1, 2, 4, 2, 64, 4000, 16, 3000, 2),
         ("bf16", 1, 300, 8, 2, 128, 2500, 64, 700, 1), ("bf16", 2, 4, 10, 2, 128, 4100, 32, 600, 64)]
