@@ -1099,7 +1099,7 @@ int pg_attention(const KvePgShape *shape, const void *q, long long q_row_stride,
         ProfScope ps("pg_prompt", 1, st);
         e = launch_pg_prompt_tc(D, A, st);
     }
-    if (e == cudaSuccess && !pg_join_own(D)) {
+    if (e == cudaSuccess && !D.prompt_own) {
         ProfScope ps("pg_own", pg_many_new(D) ? 2 : 1, st);
         e = launch_pg_own(D, A, st);
     }

@@ -40,20 +40,32 @@ static void pg_split(PgDims *D) {
     D->psplit = 128;
     D->ssplit = 256;
     D->direct = pg_direct(*D);
+    D->prompt_own = false;
     D->line = D->n > 0;
     if (D->dtype == KVE_F32 || D->direct) return;
-    D->line = D->line && pg_short_prompts(*D);
-    if (D->n > 0 && !D->line) {
-        const long long per = pg_tile_rows(*D) * pg_pairs(*D, D->group_rows());
+    if (D->n > 0) {
+        const int pairs = pg_pairs(*D, D->group_rows());
+        const long long per = pg_tile_rows(*D) * pairs;
         const long long most = (long long)D->S * pg_tc_blocks(*D, false);  // launched per KV head
         const long long all = D->rows / per + D->S;                        // of which hold rows
         const long long items = D->Hkv * (most < all ? most : all);
         tiles_split(items, D->n, &D->np, &D->psplit);
-        // (the prompt's kernel starts first)
-        const long long ctas = D->Hkv * most * D->np;
-        if (ctas < kPgShare) D->own_sms = (int)(kPgSms - ctas);
+        // two warps per CTA, beside its tiles: about two microseconds a row, half a microsecond a tile
+        const long long rows = D->group_rows() * D->g < 128 ? D->group_rows() * D->g : 128;
+        D->prompt_own = pairs == 1 && D->cap() <= kPgFewOwn && !pg_many_new(*D) &&
+                        rows <= 2 * D->np * (1 + D->psplit / 512);
+        D->line = !D->prompt_own && pg_short_prompts(*D);
+        if (D->line) {
+            D->np = 0;
+        } else {  // (the prompt's kernel starts first)
+            const long long ctas = D->Hkv * most * D->np;
+            if (ctas < kPgShare) D->own_sms = (int)(kPgSms - ctas);
+        }
     }
-    if (pg_many_new(*D)) {
+    if (D->prompt_own) {
+        D->ns = 1;
+        D->ssplit = D->cap();
+    } else if (pg_many_new(*D)) {
         const long long per = pg_tile_rows(*D) * pg_pairs(*D, D->max_new);
         const long long most = (long long)D->R * pg_tc_blocks(*D, true), all = D->rows / per + D->R;
         tiles_split(D->Hkv * (most < all ? most : all), D->cap(), &D->ns, &D->ssplit);
@@ -122,7 +134,7 @@ PgWorkspace pg_ws_layout(const PgDims &D) {
     const size_t rows = (size_t)D.rows * D.Hq * (D.np + D.ns);
     W.part_ml = take(sizeof(float2) * rows);
     W.part_o = take(sizeof(float) * rows * D.d);
-    const size_t segs = pg_join_own(D) || D.direct ? 0 : (size_t)pg_own_segs(D) * pg_seg_rows(D);
+    const size_t segs = D.prompt_own || D.direct ? 0 : (size_t)pg_own_segs(D) * pg_seg_rows(D);
     W.own_ml = take(sizeof(float2) * segs);
     W.own_o = take(sizeof(float) * segs * D.d);
     W.own_base = take(sizeof(long long) * (D.S + D.R));
@@ -396,18 +408,6 @@ __global__ void __launch_bounds__(256)
 // kernels that make them have ended, and eight are on their way at a time. Many are bound by reading
 // them from L2. (A warp for all heads of a KV head, to share the search, was slower: 28 against 22 us
 // for 21K rows and heads.)
-template <typename T, int E> __device__ __forceinline__ void row_cols(const T *p, float (&v)[E]) {
-    if (sizeof(T) * E == 8) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
-        const T *y = reinterpret_cast<const T *>(&x);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = to_f(y[e]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = to_f(__ldg(p + e));
-    }
-}
-
 // What the partial results of a row's heads have in common, read before the kernels that make them have
 // ended; `where` then says where those of a head lie: two runs, the prompt's and the own rows', each with its
 // first row, the rows from one to the next, and how many there are.
@@ -415,7 +415,7 @@ template <bool F32> struct PgFound {
     int r, first, all, nq, len, cr, nb, pfirst, pcr, pnb;
     int np, nd;  // splits of its prompt and, if dense, of its own rows
     bool mine;   // the row has a place
-    bool dense;  // own rows on tcgen05: splits of [splits][rows][Hq], like the prompt's of 16-bit types
+    bool dense;  // own rows by the tcgen05 kernel: splits of [splits][rows][Hq], like the prompt's
     struct Runs {
         const float *po, *oo;
         const float2 *pm, *om;
@@ -437,12 +437,11 @@ template <bool F32> struct PgFound {
         all = nq;
         nq = min(nq, D.max_new);
         mine = r >= 0 && tok >= first && tok - first < nq;
-        dense = !F32 && pg_on_tc((long long)nq * D.g, len);
+        dense = !F32 && (D.prompt_own || pg_on_tc((long long)nq * D.g, len));
         np = D.np == 0 ? 0 : (plen + D.psplit - 1) / D.psplit;
         nd = dense ? (len + D.ssplit - 1) / D.ssplit : 0;
     }
-    // own: its own rows have results (they are not worked out by the join)
-    __device__ __forceinline__ Runs where(const PgDims &D, const PgAttn &A, int tok, int h, int kh, bool own) const {
+    __device__ __forceinline__ Runs where(const PgDims &D, const PgAttn &A, int tok, int h, int kh) const {
         const int hk = h - kh * D.g;
         const long long row = (long long)tok * D.Hq + h, step = (long long)D.rows * D.Hq;
         Runs x;
@@ -467,7 +466,7 @@ template <bool F32> struct PgFound {
             *count = at < 0 ? 0 : (int)max(min(w1 - w0 + 1, (long long)A.own.segs - at), 0LL);
             *at_row = at * A.own.seg_rows + (rr & ((1 << lg) - 1));
         };
-        if (own && !dense) {
+        if (!dense) {
             pieces((line ? D.S : 0) + r, (tok - first) * D.g + hk, cr, nb, &x.orow, &x.no);
             x.ostep = A.own.seg_rows;
         }
@@ -479,12 +478,9 @@ template <bool F32> struct PgFound {
     }
 };
 
-// OWN (tables of at most kPgJoinOwn rows behind a prompt: the lookahead's trajectories): the warp works
-// out the own rows itself, 8 tokens at a time, while the prompt's kernel is still running: a launch less
-// (16K lookahead step: 23.3 -> 20.5 us).
 // W: warps per row and head, 1 or all 4 of the block, which then take turns of U results and are joined in
 // shared memory, in order.
-template <typename T, int D, int U, bool OWN, int W>
+template <typename T, int D, int U, int W>
 __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
     constexpr int E = D / 32;
     constexpr bool F32 = sizeof(T) == 4;
@@ -497,53 +493,10 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
     float M = kPgNoMax, L = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    if (OWN && mine) {
-        float q[E];
-        row_cols<T, E>(static_cast<const T *>(A.q) + tok * A.q_row + (size_t)h * D + lane * E, q);
-        const int see = at.len - at.all + 1 + (tok - at.first);
-        const float k1 = kLog2e * rsqrtf((float)D);
-        for (int t0 = 8 * w; t0 < see; t0 += 8 * W) {
-            float k[8][E], v[8][E], s[8], Mn = M;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) k[j][e] = v[j][e] = 0.f;
-                if (t0 + j < see) {
-                    const int t = t0 + j;
-                    const int page =
-                        pg_page(A.table + (size_t)at.r * D_.maxp, t, D_.lgP, D_.npages, A.err);
-                    const size_t x = ((((size_t)page * D_.Hkv + kh) << D_.lgP) + (t & (D_.P - 1))) * D +
-                                      lane * E;
-                    row_cols<T, E>(static_cast<const T *>(A.K) + x, k[j]);
-                    row_cols<T, E>(static_cast<const T *>(A.V) + x, v[j]);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float x = 0.f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) x = fmaf(q[e], k[j][e], x);
-                s[j] = t0 + j < see ? warp_sum(x) * k1 : -INFINITY;  // (the same in every lane)
-                Mn = fmaxf(Mn, s[j]);
-            }
-            const float f = exp2f(M - Mn);
-            M = Mn;
-            L *= f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] *= f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float p = exp2f(s[j] - M);
-                L += p;
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = fmaf(p, v[j][e], acc[e]);
-            }
-        }
-    }
     pg_wait_prior();
     pg_launch_dependents();
     if (!mine) return;
-    const auto x = at.where(D_, A, tok, h, kh, !OWN);
+    const auto x = at.where(D_, A, tok, h, kh);
     const int np = x.np, nsp = np + x.no;
     // U at a time: a running maximum over the groups, in order
     for (int s0 = U * w; s0 < nsp; s0 += U * W) {
@@ -649,7 +602,7 @@ __global__ void __launch_bounds__(128) pg_join_many_kernel(PgDims D_, PgAttn A) 
     int most = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        x[i] = at.where(D_, A, tok, min(h0 + i * PAR + sub, D_.Hq - 1), kh[i], true);
+        x[i] = at.where(D_, A, tok, min(h0 + i * PAR + sub, D_.Hq - 1), kh[i]);
         most = max(most, x[i].np + x[i].no);
         M[i] = kPgNoMax;
         L[i] = 0.f;
@@ -707,22 +660,17 @@ __global__ void __launch_bounds__(128) pg_join_many_kernel(PgDims D_, PgAttn A) 
 
 template <typename T, int D> cudaError_t join_d(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
     // few rows: all warps of a block for one, 8 partial results on their way in each (lookahead over 32K
-    // rows of fp32, 152 pieces a row: the join 20 -> 12 us), unless there are few results to each (4 prompts
-    // of 32K rows, 9 results a row: 91 us against 87.5 with a warp a row); many: fewer instructions
-    const bool alone = (long long)D_.rows * D_.Hq <= kPgSms * 8 &&
-                       !(pg_join_own(D_) && D_.np <= 16);
+    // rows of fp32, 152 pieces a row: the join 20 -> 12 us); many: fewer instructions
+    const bool alone = (long long)D_.rows * D_.Hq <= kPgSms * 8;
     const bool few = (long long)D_.rows * D_.Hq < kPgSms * 32;
     if constexpr (D < 128)
-        if (!few && !pg_join_own(D_)) {
+        if (!few) {
             const long long warps = (long long)D_.rows * ((D_.Hq + 3) / 4);
             return pg_launch(pg_join_many_kernel<T, D>, (unsigned)((warps + 3) / 4), 128, 0, true, st, D_,
                              A);
         }
-    auto kern = few ? pg_join_kernel<T, D, 8, false, 1> : pg_join_kernel<T, D, 4, false, 1>;
-    if (alone) kern = pg_join_kernel<T, D, 8, false, 4>;
-    if constexpr (sizeof(T) == 2)
-        if (pg_join_own(D_))
-            kern = alone ? pg_join_kernel<T, D, 8, true, 4> : pg_join_kernel<T, D, 8, true, 1>;
+    auto kern = few ? pg_join_kernel<T, D, 8, 1> : pg_join_kernel<T, D, 4, 1>;
+    if (alone) kern = pg_join_kernel<T, D, 8, 4>;
     return pg_launch(kern, dim3(D_.rows, alone ? D_.Hq : (D_.Hq + 3) / 4), 128, 0, true, st, D_, A);
 }
 
@@ -780,7 +728,7 @@ cudaError_t launch_pg_append(const PgDims &D, const void *K_new, const void *V_n
 
 cudaError_t launch_pg_own(const PgDims &D, const PgAttn &A, cudaStream_t st) {
     if (D.dtype == KVE_F32) return launch_pg_f32(D, A, st);
-    if (pg_join_own(D)) return cudaSuccess;
+    if (D.prompt_own) return cudaSuccess;
     const cudaError_t e = launch_pg_own16(D, A, st);
     return e == cudaSuccess && pg_many_new(D) ? launch_pg_own_tc(D, A, st) : e;
 }

@@ -20,6 +20,7 @@ struct PgDims {
     int own_sms;               // SMs for the kernel that deals out units
     bool line;                 // that kernel takes the prompts too (fp32; 16-bit types: short work)
     bool direct;               // it does all, a warp per request and KV head
+    bool prompt_own;           // the prompt's kernel does the own rows too (split np)
     // rows behind one prompt, when no request packs more than max_new
     __host__ __device__ long long group_rows() const {
         return (long long)F * max_new < rows ? (long long)F * max_new : rows;
@@ -76,11 +77,10 @@ __host__ __device__ inline bool pg_many_new(const PgDims &D) {
     return D.dtype != KVE_F32 && pg_on_tc((long long)D.max_new * D.g, D.cap());
 }
 
-// The join works out the own rows itself where a table holds few rows behind a prompt (16-bit types).
-constexpr int kPgJoinOwn = 32;
-inline bool pg_join_own(const PgDims &D) {
-    return D.np > 0 && D.cap() <= kPgJoinOwn && !pg_many_new(D);
-}
+// Tables of at most this many rows behind a prompt of a 16-bit type (the lookahead's trajectories): two idle
+// warps of the prompt's kernel work out the own rows, a launch less (16K lookahead step: with a kernel of their
+// own 23.3 us, in the join, which cannot start beside the prompt's CTAs, 20.5, so 16.4).
+constexpr int kPgFewOwn = 32;
 // Query rows of a unit: 8 when no request has more, else 16 (the rows of a unit share its K/V loads; more
 // than 16 would not leave registers for two blocks per SM).
 __host__ __device__ inline int pg_unit_rows(const PgDims &D) {
@@ -88,15 +88,15 @@ __host__ __device__ inline int pg_unit_rows(const PgDims &D) {
 }
 // 16-bit types: the warps of pages_own.cu take the prompts too when all there is to do is short, so that a
 // call has one launch less and no tcgen05 kernel, which costs several microseconds whatever it does (a step of
-// 4 requests behind 11 rows 12.0 -> 8.7 us); not when the join takes the own rows, since there are two launches
-// either way, nor with long own rows (64 requests of up to 1875: 54 us, in one line 70).
+// 4 requests behind 11 rows 12.0 -> 8.7 us); not with long own rows (64 requests of up to 1875: 54 us, in one
+// line 70).
 inline bool pg_short_prompts(const PgDims &D) {
     const int rb = pg_unit_rows(D);
     auto chunks = [&](long long of, long long rows, int tokens) {  // at most
         return of * D.Hkv * ((rows * D.g + rb - 1) / rb) * ((tokens + kPgChunk - 1) / kPgChunk);
     };
     return D.n <= 256 && chunks(D.S, D.group_rows(), D.n) <= 2048 &&
-           chunks(D.R, D.max_new, D.cap()) <= 16384 && (D.cap() > kPgJoinOwn || pg_many_new(D));
+           chunks(D.R, D.max_new, D.cap()) <= 16384;
 }
 // Very short work of 16-bit types: a warp takes all that one request and KV head see, prompt and own rows, and
 // writes the output, so a call is one launch (183 requests behind 11 rows, up to 16 own ones: 16.8 -> 7.3 us).
@@ -110,8 +110,7 @@ inline bool pg_direct(const PgDims &D) {
            (D.n + kPgChunk - 1) / kPgChunk + (D.cap() + kPgChunk - 1) / kPgChunk <= (D.d == 128 ? 7 : 11);
 }
 // Rows of a unit that can hold a query, CTAs of the kernel that deals out units (three per SM, two for units
-// of 16 rows, fp32 one;
-// fewer when there cannot be a chunk for each warp), and the places its pieces need.
+// of 16 rows, fp32 one; fewer when there cannot be a chunk for each warp), and the places its pieces need.
 inline int pg_seg_rows(const PgDims &D) {
     // (a prompt's rows may be all there are: a refused request can pack more than max_new)
     const long long rows = (long long)(D.line ? D.rows : D.max_new) * D.g;
@@ -323,6 +322,19 @@ __device__ __forceinline__ void pg_share_find(const long long *csum, const int *
     *e = grp * s.q;
     *x = X - csum[grp];
     *unit = usum[grp];
+}
+
+// E consecutive columns of a row of K, V or q (E = 4: 8 bytes of a 16-bit type).
+template <typename T, int E> __device__ __forceinline__ void row_cols(const T *p, float (&v)[E]) {
+    if (sizeof(T) * E == 8) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
+        const T *y = reinterpret_cast<const T *>(&x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = to_f(y[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = to_f(__ldg(p + e));
+    }
 }
 
 // Programmatic dependent launch: a dependent kernel of the same call may start when every block of the

@@ -69,10 +69,74 @@ struct PtArgs {
     int nrt, tt;  // row tiles (or pairs) per prompt and KV head, new rows per tile
     float k1;
     const int32_t *plen, *q_start, *len, *table;
+    const void *q, *K, *V;  // and row_req: for the own rows
+    long long q_row;
+    const int32_t *row_req;
     float2 *part_ml;
     float *part_o;
     unsigned *err;
 };
+
+// Own rows of the prompt's requests whose tables hold few rows, a warp per row and head, 8 tokens at a time:
+// query rows first, first + step, ... below `end` of the prompt's, into split np of the partial results.
+template <typename T, int E>
+__device__ __forceinline__ void pt_own_rows(const PtArgs &A, int s, int kh, int tok0, int first, int end,
+                                            int step, int lane) {
+    const PgDims &D = A.D;
+    constexpr int d = 32 * E;
+    for (int rr = first; rr < end; rr += step) {
+        const int tok = tok0 + rr / D.g, h = kh * D.g + rr % D.g, r = __ldg(A.row_req + tok);
+        if (r < s * D.F || r >= (s + 1) * D.F) continue;
+        const int start = pg_start(A.q_start, r, D.rows);
+        const int nq = pg_start(A.q_start, r + 1, D.rows) - start;
+        if (tok < start || tok - start >= min(nq, D.max_new)) continue;
+        float q[E], M = kPgNoMax, L = 0.f, acc[E];
+        row_cols<T, E>(static_cast<const T *>(A.q) + tok * A.q_row + (size_t)h * d + lane * E, q);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        const int see = pg_clamp(__ldg(A.len + r), 0, D.cap()) - nq + 1 + (tok - start);
+        for (int t0 = 0; t0 < see; t0 += 8) {
+            float k[8][E], v[8][E], x[8], Mn = M;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) k[j][e] = v[j][e] = 0.f;
+                if (t0 + j < see) {
+                    const int t = t0 + j;
+                    const int page = pg_page(A.table + (size_t)r * D.maxp, t, D.lgP, D.npages, A.err);
+                    const size_t at = ((((size_t)page * D.Hkv + kh) << D.lgP) + (t & (D.P - 1))) * d +
+                                      lane * E;
+                    row_cols<T, E>(static_cast<const T *>(A.K) + at, k[j]);
+                    row_cols<T, E>(static_cast<const T *>(A.V) + at, v[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float y = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) y = fmaf(q[e], k[j][e], y);
+                x[j] = t0 + j < see ? warp_sum(y) * A.k1 : -INFINITY;  // (the same in every lane)
+                Mn = fmaxf(Mn, x[j]);
+            }
+            const float f = exp2f(M - Mn);
+            M = Mn;
+            L *= f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] *= f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float p = exp2f(x[j] - M);
+                L += p;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(p, v[j][e], acc[e]);
+            }
+        }
+        const size_t row = ((size_t)D.np * D.rows + tok) * D.Hq + h;
+        if (lane == 0) A.part_ml[row] = make_float2(M, L);
+#pragma unroll
+        for (int e = 0; e < E; ++e) A.part_o[row * d + lane * E + e] = acc[e];
+    }
+}
 
 // Barriers of a CTA, in shared memory.
 template <int D, int QT> struct PtBars {
@@ -363,6 +427,7 @@ __device__ __forceinline__ void pt_softmax(const PtArgs &A, const PtBars<D, QT> 
         const size_t place =  // of this lane's row
             ((size_t)(OWN ? A.D.np + sp : sp) * A.D.rows + tok0 + rr / g) * A.D.Hq + kh * g + rr % g;
         const int lpr = d / 4, col = (lane % lpr) * 4;  // lanes per row: 32, 16 or 8
+#pragma unroll 8
         for (int x0 = 0; x0 < rows; x0 += 32 / lpr) {
             const int x = x0 + lane / lpr;
             const size_t to = __shfl_sync(0xffffffffu, place, x & 31);
@@ -374,7 +439,7 @@ __device__ __forceinline__ void pt_softmax(const PtArgs &A, const PtBars<D, QT> 
     }
 }
 
-// Warps: 0 TMA, 1 MMA, 2-3 idle, then 4 softmax warps per row tile.
+// Warps: 0 TMA, 1 MMA, 2-3 own rows of short tables, then 4 softmax warps per row tile.
 template <typename T, int D, int QT, bool OWN>
 __global__ void __launch_bounds__(pt_threads<QT>(), 1)
     pg_prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -420,6 +485,18 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
         nrow = min(tok1 - tok0, A.D.max_new) * A.D.g;
         if (!pg_on_tc(nrow, end)) nrow = 0;  // pages_own.cu's
     }
+    const int all = nrow;  // query rows, with or without tokens of this split
+    // warps 2 and 3, once: the own rows of this CTA's row blocks, shared with the other splits
+    bool own_done = OWN || QT == 2 || !A.D.prompt_own || (warp != 2 && warp != 3);
+    auto own_rows = [&]() {
+        for (int rt = rt0; rt * QT * per < all; rt += A.nrt) {
+            const int first = rt * QT * per + 2 * sp + warp - 2, end = min(all, (rt + 1) * QT * per);
+            if (D == 128) pt_own_rows<T, 4>(A, s, kh, tok0, first, end, 2 * nsplit, lane);
+            else if (A.D.d == 64) pt_own_rows<T, 2>(A, s, kh, tok0, first, end, 2 * nsplit, lane);
+            else pt_own_rows<T, 1>(A, s, kh, tok0, first, end, 2 * nsplit, lane);
+        }
+        own_done = true;
+    };
     const int step = OWN ? A.D.ssplit : A.D.psplit;
     const int t0 = sp * step, t_end = min(end, t0 + step);
     if (t_end <= t0) nrow = 0;
@@ -546,6 +623,8 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
                     pt_softmax<T, D, QT, OWN, false>(A, B, sm, tmem, warp, lane, row0, nrow, tok0,
                                                      kh, t0, t1, see0, ntl, sp, abort_flag);
             }
+        } else if (!OWN && QT == 1 && !own_done) {
+            own_rows();
         }
         tc::fence_before_sync();
         tc::fence_proxy_async_smem();  // the ring's plain reads and writes before the next TMA loads
@@ -555,6 +634,7 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
         if (threadIdx.x == 0)
             for (int i = 0; i < L::NBAR; ++i) mbar_inval(bars + i);
     }
+    if (!OWN && QT == 1 && !own_done) own_rows();
     __syncthreads();
     if (warp == 1) tc::tmem_dealloc(*tmem_slot, 512);
     if (OWN) pg_end_after_prior();
@@ -590,6 +670,11 @@ cudaError_t go(const PgDims &D_, const PgAttn &A, cudaStream_t st) {
     P.q_start = A.q_start;
     P.len = A.len;
     P.table = A.table;
+    P.q = A.q;
+    P.q_row = A.q_row;
+    P.K = A.K;
+    P.V = A.V;
+    P.row_req = A.row_req;
     P.part_ml = A.part_ml;
     P.part_o = A.part_o;
     P.err = A.err;

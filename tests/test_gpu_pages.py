@@ -411,6 +411,31 @@ def test_brief_work(case):
     assert torch.equal(out[~hit], ref[~hit])
 
 
+@pytest.mark.parametrize("case", [
+    ("bf16", 1, 4, 8, 2, 128, 3000, 16, 14, 1), ("f16", 3, 3, 8, 1, 64, 1500, 4, 20, 2),
+    ("bf16", 5, 2, 12, 4, 32, 800, 1, 20, 3), ("f16", 2, 4, 16, 16, 128, 700, 8, 12, 1),
+], ids=ids)
+def test_few_own_rows_behind_long_prompts(case):
+    """The lookahead's shape: tables of at most 32 rows; prompts of no length among them, requests
+    without rows, rows that see nothing of their own, rows of nobody and of another request."""
+    for seed in (34, 35):
+        c = Case(*case, seed=seed, ragged=True, idle=0.2, stride=seed == 34)
+        assert c.pb.max_pages * c.pb.page_size <= 32
+        c.plen.mul_((torch.arange(case[1], device=DEV) != 1).to(torch.int32))
+        c.np_plen = c.plen.tolist()
+        c.check()
+    Case(*case, seed=36, nothing=True, ragged=True).check()
+    c = Case(*case, seed=37)
+    ref, _ = c.run()
+    keep = c.row_req.copy()
+    c.row_req[keep == 1] = -1
+    c.row_req[keep == 2] = 0
+    out, lse = c.run()
+    hit = torch.as_tensor((keep == 1) | (keep == 2) | (keep < 0), device=DEV)
+    assert (out[hit] == 3.0).all() and (lse[hit] == 5.0).all()
+    assert torch.equal(out[~hit], ref[~hit])
+
+
 LONG = [("bf16", 1, 4, 32, 8, 128, 16384, 16, 7, 1), ("f16", 2, 3, 8, 2, 64, 9001, 16, 5000, 1),
         ("bf16", 1, 2, 5, 1, 128, 3, 256, 20000, 2), ("f32", 1, 2, 4, 2, 64, 4000, 16, 3000, 2),
         ("bf16", 1, 300, 8, 2, 128, 2500, 64, 700, 1), ("bf16", 2, 4, 10, 2, 128, 4100, 32, 600, 64)]
