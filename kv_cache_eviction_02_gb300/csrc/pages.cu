@@ -50,10 +50,13 @@ static void pg_split(PgDims *D) {
         const long long all = D->rows / per + D->S;                        // of which hold rows
         const long long items = D->Hkv * (most < all ? most : all);
         tiles_split(items, D->n, &D->np, &D->psplit);
-        // two warps per CTA, beside its tiles: about two microseconds a row, half a microsecond a tile
+        // two warps per CTA, beside its tiles: a row takes 1 us and 1.3 for every 8 tokens, a tile 0.6, and there
+        // are 3 besides (measured: 16 prompts of 2K rows with 4 requests of up to 32 own rows 115 us so, 33 with
+        // a launch for the own rows; 4 of 32K 93 and 107)
         const long long rows = D->group_rows() * D->g < 128 ? D->group_rows() * D->g : 128;
+        const long long own = (rows + 2 * D->np - 1) / (2 * D->np) * (10 + 13 * ((D->cap() + 7) / 8));
         D->prompt_own = pairs == 1 && D->cap() <= kPgFewOwn && !pg_many_new(*D) &&
-                        rows <= 2 * D->np * (1 + D->psplit / 512);
+                        own <= 30 + 6 * (D->psplit / 128);
         D->line = !D->prompt_own && pg_short_prompts(*D);
         if (D->line) {
             D->np = 0;

@@ -77,64 +77,86 @@ struct PtArgs {
     unsigned *err;
 };
 
-// Own rows of the prompt's requests whose tables hold few rows, a warp per row and head, 8 tokens at a time:
-// query rows first, first + step, ... below `end` of the prompt's, into split np of the partial results.
+// Own rows of the prompt's requests whose tables hold at most 32 rows, a warp per row and head: query rows
+// first, first + step, ... below `end` of the prompt's, into split np of the partial results. Each lane looks up
+// one of them (request, tokens that it sees), then for each row one of its tokens' pages, a row ahead: what is
+// left of a row is its K/V's way from memory.
 template <typename T, int E>
 __device__ __forceinline__ void pt_own_rows(const PtArgs &A, int s, int kh, int tok0, int first, int end,
                                             int step, int lane) {
     const PgDims &D = A.D;
     constexpr int d = 32 * E;
-    for (int rr = first; rr < end; rr += step) {
-        const int tok = tok0 + rr / D.g, h = kh * D.g + rr % D.g, r = __ldg(A.row_req + tok);
-        if (r < s * D.F || r >= (s + 1) * D.F) continue;
-        const int start = pg_start(A.q_start, r, D.rows);
-        const int nq = pg_start(A.q_start, r + 1, D.rows) - start;
-        if (tok < start || tok - start >= min(nq, D.max_new)) continue;
-        float q[E], M = kPgNoMax, L = 0.f, acc[E];
-        row_cols<T, E>(static_cast<const T *>(A.q) + tok * A.q_row + (size_t)h * d + lane * E, q);
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        const int see = pg_clamp(__ldg(A.len + r), 0, D.cap()) - nq + 1 + (tok - start);
-        for (int t0 = 0; t0 < see; t0 += 8) {
-            float k[8][E], v[8][E], x[8], Mn = M;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) k[j][e] = v[j][e] = 0.f;
-                if (t0 + j < see) {
-                    const int t = t0 + j;
-                    const int page = pg_page(A.table + (size_t)r * D.maxp, t, D.lgP, D.npages, A.err);
-                    const size_t at = ((((size_t)page * D.Hkv + kh) << D.lgP) + (t & (D.P - 1))) * d +
-                                      lane * E;
-                    row_cols<T, E>(static_cast<const T *>(A.K) + at, k[j]);
-                    row_cols<T, E>(static_cast<const T *>(A.V) + at, v[j]);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float y = 0.f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) y = fmaf(q[e], k[j][e], y);
-                x[j] = t0 + j < see ? warp_sum(y) * A.k1 : -INFINITY;  // (the same in every lane)
-                Mn = fmaxf(Mn, x[j]);
-            }
-            const float f = exp2f(M - Mn);
-            M = Mn;
-            L *= f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] *= f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float p = exp2f(x[j] - M);
-                L += p;
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = fmaf(p, v[j][e], acc[e]);
+    for (; first < end; first += 32 * step) {
+        const int rr = first + lane * step;
+        int tok = 0, h = 0, r = 0, see = 0;
+        bool mine = false;  // the row is its request's
+        if (rr < end) {
+            tok = tok0 + rr / D.g;
+            h = kh * D.g + rr % D.g;
+            r = __ldg(A.row_req + tok);
+            if (r >= s * D.F && r < (s + 1) * D.F) {
+                const int start = pg_start(A.q_start, r, D.rows);
+                const int nq = pg_start(A.q_start, r + 1, D.rows) - start;
+                mine = tok >= start && tok - start < min(nq, D.max_new);
+                see = pg_clamp(__ldg(A.len + r), 0, D.cap()) - nq + 1 + (tok - start);
             }
         }
-        const size_t row = ((size_t)D.np * D.rows + tok) * D.Hq + h;
-        if (lane == 0) A.part_ml[row] = make_float2(M, L);
+        unsigned todo = __ballot_sync(0xffffffffu, mine);
+        auto pages = [&](int i) {  // of row i's tokens, one per lane
+            const int ri = __shfl_sync(0xffffffffu, r, i), n = __shfl_sync(0xffffffffu, see, i);
+            return lane < n ? pg_page(A.table + (size_t)ri * D.maxp, lane, D.lgP, D.npages, A.err) : 0;
+        };
+        int next = todo ? pages(__ffs(todo) - 1) : 0;
+        while (todo) {
+            const int i = __ffs(todo) - 1, page = next;
+            todo &= todo - 1;
+            const int ti = __shfl_sync(0xffffffffu, tok, i), hi = __shfl_sync(0xffffffffu, h, i);
+            const int n = __shfl_sync(0xffffffffu, see, i);
+            float q[E], M = kPgNoMax, L = 0.f, acc[E];
+            row_cols<T, E>(static_cast<const T *>(A.q) + ti * A.q_row + (size_t)hi * d + lane * E, q);
+            if (todo) next = pages(__ffs(todo) - 1);
 #pragma unroll
-        for (int e = 0; e < E; ++e) A.part_o[row * d + lane * E + e] = acc[e];
+            for (int e = 0; e < E; ++e) acc[e] = 0.f;
+            for (int t0 = 0; t0 < n; t0 += 8) {
+                float k[8][E], v[8][E], x[8], Mn = M;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int p = __shfl_sync(0xffffffffu, page, (t0 + j) & 31);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) k[j][e] = v[j][e] = 0.f;
+                    if (t0 + j < n) {
+                        const size_t at =
+                            ((((size_t)p * D.Hkv + kh) << D.lgP) + ((t0 + j) & (D.P - 1))) * d + lane * E;
+                        row_cols<T, E>(static_cast<const T *>(A.K) + at, k[j]);
+                        row_cols<T, E>(static_cast<const T *>(A.V) + at, v[j]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float y = 0.f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) y = fmaf(q[e], k[j][e], y);
+                    x[j] = t0 + j < n ? warp_sum(y) * A.k1 : -INFINITY;  // (the same in every lane)
+                    Mn = fmaxf(Mn, x[j]);
+                }
+                const float f = exp2f(M - Mn);
+                M = Mn;
+                L *= f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] *= f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float w = exp2f(x[j] - M);
+                    L += w;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[j][e], acc[e]);
+                }
+            }
+            const size_t row = ((size_t)D.np * D.rows + ti) * D.Hq + hi;
+            if (lane == 0) A.part_ml[row] = make_float2(M, L);
+#pragma unroll
+            for (int e = 0; e < E; ++e) A.part_o[row * d + lane * E + e] = acc[e];
+        }
     }
 }
 
