@@ -350,9 +350,17 @@ __global__ void __launch_bounds__(1024)
         for (; done; done &= done - 1) {
             const int r = r0 + __ffs(done) - 1;
             const int have = (len[r] + P - 1) >> lgP;
-            for (int j = lane; j < have; j += 32) {
-                const unsigned at = (unsigned)head + (unsigned)n_free + (unsigned)(-2 - off[r]) + j;
-                A.free_pages[at % (unsigned)npages] = __ldg(A.table + (size_t)r * maxp + j);
+            for (int j0 = lane; j0 < have; j0 += 256) {  // 8 loads of the table on their way at a time
+                int page[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    page[k] = j0 + 32 * k < have ? __ldg(A.table + (size_t)r * maxp + j0 + 32 * k) : 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const unsigned at =
+                        (unsigned)head + (unsigned)n_free + (unsigned)(-2 - off[r]) + j0 + 32 * k;
+                    if (j0 + 32 * k < have) A.free_pages[at % (unsigned)npages] = page[k];
+                }
             }
         }
     }
