@@ -649,7 +649,10 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
             own_rows();
         }
         tc::fence_before_sync();
-        tc::fence_proxy_async_smem();  // the ring's plain reads and writes before the next TMA loads
+        if ((rt + A.nrt) * QT * per >= nrow) break;
+        // another round (the fence waits for the stores of the one before, so not after the last): the ring's
+        // plain reads and writes before the next TMA loads
+        tc::fence_proxy_async_smem();
         __syncthreads();
         tc::fence_after_sync();
         if (*abort_flag) break;
@@ -658,6 +661,7 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
     }
     if (!OWN && QT == 1 && !own_done) own_rows();
     __syncthreads();
+    tc::fence_after_sync();
     if (warp == 1) tc::tmem_dealloc(*tmem_slot, 512);
     if (OWN) pg_end_after_prior();
 }
