@@ -88,15 +88,16 @@ __host__ __device__ inline int pg_unit_rows(const PgDims &D) {
 }
 // 16-bit types: the warps of pages_own.cu take the prompts too when all there is to do is short, so that a
 // call has one launch less and no tcgen05 kernel, which costs several microseconds whatever it does (a step of
-// 4 requests behind 11 rows 12.0 -> 8.7 us); not with long own rows (64 requests of up to 1875: 54 us, in one
-// line 70).
+// 4 requests behind 11 rows 12.0 -> 8.7 us); not with long own rows, where the prompt's kernel
+// hides behind them (172 requests of up to 268 own rows, 23K chunks: 26.7 us, in one line 24.6; 64 of up to
+// 1875, 60K: 54 and 59).
 inline bool pg_short_prompts(const PgDims &D) {
     const int rb = pg_unit_rows(D);
     auto chunks = [&](long long of, long long rows, int tokens) {  // at most
         return of * D.Hkv * ((rows * D.g + rb - 1) / rb) * ((tokens + kPgChunk - 1) / kPgChunk);
     };
     return D.n <= 256 && chunks(D.S, D.group_rows(), D.n) <= 2048 &&
-           chunks(D.R, D.max_new, D.cap()) <= 16384;
+           chunks(D.R, D.max_new, D.cap()) <= 24576;
 }
 // Very short work of 16-bit types: a warp takes all that one request and KV head see, prompt and own rows, and
 // writes the output, so a call is one launch (183 requests behind 11 rows, up to 16 own ones: 16.8 -> 7.3 us).
