@@ -33,6 +33,7 @@ constexpr int kPgShare = 100;  // most SMs the prompt's kernel takes beside the 
 
 // Units of 8 or 16 query rows (fp32: 16), chunks of 16 tokens, dealt out to the warps of pages_own.cu
 // (16-bit types) or pages_f32.cu.
+constexpr long long kPgDirectMost = 1 << 20;  // most chunks of a call without partial results
 constexpr int kPgChunk = 16, kPgOwnWarps = 4, kPgF32Warps = 8, kPgF32Rows = 16;
 
 // Workspace carve-up (byte offsets, 256-aligned): partial results [splits][rows][Hq] (m in log2 and l;
@@ -104,11 +105,14 @@ inline bool pg_short_prompts(const PgDims &D) {
 // A lone warp takes 0.5 to 0.8 us a chunk of d_head 128, half that of 64 and 32, and two launches 9 us: 8
 // requests of up to 143 own rows 9.0 us, so 12.0. (With fp32, 1.2 us a chunk and more, it paid for next to
 // nothing.)
+__host__ __device__ inline int pg_direct_blocks(const PgDims &D) {  // row blocks per request and KV head
+    const int rb = pg_unit_rows(D);
+    return (int)(((long long)D.max_new * D.g + rb - 1) / rb);
+}
 inline bool pg_direct(const PgDims &D) {
-    const long long warps = kPgSms * kPgOwnWarps * (pg_unit_rows(D) == 8 ? 3 : 2);
-    return D.dtype != KVE_F32 && (long long)D.max_new * D.g <= pg_unit_rows(D) &&
-           (long long)D.R * D.Hkv <= warps &&
-           (D.n + kPgChunk - 1) / kPgChunk + (D.cap() + kPgChunk - 1) / kPgChunk <= (D.d == 128 ? 7 : 11);
+    const long long chunks = (D.n + kPgChunk - 1) / kPgChunk + (D.cap() + kPgChunk - 1) / kPgChunk;
+    return D.dtype != KVE_F32 && chunks <= (D.d == 128 ? 7 : 11) &&
+           (long long)D.R * D.Hkv * pg_direct_blocks(D) * chunks <= kPgDirectMost;
 }
 // Rows of a unit that can hold a query, CTAs of the kernel that deals out units (three per SM, two for units
 // of 16 rows, fp32 one; fewer when there cannot be a chunk for each warp), and the places its pieces need.
@@ -118,7 +122,7 @@ inline int pg_seg_rows(const PgDims &D) {
     return rows < pg_unit_rows(D) ? (int)rows : pg_unit_rows(D);
 }
 inline int pg_own_ctas(const PgDims &D) {
-    if (D.direct) return (D.R * D.Hkv + kPgOwnWarps - 1) / kPgOwnWarps;
+    if (D.direct) return (D.R * D.Hkv * pg_direct_blocks(D) + kPgOwnWarps - 1) / kPgOwnWarps;
     const int rb = pg_unit_rows(D);
     long long rows = (long long)D.max_new * D.g;
     long long chunks =

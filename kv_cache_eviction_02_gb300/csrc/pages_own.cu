@@ -156,11 +156,13 @@ __global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
     int prompt = 0, plen = 0, pchunks = 0;  // kDirect: chunks c < pchunks are the prompt's
     if constexpr (DIRECT) {
         __syncthreads();  // the barriers and s_abort are set
-        cc.rows = 0;
-        if (w < D_.R * D_.Hkv) {
-            const int r = w / D_.Hkv;
+        cc.rows = cc.rb = 0;
+        const int blocks = pg_direct_blocks(D_), u = w / blocks;
+        if (u < D_.R * D_.Hkv) {
+            const int r = u / D_.Hkv;
             cc.enter(D_, A, D_.S + r);
-            cc.kh = w - r * D_.Hkv;
+            cc.kh = u - r * D_.Hkv;
+            cc.rb = w - u * blocks;
             prompt = r / D_.F;
             plen = A.plen ? pg_clamp(__ldg(A.plen + prompt), 0, D_.n) : D_.n;
             pchunks = (plen + kMmTok - 1) / kMmTok;
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
             unit += u;
         }
     }
-    if (DIRECT ? cc.rows > 0 : n > 0) {
+    if (DIRECT ? cc.rb * RB < cc.rows : n > 0) {
         Cursor ca = cc;  // runs ahead: the addresses of the chunks to load
 
         uint8_t *ring = smem + warp * NST * SB;
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
                     x += __shfl_xor_sync(0xffffffffu, x, 4);
                     x += __shfl_xor_sync(0xffffffffu, x, 8);
                     x += __shfl_xor_sync(0xffffffffu, x, 16);
-                    const int qr = 8 * b + (lane & 3) * 2 + e, t = qr / D_.g, tok = cc.first + t;
+                    const int qr = row0 + 8 * b + (lane & 3) * 2 + e, t = qr / D_.g, tok = cc.first + t;
                     if (qr >= rows || __ldg(A.row_req + tok) != cc.e - D_.S) continue;
                     const float inv = x > 0.f ? 1.f / x : 0.f;
                     const long long row = (long long)tok * D_.Hq + cc.kh * D_.g + (qr - t * D_.g);
