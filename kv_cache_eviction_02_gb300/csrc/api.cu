@@ -1100,7 +1100,7 @@ int pg_attention(const KvePgShape *shape, const void *q, long long q_row_stride,
         e = launch_pg_prompt_tc(D, A, st);
     }
     if (e == cudaSuccess && !D.prompt_own) {
-        ProfScope ps("pg_own", pg_many_new(D) ? 2 : 1, st);
+        ProfScope ps("pg_own", D.ns > 0 ? 2 : 1, st);
         e = launch_pg_own(D, A, st);
     }
     if (e == cudaSuccess && !D.direct) {

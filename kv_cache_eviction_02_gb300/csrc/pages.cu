@@ -741,7 +741,7 @@ cudaError_t launch_pg_own(const PgDims &D, const PgAttn &A, cudaStream_t st) {
     if (D.dtype == KVE_F32) return launch_pg_f32(D, A, st);
     if (D.prompt_own) return cudaSuccess;
     const cudaError_t e = launch_pg_own16(D, A, st);
-    return e == cudaSuccess && pg_many_new(D) ? launch_pg_own_tc(D, A, st) : e;
+    return e == cudaSuccess && D.ns > 0 ? launch_pg_own_tc(D, A, st) : e;
 }
 
 cudaError_t launch_pg_join(const PgDims &D, const PgAttn &A, cudaStream_t st) {

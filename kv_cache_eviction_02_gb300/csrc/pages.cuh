@@ -100,19 +100,22 @@ inline bool pg_short_prompts(const PgDims &D) {
     return D.n <= 256 && chunks(D.S, D.group_rows(), D.n) <= 2048 &&
            chunks(D.R, D.max_new, D.cap()) <= 24576;
 }
-// Very short work of 16-bit types: a warp takes all that one request and KV head see, prompt and own rows, and
-// writes the output, so a call is one launch (183 requests behind 11 rows, up to 16 own ones: 16.8 -> 7.3 us).
-// A lone warp takes 0.5 to 0.8 us a chunk of d_head 128, half that of 64 and 32, and two launches 9 us: 8
-// requests of up to 143 own rows 9.0 us, so 12.0. (With fp32, 1.2 us a chunk and more, it paid for next to
-// nothing.)
+// Very short work of 16-bit types: a warp takes all that a block of query rows of one request and KV head sees,
+// prompt and own rows, and writes the output, so a call is one launch without partial results (183 requests
+// behind 11 rows, up to 16 own ones: 16.8 -> 7.3 us; 687 of up to 57 new rows behind 2 rows 361 -> 168). A lone
+// warp takes 0.5 to 0.8 us a chunk of d_head 128, half that of 64 and 32, and two launches 9 us: 8 requests of up
+// to 143 own rows 9.0 us, so 12.0; more warps than the SMs hold hide that (253 requests of up to 157 own rows 61
+// -> 38 us; 256 with 200 and 121 rows, 24 chunks, 33 and 34). (With fp32, 1.2 us a chunk and more, it paid for
+// next to nothing.)
 __host__ __device__ inline int pg_direct_blocks(const PgDims &D) {  // row blocks per request and KV head
     const int rb = pg_unit_rows(D);
     return (int)(((long long)D.max_new * D.g + rb - 1) / rb);
 }
 inline bool pg_direct(const PgDims &D) {
     const long long chunks = (D.n + kPgChunk - 1) / kPgChunk + (D.cap() + kPgChunk - 1) / kPgChunk;
-    return D.dtype != KVE_F32 && chunks <= (D.d == 128 ? 7 : 11) &&
-           (long long)D.R * D.Hkv * pg_direct_blocks(D) * chunks <= kPgDirectMost;
+    const long long units = (long long)D.R * D.Hkv * pg_direct_blocks(D);
+    const int most = units > kPgSms * 12 ? 20 : (D.d == 128 ? 7 : 11);
+    return D.dtype != KVE_F32 && chunks <= most && units * chunks <= kPgDirectMost;
 }
 // Rows of a unit that can hold a query, CTAs of the kernel that deals out units (three per SM, two for units
 // of 16 rows, fp32 one; fewer when there cannot be a chunk for each warp), and the places its pieces need.

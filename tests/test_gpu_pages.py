@@ -412,6 +412,18 @@ def test_brief_work(case):
 
 
 @pytest.mark.parametrize("case", [
+    ("bf16", 3, 60, 12, 4, 128, 2, 16, 2, 57),      # up to 171 query rows: blocks of 16
+    ("f16", 1, 300, 16, 8, 64, 100, 16, 150, 2), ("bf16", 2, 100, 28, 4, 32, 33, 8, 60, 5),
+], ids=ids)
+def test_brief_work_of_many_requests(case):
+    """More warps than the GPU holds at a time, several blocks of rows per request."""
+    for kw in (dict(seed=38), dict(seed=39, ragged=True, idle=0.3, stride=True), dict(seed=40, nothing=True)):
+        c = Case(*case, **kw)
+        out, _ = c.check(set(range(0, c.rows, max(1, c.rows // 25))) | {c.rows - 1})
+        assert torch.isfinite(out[:c.rows].float()).all()
+
+
+@pytest.mark.parametrize("case", [
     ("bf16", 1, 4, 8, 2, 128, 3000, 16, 14, 1), ("f16", 3, 3, 8, 1, 64, 1500, 4, 20, 2),
     ("bf16", 5, 2, 12, 4, 32, 800, 1, 20, 3), ("f16", 2, 4, 16, 16, 128, 700, 8, 12, 1),
 ], ids=ids)
