@@ -228,7 +228,7 @@ __device__ __forceinline__ void pg_unit_entity(const PgDims &D, const PgAttn &A,
     *rows = (own ? min(*nq, D.max_new) : *nq) * D.g;
     *cr = (*len + kPgChunk - 1) / kPgChunk;
     const int lg = F32 || pg_unit_rows(D) == 16 ? 4 : 3;
-    *nb = (*rows + (1 << lg) - 1) >> lg;
+    *nb = *cr > 0 ? (*rows + (1 << lg) - 1) >> lg : 0;  // (without tokens no units: warps step over it)
     if (!F32 && (own ? pg_on_tc(*rows, *len) : !D.line)) *nb = 0;
 }
 

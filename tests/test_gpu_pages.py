@@ -378,6 +378,21 @@ def test_many_requests_with_several_blocks_of_rows_each(dtype, S):
         c.check(set(range(0, c.rows, 61)) | {c.rows - 1})
 
 
+@pytest.mark.parametrize("dtype,n", [("f32", 400), ("bf16", 180), ("f16", 600)])
+@pytest.mark.parametrize("new", [1, 5])
+def test_prompts_and_requests_without_tokens_between_others(dtype, n, new):
+    """A prompt of no length with rows behind it, and requests with rows but nothing in their pages, in the
+    middle of the line of work: the results behind them are the right ones."""
+    c = Case(dtype, 4, 5, 6, 2, 64, n, 16, 90, new, seed=41, ragged=True)
+    c.plen[1] = c.plen[2] = 0
+    c.np_plen = c.plen.tolist()
+    c.lens[[1, 6, 7, 8, 13]] = 0
+    c.check()
+    c.plen[:] = 0
+    c.np_plen = c.plen.tolist()
+    c.check()
+
+
 # little enough for one warp per request and KV head, which writes the output itself
 BRIEF = [
     # dtype, S, F, Hq, Hkv, d, n, page, own_hi, new_hi
