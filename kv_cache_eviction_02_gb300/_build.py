@@ -1,6 +1,6 @@
 """Builds libkvevict.so in-tree with nvcc for sm_103a (one -gencode, translation units compiled
-in parallel) and the Python module _binding with g++ against the installed torch; liboracle.so is
-built separately by ``oracle.build``."""
+in parallel) and, where torch's headers and a C++ compiler for them are at hand, the Python module
+_binding with g++ against the installed torch; liboracle.so is built separately by ``oracle.build``."""
 from __future__ import annotations
 
 import concurrent.futures
@@ -37,7 +37,10 @@ def sources():
 
 def binding_command(out: str):
     """g++ on csrc/binding.cpp."""
-    torch = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch is not installed")
+    torch = list(spec.submodule_search_locations)[0]
     inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
     return [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
             "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"], "-I", inc,
@@ -65,16 +68,6 @@ def build(verbose: bool = False, extra=()) -> str:
         if _stale(obj, [src] + headers):
             jobs.append([cc, *ARCH, *NVFLAGS, *extra, "-c", src, "-o", obj])
 
-    # the binding is built for the Python and torch that are installed
-    stamp, made = os.path.join(BUILD, "binding.txt"), BINDING + f".tmp{os.getpid()}"
-    for_ = f"python {sys.version_info[:2]} torch {importlib.metadata.version('torch')}"
-    bind = _stale(BINDING, [os.path.join(CSRC, "binding.cpp"), headers[-1]])
-    if not bind and os.path.exists(stamp):
-        with open(stamp) as f:
-            bind = f.read() != for_
-    if bind:
-        jobs.insert(0, binding_command(made))
-
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if verbose or r.returncode != 0:
@@ -82,16 +75,34 @@ def build(verbose: bool = False, extra=()) -> str:
         if r.returncode != 0:
             raise RuntimeError("compilation failed: " + " ".join(cmd))
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        list(ex.map(run, jobs))
-    if bind:
+    def binding():
+        # built for the Python and torch that are installed
+        stamp, made = os.path.join(BUILD, "binding.txt"), BINDING + f".tmp{os.getpid()}"
+        for_ = f"python {sys.version_info[:2]} torch {importlib.metadata.version('torch')}"
+        bind = _stale(BINDING, [os.path.join(CSRC, "binding.cpp"), headers[-1]])
+        if not bind and os.path.exists(stamp):
+            with open(stamp) as f:
+                bind = f.read() != for_
+        if not bind:
+            return
+        run(binding_command(made))
         os.replace(made, BINDING)
         with open(stamp, "w") as f:
             f.write(for_)
+
+    with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        bound = ex.submit(binding)
+        list(ex.map(run, jobs))
     if jobs or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    try:
+        bound.result()
+    except Exception as e:  # the library does without: its calls then take the checks of api.py
+        if os.path.exists(BINDING):
+            os.remove(BINDING)  # one of other sources, another Python or another torch
+        sys.stderr.write(f"_binding is not built, the library is: {e}\n")
     return LIB
 
 

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import warnings
 from dataclasses import dataclass
 
 import torch
@@ -482,8 +483,16 @@ class PgProblem:
 
 # These calls are made once per layer and decoded token: the module _binding (csrc/binding.cpp) checks their
 # tensors and makes them. What it does not take, addresses and arguments that do not fit the shape, goes
-# through the checks here, which say what is wrong.
+# through the checks here, which say what is wrong; so does everything where the module is not built.
 _native, _OTHER = None, -1
+
+
+class _NoBinding:
+    @staticmethod
+    def plan(*_):
+        return _OTHER
+
+    append = attention = plan
 
 
 def _bind():
@@ -492,8 +501,11 @@ def _bind():
     try:
         from . import _binding
     except ImportError as e:
-        raise RuntimeError("the module _binding is missing or does not load: build it with "
-                           "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        warnings.warn("the module _binding is missing or does not load, shared-prompt calls take "
+                      f"several microseconds longer ({e}); to build it: "
+                      "python -c 'import __graft_entry__ as g; g.build()'", RuntimeWarning, 3)
+        _native = _NoBinding
+        return _native
     _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                     for f in (L.pg_plan, L.pg_append, L.pg_attention)))
     _native = _binding
