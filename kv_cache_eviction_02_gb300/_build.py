@@ -76,16 +76,17 @@ def build(verbose: bool = False, extra=()) -> str:
             raise RuntimeError("compilation failed: " + " ".join(cmd))
 
     def binding():
-        # built for the Python and torch that are installed
+        # built for the Python and torch that are installed, which the stamp names; without one it may be of
+        # any others
         stamp, made = os.path.join(BUILD, "binding.txt"), BINDING + f".tmp{os.getpid()}"
         for_ = f"python {sys.version_info[:2]} torch {importlib.metadata.version('torch')}"
-        bind = _stale(BINDING, [os.path.join(CSRC, "binding.cpp"), headers[-1]])
-        if not bind and os.path.exists(stamp):
+        if not _stale(BINDING, [os.path.join(CSRC, "binding.cpp"), headers[-1]]) and os.path.exists(stamp):
             with open(stamp) as f:
-                bind = f.read() != for_
-        if not bind:
-            return
+                if f.read() == for_:
+                    return
         run(binding_command(made))
+        if os.path.exists(stamp):
+            os.remove(stamp)
         os.replace(made, BINDING)
         with open(stamp, "w") as f:
             f.write(for_)

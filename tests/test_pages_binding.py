@@ -75,6 +75,37 @@ def test_the_library_is_built_without_the_binding(small, monkeypatch, capfd, mis
 COMMAND = _build.binding_command
 
 
+@pytest.mark.parametrize("stamp", ["none", "another"])
+def test_a_binding_of_unknown_or_other_versions_is_made_anew(small, stamp):
+    """A binding that came without its stamp, or was written when the build was cut off before the stamp,
+    may be of any Python and torch."""
+    _build.build()
+    path = os.path.join(_build.BUILD, "binding.txt")
+    if stamp == "none":
+        os.remove(path)
+    else:
+        with open(path, "w") as f:
+            f.write("python (3, 0) torch 0")
+    _build.build()
+    assert len(small) == 2
+    _build.build()
+    assert len(small) == 2
+
+
+def test_a_build_cut_off_behind_the_binding_leaves_no_stamp(small, monkeypatch):
+    """The stamp of the binding before would vouch for the new one."""
+    _build.build()
+    path = os.path.join(_build.BUILD, "binding.txt")
+    os.utime(_build.BINDING, (0, 0))
+
+    def cut(*a):
+        raise OSError("cut off")
+
+    monkeypatch.setattr(_build.os, "replace", cut)
+    _build.build()
+    assert not os.path.exists(path)
+
+
 @pytest.fixture
 def unbound(api, monkeypatch):
     """The package without its binding."""
