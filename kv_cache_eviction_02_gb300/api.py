@@ -11,7 +11,7 @@ import ctypes
 import functools
 import os
 import warnings
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 
 import torch
 
@@ -457,6 +457,10 @@ class PgProblem:
         return KvePgShape(self.n_prompts, self.fan, self.n_q_heads, self.n_kv_heads, self.d_head,
                           self.n_prefix, self.page_size, self.n_pages, self.max_pages, self.n_rows,
                           self.max_new, self.dtype)
+
+    def __getstate__(self):
+        """The sizes: an address made from them is of this process and this object."""
+        return {f.name: getattr(self, f.name) for f in fields(self)}
 
     @functools.cached_property
     def c_shape(self):
