@@ -705,13 +705,10 @@ cudaError_t launch_pg_plan(const PgDims &D, const PgPlanArgs &A, cudaStream_t st
     if (ctas > kPgSms) ctas = kPgSms;
     const bool vec = (reinterpret_cast<uintptr_t>(A.row_req) | reinterpret_cast<uintptr_t>(A.row_pos) |
                       reinterpret_cast<uintptr_t>(A.slot_map)) % 16 == 0;
-    const size_t smem = 3 * sizeof(int) * (size_t)D.R;
+    // (small steps do without a change of the limit, a call into the driver)
+    const size_t bytes = 3 * sizeof(int) * (size_t)D.R;
+    const PgSmem smem(bytes, bytes > 40 * 1024 ? 3 * sizeof(int) * 16384 : bytes);
     auto go = [&](auto kern, int grid, int block, bool rows, bool lens) {
-        if (smem > 40 * 1024) {  // with the static arrays above 48 KB
-            cudaError_t e = cudaFuncSetAttribute(
-                kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * 4 * 16384);
-            if (e != cudaSuccess) return e;
-        }
         return pg_launch(kern, grid, block, smem, true, st, A, D.R, D.lgP, D.npages, D.maxp, D.rows,
                          D.max_new, vec, rows, lens);
     };

@@ -374,9 +374,18 @@ __device__ __forceinline__ int pg_page(const int32_t *trow, int pos, int lgP, in
     return pg_page_id(__ldg(trow + (pos >> lgP)), npages, err);
 }
 
+// Dynamic shared memory of a launch, and the most that any launch of its kernel takes. A kernel's limit is one
+// for all threads of the process: set to what the launch at hand takes, it would fail the larger launch of another
+// thread that stands between its own setting and its launch.
+struct PgSmem {
+    size_t bytes, most;
+    PgSmem(size_t bytes) : bytes(bytes), most(bytes) {}
+    PgSmem(size_t bytes, size_t most) : bytes(bytes), most(most) {}
+};
+
 // Launches `kern` on `st`, as a dependent of the kernel before it if asked.
 template <typename... P, typename... Q>
-cudaError_t pg_launch(void (*kern)(P...), dim3 grid, unsigned block, size_t smem, bool dependent,
+cudaError_t pg_launch(void (*kern)(P...), dim3 grid, unsigned block, PgSmem smem, bool dependent,
                       cudaStream_t st, Q &&...args) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at[1];
@@ -384,13 +393,13 @@ cudaError_t pg_launch(void (*kern)(P...), dim3 grid, unsigned block, size_t smem
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = grid;
     cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = smem.bytes;
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = dependent ? 1 : 0;
-    if (smem > 48 * 1024) {
+    if (smem.most > 40 * 1024) {  // with the static arrays above 48 KB
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem);
+                                             (int)smem.most);
         if (e != cudaSuccess) return e;
     }
     return cudaLaunchKernelEx(&cfg, kern, P(args)...);
