@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(256)
 // ended; `where` then says where those of a head lie: two runs, the prompt's and the own rows', each with its
 // first row, the rows from one to the next, and how many there are.
 template <bool F32> struct PgFound {
-    int r, first, all, nq, len, cr, nb, pfirst, pcr, pnb;
+    int r, first, nq, len, cr, nb, pfirst, pcr, pnb;
     int np, nd;  // splits of its prompt and, if dense, of its own rows
     bool mine;   // the row has a place
     bool dense;  // own rows by the tcgen05 kernel: splits of [splits][rows][Hq], like the prompt's
@@ -445,7 +445,6 @@ template <bool F32> struct PgFound {
             if (D.line) pg_unit_entity<F32>(D, A, p, &plen, &pfirst, &x0, &x1, &pcr, &pnb);
             else if (!F32) plen = A.plen ? pg_clamp(__ldg(A.plen + p), 0, D.n) : D.n;
         }
-        all = nq;
         nq = min(nq, D.max_new);
         mine = r >= 0 && tok >= first && tok - first < nq;
         dense = !F32 && (D.prompt_own || pg_on_tc((long long)nq * D.g, len));
@@ -674,13 +673,16 @@ template <typename T, int D> cudaError_t join_d(const PgDims &D_, const PgAttn &
     // rows of fp32, 152 pieces a row: the join 20 -> 12 us); many: fewer instructions
     const bool alone = (long long)D_.rows * D_.Hq <= kPgSms * 8;
     const bool few = (long long)D_.rows * D_.Hq < kPgSms * 32;
-    if constexpr (D < 128)
+    auto kern = pg_join_kernel<T, D, 8, 1>;
+    if constexpr (D < 128) {
         if (!few) {
             const long long warps = (long long)D_.rows * ((D_.Hq + 3) / 4);
             return pg_launch(pg_join_many_kernel<T, D>, (unsigned)((warps + 3) / 4), 128, 0, true, st, D_,
                              A);
         }
-    auto kern = few ? pg_join_kernel<T, D, 8, 1> : pg_join_kernel<T, D, 4, 1>;
+    } else {
+        if (!few) kern = pg_join_kernel<T, D, 4, 1>;
+    }
     if (alone) kern = pg_join_kernel<T, D, 8, 4>;
     return pg_launch(kern, dim3(D_.rows, alone ? D_.Hq : (D_.Hq + 3) / 4), 128, 0, true, st, D_, A);
 }
