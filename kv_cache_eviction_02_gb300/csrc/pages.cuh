@@ -232,6 +232,28 @@ __device__ __forceinline__ void pg_unit_entity(const PgDims &D, const PgAttn &A,
     if (!F32 && (own ? pg_on_tc(*rows, *len) : !D.line)) *nb = 0;
 }
 
+// Where a warp stands in the line of chunks.
+template <bool F32> struct PgCursor {
+    int e, len, first, rows, nq;  // entity, its tokens, its first packed row, its query rows per KV head
+    int cr, nb;                   // chunks per unit, row blocks
+    int kh, rb, c;                // KV head, row block, chunk of the unit
+    __device__ __forceinline__ void enter(const PgDims &D, const PgAttn &A, int entity) {
+        e = entity;
+        pg_unit_entity<F32>(D, A, e, &len, &first, &nq, &rows, &cr, &nb);
+        kh = rb = c = 0;
+    }
+    // to the next chunk; only called when there is one
+    __device__ __forceinline__ void next(const PgDims &D, const PgAttn &A) {
+        if (++c < cr) return;
+        c = 0;
+        if (++rb < nb) return;
+        rb = 0;
+        if (++kh < D.Hkv) return;
+        do enter(D, A, e + 1);
+        while ((cr == 0 || nb == 0) && e + 1 < D.S + D.R);
+    }
+};
+
 __device__ __forceinline__ long long pg_div(long long a, long long b) {  // of non-negative numbers
     if (((unsigned long long)(a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
     return a / b;

@@ -64,28 +64,6 @@ __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], u
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Where a warp stands in the line of chunks.
-struct Cursor {
-    int e, len, first, rows, nq;  // entity, its tokens, its first packed row, its query rows per KV head
-    int cr, nb;                   // chunks per unit, row blocks
-    int kh, rb, c;                // KV head, row block, chunk of the unit
-    __device__ __forceinline__ void enter(const PgDims &D, const PgAttn &A, int entity) {
-        e = entity;
-        pg_unit_entity<true>(D, A, e, &len, &first, &nq, &rows, &cr, &nb);
-        kh = rb = c = 0;
-    }
-    // to the next chunk; only called when there is one
-    __device__ __forceinline__ void next(const PgDims &D, const PgAttn &A) {
-        if (++c < cr) return;
-        c = 0;
-        if (++rb < nb) return;
-        rb = 0;
-        if (++kh < D.Hkv) return;
-        do enter(D, A, e + 1);
-        while ((cr == 0 || nb == 0) && e + 1 < D.S + D.R);
-    }
-};
-
 template <int D>
 __global__ void __launch_bounds__(kF3Threads, 1) pg_f32_kernel(PgDims D_, PgAttn A, PgOwn W) {
     constexpr int NS = f3_slots<D>(), SF = f3_item<D>(), NT = kF3NT;
@@ -106,7 +84,7 @@ __global__ void __launch_bounds__(kF3Threads, 1) pg_f32_kernel(PgDims D_, PgAttn
     const long long X0 = w * sh.cpw;
     const int n = (int)min(sh.total - X0, sh.cpw);  // chunks of this warp
     if (n <= 0) return;
-    Cursor cc;
+    PgCursor<true> cc;
     int unit;
     {
         long long x;
@@ -124,7 +102,7 @@ __global__ void __launch_bounds__(kF3Threads, 1) pg_f32_kernel(PgDims D_, PgAttn
         cc.rb = u - cc.kh * cc.nb;
         unit += u;
     }
-    Cursor ca = cc;  // runs ahead: the chunks to load
+    PgCursor<true> ca = cc;  // runs ahead: the chunks to load
 
     float *ring = sm + warp * (NS * SF);
     const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(ring));

@@ -95,29 +95,6 @@ __device__ __forceinline__ uint32_t mm_off(int row, int c) {
     return (uint32_t)((c >> 3) * (kMmTok * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
 }
 
-
-// Where a warp stands in the line of chunks.
-struct Cursor {
-    int e, len, first, rows, nq;  // entity, its tokens, its first packed row, its query rows per KV head
-    int cr, nb;                   // chunks per unit, row blocks
-    int kh, rb, c;                // KV head, row block, chunk of the unit
-    __device__ __forceinline__ void enter(const PgDims &D, const PgAttn &A, int entity) {
-        e = entity;
-        pg_unit_entity<false>(D, A, e, &len, &first, &nq, &rows, &cr, &nb);
-        kh = rb = c = 0;
-    }
-    // to the next chunk; only called when there is one
-    __device__ __forceinline__ void next(const PgDims &D, const PgAttn &A) {
-        if (++c < cr) return;
-        c = 0;
-        if (++rb < nb) return;
-        rb = 0;
-        if (++kh < D.Hkv) return;
-        do enter(D, A, e + 1);
-        while ((cr == 0 || nb == 0) && e + 1 < D.S + D.R);
-    }
-};
-
 // NT: blocks of 8 query rows per unit. RB = 8 NT is the unit's rows. MODE: what a warp takes, its share of the
 // requests' units, of the prompts' and the requests', or all of one request and KV head.
 enum { kOwn, kLine, kDirect };
@@ -152,7 +129,7 @@ __global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
 
     const int w = blockIdx.x * kPgOwnWarps + warp;
     int n = 0, unit = 0;  // chunks of this warp; the index of its first unit
-    Cursor cc;
+    PgCursor<false> cc;
     int prompt = 0, plen = 0, pchunks = 0;  // kDirect: chunks c < pchunks are the prompt's
     if constexpr (DIRECT) {
         __syncthreads();  // the barriers and s_abort are set
@@ -194,7 +171,7 @@ __global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
         }
     }
     if (DIRECT ? cc.rb * RB < cc.rows : n > 0) {
-        Cursor ca = cc;  // runs ahead: the addresses of the chunks to load
+        PgCursor<false> ca = cc;  // runs ahead: the addresses of the chunks to load
 
         uint8_t *ring = smem + warp * NST * SB;
         uint64_t *bar = bars[warp];
