@@ -147,3 +147,16 @@ def test_rows_of_a_refused_request_in_front_of_the_others(n, want):
     assert got == want
     c.check(set(range(pad + mine, c.rows)))
     assert (f64(out)[:pad + mine] == 3.0).all() and (f64(lse)[:pad + mine] == 5.0).all()
+
+
+@pytest.mark.parametrize("case,want", [
+    (("bf16", 2, 3, 8, 2, 64, 9000, 8, 6, 2), BESIDE), (("bf16", 2, 5, 28, 4, 64, 270, 16, 300, 3), SPLIT),
+    (("bf16", 1, 9, 7, 1, 128, 400, 32, 300, 9), SPLIT_TC), (("bf16", 1, 9, 7, 1, 128, 129, 32, 300, 9), LINE_TC),
+    (("bf16", 1, 33, 4, 4, 64, 5, 4, 9, 1), DIRECT), (("f32", 2, 5, 10, 2, 64, 300, 8, 70, 3), LINE),
+], ids=lambda x: ids(x) if isinstance(x, tuple) else "")
+def test_large_values(case, want):
+    """V up to about 2^88: sums of unnormalised weights (2^8 at most) times V stay finite."""
+    c = Case(*case, seed=76, ragged=True)
+    c.Vp, c.V = c.Vp * 2.0 ** 86, c.V * 2.0 ** 86
+    out, _ = check(c, want)
+    assert torch.isfinite(out[:c.rows]).all() and out[:c.rows].abs().max() > 2.0 ** 80
