@@ -322,8 +322,8 @@ void cc_cache_destroy(KveCcCache *c);
 /* Decoding several requests behind one cached prompt: the M lookahead trajectories of LORE-KV
  * (project page, Method, Monte Carlo lookahead, Eq. 1: every trajectory continues the same prompt)
  * and the answers decoded from one compressed cache (Eq. 8). The prompt's K/V are read where they
- * are (the arrays of lorekv_score, or the compacted K_out/V_out of lorekv_select_compact), once for
- * all requests behind them; the rows that a request adds lie in pages of its own.
+ * are (the arrays of lorekv_score, or the compacted K_out/V_out of lorekv_select_compact), for all
+ * requests behind them together; the rows that a request adds lie in pages of its own.
  *
  * n_prompts prompts are each continued by `fan` requests; request r (0 <= r < n_prompts * fan)
  * continues prompt r / fan. A request that has nothing to do in a step adds 0 rows, so prompts with
@@ -333,6 +333,11 @@ void cc_cache_destroy(KveCcCache *c);
  *   page_size  rows per page: a power of two, 1 to 256
  *   n_pages    pages in the pool; max_pages: entries per request in the block table
  *   max_new    the most rows a request adds in one step
+ * Lengths are known on the device only, so the kernels of an attention call, their splits and the
+ * workspace go by these sizes: n_prefix, n_rows, max_new and max_pages * page_size near what the steps
+ * need give the shorter call (lookahead steps take fewer launches with tables of at most 32 rows, and
+ * prompts far shorter than n_prefix leave most of the GPU idle with 16-bit types). K_prefix and V_prefix
+ * may hold more rows than n_prefix.
  *   dtype      KVE_F32, KVE_BF16 or KVE_F16: queries, K, V and outputs
  * d_head is 32, 64 or 128; query head h reads KV head h / (n_q_heads/n_kv_heads), at most 128 query
  * heads per KV head. n_prompts * fan at most 16384; n_rows, n_pages * page_size, max_pages *
@@ -389,11 +394,17 @@ size_t pg_workspace_size(const KvePgShape *shape);
  * (stored before by pg_append) included. Row i of request r, query head h:
  *   out = sum_j a_j v_j, a = softmax_j(q.k_j / sqrt(d_head)) over the first prefix_len[r / fan] rows
  *   of the prompt and the own rows 0 .. len[r] - (q_start[r + 1] - q_start[r]) + i of the request.
- * Every prompt's K/V are read once for all its rows. Nothing to see: out 0 and lse -inf. Rows with
+ * How often a prompt's K/V are read goes by its query rows (new rows of its requests times query heads
+ * per KV head): 16-bit types once for every 128 or 256 of them, or, where there is little to do, for
+ * every 8 or 16 or once per request; fp32 once for every 16.
+ * Scores, maxima, sums and results before the last rounding are fp32. 16-bit types round each
+ * unnormalised softmax weight to the type before it meets V (half a step of the type, as V's own
+ * entries; their sum takes them unrounded); fp32 products are sums of three tf32 products, off by up
+ * to 2^-21 of each. Nothing to see: out 0 and lse -inf. Rows with
  * row_req < 0, whose row_req is not the request that q_start gives, or behind a request's first
  * max_new rows are left as they were.
  *   q        [n_rows][n_q_heads][d_head], q_row_stride elements from one row to the next
- *   K_prefix, V_prefix [n_prompts][n_kv_heads][n_prefix][d_head] with the strides (elements) of
+ *   K_prefix, V_prefix [n_prompts][n_kv_heads][>= n_prefix][d_head] with the strides (elements) of
  *            prompt, head and row given: a layer's slice of a larger cache, or rows of several
  *            heads, are read in place
  *   prefix_len [n_prompts] int32 or NULL (every prompt has n_prefix rows)
@@ -402,7 +413,9 @@ size_t pg_workspace_size(const KvePgShape *shape);
  *            log-sum-exp of the scores
  * Addresses and strides of q, K, V and out are multiples of 16 bytes, the workspace is 256-byte
  * aligned. K/V rows that no row of the request can see (behind prefix_len, behind len, in other
- * pages) may hold anything, infinities and NaN included; rows that one of them sees are finite.
+ * pages) may hold anything, infinities and NaN included; rows that one of them sees are finite, and
+ * they, q and the scores q.k are below 2^89 in magnitude (sums of weights times V are held before they
+ * are normalised).
  * Page ids outside the pool are read as page 0 and reported by kve_check_device as KVE_EINVAL.
  * Results do not depend on the order in which blocks run. Calls that overlap on the GPU need a
  * workspace each. */

@@ -7,12 +7,13 @@ namespace kve {
 // How an attention call is split.
 //   Prompt, 16-bit types (one CTA per SM): the split count that minimises
 //     ceil(items * splits / 152) * (tiles per split + 4): a CTA's set-up and the partial result that
-//     it writes and the join reads cost about four tiles. A short prompt leaves SMs over; the own
-//     rows' kernel then runs on those beside it (with blocks for all SMs, the last of its equal shares
-//     would begin when the prompt's kernel has ended: 51 instead of 41 us for 64 answers behind 164
-//     rows). Holding a long prompt's kernel back to a share of the SMs so that both end together was
-//     no faster than one after the other (256 requests behind 8K rows: 139 and 137 us): own rows need
-//     all SMs' buffers in flight to reach the HBM rate.
+//     it writes and the join reads cost about four tiles. One number for all prompts, from n_prefix: of
+//     prompts much shorter than that, the CTAs of splits behind their end return at once, and a long one
+//     among many short ones keeps its few splits (lengths are known on the device only). A short prompt
+//     leaves SMs over; the own rows' kernel then runs on those beside it (with blocks for all SMs, the last
+//     of its equal shares would begin when the prompt's kernel has ended: figures at kPgShare). Holding a
+//     long prompt's kernel back to a share of the SMs so that both end together was no faster than one
+//     after the other: own rows need all SMs' buffers in flight to reach the HBM rate.
 //   Own rows of requests with many new rows: the same by the table's width, since lengths are known on
 //     the device only (the CTAs of splits that a request does not reach return at once).
 //   Other own rows, and all of fp32: dealt out on the device (pages_own.cu, pages_f32.cu).

@@ -29,7 +29,14 @@ struct PgDims {
 };
 
 constexpr int kPgSms = 152;    // GB300
-constexpr int kPgShare = 100;  // most SMs the prompt's kernel takes beside the own rows' one
+// A prompt kernel of fewer CTAs than this has its SMs left out of the own rows' grid (pg_split). Grid over the SMs
+// left, and over all, us (32/8 heads of d 128, bf16; prompt CTAs in brackets): 64 requests of up to 1023 own rows
+// behind 164 rows 36.1 and 43.0 [16], behind 512 36.4 and 42.9 [32], behind 1000 39.6 and 44.5 [64]; 64 of up to
+// 255 behind 1000 20.6 and 22.6 [64]; but 256 of up to 1023 behind 164 105 and 107 [64], behind 300 129 and 109
+// [96], 2 x 213 behind 10 rows (40/8 heads) 177 and 168 [80]: with own rows for much longer than the prompt the SMs
+// left out are missed. Few requests (16) and other prompts: within 5 % of one another. (A rule by the two
+// kernels' times instead of one number would take both.)
+constexpr int kPgShare = 100;
 
 // Units of 8 or 16 query rows (fp32: 16), chunks of 16 tokens, dealt out to the warps of pages_own.cu
 // (16-bit types) or pages_f32.cu.
@@ -69,7 +76,12 @@ inline int pg_tc_blocks(const PgDims &D, bool own) {
 // A request with more query rows per KV head than kPgFewRows (the warps of pages_own.cu would read its K/V
 // more than twice) and more than kPgFewScores scores has its own rows done on tcgen05, where a CTA costs
 // several microseconds whatever it does; the others go to pages_own.cu. The choice is made per request on
-// the device, so a batch of both runs both kernels.
+// the device, so a batch of both runs both kernels. On tcgen05, and by warps, us, of whole calls behind 1000 rows
+// (bf16, up to `new` new rows): 32/8 heads of d 128, 64 requests: new 16 and 256 own rows (17K scores at
+// most) 69 and 58, 32 and 64 (12K) 72 and 69, 32 and 256 (37K) 89 and 92, 64 and 64 (33K) 118 and 130, 64 and 512
+// (147K) 152 and 223; 40/8 of d 64: 9 and 256 (12K) 45 and 40, 16 and 128 (12K) 46 and 47, 32 and 64 (15K)
+// 66 and 72, 32 and 512 (87K) 93 and 131. Eight requests alone are better off with warps until about 40K scores
+// (32/8 heads, 9 and 512: 28 and 19; 32 and 128: 25 and 25; 64 and 512: 36 and 45).
 constexpr int kPgFewRows = 32, kPgFewScores = 12288;
 __host__ __device__ inline bool pg_on_tc(long long rows, int len) {
     return rows > kPgFewRows && rows * len > kPgFewScores;
@@ -91,7 +103,10 @@ __host__ __device__ inline int pg_unit_rows(const PgDims &D) {
 // call has one launch less and no tcgen05 kernel, which costs several microseconds whatever it does (a step of
 // 4 requests behind 11 rows 12.0 -> 8.7 us); not with long own rows, where the prompt's kernel
 // hides behind them (172 requests of up to 268 own rows, 23K chunks: 26.7 us, in one line 24.6; 64 of up to
-// 1875, 60K: 54 and 59).
+// 1875, 60K: 54 and 59). The prompt's kernel, and one line, by the prompt's rows (32/8 heads of d 128, up to 60 own
+// rows): 4 requests 128 rows 8.8 and 7.5, 256 9.0 and 8.3, 400 9.6 and 9.5, 700 9.9 and 11.5; 64 requests 128
+// 15.9 and 13.0, 256 15.9 and 15.1, 400 16.3 and 18.6. By the prompts' chunks (250 rows, 8 requests each): 512 11.1
+// and 9.5, 2048 13.4 and 13.1, 4096 19.1 and 16.9, 8192 25.5 and 27.5.
 inline bool pg_short_prompts(const PgDims &D) {
     const int rb = pg_unit_rows(D);
     auto chunks = [&](long long of, long long rows, int tokens) {  // at most

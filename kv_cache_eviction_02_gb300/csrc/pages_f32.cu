@@ -14,7 +14,8 @@
 // query rows on the narrow one. The tensor cores' own sums are kept short: the scores in three
 // accumulators, O of each chunk in fresh ones that are then added to the running O in fp32. A
 // lookahead step over 32K rows (8 KV heads of d 128, 268 MB) takes 58 us, 4.6 TB/s: bound by the
-// instructions of 8 warps per SM and their latencies, 1.5 times the time of its bytes (FFMA with a lane per
+// instructions of 8 warps per SM and their latencies, 1.5 times the time of its bytes (d 128: 255 registers
+// and 114 bytes of spills a thread, 64 and 32 none. FFMA with a lane per
 // D/32 columns 143 us; 6 warps with whole chunks in the ring and 4-byte fragment loads 88).
 // Everything else is fp32; the factor log2 e / sqrt d is carried as two floats, since its rounding would
 // shift every score the same way.

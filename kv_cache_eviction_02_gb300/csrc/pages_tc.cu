@@ -352,7 +352,7 @@ __device__ __forceinline__ void pt_softmax(const PtArgs &A, const PtBars<D, QT> 
             tc::fence_proxy_async_smem();
         }
         // weights of a half from its scores: p = 2^(s k1 - m), rounded to the type of V (half a step,
-        // like V's own entries); their sum takes p before the rounding
+        // like V's own entries; ex2.approx is off by 2^-22 of p); their sum takes p before the rounding
         float pk[32], l0, l1;
         auto half_weights = [&](const float (&x)[32], const float (&y)[32]) {
             const uint64_t k1_2 = tc::pk2(A.k1, A.k1), negm_2 = tc::pk2(-m, -m);
