@@ -158,3 +158,62 @@ def test_arrays_beyond_32_bit_offsets(case):
         assert torch.equal(pool[slot.long() // page, :, slot.long() % page], small)
     del K, V, wide, rows, c, K_new, pool
     torch.cuda.empty_cache()
+
+
+TWO = [[("bf16", 1, 8, 8, 2, 128, 2000, 16, 300, 1), ("bf16", 2, 3, 8, 2, 128, 700, 16, 100, 20)],
+       [("f32", 1, 8, 8, 2, 64, 900, 16, 300, 1), ("f16", 2, 9, 8, 2, 64, 20, 16, 15, 1)]]
+
+
+@pytest.mark.parametrize("pair", TWO, ids=["bf16", "mixed"])
+def test_two_branches_of_one_graph(pair):
+    """Attention of two batches on forked streams of one captured step, each with its own workspace."""
+    cs = [Case(*c, seed=81 + i) for i, c in enumerate(pair)]
+    want = [c.run()[0] for c in cs]
+    args = [c.args() for c in cs]
+    outs = [torch.full_like(w, 3.0) for w in want]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cur = torch.cuda.current_stream()
+        side = [torch.cuda.Stream() for _ in cs]
+        for _ in range(3):
+            for c, a, o, s in zip(cs, args, outs, side):
+                s.wait_stream(cur)
+                with torch.cuda.stream(s):
+                    api.pg_attention(c.pb, c.q, c.Kp, c.Vp, c.plen, *a, o, None, c.ws)
+        for s in side:
+            cur.wait_stream(s)
+    for _ in range(5):
+        for o in outs:
+            o.fill_(3.0)
+        g.replay()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    api.kve_check_device()
+
+
+@pytest.mark.parametrize("pair", TWO, ids=["bf16", "mixed"])
+def test_attention_from_two_threads(pair):
+    cs = [Case(*c, seed=83 + i) for i, c in enumerate(pair)]
+    want = [c.run()[0] for c in cs]
+    args = [c.args() for c in cs]
+    outs = [[torch.full_like(w, 3.0) for _ in range(8)] for w in want]
+    faults = []
+    torch.cuda.synchronize()
+
+    def calls(c, a, o):
+        try:
+            s = torch.cuda.Stream()
+            for k in range(400):
+                api.pg_attention(c.pb, c.q, c.Kp, c.Vp, c.plen, *a, o[k % 8], None, c.ws, stream=s)
+            s.synchronize()
+        except Exception as e:
+            faults.append(e)
+
+    threads = [threading.Thread(target=calls, args=x) for x in zip(cs, args, outs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    api.kve_check_device()
+    assert not faults
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, x) for x in o)
