@@ -81,7 +81,9 @@ inline int pg_tc_blocks(const PgDims &D, bool own) {
 // most) 69 and 58, 32 and 64 (12K) 72 and 69, 32 and 256 (37K) 89 and 92, 64 and 64 (33K) 118 and 130, 64 and 512
 // (147K) 152 and 223; 40/8 of d 64: 9 and 256 (12K) 45 and 40, 16 and 128 (12K) 46 and 47, 32 and 64 (15K)
 // 66 and 72, 32 and 512 (87K) 93 and 131. Eight requests alone are better off with warps until about 40K scores
-// (32/8 heads, 9 and 512: 28 and 19; 32 and 128: 25 and 25; 64 and 512: 36 and 45).
+// (32/8 heads, 9 and 512: 28 and 19; 32 and 128: 25 and 25; 64 and 512: 36 and 45). With at most 32 query rows
+// tcgen05 is never ahead (64 requests of up to 8 new rows, 32/8 heads: 1024 own rows 104 and 95, 4096 278 and 278;
+// of 4, 8/1 heads: 4096 own rows 67 and 48); with 64 it is (8 new rows, 8/1 heads, 4096: 71 and 82).
 constexpr int kPgFewRows = 32, kPgFewScores = 12288;
 __host__ __device__ inline bool pg_on_tc(long long rows, int len) {
     return rows > kPgFewRows && rows * len > kPgFewScores;
