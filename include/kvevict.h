@@ -427,6 +427,76 @@ int pg_attention(const KvePgShape *shape, const void *q, long long q_row_stride,
                  const int32_t *row_req, void *out, float *lse_out, void *workspace,
                  size_t ws_bytes, void *stream);
 
+/* ---- cache in 4 bits --------------------------------------------------------------------------- */
+
+/* Prompts and pages of shared-prompt decoding held in 4 bits: the compressed cache of an eviction, or any
+ * prompt, quantised as a whole; rows quantised as they are written into pages; both read back (for
+ * the next eviction pass over them); and the attention over them. Shapes, steps and page plans are those of
+ * shared-prompt decoding (KvePgShape, pg_plan); page_size is 16 or more.
+ *
+ * What is held: a row of a KV head in groups of `group` (32, 64 or 128, at most d_head) neighbouring channels, each as
+ * whole numbers m and a step s, for the values s m. With lo = min(0, least value) and hi = max(0, largest):
+ *   s is the smallest number of four significant bits, 2^-126 at least, with 15 s >= hi - lo;
+ *   M = floor(F / s), F the largest finite number of shape->dtype; k = min(M, -lo / s to the nearest);
+ *   m = x / s to the nearest, no less than -k and no more than min(15 - k, M),
+ * what lies halfway going toward zero. s m is exact in bf16, and in fp16 off by at most 2^-25. A group that
+ * holds an infinity or a NaN stands for NaN. No value is further than s / 2 away (but for the limit M next to F), and
+ * s is at most 0.075 (hi - lo).
+ *
+ * The arrays are opaque bytes on the device, 16-byte aligned: K and V of a KV head's 16 tokens in one block of 16
+ * d_head + 64 d_head / group bytes.
+ *   prefix  [n_prompts][n_kv_heads][ceil(n_prefix / 16)] such blocks, q4_prefix_size() bytes
+ *   pages   [n_pages][n_kv_heads][page_size / 16], q4_pages_size() bytes
+ * Both are independent of shape->dtype but for F: an array written from one type may be read as another. They need no
+ * initial values. */
+
+/* Bytes of the arrays; 0 on invalid input, and for q4_prefix_size without a prompt. */
+size_t q4_prefix_size(const KvePgShape *shape, int group);
+size_t q4_pages_size(const KvePgShape *shape, int group);
+
+/* Quantises prompts: rows 0 .. prefix_len[p] - 1 of each (NULL: n_prefix rows).
+ *   K, V [n_prompts][n_kv_heads][>= n_prefix][d_head] with the strides (elements) of prompt, head and row given, e.g.
+ *        the compacted K_out, V_out of lorekv_select_compact; addresses and strides multiples of 16 bytes
+ * Blocks behind a prompt's last row are left as they were. */
+int q4_pack(const KvePgShape *shape, int group, const void *K, const void *V, long long prompt_stride,
+            long long head_stride, long long row_stride, const int32_t *prefix_len, void *prefix,
+            void *stream);
+
+/* Quantises a step's new rows into the pages that slot_map names; arguments and refusals as in pg_append. The other
+ * rows of a page stay as they are, byte for byte. */
+int q4_append(const KvePgShape *shape, int group, const void *K_new, const void *V_new,
+              long long K_row_stride, long long V_row_stride, const int32_t *slot_map, void *pages,
+              void *stream);
+
+/* Reads back: the values s m, rounded to shape->dtype.
+ *   cache, block_table, len: prefix, NULL and prefix_len (or NULL: n_prefix rows each); or pages, block_table
+ *            [n_prompts * fan][max_pages] and len [n_prompts * fan]
+ *   K_out, V_out [n_prompts, or n_prompts * fan][n_kv_heads][n_out][d_head] with the strides (elements) of prompt or
+ *            request, head and row given; addresses and strides multiples of 16 bytes
+ * Of each prompt or request the first min(len, n_out) rows (n_out at most n_prefix, or max_pages * page_size)
+ * are written; rows behind them are left as they were. Page ids outside the pool are read as page 0 and
+ * reported by kve_check_device as KVE_EINVAL. */
+int q4_unpack(const KvePgShape *shape, int group, const void *cache, const int32_t *block_table,
+              const int32_t *len, int n_out, void *K_out, void *V_out, long long outer_stride,
+              long long head_stride, long long row_stride, void *stream);
+
+/* Bytes of workspace q4_attention() needs. 0 on invalid input. */
+size_t q4_workspace_size(const KvePgShape *shape, int group);
+
+/* pg_attention with K and V held in 4 bits: the same rows see the same rows, with prefix for K_prefix and V_prefix and
+ * pages for K_pages and V_pages (prefix may be NULL where n_prefix is 0). Scores, maxima, sums and results
+ * before the last rounding are fp32. Products with the codes are exact but for these roundings: 16-bit queries are
+ * off by at most 2^-32 of their row's largest entry (fp32 ones by 2^-22 of themselves), sums of q that go with zero
+ * codes by 2^-22 (fp32: 2^-33); 16-bit types round each unnormalised weight times its step once to 16 bits
+ * before it meets V's codes (half a step; fp32: 2^-22). Weights times steps below 2^-31 of the largest are lost.
+ * Requirements as in pg_attention; q and steps are below 2^89 and the scores q.k too. A NaN that a row sees in K makes
+ * its output NaN, one in V the channels of its group. */
+int q4_attention(const KvePgShape *shape, int group, const void *q, long long q_row_stride,
+                 const void *prefix, const int32_t *prefix_len, const void *pages,
+                 const int32_t *block_table, const int32_t *len, const int32_t *q_start,
+                 const int32_t *row_req, void *out, float *lse_out, void *workspace, size_t ws_bytes,
+                 void *stream);
+
 /* ---- diagnostics ---------------------------------------------------------------------------- */
 
 /* Message of the last failing call on this thread ("" if none). Valid until the next call. */
@@ -434,8 +504,8 @@ const char *kve_last_error(void);
 
 /* Synchronises `stream`, then reads and clears the device error word that bounded on-device
  * waits and device-side index checks set. Returns KVE_OK, KVE_ETIMEOUT (a wait gave up),
- * KVE_EINVAL (cc_surprise met a token id outside [0, vocab), or pg_append or pg_attention a slot or
- * page id outside the pool) or KVE_ECUDA. */
+ * KVE_EINVAL (cc_surprise met a token id outside [0, vocab), or pg_append, pg_attention, q4_append, q4_unpack
+ * or q4_attention a slot or page id outside the pool) or KVE_ECUDA. */
 int kve_check_device(void *stream);
 
 /* Self-test of the bounded on-device waits: launches one CTA whose thread waits, through the same

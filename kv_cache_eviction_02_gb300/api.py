@@ -32,7 +32,9 @@ EXPORTED = ("lorekv_prepare_wo", "lorekv_workspace_size", "lorekv_score",
             "cc_workspace_size", "cc_surprise", "cc_select_compact", "cc_cache_create",
             "cc_cache_append", "cc_cache_refresh", "cc_cache_step", "cc_cache_export",
             "cc_cache_length", "cc_cache_seen", "cc_cache_destroy",
-            "pg_plan", "pg_append", "pg_workspace_size", "pg_attention")
+            "pg_plan", "pg_append", "pg_workspace_size", "pg_attention",
+            "q4_prefix_size", "q4_pages_size", "q4_pack", "q4_append", "q4_unpack", "q4_workspace_size",
+            "q4_attention")
 
 
 class KveError(RuntimeError):
@@ -120,6 +122,12 @@ def lib():
         L.pg_workspace_size.argtypes = [GS]
         L.pg_workspace_size.restype = Z
         L.pg_attention.argtypes = [GS, P, LL, P, P, LL, LL, LL, P, P, P, P, P, P, P, P, P, P, Z, P]
+        for f in (L.q4_prefix_size, L.q4_pages_size, L.q4_workspace_size):
+            f.argtypes, f.restype = [GS, I], Z
+        L.q4_pack.argtypes = [GS, I, P, P, LL, LL, LL, P, P, P]
+        L.q4_append.argtypes = [GS, I, P, P, LL, LL, P, P, P]
+        L.q4_unpack.argtypes = [GS, I, P, P, P, I, P, P, LL, LL, LL, P]
+        L.q4_attention.argtypes = [GS, I, P, LL, P, P, P, P, P, P, P, P, P, P, Z, P]
         _lib = L
     return _lib
 
@@ -496,7 +504,7 @@ class _NoBinding:
     def plan(*_):
         return _OTHER
 
-    append = attention = plan
+    append = attention = q4_pack = q4_append = q4_unpack = q4_attention = plan
 
 
 def _bind():
@@ -512,6 +520,8 @@ def _bind():
         return _native
     _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                     for f in (L.pg_plan, L.pg_append, L.pg_attention)))
+    _binding.bind_q4(*(ctypes.cast(f, ctypes.c_void_p).value
+                       for f in (L.q4_pack, L.q4_append, L.q4_unpack, L.q4_attention)))
     _native = _binding
     return _native
 
@@ -705,6 +715,181 @@ class PgCache:
         pg_attention(self.pb, q, K_prefix, V_prefix, prefix_len, self.K_pages[layer],
                      self.V_pages[layer], self.block_table, self.lens, self.q_start, self.row_req,
                      out, lse_out, self.workspace, stream)
+
+
+# ---- cache in 4 bits ---------------------------------------------------------------------------------
+@dataclass(frozen=True)
+class Q4Problem(PgProblem):
+    """A PgProblem whose prompts and pages are held in 4 bits, in groups of `group` channels (32, 64 or 128, at
+    most d_head). page_size is 16 or more; pg_plan takes it as it is."""
+    group: int = 32
+
+    @functools.cached_property
+    def prefix_bytes(self) -> int:
+        """Bytes of the prompts' array."""
+        return int(lib().q4_prefix_size(self.c_shape, self.group))
+
+    @functools.cached_property
+    def pool_bytes(self) -> int:
+        """Bytes of the pages."""
+        return int(lib().q4_pages_size(self.c_shape, self.group))
+
+
+def _q4_rows(t, name, pb, count, rows, dev):
+    """Address and (outer, head, row) strides of rows [count][n_kv_heads][>= rows][d_head]."""
+    if t is None or t.__class__ is int or t.dim() != 4:
+        return (_pg(t, name, pb.torch_dtype, count * pb.n_kv_heads * rows * pb.d_head, dev),
+                pb.n_kv_heads * rows * pb.d_head, rows * pb.d_head, pb.d_head)
+    S, H, n, d = t.shape
+    if S != count or H != pb.n_kv_heads or n < rows or d != pb.d_head:
+        raise ValueError(f"{name}: {tuple(t.shape)} elements, the shape needs "
+                         f"{(count, pb.n_kv_heads, rows, pb.d_head)}")
+    if t.dtype is not pb.torch_dtype or t.get_device() != dev:
+        _pg_refuse(t, name, pb.torch_dtype, 0, dev)
+    s0, s1, s2, s3 = t.stride()
+    if d > 1 and s3 != 1:
+        raise ValueError(f"{name}: a head's row must be contiguous")
+    return t.data_ptr(), s0, s1, s2
+
+
+def q4_pack(pb: Q4Problem, K, V, prefix_len, prefix, stream=None):
+    """Quantises prompts K, V [n_prompts][n_kv_heads][>= n_prefix][d_head] (a layer's slice of a larger cache, or
+    what lorekv_select_compact leaves; the same strides for both) into prefix (uint8, pb.prefix_bytes). prefix_len
+    int32 [n_prompts] may be None: n_prefix rows each."""
+    dev, st = _pg_launch(stream)
+    status = (_native or _bind()).q4_pack(pb.c_address, dev, st, pb.group, K, V, prefix_len, prefix)
+    if status != _OTHER:
+        return _check(status)
+    k, *ks = _q4_rows(K, "K", pb, pb.n_prompts, pb.n_prefix, dev)
+    v, *vs = _q4_rows(V, "V", pb, pb.n_prompts, pb.n_prefix, dev)
+    if ks != vs:
+        raise ValueError("V: the strides differ from K's")
+    _check(lib().q4_pack(pb.c_shape, pb.group, k, v, *ks,
+                         _pg(prefix_len, "prefix_len", torch.int32, pb.n_prompts, dev),
+                         _pg(prefix, "prefix", torch.uint8, pb.prefix_bytes, dev), st))
+
+
+def q4_append(pb: Q4Problem, K_new, V_new, slot_map, pages, stream=None):
+    """Quantises a step's K/V rows [n_rows][n_kv_heads][d_head] into the pages (uint8, pb.pool_bytes) that slot_map
+    names. The rows may be slices of a wider projection's output."""
+    dev, st = _pg_launch(stream)
+    status = (_native or _bind()).q4_append(pb.c_address, dev, st, pb.group, K_new, V_new, slot_map, pages)
+    if status != _OTHER:
+        return _check(status)
+    dt, n = pb.torch_dtype, pb.n_rows
+    k, kr = _pg_rows(K_new, "K_new", dt, n, pb.n_kv_heads, pb.d_head, dev)
+    v, vr = _pg_rows(V_new, "V_new", dt, n, pb.n_kv_heads, pb.d_head, dev)
+    _check(lib().q4_append(pb.c_shape, pb.group, k, v, kr, vr,
+                           _pg(slot_map, "slot_map", torch.int32, n, dev),
+                           _pg(pages, "pages", torch.uint8, pb.pool_bytes, dev), st))
+
+
+def q4_unpack(pb: Q4Problem, cache, block_table, lens, K_out, V_out, stream=None):
+    """Reads back prompts (cache: prefix, block_table None, lens prefix_len or None) or the requests' own rows
+    (cache: pages, with block_table and lens) into K_out, V_out [n_prompts or requests][n_kv_heads][n_out][d_head]
+    (the same strides for both): the first n_out rows of each, as far as it has them, n_out being at most n_prefix
+    or max_pages * page_size. Rows behind them are left as they were."""
+    dev, st = _pg_launch(stream)
+    status = (_native or _bind()).q4_unpack(pb.c_address, dev, st, pb.group, cache, block_table, lens, K_out,
+                                            V_out)
+    if status != _OTHER:
+        return _check(status)
+    paged = block_table is not None
+    count, most = (pb.requests, pb.max_pages * pb.page_size) if paged else (pb.n_prompts, pb.n_prefix)
+    if K_out is not None and K_out.__class__ is not int and K_out.dim() == 4:
+        most = min(most, K_out.shape[2])
+    k, *ks = _q4_rows(K_out, "K_out", pb, count, most, dev)
+    v, *vs = _q4_rows(V_out, "V_out", pb, count, most, dev)
+    if ks != vs:
+        raise ValueError("V_out: the strides differ from K_out's")
+    _check(lib().q4_unpack(
+        pb.c_shape, pb.group, _pg(cache, "cache", torch.uint8, pb.pool_bytes if paged else pb.prefix_bytes, dev),
+        _pg(block_table, "block_table", torch.int32, count * pb.max_pages, dev),
+        _pg(lens, "lens", torch.int32, count, dev), most, k, v, *ks, st))
+
+
+def q4_workspace_size(pb: Q4Problem) -> int:
+    return int(lib().q4_workspace_size(pb.c_shape, pb.group))
+
+
+def q4_attention(pb: Q4Problem, q, prefix, prefix_len, pages, block_table, lens, q_start, row_req, out, lse_out,
+                 workspace, stream=None):
+    """pg_attention over prompts and pages held in 4 bits. prefix may be None without prompts, prefix_len and
+    lse_out may be None."""
+    dev, st = _pg_launch(stream)
+    status = (_native or _bind()).q4_attention(pb.c_address, dev, st, pb.group, q, prefix, prefix_len, pages,
+                                               block_table, lens, q_start, row_req, out, lse_out, workspace)
+    if status != _OTHER:
+        return _check(status)
+    dt, R, n, i32 = pb.torch_dtype, pb.requests, pb.n_rows, torch.int32
+    qp, qr = _pg_rows(q, "q", dt, n, pb.n_q_heads, pb.d_head, dev)
+    heads = n * pb.n_q_heads
+    args = (_pg(prefix, "prefix", torch.uint8, pb.prefix_bytes, dev),
+            _pg(prefix_len, "prefix_len", i32, pb.n_prompts, dev),
+            _pg(pages, "pages", torch.uint8, pb.pool_bytes, dev),
+            _pg(block_table, "block_table", i32, R * pb.max_pages, dev),
+            _pg(lens, "lens", i32, R, dev), _pg(q_start, "q_start", i32, R + 1, dev),
+            _pg(row_req, "row_req", i32, n, dev), _pg(out, "out", dt, heads * pb.d_head, dev),
+            _pg(lse_out, "lse_out", torch.float32, heads, dev))
+    ws = ws_bytes = None
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            _pg_refuse(workspace, "workspace", workspace.dtype, 0, dev)
+    _check(lib().q4_attention(pb.c_shape, pb.group, qp, qr, *args, ws, ws_bytes or 0, st))
+
+
+class Q4Cache:
+    """What PgCache is, with the prompts and the pages of n_layers layers held in 4 bits: ``pack`` quantises a layer's
+    prompts (once, or again after another eviction), a step is ``plan`` once, then per layer ``append`` and
+    ``attend``; ``unpack`` reads a layer's own rows or, with prompts=True, its prompts back. Every call only enqueues
+    work, so a step can be captured into a CUDA graph and replayed."""
+
+    def __init__(self, pb: Q4Problem, n_layers: int = 1, device="cuda"):
+        size = q4_workspace_size(pb)
+        if size == 0:
+            raise KveError(KVE_EINVAL, "Q4Cache: invalid shape")
+        dev, i32 = torch.device(device), torch.int32
+        R = pb.requests
+        self.pb = pb
+        self.prefix = torch.zeros(n_layers, pb.prefix_bytes, dtype=torch.uint8, device=dev)
+        self.pages = torch.zeros(n_layers, pb.pool_bytes, dtype=torch.uint8, device=dev)
+        self.prefix_len = None  # int32 [n_prompts], set by pack
+        self.block_table = torch.full((R, pb.max_pages), -1, dtype=i32, device=dev)
+        self.free_pages = torch.arange(pb.n_pages, dtype=i32, device=dev)
+        self.pool = torch.tensor([0, pb.n_pages, 0, 0], dtype=i32, device=dev)
+        self.lens = torch.zeros(R, dtype=i32, device=dev)
+        self.q_start = torch.zeros(R + 1, dtype=i32, device=dev)
+        self.row_req = torch.full((pb.n_rows,), -1, dtype=i32, device=dev)
+        self.row_pos = torch.full_like(self.row_req, -1)
+        self.slot_map = torch.full_like(self.row_req, -1)
+        self.workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+
+    def pack(self, layer, K, V, prefix_len=None, stream=None):
+        """Quantises the prompts of a layer. prefix_len (int32 [n_prompts], kept, not copied) holds for all
+        layers."""
+        q4_pack(self.pb, K, V, prefix_len, self.prefix[layer], stream)
+        self.prefix_len = prefix_len
+
+    def plan(self, new_len, stream=None):
+        """Takes (or returns) pages for a step in which request r adds new_len[r] rows (int32)."""
+        pg_plan(self.pb, new_len, self.lens, self.pool, self.free_pages, self.block_table,
+                self.lens, self.pool, self.q_start, self.row_req, self.row_pos, self.slot_map,
+                stream)
+
+    def append(self, layer, K_new, V_new, stream=None):
+        q4_append(self.pb, K_new, V_new, self.slot_map, self.pages[layer], stream)
+
+    def attend(self, layer, q, out, lse_out=None, stream=None):
+        q4_attention(self.pb, q, self.prefix[layer] if self.pb.n_prefix else None, self.prefix_len,
+                     self.pages[layer], self.block_table, self.lens, self.q_start, self.row_req, out, lse_out,
+                     self.workspace, stream)
+
+    def unpack(self, layer, K_out, V_out, prompts=False, stream=None):
+        if prompts:
+            q4_unpack(self.pb, self.prefix[layer], None, self.prefix_len, K_out, V_out, stream)
+        else:
+            q4_unpack(self.pb, self.pages[layer], self.block_table, self.lens, K_out, V_out, stream)
 
 
 def kve_check_device(stream=None):

@@ -9,7 +9,7 @@
 #include <string>
 #include <vector>
 
-#include "pages.cuh"
+#include "q4.cuh"
 
 namespace kve {
 
@@ -372,8 +372,8 @@ int kve_check_device(void *stream) {
                         word);
         if (word & KVE_DEVERR_BADPAGE)
             return fail(KVE_EINVAL,
-                        "a slot or page id outside the pool reached pg_append or pg_attention "
-                        "(error word 0x%x)",
+                        "a slot or page id outside the pool reached pg_append or pg_attention, or a call on a "
+                        "cache in 4 bits (error word 0x%x)",
                         word);
         return fail(KVE_ECUDA, "device error word 0x%x", word);
     }
@@ -975,6 +975,18 @@ static int pg_common(const char *fn, const KvePgShape *shape, PgDims *D) {
     return KVE_OK;
 }
 
+// where a call's partial results lie in its workspace
+static void pg_workspace(const PgWorkspace &W, void *workspace, PgAttn *A) {
+    char *ws = static_cast<char *>(workspace);
+    A->part_ml = reinterpret_cast<float2 *>(ws + W.part_ml);
+    A->part_o = reinterpret_cast<float *>(ws + W.part_o);
+    A->own.ml = reinterpret_cast<float2 *>(ws + W.own_ml);
+    A->own.o = reinterpret_cast<float *>(ws + W.own_o);
+    A->own.base = reinterpret_cast<long long *>(ws + W.own_base);
+    A->own.unit = reinterpret_cast<int *>(ws + W.own_unit);
+    A->own.cpw = reinterpret_cast<long long *>(ws + W.own_cpw);
+}
+
 int pg_plan(const KvePgShape *shape, const int32_t *new_len, const int32_t *len_in,
             const int32_t *pool_in, int32_t *free_pages, int32_t *block_table, int32_t *len_out,
             int32_t *pool_out, int32_t *q_start, int32_t *row_req, int32_t *row_pos,
@@ -1082,14 +1094,7 @@ int pg_attention(const KvePgShape *shape, const void *q, long long q_row_stride,
     A.row_req = row_req;
     A.out = out;
     A.lse = lse_out;
-    char *ws = static_cast<char *>(workspace);
-    A.part_ml = reinterpret_cast<float2 *>(ws + W.part_ml);
-    A.part_o = reinterpret_cast<float *>(ws + W.part_o);
-    A.own.ml = reinterpret_cast<float2 *>(ws + W.own_ml);
-    A.own.o = reinterpret_cast<float *>(ws + W.own_o);
-    A.own.base = reinterpret_cast<long long *>(ws + W.own_base);
-    A.own.unit = reinterpret_cast<int *>(ws + W.own_unit);
-    A.own.cpw = reinterpret_cast<long long *>(ws + W.own_cpw);
+    pg_workspace(W, workspace, &A);
     A.own.segs = pg_own_segs(D);
     A.own.seg_rows = pg_seg_rows(D);
     A.err = err;
@@ -1108,6 +1113,202 @@ int pg_attention(const KvePgShape *shape, const void *q, long long q_row_stride,
         e = launch_pg_join(D, A, st);
     }
     if (e != cudaSuccess) return cuda_fail(e, "pg_attention: launch");
+    return KVE_OK;
+}
+
+// ---- cache in 4 bits -------------------------------------------------------------------------------
+static int q4_common(const char *fn, const KvePgShape *shape, int group, PgDims *D, Q4Shape *Q) {
+    if (int s = injected()) return s;
+    const char *why;
+    if (!shape) return fail(KVE_EINVAL, "%s: null shape", fn);
+    if (shape->dtype != KVE_F32 && shape->dtype != KVE_BF16 && shape->dtype != KVE_F16)
+        return fail(KVE_EDTYPE, "%s: dtype must be KVE_F32, KVE_BF16 or KVE_F16", fn);
+    if (!q4_dims(shape, group, D, Q, &why)) return fail(KVE_EINVAL, "%s: %s", fn, why);
+    return KVE_OK;
+}
+
+size_t q4_prefix_size(const KvePgShape *shape, int group) {
+    PgDims D;
+    Q4Shape Q;
+    const char *why;
+    if (!q4_dims(shape, group, &D, &Q, &why)) return 0;
+    return (size_t)D.S * D.Hkv * Q.ptiles * Q.tile;
+}
+
+size_t q4_pages_size(const KvePgShape *shape, int group) {
+    PgDims D;
+    Q4Shape Q;
+    const char *why;
+    if (!q4_dims(shape, group, &D, &Q, &why)) return 0;
+    return (size_t)D.npages * D.Hkv * (D.P / kQ4Tile) * Q.tile;
+}
+
+// The strides of [count][n_kv_heads][rows][d_head]; the stride of a dimension of one entry is never used.
+static bool q4_strides(const PgDims &D, long long count, long long rows, long long *outer, long long *head,
+                       long long *row) {
+    const long long es = (long long)dtype_size(D.dtype);
+    if (count == 1) *outer = (long long)D.Hkv * rows * D.d;
+    if (D.Hkv == 1) *head = rows * D.d;
+    if (rows == 1) *row = D.d;
+    for (long long s : {*outer, *head, *row})
+        if (s < D.d || s * es % 16 != 0 || s >= (1LL << 36)) return false;
+    return true;
+}
+
+int q4_pack(const KvePgShape *shape, int group, const void *K, const void *V, long long prompt_stride,
+            long long head_stride, long long row_stride, const int32_t *prefix_len, void *prefix,
+            void *stream) {
+    Q4Cache C{};
+    if (int s = q4_common("q4_pack", shape, group, &C.D, &C.Q)) return s;
+    if (C.D.n == 0) return fail(KVE_EINVAL, "q4_pack: n_prefix is 0");
+    if (!K || !V || !prefix) return fail(KVE_EINVAL, "q4_pack: null argument");
+    if (!q4_strides(C.D, C.D.S, C.D.n, &prompt_stride, &head_stride, &row_stride))
+        return fail(KVE_EINVAL, "q4_pack: strides must hold a head row and be multiples of 16 bytes");
+    if (!aligned16(K) || !aligned16(V) || !aligned16(prefix))
+        return fail(KVE_EINVAL, "q4_pack: K, V and prefix must be 16-byte aligned");
+    C.K = K;
+    C.V = V;
+    C.s0 = C.v0 = prompt_stride;
+    C.s1 = C.v1 = head_stride;
+    C.s2 = C.v2 = row_stride;
+    C.len = prefix_len;
+    C.cache = static_cast<uint8_t *>(prefix);
+    C.count = C.D.S;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    {
+        ProfScope ps("q4_pack", 1, st);
+        e = launch_q4_pack(C, st);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "q4_pack: launch");
+    return KVE_OK;
+}
+
+int q4_append(const KvePgShape *shape, int group, const void *K_new, const void *V_new,
+              long long K_row_stride, long long V_row_stride, const int32_t *slot_map, void *pages,
+              void *stream) {
+    Q4Cache C{};
+    if (int s = q4_common("q4_append", shape, group, &C.D, &C.Q)) return s;
+    if (!K_new || !V_new || !slot_map || !pages) return fail(KVE_EINVAL, "q4_append: null argument");
+    const long long es = (long long)dtype_size(C.D.dtype), row = (long long)C.D.Hkv * C.D.d;
+    if (K_row_stride < row || V_row_stride < row || K_row_stride * es % 16 != 0 ||
+        V_row_stride * es % 16 != 0)
+        return fail(KVE_EINVAL, "q4_append: row strides must hold a row and be multiples of 16 bytes");
+    if (!aligned16(K_new) || !aligned16(V_new) || !aligned16(pages))
+        return fail(KVE_EINVAL, "q4_append: K, V and pages must be 16-byte aligned");
+    if (!(C.err = device_error_word())) return fail(KVE_ECUDA, "q4_append: no device error word");
+    C.K = K_new;
+    C.V = V_new;
+    C.s1 = C.v1 = C.D.d;
+    C.s2 = K_row_stride;
+    C.v2 = V_row_stride;
+    C.slots = slot_map;
+    C.cache = static_cast<uint8_t *>(pages);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    {
+        ProfScope ps("q4_append", 1, st);
+        e = launch_q4_append(C, st);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "q4_append: launch");
+    return KVE_OK;
+}
+
+int q4_unpack(const KvePgShape *shape, int group, const void *cache, const int32_t *block_table,
+              const int32_t *len, int n_out, void *K_out, void *V_out, long long outer_stride,
+              long long head_stride, long long row_stride, void *stream) {
+    Q4Cache C{};
+    if (int s = q4_common("q4_unpack", shape, group, &C.D, &C.Q)) return s;
+    if (!cache || !K_out || !V_out || (block_table && !len))
+        return fail(KVE_EINVAL, "q4_unpack: null argument");
+    if (!block_table && C.D.n == 0) return fail(KVE_EINVAL, "q4_unpack: n_prefix is 0");
+    const int most = block_table ? C.D.cap() : C.D.n;
+    if (n_out < 1 || n_out > most)
+        return fail(KVE_EINVAL, "q4_unpack: n_out must be 1 to n_prefix, or max_pages * page_size");
+    C.count = block_table ? C.D.R : C.D.S;
+    if (!q4_strides(C.D, C.count, n_out, &outer_stride, &head_stride, &row_stride))
+        return fail(KVE_EINVAL, "q4_unpack: strides must hold a head row and be multiples of 16 bytes");
+    if (!aligned16(cache) || !aligned16(K_out) || !aligned16(V_out))
+        return fail(KVE_EINVAL, "q4_unpack: the cache, K_out and V_out must be 16-byte aligned");
+    if (!(C.err = device_error_word())) return fail(KVE_ECUDA, "q4_unpack: no device error word");
+    C.Ko = K_out;
+    C.Vo = V_out;
+    C.s0 = C.v0 = outer_stride;
+    C.s1 = C.v1 = head_stride;
+    C.s2 = C.v2 = row_stride;
+    C.cache = static_cast<uint8_t *>(const_cast<void *>(cache));
+    C.table = block_table;
+    C.len = len;
+    C.width = C.D.maxp;
+    C.rows = n_out;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    {
+        ProfScope ps("q4_unpack", 1, st);
+        e = launch_q4_unpack(C, st);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "q4_unpack: launch");
+    return KVE_OK;
+}
+
+size_t q4_workspace_size(const KvePgShape *shape, int group) {
+    PgDims D;
+    Q4Shape Q;
+    const char *why;
+    if (!q4_dims(shape, group, &D, &Q, &why)) return 0;
+    return q4_ws_layout(D).total;
+}
+
+int q4_attention(const KvePgShape *shape, int group, const void *q, long long q_row_stride,
+                 const void *prefix, const int32_t *prefix_len, const void *pages,
+                 const int32_t *block_table, const int32_t *len, const int32_t *q_start,
+                 const int32_t *row_req, void *out, float *lse_out, void *workspace, size_t ws_bytes,
+                 void *stream) {
+    PgDims D;
+    Q4Shape Q;
+    if (int s = q4_common("q4_attention", shape, group, &D, &Q)) return s;
+    if (!q || !pages || !block_table || !len || !q_start || !row_req || !out || (D.n > 0 && !prefix))
+        return fail(KVE_EINVAL, "q4_attention: null argument");
+    const long long es = (long long)dtype_size(D.dtype);
+    if (q_row_stride < (long long)D.Hq * D.d || q_row_stride * es % 16 != 0)
+        return fail(KVE_EINVAL, "q4_attention: q_row_stride must hold a row and be a multiple of 16 bytes");
+    if (!aligned16(q) || !aligned16(pages) || !aligned16(out) || (D.n > 0 && !aligned16(prefix)))
+        return fail(KVE_EINVAL, "q4_attention: q, prefix, pages and out must be 16-byte aligned");
+    const PgWorkspace W = q4_ws_layout(D);
+    if (!workspace || ws_bytes < W.total)
+        return fail(KVE_EWORKSPACE, "q4_attention: workspace of %zu bytes needed, %zu given", W.total,
+                    workspace ? ws_bytes : (size_t)0);
+    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+        return fail(KVE_EINVAL, "q4_attention: workspace must be 256-byte aligned");
+    unsigned *err = device_error_word();
+    if (!err) return fail(KVE_ECUDA, "q4_attention: no device error word");
+    PgAttn A{};
+    A.q = q;
+    A.q_row = q_row_stride;
+    A.Kp = prefix;
+    A.plen = D.n > 0 ? prefix_len : nullptr;
+    A.K = pages;
+    A.table = block_table;
+    A.len = len;
+    A.q_start = q_start;
+    A.row_req = row_req;
+    A.out = out;
+    A.lse = lse_out;
+    pg_workspace(W, workspace, &A);
+    A.own.segs = q4_segs(D);
+    A.own.seg_rows = pg_seg_rows(D);
+    A.err = err;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    {
+        ProfScope ps("q4_lines", 1, st);
+        e = launch_q4_lines(D, Q, A, st);
+    }
+    if (e == cudaSuccess) {
+        ProfScope ps("q4_join", 1, st);
+        e = launch_pg_join(D, A, st);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "q4_attention: launch");
     return KVE_OK;
 }
 

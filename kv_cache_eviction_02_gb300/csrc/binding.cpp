@@ -1,5 +1,5 @@
-// Python module _binding: the tensor arguments of the shared-prompt decoding calls, which are made once
-// per layer and decoded token. Each function checks every tensor against the declared shape (CUDA, on the
+// Python module _binding: the tensor arguments of the shared-prompt decoding calls, with 16 or 32 bits or in 4, which
+// are made once per layer and decoded token. Each function checks every tensor against the declared shape (CUDA, on the
 // call's device, of the element type, large enough, contiguous or with rows a stride apart) and calls the
 // C-ABI, for which it takes under a microsecond; the same checks through ctypes and tensor attributes cost
 // more than the launches (7 us of a 14 us pg_attention call). A call whose arguments do not fit, or are
@@ -16,6 +16,10 @@ constexpr long kOther = -1;
 decltype(&pg_plan) g_plan;
 decltype(&pg_append) g_append;
 decltype(&pg_attention) g_attention;
+decltype(&q4_pack) g_q4_pack;
+decltype(&q4_append) g_q4_append;
+decltype(&q4_unpack) g_q4_unpack;
+decltype(&q4_attention) g_q4_attention;
 
 struct Args {
     PyObject *const *at;
@@ -82,6 +86,40 @@ struct Args {
         if (x->size(0) != S || x->size(1) != H || x->size(2) < n || x->size(3) != d ||
             (d > 1 && x->stride(3) != 1))
             return ok = false, nullptr;
+        for (int k = 0; k < 3; ++k) s[k] = x->stride(k);
+        return x->data_ptr();
+    }
+    // the bytes of the prompts or pages in 4 bits; their group is argument 0
+    int group() {
+        const long g = ok ? PyLong_AsLong(at[0]) : 0;
+        ok = ok && !PyErr_Occurred() && (g == 32 || g == 64 || g == 128) && shape->d_head % g == 0;
+        return (int)g;
+    }
+    long long bytes(int g, bool pages) const {
+        if (!ok) return 0;
+        const long long tile = 16LL * shape->d_head + 64LL * (shape->d_head / g), heads = shape->n_kv_heads;
+        return pages ? shape->n_pages * heads * (shape->page_size / 16) * tile
+                     : shape->n_prompts * heads * ((shape->n_prefix + 15LL) / 16) * tile;
+    }
+    void *workspace(int i, size_t *size) {
+        *size = 0;
+        if (!ok || at[i] == Py_None) return nullptr;
+        if (!THPVariable_Check(at[i])) return ok = false, nullptr;
+        const at::Tensor &x = THPVariable_Unpack(at[i]);
+        ok = x.is_cuda() && x.get_device() == device && x.is_contiguous();
+        if (!ok) return nullptr;
+        *size = x.nbytes();
+        return x.data_ptr();
+    }
+    // rows [count][n_kv_heads][>= *n][d_head], or with *n 0 as many as there are, at most `most`
+    void *cache_rows(int i, long long count, long long *n, long long most, long long (&s)[3]) {
+        const at::Tensor *x = tensor(i, type);
+        if (!x) return nullptr;
+        if (x->dim() != 4 || x->size(0) != count || x->size(1) != shape->n_kv_heads ||
+            x->size(3) != shape->d_head || (shape->d_head > 1 && x->stride(3) != 1))
+            return ok = false, nullptr;
+        if (*n == 0) *n = x->size(2) < most ? x->size(2) : most;
+        if (x->size(2) < *n) return ok = false, nullptr;
         for (int k = 0; k < 3; ++k) s[k] = x->stride(k);
         return x->data_ptr();
     }
@@ -154,22 +192,71 @@ PyObject *attention(Args &a) {
     const int32_t *q_start = a.ints(8, R + 1), *row_req = a.ints(9, n);
     void *out = a.array(10, a.type, a.ok ? heads * a.shape->d_head : 0);
     float *lse = a.array<float>(11, at::kFloat, heads, true);
-    void *ws = nullptr;
-    size_t bytes = 0;
-    if (a.ok && a.at[12] != Py_None) {
-        a.ok = THPVariable_Check(a.at[12]);
-        if (a.ok) {
-            const at::Tensor &x = THPVariable_Unpack(a.at[12]);
-            a.ok = x.is_cuda() && x.get_device() == a.device && x.is_contiguous();
-            if (a.ok) {
-                ws = x.data_ptr();
-                bytes = x.nbytes();
-            }
-        }
-    }
+    size_t bytes;
+    void *ws = a.workspace(12, &bytes);
     return result(a, [&] {
         return g_attention(a.shape, q, qs, Kp, Vp, s[0], s[1], s[2], plen, K, V, table, len, q_start,
                            row_req, out, lse, ws, bytes, a.stream);
+    });
+}
+
+PyObject *pack4(Args &a) {
+    const int g = a.group();
+    long long s[3], t[3], n = a.ok ? a.shape->n_prefix : 0;
+    a.ok = a.ok && n > 0;
+    const long long S = a.ok ? a.shape->n_prompts : 0;
+    const void *K = a.cache_rows(1, S, &n, n, s), *V = a.cache_rows(2, S, &n, n, t);
+    a.ok = a.ok && s[0] == t[0] && s[1] == t[1] && s[2] == t[2];
+    const int32_t *len = a.ints(3, S, true);
+    void *prefix = a.array(4, at::kByte, a.bytes(g, false));
+    return result(a, [&] { return g_q4_pack(a.shape, g, K, V, s[0], s[1], s[2], len, prefix, a.stream); });
+}
+
+PyObject *append4(Args &a) {
+    const int g = a.group(), heads = a.ok ? a.shape->n_kv_heads : 0;
+    long long ks, vs;
+    const void *k = a.rows(1, heads, &ks), *v = a.rows(2, heads, &vs);
+    const int32_t *slots = a.ints(3, a.ok ? a.shape->n_rows : 0);
+    void *pages = a.array(4, at::kByte, a.bytes(g, true));
+    return result(a, [&] { return g_q4_append(a.shape, g, k, v, ks, vs, slots, pages, a.stream); });
+}
+
+PyObject *unpack4(Args &a) {
+    const int g = a.group();
+    const bool paged = a.at[2] != Py_None;
+    const long long count = !a.ok ? 0 : (paged ? a.requests() : a.shape->n_prompts);
+    const long long most =
+        !a.ok ? 0 : (paged ? (long long)a.shape->max_pages * a.shape->page_size : a.shape->n_prefix);
+    const void *cache = a.array(1, at::kByte, a.bytes(g, paged));
+    const int32_t *table = a.ints(2, a.ok ? count * a.shape->max_pages : 0, true), *len = a.ints(3, count, !paged);
+    long long s[3], t[3], n = 0;
+    void *K = a.cache_rows(4, count, &n, most, s);
+    a.ok = a.ok && n > 0;
+    void *V = a.cache_rows(5, count, &n, most, t);
+    a.ok = a.ok && s[0] == t[0] && s[1] == t[1] && s[2] == t[2];
+    return result(a, [&] {
+        return g_q4_unpack(a.shape, g, cache, table, len, (int)n, K, V, s[0], s[1], s[2], a.stream);
+    });
+}
+
+PyObject *attention4(Args &a) {
+    const int g = a.group();
+    const long long R = a.requests(), n = a.ok ? a.shape->n_rows : 0;
+    const long long heads = a.ok ? n * a.shape->n_q_heads : 0;
+    long long qs;
+    const void *q = a.rows(1, a.ok ? a.shape->n_q_heads : 0, &qs);
+    const void *prefix = a.array(2, at::kByte, a.bytes(g, false), true);
+    const int32_t *plen = a.ints(3, a.ok ? a.shape->n_prompts : 0, true);
+    const void *pages = a.array(4, at::kByte, a.bytes(g, true));
+    const int32_t *table = a.ints(5, a.ok ? R * a.shape->max_pages : 0), *len = a.ints(6, R);
+    const int32_t *q_start = a.ints(7, R + 1), *row_req = a.ints(8, n);
+    void *out = a.array(9, a.type, a.ok ? heads * a.shape->d_head : 0);
+    float *lse = a.array<float>(10, at::kFloat, heads, true);
+    size_t bytes;
+    void *ws = a.workspace(11, &bytes);
+    return result(a, [&] {
+        return g_q4_attention(a.shape, g, q, qs, prefix, plen, pages, table, len, q_start, row_req, out, lse, ws,
+                              bytes, a.stream);
     });
 }
 
@@ -186,12 +273,31 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
+// the same of q4_pack, q4_append, q4_unpack and q4_attention
+PyObject *bind_q4(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 4) {
+        PyErr_SetString(PyExc_TypeError, "four addresses");
+        return nullptr;
+    }
+    g_q4_pack = reinterpret_cast<decltype(g_q4_pack)>(PyLong_AsVoidPtr(args[0]));
+    g_q4_append = reinterpret_cast<decltype(g_q4_append)>(PyLong_AsVoidPtr(args[1]));
+    g_q4_unpack = reinterpret_cast<decltype(g_q4_unpack)>(PyLong_AsVoidPtr(args[2]));
+    g_q4_attention = reinterpret_cast<decltype(g_q4_attention)>(PyLong_AsVoidPtr(args[3]));
+    if (PyErr_Occurred()) return nullptr;
+    Py_RETURN_NONE;
+}
+
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f))
 PyMethodDef methods[] = {
     {"bind", FAST(&bind), METH_FASTCALL, nullptr},
     {"plan", FAST((&entry<plan, 11>)), METH_FASTCALL, nullptr},
     {"append", FAST((&entry<append, 5>)), METH_FASTCALL, nullptr},
     {"attention", FAST((&entry<attention, 13>)), METH_FASTCALL, nullptr},
+    {"bind_q4", FAST(&bind_q4), METH_FASTCALL, nullptr},
+    {"q4_pack", FAST((&entry<pack4, 5>)), METH_FASTCALL, nullptr},
+    {"q4_append", FAST((&entry<append4, 5>)), METH_FASTCALL, nullptr},
+    {"q4_unpack", FAST((&entry<unpack4, 6>)), METH_FASTCALL, nullptr},
+    {"q4_attention", FAST((&entry<attention4, 12>)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module{PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr,

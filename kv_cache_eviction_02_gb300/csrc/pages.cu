@@ -123,6 +123,9 @@ bool pg_dims(const KvePgShape *sh, PgDims *D, const char **why) {
     D->rows = sh->n_rows;
     D->max_new = sh->max_new < sh->n_rows ? sh->max_new : sh->n_rows;
     D->dtype = sh->dtype;
+    D->unit_rows = D->dtype != KVE_F32 && (long long)D->max_new * D->g <= 8 ? 8 : 16;
+    D->few_rows = kPgFewRows;
+    D->few_scores = kPgFewScores;
     pg_split(D);
     return true;
 }
@@ -448,7 +451,7 @@ template <bool F32> struct PgFound {
         }
         nq = min(nq, D.max_new);
         mine = r >= 0 && tok >= first && tok - first < nq;
-        dense = !F32 && (D.prompt_own || pg_on_tc((long long)nq * D.g, len));
+        dense = !F32 && (D.prompt_own || pg_on_tc(D, (long long)nq * D.g, len));
         np = D.np == 0 ? 0 : (plen + D.psplit - 1) / D.psplit;
         nd = dense ? (len + D.ssplit - 1) / D.ssplit : 0;
     }
@@ -469,7 +472,7 @@ template <bool F32> struct PgFound {
         x.no = nd;
         // pieces of a unit: query row rr of entity e
         auto pieces = [&](int e, int rr, int chunks, int blocks, long long *at_row, int *count) {
-            const int lg = F32 || pg_unit_rows(D) == 16 ? 4 : 3, u = kh * blocks + (rr >> lg);
+            const int lg = pg_unit_rows(D) == 16 ? 4 : 3, u = kh * blocks + (rr >> lg);
             const long long c = A.own.base[e] + (long long)u * chunks, cpw = *A.own.cpw;
             const long long w0 = pg_div(c, cpw), w1 = chunks > 0 ? pg_div(c + chunks - 1, cpw) : w0 - 1;
             const long long at = A.own.unit[e] + u + w0;

@@ -21,6 +21,8 @@ struct PgDims {
     bool line;                 // that kernel takes the prompts too (fp32; 16-bit types: short work)
     bool direct;               // it does all, a warp per request and KV head
     bool prompt_own;           // the prompt's kernel does the own rows too (split np)
+    int few_rows, few_scores;  // pg_on_tc
+    int unit_rows;             // pg_unit_rows
     // rows behind one prompt, when no request packs more than max_new
     __host__ __device__ long long group_rows() const {
         return (long long)F * max_new < rows ? (long long)F * max_new : rows;
@@ -85,22 +87,20 @@ inline int pg_tc_blocks(const PgDims &D, bool own) {
 // tcgen05 is never ahead (64 requests of up to 8 new rows, 32/8 heads: 1024 own rows 104 and 95, 4096 278 and 278;
 // of 4, 8/1 heads: 4096 own rows 67 and 48); with 64 it is (8 new rows, 8/1 heads, 4096: 71 and 82).
 constexpr int kPgFewRows = 32, kPgFewScores = 12288;
-__host__ __device__ inline bool pg_on_tc(long long rows, int len) {
-    return rows > kPgFewRows && rows * len > kPgFewScores;
+__host__ __device__ inline bool pg_on_tc(const PgDims &D, long long rows, int len) {
+    return rows > D.few_rows && rows * len > D.few_scores;
 }
 __host__ __device__ inline bool pg_many_new(const PgDims &D) {
-    return D.dtype != KVE_F32 && pg_on_tc((long long)D.max_new * D.g, D.cap());
+    return D.dtype != KVE_F32 && pg_on_tc(D, (long long)D.max_new * D.g, D.cap());
 }
 
 // Tables of at most this many rows behind a prompt of a 16-bit type (the lookahead's trajectories): two idle
 // warps of the prompt's kernel work out the own rows, a launch less (16K lookahead step: with a kernel of their
 // own 23.3 us, in the join, which cannot start beside the prompt's CTAs, 20.5, so 16.4).
 constexpr int kPgFewOwn = 32;
-// Query rows of a unit: 8 when no request has more, else 16 (the rows of a unit share its K/V loads; more
-// than 16 would not leave registers for two blocks per SM).
-__host__ __device__ inline int pg_unit_rows(const PgDims &D) {
-    return D.dtype != KVE_F32 && (long long)D.max_new * D.g <= 8 ? 8 : 16;
-}
+// Query rows of a unit (D.unit_rows): 8 when no request has more, else 16 (the rows of a unit share its K/V loads;
+// more than 16 would not leave registers for two blocks per SM).
+__host__ __device__ inline int pg_unit_rows(const PgDims &D) { return D.unit_rows; }
 // 16-bit types: the warps of pages_own.cu take the prompts too when all there is to do is short, so that a
 // call has one launch less and no tcgen05 kernel, which costs several microseconds whatever it does (a step of
 // 4 requests behind 11 rows 12.0 -> 8.7 us); not with long own rows, where the prompt's kernel
@@ -244,9 +244,9 @@ __device__ __forceinline__ void pg_unit_entity(const PgDims &D, const PgAttn &A,
     *nq = max(0, pg_start(A.q_start, r1, D.rows) - *first);
     *rows = (own ? min(*nq, D.max_new) : *nq) * D.g;
     *cr = (*len + kPgChunk - 1) / kPgChunk;
-    const int lg = F32 || pg_unit_rows(D) == 16 ? 4 : 3;
+    const int lg = pg_unit_rows(D) == 16 ? 4 : 3;
     *nb = *cr > 0 ? (*rows + (1 << lg) - 1) >> lg : 0;  // (without tokens no units: warps step over it)
-    if (!F32 && (own ? pg_on_tc(*rows, *len) : !D.line)) *nb = 0;
+    if (!F32 && (own ? pg_on_tc(D, *rows, *len) : !D.line)) *nb = 0;
 }
 
 // Where a warp stands in the line of chunks.
@@ -278,13 +278,13 @@ __device__ __forceinline__ long long pg_div(long long a, long long b) {  // of n
 
 // Equal shares of the line of chunks. All threads of the block: sums chunks and units of n entities
 // (thread t of q consecutive ones; csum[t], usum[t]: those before its), shares the chunks out evenly over
-// the launch's warps, and lets block 0 write down what the join needs. A share is at least a 16th of the
+// the launch's warps (SHARES per block), and lets block 0 write down what the join needs. A share is at least a 16th of the
 // longest unit, up to 4 chunks: smaller ones would leave more pieces to join than they save.
 struct PgShare {
     long long total, cpw;  // chunks in all, chunks per warp
     int q;                 // entities per thread
 };
-template <int THREADS, typename F>
+template <int THREADS, int SHARES = THREADS / 32, typename F>
 __device__ __forceinline__ PgShare pg_share(int n, int Hkv, long long *csum, int *usum,
                                             const PgOwn &W, F entity) {
     const int lane = threadIdx.x & 31, q = (n + THREADS - 1) / THREADS;
@@ -338,7 +338,7 @@ __device__ __forceinline__ PgShare pg_share(int n, int Hkv, long long *csum, int
     PgShare s;
     s.total = csum[THREADS];
     s.q = q;
-    const int nw = gridDim.x * (THREADS / 32);
+    const int nw = gridDim.x * SHARES;
     s.cpw = max(max(1LL, pg_div(s.total + nw - 1, nw)), min(4LL, (s_longest + 15) / 16LL));
     if (blockIdx.x == 0) {
         cs = csum[threadIdx.x];

@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(pt_threads<QT>(), 1)
     int nrow = (tok1 - tok0) * A.D.g;
     if (OWN) {
         nrow = min(tok1 - tok0, A.D.max_new) * A.D.g;
-        if (!pg_on_tc(nrow, end)) nrow = 0;  // pages_own.cu's
+        if (!pg_on_tc(A.D, nrow, end)) nrow = 0;  // pages_own.cu's
     }
     const int all = nrow;  // query rows, with or without tokens of this split
     // warps 2 and 3, once: the own rows of this CTA's row blocks, shared with the other splits

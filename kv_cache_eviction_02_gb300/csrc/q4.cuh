@@ -1,0 +1,70 @@
+// Cache in 4 bits: its layout, and what the kernels that write, read and attend to it share (q4_*.cu).
+//
+// A row of a KV head is held in groups of G channels, each as whole numbers m of 16 neighbouring ones and a
+// step s of four significant bits, for the values s m. s m has at most 8 significant bits, so it is
+// exact in bf16 (and in fp16 wherever that reaches), and a product of two operands that the tensor cores take is
+// a product with the value itself. Codes n = m + k are 0 .. 15; a group's parameter is s as bf16, whose last four
+// bits are 0, with k in them (0x7FF0, a NaN: the group stands for NaN).
+//
+// Codes lie in the order in which the warps of q4_attn.cu read them: a tile of 16 tokens is one contiguous block
+// [K codes][V codes][K parameters][V parameters], read by one bulk copy. A lane's word for 16 channels is the A
+// operand of an m16n8k16 product: a nibble at bit 0 or 4 of each half is the fp16 number n 2^-24 or n 2^-20 as it
+// stands (below fp16's normal numbers, which the tensor cores multiply exactly), so a word takes four ANDs
+// and one shift. Every byte of a word belongs to one token, so tokens of a tile can be written apart.
+//   K: lane 4 r + j (r < 8, j < 4), words 2 c, 2 c + 1: channels 32 c + 8 j .. + 7 of tokens r (bytes 0 and 2) and
+//      r + 8 (bytes 1 and 3); channels e, e + 2 (e = 0, 1 mod 4) in the low and high nibble of a byte
+//   V: lane 4 r + j, word c: channels 16 c + 2 r (low nibble) and + 1 (high) of tokens 2 j (byte 0), 2 j + 8 (1),
+//      2 j + 1 (2), 2 j + 9 (3)
+//   parameters: [16 tokens][groups]
+// A lane's words lie in pieces of 16 bytes (8 with d_head 32), lane after lane.
+#pragma once
+
+#include "pages_ptx.cuh"
+
+namespace kve {
+
+constexpr int kQ4Tile = 16;  // tokens
+__host__ __device__ constexpr int q4_codes(int d) { return 8 * d; }              // bytes, K or V of a tile
+__host__ __device__ constexpr int q4_params(int d, int group) { return 32 * (d / group); }
+__host__ __device__ constexpr int q4_tile_bytes(int d, int group) {
+    return 2 * (q4_codes(d) + q4_params(d, group));
+}
+// byte offset of word w of a lane among its K (or V) codes
+template <int D> __host__ __device__ constexpr int q4_word(int lane, int w) {
+    constexpr int per = D == 32 ? 8 : 16;
+    return (w >> 2) * 512 + lane * per + (w & 3) * 4;
+}
+
+constexpr unsigned short kQ4Nan = 0x7FF0;
+
+// A 4-bit array as the kernels see it: tiles [block][KV head][tiles_per_block], a block being a prompt or a page.
+struct Q4Shape {
+    int d, group, tile;  // bytes per tile
+    int ptiles;          // tiles per prompt and KV head
+};
+
+// Calls of the cache's own kernels.
+struct Q4Cache {
+    PgDims D;
+    Q4Shape Q;
+    const void *K, *V;  // 16-bit or fp32 rows
+    void *Ko, *Vo;
+    long long s0, s1, s2;  // strides (elements) of prompt or request, head, row; V's
+    long long v0, v1, v2;
+    uint8_t *cache;
+    const int32_t *table, *len, *slots;
+    int count, width, rows;  // prompts or requests, table entries each, rows that the arrays have
+    unsigned *err;
+};
+cudaError_t launch_q4_pack(const Q4Cache &C, cudaStream_t st);
+cudaError_t launch_q4_append(const Q4Cache &C, cudaStream_t st);
+cudaError_t launch_q4_unpack(const Q4Cache &C, cudaStream_t st);
+
+// Sizes and splits of an attention call over 4-bit arrays; its partial results are joined by launch_pg_join.
+// A.Kp is the prompts' array, A.K the pages'.
+bool q4_dims(const KvePgShape *sh, int group, PgDims *D, Q4Shape *Q, const char **why);
+PgWorkspace q4_ws_layout(const PgDims &D);
+unsigned long long q4_segs(const PgDims &D);
+cudaError_t launch_q4_lines(const PgDims &D, const Q4Shape &Q, const PgAttn &A, cudaStream_t st);
+
+}  // namespace kve

@@ -1,0 +1,754 @@
+// Cache in 4 bits: attention over prompts and pages by warps, a lane's codes as tensor-core operands as they stand.
+//
+// Few query rows (a decode step's g heads per KV head) read all of a cache: bound by HBM, then by the
+// instructions that a code costs. The products run transposed, S^T = K Q^T and O^T += V^T P^T, as
+// m16n8k16 fragments of fp16 numbers whose A operand is the cache's own words (q4.cuh): no code is converted, a
+// nibble is the number n 2^-24 or n 2^-20. With a group's step and zero code taken out of the sums,
+//   q.k = sum over groups of s_g (q_g.n_g - k_g sum q_g),   o_c = sum over tokens of (p_t s_t,g) (n_t,c - k_t,g),
+// a score is a product per group, times s in fp32, and the terms of the zero codes are products too: A holds k_g of
+// the 16 tokens, B the sums of q (as two fp16 numbers, off by 2^-22; fp32 three), or the same weights p s as the codes'.
+// Queries are carried as fp16 after their row's largest entry is brought to 2^7 .. 2^8 (bf16 and fp16 entries keep all
+// their bits down to 2^-17 of the largest, smaller ones are off by 2^-32 of it; fp32 ones are two fp16
+// numbers). Weights p s are fp32 numbers rounded once to fp16, half a step (fp32: two fp16 numbers).
+//
+// Work is dealt out as in pages_own.cu: units (request or prompt, KV head, 8 or 16 query rows) and their tiles of 16
+// tokens in one line, equal shares for all CTAs (one per SM) and in them for their warps, a ring of tiles per warp that
+// runs on across units. A tile is one contiguous block: one bulk copy by one lane. Pieces of a unit that several
+// warps of a CTA have seen are joined in shared memory, so a CTA hands on one partial result of a unit.
+#include <type_traits>
+
+#include "q4.cuh"
+
+namespace kve {
+namespace {
+
+// Weights are carried up to 2^15 of the reference m, which is set 2^7 below the largest weight p s: of two pieces that
+// are joined, references may lie as far apart as steps do, so a step below 2^-32 does not raise it further.
+constexpr float kLnUp = 7.f, kLnGrow = 15.f, kLnLeastStep = 0x1p-32f;
+
+// The tensor cores cut the sums' bits at 2^-24 of the largest product's exponent, which for a number as it stands in the
+// cache counts as 2^-14: to 2^-17 of a product of V's. That is enough for outputs of bf16 (2^-9). For fp16 and fp32 V's
+// codes (for fp32 K's too) are made normal numbers n - k, by one subtraction from 1024 + n.
+enum { kLnBf16, kLnF16, kLnF32 };
+
+constexpr int kLnStage = 2;  // tiles per ring place: at most, of one unit
+// One CTA per SM, of as many warps as its registers hold, and a ring of what shared memory has room for.
+template <int D, int G, int NT, int MODE> struct Ln {
+    static constexpr int WARPS = NT == 2 && D == 128 ? 8 : 12, THREADS = 32 * WARPS, RB = 8 * NT;
+    static constexpr int TB = q4_tile_bytes(D, G), SB = kLnStage * TB;
+    static constexpr int ROW = D + 4;                    // floats per row of a piece in shared memory
+    static constexpr int PIECE = RB * ROW * 4 + RB * 8;  // o [RB][ROW], (m, l) [RB]
+    static constexpr int FIT = ((227 * 1024 - 12 * 1024) / WARPS - PIECE) / SB, NST = FIT < 6 ? FIT : 6;
+    static constexpr int WARP = NST * SB + PIECE;        // bytes per warp: ring, first piece
+    static constexpr int SMEM = WARPS * WARP + 128;
+    static_assert(NST >= 2 && PIECE <= NST * SB && SB % 16 == 0 && PIECE % 16 == 0);
+};
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the same onto zeros
+__device__ __forceinline__ void mma0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                     uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ float2 unpack(uint32_t x) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&x));
+}
+__device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b) {
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ float lg2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// one contiguous block into shared memory; addresses and size are multiples of 16 bytes
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(tc::smem_u32(bar))
+        : "memory");
+}
+
+// A lane's words of a tile's K or V codes (shared-memory addresses, the lane's own offset among them).
+template <int D> __device__ __forceinline__ void words(uint32_t at, uint32_t (&w)[D / 16]) {
+    if constexpr (D == 32) {
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                         : "r"(at + i * 512)
+                         : "memory");
+    }
+}
+// The parameters of a token: NG of 16 bits in (NG + 1) / 2 words.
+template <int NG> __device__ __forceinline__ void params_of(uint32_t at, uint32_t (&w)[(NG + 1) / 2]) {
+    if constexpr (NG == 4)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+    else if constexpr (NG == 2)
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
+    else
+        asm volatile("{\n\t.reg .u16 x;\n\tld.shared.u16 x, [%1];\n\tcvt.u32.u16 %0, x;\n\t}" : "=r"(w[0]) : "r"(at) : "memory");
+}
+template <int NG> __device__ __forceinline__ void steps_of(const uint32_t (&w)[(NG + 1) / 2], float (&s)[NG]) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+        s[g] = __uint_as_float((g & 1 ? w[g >> 1] : w[g >> 1] << 16) & 0xFFF00000u);
+}
+constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u, k1024 = 0x64006400u;
+
+template <int D, int G, int NT, int MODE>
+__global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
+    q4_line_kernel(PgDims D_, PgAttn A, PgOwn W, int ptiles) {
+    using L = Ln<D, G, NT, MODE>;
+    constexpr int NST = L::NST, TB = L::TB, SB = L::SB, RB = L::RB, WARPS = L::WARPS, THREADS = L::THREADS;
+    constexpr bool F32 = MODE == kLnF32, KC = F32, VC = MODE != kLnBf16;  // codes less their zero codes, of K and of V
+    constexpr int NG = D / G, KW = D / 16, PW = (NG + 1) / 2, NS = F32 ? 2 : 1;
+    constexpr bool PAIR = NT == 1;  // two tiles at once: one alone leaves the warps waiting for its products
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    __shared__ long long csum[THREADS + 1];
+    __shared__ int usum[THREADS + 1];
+    __shared__ uint64_t bars[WARPS][NST];
+    __shared__ int piece_unit[2 * WARPS], piece_rows[2 * WARPS];  // of a warp's first and last piece: -1 or what joins
+    __shared__ int s_abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane & 3;
+    if (lane < NST) tc::mbar_init(&bars[warp][lane], 1);
+    if (lane < 2) piece_unit[2 * warp + lane] = -1;
+    if (threadIdx.x == 0) s_abort = 0;
+    tc::mbar_fence_init();
+    pg_wait_prior();
+    pg_launch_dependents();
+
+    const int e0 = F32 || D_.line ? 0 : D_.S;  // the line's first entity
+    const PgShare sh = pg_share<THREADS, 1>(D_.S + D_.R - e0, D_.Hkv, csum, usum, W, [&](int e, int *cr, int *nb) {
+        int len, first, nq, rows;
+        pg_unit_entity<F32>(D_, A, e + e0, &len, &first, &nq, &rows, cr, nb);
+    });
+    long long X0 = blockIdx.x * sh.cpw;
+    int n = 0;  // tiles of this warp
+    {
+        const long long all = min(sh.total - X0, sh.cpw);  // of the CTA
+        if (all > 0) {
+            const long long from = all * warp / WARPS;
+            n = (int)(all * (warp + 1) / WARPS - from);
+            X0 += from;
+        }
+    }
+    if (n > 0) {
+        int unit;  // the index of its first unit
+        PgCursor<F32> cc;
+        long long x;
+        int e;
+        pg_share_find<THREADS>(csum, usum, sh, X0, &e, &x, &unit);
+        cc.enter(D_, A, e + e0);
+        while (x >= (long long)cc.cr * cc.nb * D_.Hkv) {
+            x -= (long long)cc.cr * cc.nb * D_.Hkv;
+            unit += cc.nb * D_.Hkv;
+            cc.enter(D_, A, cc.e + 1);
+        }
+        const int u = (int)pg_div(x, cc.cr);
+        cc.c = (int)(x - (long long)u * cc.cr);
+        cc.kh = u / cc.nb;
+        cc.rb = u - cc.kh * cc.nb;
+        unit += u;
+        PgCursor<F32> ca = cc;  // runs ahead: the tiles to load
+
+        uint8_t *ring = smem + warp * L::WARP;
+        uint64_t *bar = bars[warp];
+        volatile int *abort_flag = &s_abort;
+        const float k1 = kLog2e * rsqrtf((float)D);
+        uint32_t qf[NT][NS][KW][2];       // B operand of S^T: query row lane / 4 of each block
+        uint32_t zq[NT][2];               // minus the sums of q over groups 2 (j & 1), + 1
+        float fc[NT][2];                  // from the products to log2 units, for this lane's columns 2 j, + 1
+        float o[NT][KW][4], z[NT][4], m[NT][2], l[NT][2];
+        int see[NT][2], see_least = 0, rows, row0;
+        uint32_t zmask[NG], rmask[NG];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            zmask[g] = (j & 1) == g >> 1 ? (g & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
+            rmask[g] = lane >> 2 == g ? ~0u : 0u;
+        }
+        auto begin = [&]() {  // of a unit, or of this warp's part of one
+            rows = cc.rows;
+            row0 = cc.rb * RB;
+            see_least = 0x7fffffff;
+#pragma unroll
+            for (int b = 0; b < NT; ++b) {
+                const int rr = row0 + 8 * b + (lane >> 2), t = rr < rows ? rr / D_.g : 0;
+                const size_t at = (cc.first + t) * A.q_row +
+                                  (size_t)(cc.kh * D_.g + (rr < rows ? rr - t * D_.g : 0)) * D + j * 8;
+                float v[D / 4], most = 0.f;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+                    if (F32) {
+                        const float *p = static_cast<const float *>(A.q) + at + 32 * c;
+                        if (rr < rows) {
+                            x0 = __ldg(reinterpret_cast<const uint4 *>(p));
+                            x1 = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+                        }
+                        v[8 * c] = __uint_as_float(x0.x);
+                        v[8 * c + 1] = __uint_as_float(x0.y);
+                        v[8 * c + 2] = __uint_as_float(x0.z);
+                        v[8 * c + 3] = __uint_as_float(x0.w);
+                        v[8 * c + 4] = __uint_as_float(x1.x);
+                        v[8 * c + 5] = __uint_as_float(x1.y);
+                        v[8 * c + 6] = __uint_as_float(x1.z);
+                        v[8 * c + 7] = __uint_as_float(x1.w);
+                    } else {
+                        if (rr < rows)
+                            x0 = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __half *>(A.q) + at + 32 * c));
+                        const uint32_t y[4] = {x0.x, x0.y, x0.z, x0.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (MODE == kLnF16) {
+                                const float2 f = unpack(y[e]);
+                                v[8 * c + 2 * e] = f.x;
+                                v[8 * c + 2 * e + 1] = f.y;
+                            } else {
+                                v[8 * c + 2 * e] = __uint_as_float(y[e] << 16);
+                                v[8 * c + 2 * e + 1] = __uint_as_float(y[e] & 0xFFFF0000u);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[8 * c + e]));
+                }
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                const int ex = most == 0.f ? 127 : min(max((int)(__float_as_uint(most) >> 23), 27), 230);
+                const float up = __uint_as_float((261 - ex) << 23);               // 2^(7 - exponent)
+                const float back = k1 * __uint_as_float((KC ? ex - 7 : ex + 17) << 23);  // 1 / up, with 2^24 for K's codes
+#pragma unroll
+                for (int e = 0; e < 2; ++e) fc[b][e] = __shfl_sync(0xffffffffu, back, (2 * j + e) * 4);
+                float sum[NG];
+#pragma unroll
+                for (int g = 0; g < NG; ++g) sum[g] = 0.f;
+#pragma unroll
+                for (int k = 0; k < KW; ++k)  // channels 16 k + 8 j .. of which 4 are this word's
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float a = v[4 * k + 2 * h] * up, c = v[4 * k + 2 * h + 1] * up;
+                        const float f = h ? 0.0625f : 1.f;  // (the second pair's codes stand 2^4 higher)
+                        a *= f;
+                        c *= f;
+#pragma unroll
+                        for (int i = 0; i < NS; ++i) {
+                            const uint32_t y = pack(a, c);
+                            qf[b][i][k][h] = y;
+                            const float2 r = unpack(y);
+                            sum[16 * k / G] += (r.x + r.y) * (h ? 16.f : 1.f);
+                            a -= r.x;
+                            c -= r.y;
+                        }
+                    }
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+                    sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+                }
+                float a = -sum[0], c = NG > 1 ? -sum[NG > 1 ? 1 : 0] : 0.f;
+                if (j & 1) {
+                    a = NG > 2 ? -sum[NG > 2 ? 2 : 0] : 0.f;
+                    c = NG > 2 ? -sum[NG > 2 ? 3 : 0] : 0.f;
+                }
+                const uint32_t y0 = pack(a, c);
+                const float2 r0 = unpack(y0);
+                const uint32_t y1 = pack(a - r0.x, c - r0.y);
+                const float2 r1 = unpack(y1);
+                zq[b][0] = j < 2 ? y0 : (F32 ? pack(a - r0.x - r1.x, c - r0.y - r1.y) : 0u);
+                zq[b][1] = j < 2 ? y1 : 0u;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int qr = row0 + 8 * b + j * 2 + e;
+                    see[b][e] = qr >= rows ? 0 : (cc.e < D_.S ? cc.len : cc.len - cc.nq + 1 + qr / D_.g);
+                    if (qr < rows) see_least = min(see_least, see[b][e]);
+                    m[b][e] = kPgNoMax;
+                    l[b][e] = 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[b][e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < KW; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[b][k][e] = 0.f;
+            }
+            see_least = __reduce_min_sync(0xffffffffu, see_least);
+        };
+        // Where a stage's pages are is asked a stage before it is loaded: the table's answer (a trip to L2) is not
+        // waited for.
+        const int tpp = D_.lgP - 4, tmask = (1 << tpp) - 1;  // tiles per page: log2, less one
+        auto stage_of = [&](const PgCursor<F32> &c, int left) { return min(min(kLnStage, left), c.cr - c.c); };
+        auto step = [&](PgCursor<F32> &c, int t) {  // to the stage behind one of t tiles
+            c.c += t - 1;
+            c.next(D_, A);
+        };
+        int fill = 0, togo = n, page[2];  // of the next stage to load
+        auto where = [&]() {
+            page[0] = page[1] = 0;
+            if (ca.e < D_.S) return;
+            const int32_t *row = A.table + (size_t)(ca.e - D_.S) * D_.maxp;
+            page[0] = __ldg(row + (ca.c >> tpp));
+            page[1] = __ldg(row + (min(ca.c + 1, ca.cr - 1) >> tpp));
+        };
+        auto load = [&]() {
+            const int t = stage_of(ca, togo);
+            const uint8_t *src[2];
+            const bool prompt = ca.e < D_.S;
+            if (prompt) {
+                src[0] = static_cast<const uint8_t *>(A.Kp) + (((size_t)ca.e * D_.Hkv + ca.kh) * ptiles + ca.c) * TB;
+                src[1] = src[0] + TB;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    src[i] = static_cast<const uint8_t *>(A.K) +
+                             ((((size_t)pg_page_id(page[i], D_.npages, A.err) * D_.Hkv + ca.kh) << tpp) +
+                              ((ca.c + i) & tmask)) * TB;
+            }
+            if (tc::elect_one()) {
+                tc::mbar_expect_tx(&bar[fill], t * TB);
+                const bool whole = src[1] == src[0] + TB || t == 1;
+                bulk_load(ring + fill * SB, src[0], whole ? t * TB : TB, &bar[fill]);
+                if (!whole) bulk_load(ring + fill * SB + TB, src[1], TB, &bar[fill]);
+            }
+            if (++fill == NST) fill = 0;
+            togo -= t;
+            if (togo > 0) {
+                step(ca, t);
+                where();
+            }
+        };
+        where();
+#pragma unroll 1
+        for (int i = 0; i < NST - 1 && togo > 0; ++i) load();
+        begin();
+
+        int slot = 0, left = n;  // ring place of this stage; tiles that are not done
+        int starts = cc.c;       // the piece's first tile of its unit
+        uint32_t phase = 0;
+        const uint32_t ring_at = tc::smem_u32(ring);
+        const uint32_t codes_at = lane * (D == 32 ? 8 : 16), param_at = 2 * q4_codes(D) + (lane >> 2) * (2 * NG);
+#pragma unroll 1
+        while (left > 0) {
+            if (togo > 0) load();
+            const int nt = stage_of(cc, left);
+            if (!tc::mbar_wait_warp(&bar[slot], phase, abort_flag, A.err)) break;
+            uint32_t tile = ring_at + slot * SB;
+            if (++slot == NST) {
+                slot = 0;
+                phase ^= 1;
+            }
+            int tok = cc.c * kQ4Tile + (lane >> 2);
+            auto work = [&](auto tiles, auto masked) {
+                constexpr int TT = decltype(tiles)::value;
+                constexpr bool MASK = decltype(masked)::value;
+                // scores: 16 tokens x 8 query rows per tile and block, a group at a time
+                float s[TT][NT][4];
+                {
+                    uint32_t kw[TT][KW], kp[TT][2][PW];
+                    float sk[TT][2][NG];
+#pragma unroll
+                    for (int i = 0; i < TT; ++i) {
+                        words<D>(tile + i * TB + codes_at, kw[i]);
+                        params_of<NG>(tile + i * TB + param_at, kp[i][0]);
+                        params_of<NG>(tile + i * TB + param_at + 16 * NG, kp[i][1]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < TT; ++i) {
+                        steps_of<NG>(kp[i][0], sk[i][0]);
+                        steps_of<NG>(kp[i][1], sk[i][1]);
+                    }
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        float c[TT][NT][4];
+                        uint32_t kc[TT][4];  // 1024 + zero code, of both tokens and of codes 2^4 higher
+#pragma unroll
+                        for (int i = 0; i < TT; ++i) {
+                            if (KC) {
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const uint32_t x = __byte_perm(kp[i][h][g >> 1], 0, g & 1 ? 0x3232 : 0x1010);
+                                    kc[i][h] = (x & kLow) | k1024;
+                                    kc[i][h + 2] = (x << 4 & kHigh) | k1024;
+                                }
+                                continue;
+                            }
+                            const uint32_t z0 = (NG == 4 && (j & 1) ? kp[i][0][PW - 1] : kp[i][0][0]) & kLow;
+                            const uint32_t z1 = (NG == 4 && (j & 1) ? kp[i][1][PW - 1] : kp[i][1][0]) & kLow;
+#pragma unroll
+                            for (int b = 0; b < NT; ++b)
+                                mma0(c[i][b], z0, z1, z0, z1, zq[b][0] & zmask[g], zq[b][1] & zmask[g]);
+                        }
+#pragma unroll
+                        for (int k = g * G / 16; k < (g + 1) * G / 16; ++k)
+#pragma unroll
+                            for (int i = 0; i < TT; ++i) {
+                                const uint32_t x = kw[i][k], h = x >> 8;
+                                uint32_t a0 = x & kLow, a1 = h & kLow, a2 = x & kHigh, a3 = h & kHigh;
+                                if (KC) {
+                                    a0 = minus(a0 | k1024, kc[i][0]);
+                                    a1 = minus(a1 | k1024, kc[i][1]);
+                                    a2 = minus(a2 | k1024, kc[i][2]);
+                                    a3 = minus(a3 | k1024, kc[i][3]);
+                                }
+#pragma unroll
+                                for (int b = 0; b < NT; ++b)
+#pragma unroll
+                                    for (int y = 0; y < NS; ++y) {
+                                        const uint32_t(&f)[2] = qf[b][y][k];
+                                        if (KC && k == g * G / 16 && y == 0) mma0(c[i][b], a0, a1, a2, a3, f[0], f[1]);
+                                        else mma(c[i][b], a0, a1, a2, a3, f[0], f[1]);
+                                    }
+                            }
+#pragma unroll
+                        for (int i = 0; i < TT; ++i)
+#pragma unroll
+                            for (int b = 0; b < NT; ++b)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    s[i][b][e] = g == 0 ? sk[i][e >> 1][0] * c[i][b][e]
+                                                        : fmaf(sk[i][e >> 1][g], c[i][b][e], s[i][b][e]);
+                    }
+                }
+                uint32_t vw[TT][KW], vp[TT][2][PW];
+                float sv[TT][2][NG], least[TT][2];
+#pragma unroll
+                for (int i = 0; i < TT; ++i) {
+                    words<D>(tile + i * TB + codes_at + q4_codes(D), vw[i]);
+                    params_of<NG>(tile + i * TB + param_at + q4_params(D, G), vp[i][0]);
+                    params_of<NG>(tile + i * TB + param_at + q4_params(D, G) + 16 * NG, vp[i][1]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        steps_of<NG>(vp[i][h], sv[i][h]);
+                        least[i][h] = kLnLeastStep;
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) least[i][h] = fmaxf(least[i][h], sv[i][h][g]);
+                        least[i][h] = lg2_approx(least[i][h]);
+                    }
+                }
+                bool grow = false;
+                float mt[NT][2];
+#pragma unroll
+                for (int b = 0; b < NT; ++b)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int i = 0; i < TT; ++i) {
+                            s[i][b][e] *= fc[b][e];
+                            s[i][b][e + 2] *= fc[b][e];
+                            if (MASK) {
+                                if (tok + 16 * i >= see[b][e]) s[i][b][e] = -INFINITY;
+                                if (tok + 16 * i + 8 >= see[b][e]) s[i][b][e + 2] = -INFINITY;
+                            }
+                            const float x = fmaxf(s[i][b][e] + least[i][0], s[i][b][e + 2] + least[i][1]);
+                            mt[b][e] = i == 0 ? x : fmaxf(mt[b][e], x);
+                        }
+                        grow = grow || mt[b][e] > m[b][e] + kLnGrow;
+                    }
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int b = 0; b < NT; ++b)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float x = mt[b][e];
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                            const float mn = fmaxf(m[b][e], x - kLnUp), f = tc::ex2_approx(m[b][e] - mn);
+                            m[b][e] = mn;
+                            l[b][e] *= f;
+                            z[b][e] *= f;
+#pragma unroll
+                            for (int k = 0; k < KW; ++k) {
+                                o[b][k][e] *= f;
+                                o[b][k][e + 2] *= f;
+                            }
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < TT; ++i)
+#pragma unroll
+                    for (int b = 0; b < NT; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            s[i][b][e] = tc::ex2_approx(s[i][b][e] - m[b][e & 1]);
+                            l[b][e & 1] += s[i][b][e];
+                        }
+                // zero codes of the tokens, group by row: those of group lane / 4
+                uint32_t v0[TT], v1[TT];
+#pragma unroll
+                for (int i = 0; i < TT; ++i) {
+                    v0[i] = transpose8(NG == 4 && (j & 1) ? vp[i][0][PW - 1] : vp[i][0][0]) & kLow;
+                    v1[i] = transpose8(NG == 4 && (j & 1) ? vp[i][1][PW - 1] : vp[i][1][0]) & kLow;
+                }
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    uint32_t pf[TT][NT][NS][2], k0[TT], k1[TT];
+#pragma unroll
+                    for (int i = 0; i < TT; ++i)
+#pragma unroll
+                        for (int b = 0; b < NT; ++b)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float a = s[i][b][2 * h] * sv[i][h][g], c = s[i][b][2 * h + 1] * sv[i][h][g];
+                                if (MASK) {  // (a row that the query must not see may hold anything)
+                                    if (tok + 16 * i + 8 * h >= see[b][0]) a = 0.f;
+                                    if (tok + 16 * i + 8 * h >= see[b][1]) c = 0.f;
+                                }
+#pragma unroll
+                                for (int y = 0; y < NS; ++y) {
+                                    const uint32_t x = pack(a, c);
+                                    pf[i][b][y][h] = transpose8(x);
+                                    const float2 r = unpack(x);
+                                    a -= r.x;
+                                    c -= r.y;
+                                }
+                            }
+#pragma unroll
+                    for (int i = 0; i < TT; ++i) {
+                        if (VC) {
+                            k0[i] = __shfl_sync(0xffffffffu, v0[i], g * 4 + j);
+                            k1[i] = __shfl_sync(0xffffffffu, v1[i], g * 4 + j);
+                        } else {
+#pragma unroll
+                            for (int b = 0; b < NT; ++b)
+                                mma(z[b], v0[i] & rmask[g], 0u, v1[i] & rmask[g], 0u, pf[i][b][0][0], pf[i][b][0][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < TT; ++i)
+#pragma unroll
+                        for (int k = g * G / 16; k < (g + 1) * G / 16; ++k) {
+                            const uint32_t x = vw[i][k], h = x >> 8;
+                            uint32_t a0 = x & kLow, a1 = x & kHigh, a2 = h & kLow, a3 = h & kHigh;
+                            if (VC) {
+                                a0 = minus(a0 | k1024, k0[i] | k1024);
+                                a1 = minus(a1 | k1024, k0[i] << 4 | k1024);
+                                a2 = minus(a2 | k1024, k1[i] | k1024);
+                                a3 = minus(a3 | k1024, k1[i] << 4 | k1024);
+                            }
+#pragma unroll
+                            for (int b = 0; b < NT; ++b)
+#pragma unroll
+                                for (int y = 0; y < NS; ++y)
+                                    mma(o[b][k], a0, a1, a2, a3, pf[i][b][y][0], pf[i][b][y][1]);
+                        }
+                }
+            };
+            // tiles that all rows see whole, then the others
+            const int whole = min(nt, see_least / kQ4Tile - cc.c);
+            if (PAIR && whole == 2) {
+                work(std::integral_constant<int, PAIR ? 2 : 1>{}, std::false_type{});
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < nt; ++i, tile += TB, tok += kQ4Tile)
+                    if (!PAIR && i < whole) work(std::integral_constant<int, 1>{}, std::false_type{});
+                    else work(std::integral_constant<int, 1>{}, std::true_type{});
+            }
+            left -= nt;
+            const bool ends = left == 0 || cc.c + nt == cc.cr;
+            // The zero codes' sums leave the codes' every few tiles: both grow with all weights, their difference only
+            // as the values do, and the tensor cores cut the bits off that a large sum has no room for.
+            if (!VC && (ends || (left & 2))) {
+#pragma unroll
+                for (int b = 0; b < NT; ++b)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            const float zero = __shfl_sync(0xffffffffu, z[b][e], g * 4 + j);
+#pragma unroll
+                            for (int k = g * G / 16; k < (g + 1) * G / 16; ++k) {
+                                o[b][k][e] -= zero;
+                                o[b][k][e + 2] = fmaf(-16.f, zero, o[b][k][e + 2]);
+                            }
+                        }
+#pragma unroll
+                for (int b = 0; b < NT; ++b) z[b][0] = z[b][1] = 0.f;
+            }
+            if (ends) {  // the piece
+                const long long seg = (long long)unit + blockIdx.x;
+                // one that does not hold all of its unit waits for the other warps' pieces: a warp's last one where its
+                // ring was, which is empty now, one before it, its first, behind the ring
+                const bool open = starts > 0 || cc.c + nt < cc.cr;
+                uint8_t *to = left == 0 ? ring : ring + NST * SB;
+                if (open && lane == 0) {
+                    piece_unit[2 * warp + (left == 0)] = unit;
+                    piece_rows[2 * warp + (left == 0)] = min(RB, rows - row0);
+                }
+#pragma unroll
+                for (int b = 0; b < NT; ++b)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = l[b][e];
+                        x += __shfl_xor_sync(0xffffffffu, x, 4);
+                        x += __shfl_xor_sync(0xffffffffu, x, 8);
+                        x += __shfl_xor_sync(0xffffffffu, x, 16);
+                        const int qr = 8 * b + j * 2 + e;
+                        float2 *ml = reinterpret_cast<float2 *>(to + RB * L::ROW * 4) + qr;
+                        float *dst = reinterpret_cast<float *>(to) + qr * L::ROW;
+                        if (!open) {
+                            // (row starts that are no sums of lengths can ask for more places than there are)
+                            if (row0 + qr >= rows || (unsigned long long)seg >= W.segs) continue;
+                            const size_t row = (size_t)seg * W.seg_rows + qr;
+                            ml = W.ml + row;
+                            dst = W.o + row * D;
+                        }
+                        if (lane < 4) *ml = make_float2(m[b][e], x);
+                        dst += (lane >> 2) * 2;
+#pragma unroll
+                        for (int k = 0; k < KW; ++k)  // channels 16 k + 2 (lane / 4), + 1
+                            *reinterpret_cast<float2 *>(dst + 16 * k) =
+                                make_float2(o[b][k][e] * (VC ? 1.f : 0x1p24f), o[b][k][e + 2] * (VC ? 0.0625f : 0x1p20f));
+                    }
+                ++unit;
+            }
+            __syncwarp();  // the stage's readers are done: the next issue may overwrite it
+            if (left > 0) {
+                step(cc, nt);
+                if (cc.c == 0) {
+                    starts = 0;
+                    begin();
+                }
+            }
+        }
+        if (s_abort) {  // copies still in flight land before the block ends
+            for (int k = 0; k < NST; ++k) {
+                tc::mbar_drain(&bar[k], 0);
+                tc::mbar_drain(&bar[k], 1);
+            }
+        }
+    }
+    // pieces of one unit stand behind one another
+    __syncthreads();
+    for (int a = 0, z; a < 2 * WARPS; a = z) {
+        const int unit = piece_unit[a];
+        z = a + 1;
+        if (unit < 0) continue;
+        while (z < 2 * WARPS && (piece_unit[z] == unit || piece_unit[z] < 0)) ++z;
+        const long long seg = (long long)unit + blockIdx.x;
+        const int rows = piece_rows[a];
+        if ((unsigned long long)seg >= W.segs) continue;
+        for (int i = threadIdx.x; i < rows * (D / 4); i += THREADS) {
+            const int qr = i / (D / 4), col = i % (D / 4) * 4;
+            float M = kPgNoMax, sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int p = a; p < z; ++p) {
+                if (piece_unit[p] < 0) continue;
+                const uint8_t *at = smem + (p >> 1) * L::WARP + (p & 1 ? 0 : NST * SB);
+                const float2 ml = reinterpret_cast<const float2 *>(at + RB * L::ROW * 4)[qr];
+                const float4 v = *reinterpret_cast<const float4 *>(at + (qr * L::ROW + col) * 4);
+                const float mn = fmaxf(M, ml.x), f = exp2f(M - mn), w = exp2f(ml.x - mn);
+                M = mn;
+                sum = fmaf(w, ml.y, sum * f);
+                acc = make_float4(fmaf(w, v.x, acc.x * f), fmaf(w, v.y, acc.y * f), fmaf(w, v.z, acc.z * f),
+                                  fmaf(w, v.w, acc.w * f));
+            }
+            const size_t row = (size_t)seg * W.seg_rows + qr;
+            if (col == 0) W.ml[row] = make_float2(M, sum);
+            *reinterpret_cast<float4 *>(W.o + row * D + col) = acc;
+        }
+    }
+}
+
+// ---- host ------------------------------------------------------------------------------------------
+int ln_ctas(const PgDims &D) {
+    const int rb = pg_unit_rows(D);
+    const long long rows = (long long)D.max_new * D.g;
+    long long chunks = (long long)D.R * D.Hkv * ((rows + rb - 1) / rb) * ((D.cap() + kPgChunk - 1) / kPgChunk);
+    if (D.line)
+        chunks += (long long)D.S * D.Hkv * ((D.group_rows() * D.g + rb - 1) / rb) * ((D.n + kPgChunk - 1) / kPgChunk);
+    return (int)(chunks < kPgSms ? chunks : kPgSms);
+}
+
+template <int D, int G, int NT, int MODE>
+cudaError_t go(const PgDims &D_, const Q4Shape &Q, const PgAttn &A, cudaStream_t st) {
+    using L = Ln<D, G, NT, MODE>;
+    return pg_launch(q4_line_kernel<D, G, NT, MODE>, ln_ctas(D_), L::THREADS, L::SMEM, true, st, D_, A, A.own, Q.ptiles);
+}
+template <int D, int G> cudaError_t by_rows(const PgDims &D_, const Q4Shape &Q, const PgAttn &A, cudaStream_t st) {
+    if (D_.dtype == KVE_F32) return go<D, G, 2, kLnF32>(D_, Q, A, st);
+    const bool one = pg_unit_rows(D_) == 8;
+    if (D_.dtype == KVE_BF16) return one ? go<D, G, 1, kLnBf16>(D_, Q, A, st) : go<D, G, 2, kLnBf16>(D_, Q, A, st);
+    return one ? go<D, G, 1, kLnF16>(D_, Q, A, st) : go<D, G, 2, kLnF16>(D_, Q, A, st);
+}
+
+}  // namespace
+
+bool q4_dims(const KvePgShape *sh, int group, PgDims *D, Q4Shape *Q, const char **why) {
+    if (!pg_dims(sh, D, why)) return false;
+    if ((group != 32 && group != 64 && group != 128) || group > D->d)
+        return (*why = "group must be 32, 64 or 128, at most d_head"), false;
+    if (D->P < kQ4Tile) return (*why = "page_size must be 16 or more"), false;
+    Q->d = D->d;
+    Q->group = group;
+    Q->tile = q4_tile_bytes(D->d, group);
+    Q->ptiles = (D->n + kQ4Tile - 1) / kQ4Tile;
+    D->direct = D->prompt_own = false;
+    D->np = D->ns = 0;
+    D->own_sms = kPgSms;
+    D->line = D->n > 0;
+    D->few_rows = 0x7fffffff;
+    if (D->dtype != KVE_F32 && (D->n > 0 ? D->group_rows() : D->max_new) * D->g > 8) D->unit_rows = 16;
+    return true;
+}
+
+unsigned long long q4_segs(const PgDims &D) {
+    const long long busy = D.R < D.rows ? D.R : D.rows, rb = pg_unit_rows(D);
+    long long units = D.Hkv * ((long long)D.rows * D.g / rb + busy);
+    if (D.line) units += D.Hkv * ((long long)D.rows * D.g / rb + (D.S < D.rows ? D.S : D.rows));
+    return units + ln_ctas(D);
+}
+
+PgWorkspace q4_ws_layout(const PgDims &D) {
+    PgWorkspace W{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = (off + bytes + 255) & ~size_t(255);
+        return at;
+    };
+    const size_t rows = (size_t)D.rows * D.Hq * (D.np + D.ns);
+    W.part_ml = take(sizeof(float2) * rows);
+    W.part_o = take(sizeof(float) * rows * D.d);
+    const size_t segs = (size_t)q4_segs(D) * pg_seg_rows(D);
+    W.own_ml = take(sizeof(float2) * segs);
+    W.own_o = take(sizeof(float) * segs * D.d);
+    W.own_base = take(sizeof(long long) * (D.S + D.R));
+    W.own_unit = take(sizeof(int) * (D.S + D.R));
+    W.own_cpw = take(sizeof(long long));
+    W.total = off;
+    return W;
+}
+
+cudaError_t launch_q4_lines(const PgDims &D, const Q4Shape &Q, const PgAttn &A, cudaStream_t st) {
+    if (Q.d == 128)
+        return Q.group == 32 ? by_rows<128, 32>(D, Q, A, st)
+                             : (Q.group == 64 ? by_rows<128, 64>(D, Q, A, st) : by_rows<128, 128>(D, Q, A, st));
+    if (Q.d == 64) return Q.group == 32 ? by_rows<64, 32>(D, Q, A, st) : by_rows<64, 64>(D, Q, A, st);
+    return by_rows<32, 32>(D, Q, A, st);
+}
+
+}  // namespace kve
