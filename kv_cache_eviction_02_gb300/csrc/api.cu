@@ -1299,10 +1299,22 @@ int q4_attention(const KvePgShape *shape, int group, const void *q, long long q_
     A.own.seg_rows = pg_seg_rows(D);
     A.err = err;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    {
+    auto tc = [&](bool own) {
+        return D.dtype == KVE_BF16 ? launch_q4_tc<__nv_bfloat16>(D, Q, A, own, st)
+                                   : launch_q4_tc<__half>(D, Q, A, own, st);
+    };
+    cudaError_t e = cudaSuccess;
+    if (D.np > 0) {
+        ProfScope ps("q4_prompt", 1, st);
+        e = tc(false);
+    }
+    if (e == cudaSuccess) {
         ProfScope ps("q4_lines", 1, st);
         e = launch_q4_lines(D, Q, A, st);
+    }
+    if (e == cudaSuccess && D.ns > 0) {
+        ProfScope ps("q4_own", 1, st);
+        e = tc(true);
     }
     if (e == cudaSuccess) {
         ProfScope ps("q4_join", 1, st);

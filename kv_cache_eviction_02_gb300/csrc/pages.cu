@@ -17,25 +17,25 @@ namespace kve {
 //   Own rows of requests with many new rows: the same by the table's width, since lengths are known on
 //     the device only (the CTAs of splits that a request does not reach return at once).
 //   Other own rows, and all of fp32: dealt out on the device (pages_own.cu, pages_f32.cu).
-static void pg_split(PgDims *D) {
-    auto tiles_split = [](long long items, long long n, int *count, int *len) {
-        const long long tiles = (n + 127) / 128;
-        long long best = -1, per = 1;
-        // the most splits that w rounds of the SMs hold, for the first few w
-        for (long long w = (items + kPgSms - 1) / kPgSms, last = w + 12; w <= last; ++w) {
-            long long p = w * kPgSms / items;
-            if (p > 64) p = 64;
-            if (p > tiles) p = tiles;
-            const long long t = (tiles + p - 1) / p, cost = w * (t + 4);
-            if (best < 0 || cost < best) {
-                best = cost;
-                per = t;
-            }
-            if (p == tiles || p == 64) break;
+void pg_tiles_split(long long items, long long n, int *count, int *len) {
+    const long long tiles = (n + 127) / 128;
+    long long best = -1, per = 1;
+    // the most splits that w rounds of the SMs hold, for the first few w
+    for (long long w = (items + kPgSms - 1) / kPgSms, last = w + 12; w <= last; ++w) {
+        long long p = w * kPgSms / items;
+        if (p > 64) p = 64;
+        if (p > tiles) p = tiles;
+        const long long t = (tiles + p - 1) / p, cost = w * (t + 4);
+        if (best < 0 || cost < best) {
+            best = cost;
+            per = t;
         }
-        *len = (int)(per * 128);
-        *count = (int)((tiles + per - 1) / per);
-    };
+        if (p == tiles || p == 64) break;
+    }
+    *len = (int)(per * 128);
+    *count = (int)((tiles + per - 1) / per);
+}
+static void pg_split(PgDims *D) {
     D->own_sms = kPgSms;
     D->np = D->ns = 0;
     D->psplit = 128;
@@ -50,7 +50,7 @@ static void pg_split(PgDims *D) {
         const long long most = (long long)D->S * pg_tc_blocks(*D, false);  // launched per KV head
         const long long all = D->rows / per + D->S;                        // of which hold rows
         const long long items = D->Hkv * (most < all ? most : all);
-        tiles_split(items, D->n, &D->np, &D->psplit);
+        pg_tiles_split(items, D->n, &D->np, &D->psplit);
         // two warps per CTA, beside its tiles: a row takes 1 us and 1.3 for every 8 tokens, a tile 0.6, and there
         // are 3 besides (measured: 16 prompts of 2K rows with 4 requests of up to 32 own rows 115 us so, 33 with
         // a launch for the own rows; 4 of 32K 93 and 107)
@@ -72,7 +72,7 @@ static void pg_split(PgDims *D) {
     } else if (pg_many_new(*D)) {
         const long long per = pg_tile_rows(*D) * pg_pairs(*D, D->max_new);
         const long long most = (long long)D->R * pg_tc_blocks(*D, true), all = D->rows / per + D->R;
-        tiles_split(D->Hkv * (most < all ? most : all), D->cap(), &D->ns, &D->ssplit);
+        pg_tiles_split(D->Hkv * (most < all ? most : all), D->cap(), &D->ns, &D->ssplit);
     }
 }
 

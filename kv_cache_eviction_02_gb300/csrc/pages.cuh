@@ -54,6 +54,8 @@ struct PgWorkspace {
     size_t total;
 };
 
+// splits of n tokens, and their tokens, for `items` units of work of one CTA each
+void pg_tiles_split(long long items, long long n, int *count, int *len);
 bool pg_dims(const KvePgShape *sh, PgDims *D, const char **why);
 PgWorkspace pg_ws_layout(const PgDims &D);
 

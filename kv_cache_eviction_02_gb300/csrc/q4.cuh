@@ -35,6 +35,8 @@ template <int D> __host__ __device__ constexpr int q4_word(int lane, int w) {
     return (w >> 2) * 512 + lane * per + (w & 3) * 4;
 }
 
+template <int D> __host__ __device__ constexpr int q4_lane(int lane) { return lane * (D == 32 ? 8 : 16); }
+
 constexpr unsigned short kQ4Nan = 0x7FF0;
 
 // A 4-bit array as the kernels see it: tiles [block][KV head][tiles_per_block], a block being a prompt or a page.
@@ -65,6 +67,43 @@ cudaError_t launch_q4_unpack(const Q4Cache &C, cudaStream_t st);
 bool q4_dims(const KvePgShape *sh, int group, PgDims *D, Q4Shape *Q, const char **why);
 PgWorkspace q4_ws_layout(const PgDims &D);
 unsigned long long q4_segs(const PgDims &D);
+template <typename T>  // partial results over the prompts, or over the own rows of requests with many new ones
+cudaError_t launch_q4_tc(const PgDims &D, const Q4Shape &Q, const PgAttn &A, bool own, cudaStream_t st);
+extern template cudaError_t launch_q4_tc<__nv_bfloat16>(const PgDims &, const Q4Shape &, const PgAttn &, bool, cudaStream_t);
+extern template cudaError_t launch_q4_tc<__half>(const PgDims &, const Q4Shape &, const PgAttn &, bool, cudaStream_t);
 cudaError_t launch_q4_lines(const PgDims &D, const Q4Shape &Q, const PgAttn &A, cudaStream_t st);
+
+// ---- device helpers --------------------------------------------------------------------------------
+// one contiguous block into shared memory; addresses and size are multiples of 16 bytes
+__device__ __forceinline__ void q4_bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(tc::smem_u32(bar))
+        : "memory");
+}
+
+// A lane's words of a tile's K or V codes (shared-memory addresses, the lane's own offset among them).
+template <int D> __device__ __forceinline__ void q4_words(uint32_t at, uint32_t (&w)[D / 16]) {
+    if constexpr (D == 32) {
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                         : "r"(at + i * 512)
+                         : "memory");
+    }
+}
+// The parameters of a token: NG of 16 bits in (NG + 1) / 2 words.
+template <int NG> __device__ __forceinline__ void q4_params_of(uint32_t at, uint32_t (&w)[(NG + 1) / 2]) {
+    if constexpr (NG == 4)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+    else if constexpr (NG == 2)
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
+    else
+        asm volatile("{\n\t.reg .u16 x;\n\tld.shared.u16 x, [%1];\n\tcvt.u32.u16 %0, x;\n\t}" : "=r"(w[0]) : "r"(at) : "memory");
+}
 
 }  // namespace kve

@@ -80,37 +80,6 @@ __device__ __forceinline__ float lg2_approx(float x) {
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// one contiguous block into shared memory; addresses and size are multiples of 16 bytes
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            tc::smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(tc::smem_u32(bar))
-        : "memory");
-}
-
-// A lane's words of a tile's K or V codes (shared-memory addresses, the lane's own offset among them).
-template <int D> __device__ __forceinline__ void words(uint32_t at, uint32_t (&w)[D / 16]) {
-    if constexpr (D == 32) {
-        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
-    } else {
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
-                         : "r"(at + i * 512)
-                         : "memory");
-    }
-}
-// The parameters of a token: NG of 16 bits in (NG + 1) / 2 words.
-template <int NG> __device__ __forceinline__ void params_of(uint32_t at, uint32_t (&w)[(NG + 1) / 2]) {
-    if constexpr (NG == 4)
-        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
-    else if constexpr (NG == 2)
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
-    else
-        asm volatile("{\n\t.reg .u16 x;\n\tld.shared.u16 x, [%1];\n\tcvt.u32.u16 %0, x;\n\t}" : "=r"(w[0]) : "r"(at) : "memory");
-}
 template <int NG> __device__ __forceinline__ void steps_of(const uint32_t (&w)[(NG + 1) / 2], float (&s)[NG]) {
 #pragma unroll
     for (int g = 0; g < NG; ++g)
@@ -138,7 +107,7 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
     if (lane < 2) piece_unit[2 * warp + lane] = -1;
     if (threadIdx.x == 0) s_abort = 0;
     tc::mbar_fence_init();
-    pg_wait_prior();
+    if (D_.np == 0) pg_wait_prior();  // first kernel of its call (else the prompts' has waited)
     pg_launch_dependents();
 
     const int e0 = F32 || D_.line ? 0 : D_.S;  // the line's first entity
@@ -330,8 +299,8 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
             if (tc::elect_one()) {
                 tc::mbar_expect_tx(&bar[fill], t * TB);
                 const bool whole = src[1] == src[0] + TB || t == 1;
-                bulk_load(ring + fill * SB, src[0], whole ? t * TB : TB, &bar[fill]);
-                if (!whole) bulk_load(ring + fill * SB + TB, src[1], TB, &bar[fill]);
+                q4_bulk_load(ring + fill * SB, src[0], whole ? t * TB : TB, &bar[fill]);
+                if (!whole) q4_bulk_load(ring + fill * SB + TB, src[1], TB, &bar[fill]);
             }
             if (++fill == NST) fill = 0;
             togo -= t;
@@ -349,7 +318,7 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
         int starts = cc.c;       // the piece's first tile of its unit
         uint32_t phase = 0;
         const uint32_t ring_at = tc::smem_u32(ring);
-        const uint32_t codes_at = lane * (D == 32 ? 8 : 16), param_at = 2 * q4_codes(D) + (lane >> 2) * (2 * NG);
+        const uint32_t codes_at = q4_lane<D>(lane), param_at = 2 * q4_codes(D) + (lane >> 2) * (2 * NG);
 #pragma unroll 1
         while (left > 0) {
             if (togo > 0) load();
@@ -371,9 +340,9 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
                     float sk[TT][2][NG];
 #pragma unroll
                     for (int i = 0; i < TT; ++i) {
-                        words<D>(tile + i * TB + codes_at, kw[i]);
-                        params_of<NG>(tile + i * TB + param_at, kp[i][0]);
-                        params_of<NG>(tile + i * TB + param_at + 16 * NG, kp[i][1]);
+                        q4_words<D>(tile + i * TB + codes_at, kw[i]);
+                        q4_params_of<NG>(tile + i * TB + param_at, kp[i][0]);
+                        q4_params_of<NG>(tile + i * TB + param_at + 16 * NG, kp[i][1]);
                     }
 #pragma unroll
                     for (int i = 0; i < TT; ++i) {
@@ -436,9 +405,9 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
                 float sv[TT][2][NG], least[TT][2];
 #pragma unroll
                 for (int i = 0; i < TT; ++i) {
-                    words<D>(tile + i * TB + codes_at + q4_codes(D), vw[i]);
-                    params_of<NG>(tile + i * TB + param_at + q4_params(D, G), vp[i][0]);
-                    params_of<NG>(tile + i * TB + param_at + q4_params(D, G) + 16 * NG, vp[i][1]);
+                    q4_words<D>(tile + i * TB + codes_at + q4_codes(D), vw[i]);
+                    q4_params_of<NG>(tile + i * TB + param_at + q4_params(D, G), vp[i][0]);
+                    q4_params_of<NG>(tile + i * TB + param_at + q4_params(D, G) + 16 * NG, vp[i][1]);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         steps_of<NG>(vp[i][h], sv[i][h]);
@@ -671,16 +640,21 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
             *reinterpret_cast<float4 *>(W.o + row * D + col) = acc;
         }
     }
+    pg_end_after_prior();
 }
 
 // ---- host ------------------------------------------------------------------------------------------
+// Prompts of 16-bit types with more query rows than this go to tcgen05, as do the own rows of a request with more than
+// kQ4FewRows and kQ4FewScores scores.
+constexpr int kQ4LineRows = 32, kQ4FewRows = 32, kQ4FewScores = 12288;
+
 int ln_ctas(const PgDims &D) {
     const int rb = pg_unit_rows(D);
     const long long rows = (long long)D.max_new * D.g;
     long long chunks = (long long)D.R * D.Hkv * ((rows + rb - 1) / rb) * ((D.cap() + kPgChunk - 1) / kPgChunk);
     if (D.line)
         chunks += (long long)D.S * D.Hkv * ((D.group_rows() * D.g + rb - 1) / rb) * ((D.n + kPgChunk - 1) / kPgChunk);
-    return (int)(chunks < kPgSms ? chunks : kPgSms);
+    return (int)(chunks < D.own_sms ? chunks : D.own_sms);
 }
 
 template <int D, int G, int NT, int MODE>
@@ -710,8 +684,23 @@ bool q4_dims(const KvePgShape *sh, int group, PgDims *D, Q4Shape *Q, const char 
     D->np = D->ns = 0;
     D->own_sms = kPgSms;
     D->line = D->n > 0;
-    D->few_rows = 0x7fffffff;
-    if (D->dtype != KVE_F32 && (D->n > 0 ? D->group_rows() : D->max_new) * D->g > 8) D->unit_rows = 16;
+    if (D->dtype == KVE_F32) return true;
+    D->few_rows = kQ4FewRows;
+    D->few_scores = kQ4FewScores;
+    auto ctas = [](const PgDims &D, bool own) {  // per KV head, of a split: launched, and those that hold rows
+        const long long of = own ? D.R : D.S;
+        const long long per = (long long)pg_tile_rows(D) * pg_pairs(D, own ? D.max_new : D.group_rows());
+        const long long most = of * pg_tc_blocks(D, own), all = D.rows / per + of;
+        return std::make_pair(most, most < all ? most : all);
+    };
+    if (D->n > 0 && D->group_rows() * D->g > kQ4LineRows) {
+        D->line = false;
+        const auto c = ctas(*D, false);
+        pg_tiles_split(D->Hkv * c.second, D->n, &D->np, &D->psplit);
+        if (D->Hkv * c.first * D->np < kPgShare) D->own_sms = (int)(kPgSms - D->Hkv * c.first * D->np);
+    }
+    if (pg_many_new(*D)) pg_tiles_split(D->Hkv * ctas(*D, true).second, D->cap(), &D->ns, &D->ssplit);
+    if ((D->line ? D->group_rows() : D->max_new) * D->g > 8) D->unit_rows = 16;
     return true;
 }
 

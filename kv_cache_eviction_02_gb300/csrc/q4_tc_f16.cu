@@ -1,0 +1,6 @@
+// Cache in 4 bits on tcgen05: f16.
+#include "q4_tc.cuh"
+
+namespace kve {
+template cudaError_t launch_q4_tc<__half>(const PgDims &D, const Q4Shape &Q, const PgAttn &A, bool own, cudaStream_t st);
+}  // namespace kve
