@@ -1256,7 +1256,7 @@ size_t q4_workspace_size(const KvePgShape *shape, int group) {
     Q4Shape Q;
     const char *why;
     if (!q4_dims(shape, group, &D, &Q, &why)) return 0;
-    return q4_ws_layout(D).total;
+    return q4_ws_layout(D, Q).total;
 }
 
 int q4_attention(const KvePgShape *shape, int group, const void *q, long long q_row_stride,
@@ -1274,7 +1274,7 @@ int q4_attention(const KvePgShape *shape, int group, const void *q, long long q_
         return fail(KVE_EINVAL, "q4_attention: q_row_stride must hold a row and be a multiple of 16 bytes");
     if (!aligned16(q) || !aligned16(pages) || !aligned16(out) || (D.n > 0 && !aligned16(prefix)))
         return fail(KVE_EINVAL, "q4_attention: q, prefix, pages and out must be 16-byte aligned");
-    const PgWorkspace W = q4_ws_layout(D);
+    const PgWorkspace W = q4_ws_layout(D, Q);
     if (!workspace || ws_bytes < W.total)
         return fail(KVE_EWORKSPACE, "q4_attention: workspace of %zu bytes needed, %zu given", W.total,
                     workspace ? ws_bytes : (size_t)0);
@@ -1304,7 +1304,31 @@ int q4_attention(const KvePgShape *shape, int group, const void *q, long long q_
                                    : launch_q4_tc<__half>(D, Q, A, own, st);
     };
     cudaError_t e = cudaSuccess;
-    if (D.np > 0) {
+    if (D.np > 0 && Q.wide) {
+        ProfScope ps("q4_prompt", 2, st);
+        char *ws = static_cast<char *>(workspace);
+        Q4Cache C{};
+        C.D = D;
+        C.Q = Q;
+        C.cache = static_cast<uint8_t *>(const_cast<void *>(prefix));
+        C.Ko = ws + W.k16;
+        C.Vo = ws + W.v16;
+        C.s2 = C.v2 = D.d;
+        C.s1 = C.v1 = (long long)D.n * D.d;
+        C.s0 = C.v0 = D.Hkv * C.s1;
+        C.len = A.plen;
+        C.count = D.S;
+        C.rows = D.n;
+        C.err = err;
+        e = launch_q4_unpack(C, st);
+        PgAttn P = A;
+        P.Kp = C.Ko;
+        P.Vp = C.Vo;
+        P.p_prompt = C.s0;
+        P.p_head = C.s1;
+        P.p_tok = D.d;
+        if (e == cudaSuccess) e = launch_pg_prompt_tc(D, P, st);
+    } else if (D.np > 0) {
         ProfScope ps("q4_prompt", 1, st);
         e = tc(false);
     }

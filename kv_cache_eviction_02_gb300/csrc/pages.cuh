@@ -51,6 +51,7 @@ constexpr int kPgChunk = 16, kPgOwnWarps = 4, kPgF32Warps = 8, kPgF32Rows = 16;
 struct PgWorkspace {
     size_t part_ml, part_o;
     size_t own_ml, own_o, own_base, own_unit, own_cpw;
+    size_t k16, v16;  // a cache in 4 bits: its prompts in 16 (q4_wide)
     size_t total;
 };
 

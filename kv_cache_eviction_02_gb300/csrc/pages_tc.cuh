@@ -468,8 +468,8 @@ __device__ __forceinline__ void pt_softmax(const PtArgs &A, const PtBars<D, QT, 
 
 // (a function of its own where other roles would take registers from it)
 template <typename T, int D, int QT, int G, bool OWN, bool DB, typename... P>
-__device__ __noinline__ void pt_softmax_apart(const PtArgs &A, P... p) {
-    pt_softmax<T, D, QT, G, OWN, DB>(A, p...);
+__device__ __noinline__ void pt_softmax_apart(const PtArgs &A, uint64_t *bars, P... p) {
+    pt_softmax<T, D, QT, G, OWN, DB>(A, PtBars<D, QT, G>(bars), p...);
 }
 
 // ---- 4 bits ----------------------------------------------------------------------------------------
@@ -631,21 +631,27 @@ __device__ __forceinline__ void pt_v_tile(uint32_t raw, uint32_t place, int row0
 }
 // K and V of ntl tiles of 128 tokens (n tokens there): K of both halves, then V. The makers take turns at the 16-token
 // tiles; one of them may also be the one that sends for the raw halves.
-template <typename T, int D, int DR, int QT, int G, typename RAW>
-__device__ __noinline__ void pt_make_of(const PtBars<D, QT, G> &B, uint8_t *sm, int part, int lane, int n, int ntl,
-                                           RAW *raw, volatile int *abort_flag, unsigned *err) {
+template <typename T, int D, int DR, int QT, int G, bool OWN, bool SENDS>
+__device__ __noinline__ void pt_make_of(const PtArgs &A, uint64_t *bars, uint8_t *sm, int part, int lane, int s, int kh,
+                                        int t0, int t1, volatile int *abort_flag) {
     using L = PtLayout<D, QT, G>;
     constexpr int MAKERS = pt_makers<QT>();
+    const PtBars<D, QT, G> B(bars);
+    PtRaw<D, QT, G, OWN> raw(A, s, kh, t0, t1);
+    unsigned *err = A.err;
     const uint32_t base = tc::smem_u32(sm);
+    const int n = t1 - t0, ntl = (n + 127) / 128;
     for (int c = 0; c < 2 * ntl; ++c) {
         const int slot = c % L::SLOTS;
-        if (raw && !raw->upto(B, sm, (c | 1) + 1, (c | 1) + L::RAWS, lane, abort_flag)) return;
-        if (!tc::mbar_wait_warp(&B.rempty[slot], ((c / L::SLOTS) & 1) ^ 1, abort_flag, err)) return;
+        if (SENDS && !raw.upto(B, sm, (c | 1) + 1, (c | 1) + L::RAWS, lane, abort_flag)) break;
+        if (!tc::mbar_wait_warp(&B.rempty[slot], ((c / L::SLOTS) & 1) ^ 1, abort_flag, err)) break;
         const uint32_t to = base + L::RING + slot * L::TILE;
+        bool ok = true;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
             const int h = (c & ~1) + half, place = h % L::RAWS;
-            if (!tc::mbar_wait_warp(&B.raw_full[place], (h / L::RAWS) & 1, abort_flag, err)) return;
+            ok = tc::mbar_wait_warp(&B.raw_full[place], (h / L::RAWS) & 1, abort_flag, err);
+            if (!ok) break;
 #pragma unroll 1
             for (int i = (part + MAKERS * 4 - h * 4 % MAKERS) % MAKERS; i < 4; i += MAKERS) {
                 const uint32_t from = base + L::RAW + place * L::HALF + i * q4_tile_bytes(DR, G);
@@ -657,23 +663,25 @@ __device__ __noinline__ void pt_make_of(const PtBars<D, QT, G> &B, uint8_t *sm, 
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&B.raw_empty[place]);
             }
-            if (raw && !raw->upto(B, sm, 0, h + 1 + L::RAWS, lane, abort_flag)) return;
+            if (SENDS) ok = raw.upto(B, sm, 0, h + 1 + L::RAWS, lane, abort_flag);
         }
+        if (!ok) break;
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&B.rfull[slot]);
     }
+    if (SENDS) raw.drain(B, lane);
 }
-template <typename T, int D, int QT, int G, typename RAW>
-__device__ __forceinline__ void pt_make(const PtArgs &A, const PtBars<D, QT, G> &B, uint8_t *sm, int part, int lane, int n,
-                                        int ntl, RAW *raw, volatile int *abort_flag) {
+template <typename T, int D, int QT, int G, bool OWN, bool SENDS>
+__device__ __forceinline__ void pt_make(const PtArgs &A, uint64_t *bars, uint8_t *sm, int part, int lane, int s, int kh,
+                                        int t0, int t1, volatile int *abort_flag) {
     if constexpr (D == 64 && G == 32) {
         if (A.D.d == 32) {
-            pt_make_of<T, D, 32, QT, G>(B, sm, part, lane, n, ntl, raw, abort_flag, A.err);
+            pt_make_of<T, D, 32, QT, G, OWN, SENDS>(A, bars, sm, part, lane, s, kh, t0, t1, abort_flag);
             return;
         }
     }
-    pt_make_of<T, D, D, QT, G>(B, sm, part, lane, n, ntl, raw, abort_flag, A.err);
+    pt_make_of<T, D, D, QT, G, OWN, SENDS>(A, bars, sm, part, lane, s, kh, t0, t1, abort_flag);
 }
 
 // Warps: 0 TMA, 1 MMA, 2-3 own rows of short tables, then 4 softmax warps per row tile, with 4 bits
@@ -682,7 +690,7 @@ template <typename T, int D, int QT, int G, bool OWN>
 __global__ void __launch_bounds__(pt_threads<QT, G>(), 1)
     pg_prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
                         const __grid_constant__ CUtensorMap tm_k,
-                        const __grid_constant__ CUtensorMap tm_v, PtArgs A) {
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PtArgs A) {
     using L = PtLayout<D, QT, G>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -796,10 +804,13 @@ __global__ void __launch_bounds__(pt_threads<QT, G>(), 1)
             }
             int issued = 0;
             if constexpr (G != 0) {
-                PtRaw<D, QT, G, OWN> raw(A, s, kh, t0, t1);
-                if (QT == 1) raw.upto(B, sm, raw.halves, raw.halves, lane, abort_flag);
-                else pt_make<T, D, QT, G>(A, B, sm, 0, lane, t1 - t0, ntl, &raw, abort_flag);
-                raw.drain(B, lane);
+                if constexpr (QT == 1) {
+                    PtRaw<D, QT, G, OWN> raw(A, s, kh, t0, t1);
+                    raw.upto(B, sm, raw.halves, raw.halves, lane, abort_flag);
+                    raw.drain(B, lane);
+                } else {
+                    pt_make<T, D, QT, G, OWN, true>(A, bars, sm, 0, lane, s, kh, t0, t1, abort_flag);
+                }
             } else if (OWN) {
                 // a tile is up to 128 / box boxes of box = min(page, 128) rows; the lanes look up 32
                 // at a time, one lane issues (TMA takes uniform operands)
@@ -869,16 +880,16 @@ __global__ void __launch_bounds__(pt_threads<QT, G>(), 1)
             }
         } else if (G != 0 && (QT == 1 ? warp >= 8 : warp == 2 || warp == 3)) {
             if constexpr (G != 0)
-                pt_make<T, D, QT, G>(A, B, sm, QT == 1 ? warp & 3 : warp - 1, lane, t1 - t0, ntl,
-                                     static_cast<PtRaw<D, QT, G, OWN> *>(nullptr), abort_flag);
+                pt_make<T, D, QT, G, OWN, false>(A, bars, sm, QT == 1 ? warp & 3 : warp - 1, lane, s, kh, t0, t1,
+                                                 abort_flag);
         } else if (warp >= 4) {
             const int t = (warp - 4) >> 2;
             if (t < nqt && (warp & 3) < warps_of(t)) {
                 if (G != 0 && nqt == 1)
-                    pt_softmax_apart<T, D, QT, G, OWN, true>(A, B, sm, tmem, warp, lane, row0, nrow, tok0, kh, t0, t1,
+                    pt_softmax_apart<T, D, QT, G, OWN, true>(A, bars, sm, tmem, warp, lane, row0, nrow, tok0, kh, t0, t1,
                                                              see0, ntl, sp, abort_flag);
                 else if (G != 0 && QT == 2)
-                    pt_softmax_apart<T, D, QT, G, OWN, false>(A, B, sm, tmem, warp, lane, row0, nrow, tok0, kh, t0, t1,
+                    pt_softmax_apart<T, D, QT, G, OWN, false>(A, bars, sm, tmem, warp, lane, row0, nrow, tok0, kh, t0, t1,
                                                               see0, ntl, sp, abort_flag);
                 else if (nqt == 1)
                     pt_softmax<T, D, QT, G, OWN, true>(A, B, sm, tmem, warp, lane, row0, nrow, tok0, kh,

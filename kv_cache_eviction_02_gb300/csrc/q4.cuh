@@ -43,6 +43,7 @@ constexpr unsigned short kQ4Nan = 0x7FF0;
 struct Q4Shape {
     int d, group, tile;  // bytes per tile
     int ptiles;          // tiles per prompt and KV head
+    bool wide;           // prompts are read back into 16-bit arrays first, for many row tiles
 };
 
 // Calls of the cache's own kernels.
@@ -65,7 +66,7 @@ cudaError_t launch_q4_unpack(const Q4Cache &C, cudaStream_t st);
 // Sizes and splits of an attention call over 4-bit arrays; its partial results are joined by launch_pg_join.
 // A.Kp is the prompts' array, A.K the pages'.
 bool q4_dims(const KvePgShape *sh, int group, PgDims *D, Q4Shape *Q, const char **why);
-PgWorkspace q4_ws_layout(const PgDims &D);
+PgWorkspace q4_ws_layout(const PgDims &D, const Q4Shape &Q);
 unsigned long long q4_segs(const PgDims &D);
 template <typename T>  // partial results over the prompts, or over the own rows of requests with many new ones
 cudaError_t launch_q4_tc(const PgDims &D, const Q4Shape &Q, const PgAttn &A, bool own, cudaStream_t st);

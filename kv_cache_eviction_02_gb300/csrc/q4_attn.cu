@@ -646,6 +646,10 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
 // ---- host ------------------------------------------------------------------------------------------
 // Prompts of 16-bit types with more query rows than this go to tcgen05, as do the own rows of a request with more than
 // kQ4FewRows and kQ4FewScores scores.
+// Prompts of more than one row tile are read back into 16-bit arrays of the workspace (one layer's, up to kQ4WideMost
+// bytes), which the kernel of pages_tc.cu then takes as they are: the operands are made once instead of once per
+// one or two row tiles, on an SM whose issue slots the softmax of two row tiles needs.
+constexpr long long kQ4WideMost = 1LL << 32;
 constexpr int kQ4LineRows = 32, kQ4FewRows = 32, kQ4FewScores = 12288;
 
 int ln_ctas(const PgDims &D) {
@@ -680,6 +684,7 @@ bool q4_dims(const KvePgShape *sh, int group, PgDims *D, Q4Shape *Q, const char 
     Q->group = group;
     Q->tile = q4_tile_bytes(D->d, group);
     Q->ptiles = (D->n + kQ4Tile - 1) / kQ4Tile;
+    Q->wide = false;
     D->direct = D->prompt_own = false;
     D->np = D->ns = 0;
     D->own_sms = kPgSms;
@@ -695,6 +700,8 @@ bool q4_dims(const KvePgShape *sh, int group, PgDims *D, Q4Shape *Q, const char 
     };
     if (D->n > 0 && D->group_rows() * D->g > kQ4LineRows) {
         D->line = false;
+        const long long bytes = 4LL * D->S * D->Hkv * D->n * D->d;  // K and V
+        Q->wide = D->group_rows() > pg_tile_rows(*D) && bytes <= kQ4WideMost;
         const auto c = ctas(*D, false);
         pg_tiles_split(D->Hkv * c.second, D->n, &D->np, &D->psplit);
         if (D->Hkv * c.first * D->np < kPgShare) D->own_sms = (int)(kPgSms - D->Hkv * c.first * D->np);
@@ -711,7 +718,7 @@ unsigned long long q4_segs(const PgDims &D) {
     return units + ln_ctas(D);
 }
 
-PgWorkspace q4_ws_layout(const PgDims &D) {
+PgWorkspace q4_ws_layout(const PgDims &D, const Q4Shape &Q) {
     PgWorkspace W{};
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -728,6 +735,9 @@ PgWorkspace q4_ws_layout(const PgDims &D) {
     W.own_base = take(sizeof(long long) * (D.S + D.R));
     W.own_unit = take(sizeof(int) * (D.S + D.R));
     W.own_cpw = take(sizeof(long long));
+    const size_t wide = Q.wide ? 2 * (size_t)D.S * D.Hkv * D.n * D.d : 0;
+    W.k16 = take(wide);
+    W.v16 = take(wide);
     W.total = off;
     return W;
 }
