@@ -528,51 +528,6 @@ template <int D, int QT, int G, bool OWN> struct PtRaw {
     }
 };
 
-// Codes as whole numbers less their zero codes times steps, two at a time: p2 holds the parameters of the two.
-// scale() and apply() are exact but for fp16 values below its normal numbers, which round once.
-template <typename T> struct PtCodes;
-template <> struct PtCodes<__nv_bfloat16> {
-    uint32_t s, k;
-    __device__ __forceinline__ explicit PtCodes(uint32_t p2) : s(p2 & 0xFFF0FFF0u), k((p2 & 0x000F000Fu) | 0x43004300u) {}
-    __device__ __forceinline__ uint32_t of(uint32_t low_nibbles) const {
-        const uint32_t x = (low_nibbles & 0x000F000Fu) | 0x43004300u;  // 128 + n
-        const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x),
-                                                 *reinterpret_cast<const __nv_bfloat162 *>(&k)),
-                                         *reinterpret_cast<const __nv_bfloat162 *>(&s));
-        return *reinterpret_cast<const uint32_t *>(&v);
-    }
-    __device__ __forceinline__ uint32_t low(uint32_t x) const { return of(x); }
-    __device__ __forceinline__ uint32_t high(uint32_t x) const { return of(x >> 4); }
-};
-template <> struct PtCodes<__half> {
-    uint32_t a, a16, e, k, k16;  // step = a e: a power of two apart, so that only the last product can round
-    __device__ __forceinline__ explicit PtCodes(uint32_t p2) {
-        float f[2], g[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float s = __uint_as_float((i ? p2 : p2 << 16) & 0xFFF00000u);
-            const int ex = min(max((int)(__float_as_uint(s) >> 23), 103), 142);  // 2^-24 .. 2^15
-            g[i] = __uint_as_float(ex << 23);
-            f[i] = s * __uint_as_float((254 - ex) << 23);
-        }
-        const __half2 fa = __floats2half2_rn(f[0], f[1]), fe = __floats2half2_rn(g[0], g[1]);
-        const __half2 f16 = __floats2half2_rn(f[0] * 0.0625f, f[1] * 0.0625f);
-        a = *reinterpret_cast<const uint32_t *>(&fa);
-        a16 = *reinterpret_cast<const uint32_t *>(&f16);
-        e = *reinterpret_cast<const uint32_t *>(&fe);
-        k = (p2 & 0x000F000Fu) | 0x64006400u;
-        k16 = (p2 << 4 & 0x00F000F0u) | 0x64006400u;
-    }
-    __device__ __forceinline__ static uint32_t of(uint32_t x, uint32_t k, uint32_t a, uint32_t e) {
-        const __half2 v = __hmul2(__hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&k)),
-                                          *reinterpret_cast<const __half2 *>(&a)),
-                                  *reinterpret_cast<const __half2 *>(&e));
-        return *reinterpret_cast<const uint32_t *>(&v);
-    }
-    __device__ __forceinline__ uint32_t low(uint32_t x) const { return of((x & 0x000F000Fu) | 0x64006400u, k, a, e); }
-    __device__ __forceinline__ uint32_t high(uint32_t x) const { return of((x & 0x00F000F0u) | 0x64006400u, k16, a16, e); }
-};
-
 // 16 tokens of K into rows row0 .. of a ring place, as TMA lays them down.
 template <typename T, int DR, int G>
 __device__ __forceinline__ void pt_k_tile(uint32_t raw, uint32_t place, int row0, int lane) {
@@ -586,7 +541,7 @@ __device__ __forceinline__ void pt_k_tile(uint32_t raw, uint32_t place, int row0
     for (int g = 0; g < NG; ++g)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const PtCodes<T> of(__byte_perm(p[h][g >> 1], 0, g & 1 ? 0x3232 : 0x1010));
+            const Q4Codes<T> of(__byte_perm(p[h][g >> 1], 0, g & 1 ? 0x3232 : 0x1010));
             const int row = row0 + r + 8 * h;
 #pragma unroll
             for (int c = g * G / 32; c < (g + 1) * G / 32; ++c) {
@@ -615,8 +570,8 @@ __device__ __forceinline__ void pt_v_tile(uint32_t raw, uint32_t place, int row0
     const int to = lane >> 3, row = row0 + (to >> 1) * 8 + (lane & 7);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        const PtCodes<T> of0(__byte_perm(p[0][g >> 1], p[1][g >> 1], g & 1 ? 0x7632 : 0x5410));
-        const PtCodes<T> of1(__byte_perm(p[2][g >> 1], p[3][g >> 1], g & 1 ? 0x7632 : 0x5410));
+        const Q4Codes<T> of0(__byte_perm(p[0][g >> 1], p[1][g >> 1], g & 1 ? 0x7632 : 0x5410));
+        const Q4Codes<T> of1(__byte_perm(p[2][g >> 1], p[3][g >> 1], g & 1 ? 0x7632 : 0x5410));
 #pragma unroll
         for (int c = g * G / 16; c < (g + 1) * G / 16; ++c) {
             const uint32_t x = w[c], y = x >> 8;

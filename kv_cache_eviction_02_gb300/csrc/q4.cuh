@@ -107,4 +107,50 @@ template <int NG> __device__ __forceinline__ void q4_params_of(uint32_t at, uint
         asm volatile("{\n\t.reg .u16 x;\n\tld.shared.u16 x, [%1];\n\tcvt.u32.u16 %0, x;\n\t}" : "=r"(w[0]) : "r"(at) : "memory");
 }
 
+// Codes as values of a 16-bit type, two at a time: p2 holds the parameters of the two, low() takes the nibbles at bits 0
+// and 16, high() those at bits 4 and 20. Exact, but for fp16 values below its normal numbers, which round once.
+template <typename T> struct Q4Codes;
+template <> struct Q4Codes<__nv_bfloat16> {
+    uint32_t s, k;
+    __device__ __forceinline__ explicit Q4Codes(uint32_t p2) : s(p2 & 0xFFF0FFF0u), k((p2 & 0x000F000Fu) | 0x43004300u) {}
+    __device__ __forceinline__ uint32_t of(uint32_t low_nibbles) const {
+        const uint32_t x = (low_nibbles & 0x000F000Fu) | 0x43004300u;  // 128 + n
+        const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x),
+                                                 *reinterpret_cast<const __nv_bfloat162 *>(&k)),
+                                         *reinterpret_cast<const __nv_bfloat162 *>(&s));
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    __device__ __forceinline__ uint32_t low(uint32_t x) const { return of(x); }
+    __device__ __forceinline__ uint32_t high(uint32_t x) const { return of(x >> 4); }
+};
+template <> struct Q4Codes<__half> {
+    // a code at bits 4 to 7 of 64's mantissa is 64 + n; step = a e, a power of two apart: (64 + n) a - (64 + k) a has 11
+    // bits at most and only the last product can round
+    uint32_t a, c, e;
+    __device__ __forceinline__ explicit Q4Codes(uint32_t p2) {
+        float f[2], g[2], z[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float s = __uint_as_float((i ? p2 : p2 << 16) & 0xFFF00000u);
+            const int ex = min(max((int)(__float_as_uint(s) >> 23), 103), 142);  // 2^-24 .. 2^15
+            g[i] = __uint_as_float(ex << 23);
+            f[i] = s * __uint_as_float((254 - ex) << 23);
+            z[i] = -64.f * f[i] - (float)(p2 >> (16 * i) & 15u) * f[i];
+        }
+        const __half2 fa = __floats2half2_rn(f[0], f[1]), fe = __floats2half2_rn(g[0], g[1]);
+        const __half2 fz = __floats2half2_rn(z[0], z[1]);
+        a = *reinterpret_cast<const uint32_t *>(&fa);
+        e = *reinterpret_cast<const uint32_t *>(&fe);
+        c = *reinterpret_cast<const uint32_t *>(&fz);
+    }
+    __device__ __forceinline__ uint32_t high(uint32_t x) const {
+        const uint32_t y = (x & 0x00F000F0u) | 0x54005400u;
+        const __half2 v = __hmul2(__hfma2(*reinterpret_cast<const __half2 *>(&y), *reinterpret_cast<const __half2 *>(&a),
+                                          *reinterpret_cast<const __half2 *>(&c)),
+                                  *reinterpret_cast<const __half2 *>(&e));
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    __device__ __forceinline__ uint32_t low(uint32_t x) const { return high(x << 4); }
+};
+
 }  // namespace kve

@@ -41,14 +41,35 @@ template <> __device__ __forceinline__ float largest<float>() { return 3.4028234
 template <> __device__ __forceinline__ float largest<__nv_bfloat16>() { return 3.3895313892515355e38f; }
 template <> __device__ __forceinline__ float largest<__half>() { return 65504.f; }
 
-template <typename T> __device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
-    alignas(16) T v[8];
-    reinterpret_cast<uint4 *>(v)[0] = __ldg(reinterpret_cast<const uint4 *>(p));
-    if (sizeof(T) == 4)
-        reinterpret_cast<uint4 *>(v)[sizeof(T) / 4] = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+// 8 neighbouring channels as they lie in memory.
+template <typename T> struct Eight {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void zero() {
+        for (auto &x : w) x = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = to_f(v[e]);
-}
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+    }
+    __device__ __forceinline__ float at(int e) const { return to_f(reinterpret_cast<const T *>(w)[e]); }
+    __device__ __forceinline__ void range(float *lo, float *hi) const {
+        if constexpr (sizeof(T) == 2) {
+            using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+            const T2 *x = reinterpret_cast<const T2 *>(w);
+            const T2 l = __hmin2_nan(__hmin2_nan(x[0], x[1]), __hmin2_nan(x[2], x[3]));
+            const T2 h = __hmax2_nan(__hmax2_nan(x[0], x[1]), __hmax2_nan(x[2], x[3]));
+            *lo = min_nan(to_f(l.x), to_f(l.y));
+            *hi = max_nan(to_f(h.x), to_f(h.y));
+        } else {
+            *lo = *hi = at(0);
+#pragma unroll
+            for (int e = 1; e < 8; ++e) {
+                *lo = min_nan(*lo, at(e));
+                *hi = max_nan(*hi, at(e));
+            }
+        }
+    }
+};
 
 // x / s rounded to a whole number, as a float (halves toward zero); r a little below 1 / s.
 template <bool EXACT> __device__ __forceinline__ float nearest(float x, float s, float r) {
@@ -60,54 +81,73 @@ template <bool EXACT> __device__ __forceinline__ float nearest(float x, float s,
     return m;
 }
 
-// The codes of 8 values, in the low nibbles of n, and the group's parameter. The G / 8 lanes that share a group
-// are neighbours and all call.
+// The codes of four rows of 8 values, in the low nibbles of n, and their groups' parameters. The G / 8 lanes that share
+// the four groups are neighbours and all call: each of four lanes works out one row's step for all of them.
 template <typename T, int G>
-__device__ __forceinline__ unsigned short quantise8(float (&x)[8], uint32_t (&n)[8]) {
+__device__ __forceinline__ void quantise(const Eight<T> (&x)[4], uint32_t (&n)[4][8], unsigned short (&p)[4]) {
     constexpr bool EXACT = sizeof(T) == 4;
-    float lo = x[0], hi = x[0];
+    float lo[4], hi[4];
 #pragma unroll
-    for (int e = 1; e < 8; ++e) {
-        lo = min_nan(lo, x[e]);
-        hi = max_nan(hi, x[e]);
-    }
+    for (int t = 0; t < 4; ++t) x[t].range(&lo[t], &hi[t]);
+    const int lane = threadIdx.x & 31;
+    const bool up2 = lane & 2, up1 = lane & 1;  // this lane's row: lane % 4
 #pragma unroll
-    for (int o = 1; o < G / 8; o <<= 1) {
-        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    for (int i = 0; i < 2; ++i) {
+        const float sl = up2 ? lo[i] : lo[i + 2], sh = up2 ? hi[i] : hi[i + 2];
+        lo[i] = min_nan(up2 ? lo[i + 2] : lo[i], __shfl_xor_sync(0xffffffffu, sl, 2));
+        hi[i] = max_nan(up2 ? hi[i + 2] : hi[i], __shfl_xor_sync(0xffffffffu, sh, 2));
     }
-    lo = min_nan(lo, 0.f);
-    hi = max_nan(hi, 0.f);
-    const bool bad = !(hi - lo <= 3.4e38f) && !(fmaxf(hi, -lo) <= largest<float>() && lo == lo);
-    if (bad) {  // an infinity or a NaN (a range above fp32's largest number is none)
+    const float sl = up1 ? lo[0] : lo[1], sh = up1 ? hi[0] : hi[1];
+    float l = min_nan(up1 ? lo[1] : lo[0], __shfl_xor_sync(0xffffffffu, sl, 1));
+    float h = max_nan(up1 ? hi[1] : hi[0], __shfl_xor_sync(0xffffffffu, sh, 1));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) n[e] = 0;
-        return kQ4Nan;
+    for (int o = 4; o < G / 8; o <<= 1) {
+        l = min_nan(l, __shfl_xor_sync(0xffffffffu, l, o));
+        h = max_nan(h, __shfl_xor_sync(0xffffffffu, h, o));
     }
-    // 15 s >= hi - lo: from a quotient that is too small, up by at most two of the numbers of four bits. hi - lo is
+    l = min_nan(l, 0.f);
+    h = max_nan(h, 0.f);
+    // an infinity or a NaN (a range above fp32's largest number is none): no step, codes do not matter
+    const bool bad = !(fmaxf(h, -l) <= largest<float>() && l == l);
+    // 15 s >= h - l: from a quotient that is too small, up by at most two of the numbers of four bits. h - l is
     // rounded up, which leaves the answer as it is, since 15 s is exact.
-    const float down = fmaxf(hi, -lo) > 0x1p100f ? 0x1p-8f : 1.f;
-    const float t = fmaxf(__fsub_ru(hi * down, lo * down), 15 * 0x1p-126f);
-    float s = __uint_as_float(__float_as_uint(t * 0.06666665f) & 0xFFF00000u);
+    const float down = fmaxf(h, -l) > 0x1p100f ? 0x1p-8f : 1.f;
+    const float d = fmaxf(__fsub_ru(h * down, l * down), 15 * 0x1p-126f);
+    float s = __uint_as_float(__float_as_uint(d * 0.06666665f) & 0xFFF00000u);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        if (15.f * s < t) s = __uint_as_float(__float_as_uint(s) + 0x00100000u);
+        if (15.f * s < d) s = __uint_as_float(__float_as_uint(s) + 0x00100000u);
     s *= down < 1.f ? 0x1p8f : 1.f;
-    const float r = rcp_approx(s) * (1.f - 0x1p-20f);
-    float most = 15.f;
+    float r = bad ? 0.f : rcp_approx(s) * (1.f - 0x1p-20f), most = 15.f;
     if (15.f * s > largest<T>()) {  // whole numbers whose values the type still holds
         most = fminf(floorf(largest<T>() * r), 15.f);
         if ((most + 1.f) * s <= largest<T>()) most += 1.f;
     }
-    const float k = fminf(nearest<EXACT>(-lo, s, r), most), top = fminf(15.f, k + most);
+    const float k = bad ? 0.f : fminf(nearest<EXACT>(-l, s, r), most);
+    // parameter, zero code, highest code; and whether a code may have to be raised (15 s above the largest number)
+    const uint32_t mine = (bad ? (uint32_t)kQ4Nan : __float_as_uint(s) >> 16 | (uint32_t)k) |
+                          (uint32_t)fminf(15.f, k + most) << 16;
+    const bool raise = __any_sync(0xffffffffu, most < 15.f);
+    auto codes = [&](auto both) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float y;
-        if (EXACT) y = nearest<true>(x[e], s, r) + (kMagic + k);
-        else y = fmaf(x[e], r, kMagic + k);
-        n[e] = __float_as_uint(fminf(fmaxf(y, kMagic), kMagic + top));  // 0x4B400000 + code
-    }
-    return (unsigned short)(__float_as_uint(s) >> 16 | (uint32_t)k);
+        for (int t = 0; t < 4; ++t) {
+            const uint32_t y = __shfl_sync(0xffffffffu, mine, (lane & ~3) | t);
+            const float rt = __shfl_sync(0xffffffffu, r, (lane & ~3) | t);
+            p[t] = (unsigned short)y;
+            const float st = __uint_as_float((y & 0xFFF0u) << 16);
+            // kMagic + k, + the highest code: its bits are 0x4B400000 + the number
+            const float zero = __uint_as_float(0x4B400000u + (y & 15u)), top = __uint_as_float(0x4B400000u + (y >> 16));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float v = x[t].at(e);
+                float c = EXACT ? nearest<true>(v, st, rt) + zero : fmaf(v, rt, zero);
+                if (decltype(both)::value) c = fmaxf(c, kMagic);
+                n[t][e] = __float_as_uint(fminf(c, top));
+            }
+        }
+    };
+    if (raise) codes(std::true_type{});
+    else codes(std::false_type{});
 }
 
 // bytes c | (c + 2) << 4 for channels c = 0, 1, 4, 5 of K, c | (c + 1) << 4 for c = 0, 2, 4, 6 of V
@@ -125,12 +165,11 @@ __device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, u
 // Quantises 8 channels (ch .. ch + 7) of the four tokens {2 j, 2 j + 1, 2 j + 8, 2 j + 9} of a tile into it. A
 // warp may hold lanes of K and of V: what they do together comes before they part.
 template <typename T, int D, int G>
-__device__ __forceinline__ void store_quad(float (&x)[4][8], int j, int ch, bool is_v, uint8_t *tile) {
+__device__ __forceinline__ void store_quad(const Eight<T> (&x)[4], int j, int ch, bool is_v, uint8_t *tile) {
     constexpr int NG = D / G;
     uint32_t n[4][8], b[4][4];
     unsigned short p[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) p[t] = quantise8<T, G>(x[t], n[t]);
+    quantise<T, G>(x, n, p);
     if (is_v) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) pairs<true>(n[t], b[t]);
@@ -159,14 +198,13 @@ __device__ __forceinline__ void store_quad(float (&x)[4][8], int j, int ch, bool
 
 constexpr int kQ4Threads = 256;
 
-// Threads of a tile: D / 8 for its channels, 4 for its quads of tokens, K and V apart.
-template <int D> __device__ __forceinline__ long long tile_of(long long i, int *j, int *ch, bool *is_v) {
-    constexpr int C = D / 8;
-    *ch = (int)(i % C) * 8;
-    i /= C;
-    *j = (int)(i & 3);
-    *is_v = (i >> 2) & 1;
-    return i >> 3;
+// Threads of a tile: D / 8 for its channels, 4 for its quads of tokens, K and V apart. Which tile of the grid's row.
+template <int D> __device__ __forceinline__ int tile_of(int *j, int *ch, bool *is_v) {
+    const unsigned i = threadIdx.x;
+    *ch = (int)(i % (D / 8)) * 8;
+    *j = (int)(i / (D / 8) & 3);
+    *is_v = i / (D / 2) & 1;
+    return (int)(blockIdx.x * (kQ4Threads / D) + i / D);
 }
 
 // ---- a prompt as a whole ---------------------------------------------------------------------------
@@ -174,31 +212,22 @@ template <typename T, int D, int G>
 __global__ void __launch_bounds__(kQ4Threads) q4_pack_kernel(Q4Cache C) {
     pg_wait_prior();
     pg_launch_dependents();
-    const long long items = (long long)C.count * C.D.Hkv * C.Q.ptiles * D;  // 8 D / 8 threads a tile
-    const long long step = (long long)gridDim.x * kQ4Threads;
-    // (whole warps stay: a tile's threads are a multiple of 32)
-    for (long long i = (long long)blockIdx.x * kQ4Threads + threadIdx.x; i < items; i += step) {
-        int j, ch;
-        bool is_v;
-        const long long at = tile_of<D>(i, &j, &ch, &is_v);
-        const long long unit = pg_div(at, C.Q.ptiles);
-        const int tile = (int)(at - unit * C.Q.ptiles), s = (int)(unit / C.D.Hkv), h = (int)(unit - (long long)s * C.D.Hkv);
-        const int len = C.len ? pg_clamp(__ldg(C.len + s), 0, C.D.n) : C.D.n;
-        if (tile * kQ4Tile >= len) continue;
-        const T *src = static_cast<const T *>(is_v ? C.V : C.K) +
-                       (is_v ? s * C.v0 + h * C.v1 : s * C.s0 + h * C.s1) + ch;
-        const long long row = is_v ? C.v2 : C.s2;
-        float x[4][8];
+    int j, ch;
+    bool is_v;
+    const int tile = tile_of<D>(&j, &ch, &is_v), s = blockIdx.y, h = blockIdx.z;
+    const int len = C.len ? pg_clamp(__ldg(C.len + s), 0, C.D.n) : C.D.n;
+    if (tile >= (len + kQ4Tile - 1) / kQ4Tile) return;  // (whole warps: a tile's threads are a multiple of 32)
+    const T *src = static_cast<const T *>(is_v ? C.V : C.K) +
+                   (is_v ? s * C.v0 + h * C.v1 : s * C.s0 + h * C.s1) + ch;
+    const long long row = is_v ? C.v2 : C.s2;
+    Eight<T> x[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const int tok = tile * kQ4Tile + 2 * j + (t & 1) + 8 * (t >> 1);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[t][e] = 0.f;
-            if (tok < len) load8(src + tok * row, x[t]);
-        }
-        uint8_t *dst = C.cache + (size_t)at * q4_tile_bytes(D, G);
-        store_quad<T, D, G>(x, j, ch, is_v, dst);
+    for (int t = 0; t < 4; ++t) {
+        const int tok = tile * kQ4Tile + 2 * j + (t & 1) + 8 * (t >> 1);
+        x[t].zero();
+        if (tok < len) x[t].load(src + tok * row);
     }
+    store_quad<T, D, G>(x, j, ch, is_v, C.cache + (((size_t)s * C.D.Hkv + h) * C.Q.ptiles + tile) * q4_tile_bytes(D, G));
 }
 
 // ---- rows into pages -------------------------------------------------------------------------------
@@ -216,144 +245,175 @@ __device__ __forceinline__ int slot_of(const Q4Cache &C, int i) {
     return slot;
 }
 
-// A thread per row and 8 channels of K or V.
+// 8 channels of four rows, row t of them the token slot[t] % 16 of a tile (none where slot[t] < 0): byte by byte, so that
+// a tile's other tokens stay as they are.
+template <typename T, int D, int G>
+__device__ __forceinline__ void store_rows(const Q4Cache &C, const Eight<T> (&x)[4], const int (&slot)[4], int h, int ch,
+                                           bool is_v) {
+    uint32_t n[4][8], b[4];
+    unsigned short p[4];
+    quantise<T, G>(x, n, p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (slot[i] < 0) continue;
+        const int t = slot[i] & 15;
+        uint8_t *tile = page_tile(C, slot[i], h, q4_tile_bytes(D, G));
+        if (is_v) {
+            pairs<true>(n[i], b);
+            uint8_t *w = tile + q4_codes(D) + ((t & 1) << 1) + (t >> 3);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                w[q4_word<D>((((ch & 8) >> 1) + y) * 4 + ((t & 7) >> 1), ch >> 4)] = (uint8_t)b[y];
+        } else {
+            pairs<false>(n[i], b);
+            uint8_t *w = tile + q4_word<D>((t & 7) * 4 + (ch >> 3 & 3), ch >> 5 << 1) + (t >> 3);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) w[2 * y] = (uint8_t)b[y];
+        }
+        if (ch % G == 0)
+            *reinterpret_cast<unsigned short *>(tile + 2 * q4_codes(D) + (is_v ? q4_params(D, G) : 0) +
+                                                2 * (t * (D / G) + ch / G)) = p[i];
+    }
+}
+
+// The threads of a tile (tile_of) take 16 rows that stand behind one another in the batch. Rows that fill a tile of the
+// cache (16 consecutive slots) are written as one by the threads of the 16 in which they begin, as whole words; other
+// rows byte by byte (64 prompts of up to 2000 rows, fp16, 8 heads of d 128: all of them byte by byte @ us, so @).
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(Q4Cache C) {
     pg_wait_prior();
     pg_launch_dependents();
-    constexpr int LPR = D / 8;
-    const long long i = (long long)blockIdx.x * kQ4Threads + threadIdx.x;
-    const int ch = (int)(i % LPR) * 8;
-    const bool is_v = (i / LPR) & 1;
-    const long long at = pg_div(i / LPR >> 1, C.D.Hkv);
-    const int h = (int)((i / LPR >> 1) - at * C.D.Hkv), row = (int)min(at, (long long)C.D.rows);
-    int slot = -1;
-    float x[8] = {};
-    if (row < C.D.rows) slot = slot_of(C, row);
-    if (slot >= 0)
-        load8(static_cast<const T *>(is_v ? C.V : C.K) + row * (is_v ? C.v2 : C.s2) +
-                  h * (is_v ? C.v1 : C.s1) + ch, x);
-    uint8_t *tile = page_tile(C, max(slot, 0), h, q4_tile_bytes(D, G));
-    // (lanes of a warp may be of K and of V, and of rows without a slot: the shuffles are among a group's lanes)
-    uint32_t n[8], b[4];
-    const unsigned short p = quantise8<T, G>(x, n);
-    if (slot < 0) return;
-    const int t = slot & 15;
-    uint8_t *codes = tile + (is_v ? q4_codes(D) : 0);
-    if (is_v) {
-        pairs<true>(n, b);
-        const int byte = ((t & 1) << 1) + (t >> 3);
+    int j, ch;
+    bool is_v;
+    const int win = tile_of<D>(&j, &ch, &is_v), h = blockIdx.y, lane = threadIdx.x & 31;
+    if (win >= (C.D.rows + 15) / 16) return;  // (whole warps)
+    const int i0 = win * 16;
+    // slots of the 16 rows before, of these, and of the 16 behind: bit p of the masks is row i0 - 16 + p
+    auto at = [&](int i) { return i >= 0 && i < C.D.rows ? slot_of(C, i) : -1; };
+    const int sa = at(i0 - 16 + lane), sb = lane < 16 ? at(i0 + 16 + lane) : -1;
+    const int pa = __shfl_up_sync(0xffffffffu, sa, 1), last = __shfl_sync(0xffffffffu, sa, 31);
+    int pb = __shfl_up_sync(0xffffffffu, sb, 1);
+    if (lane == 0) pb = last;
+    auto follows = [](int s, int before) { return s >= 0 && (s & 15) != 0 && before >= 0 && s == before + 1; };
+    unsigned long long run = __ballot_sync(0xffffffffu, lane > 0 && follows(sa, pa)) |
+                             (unsigned long long)__ballot_sync(0xffffffffu, follows(sb, pb)) << 32;
+    run &= run >> 1;
+    run &= run >> 2;
+    run &= run >> 4;  // of 8 rows
+    run &= run >> 7;  // of 15
+    const unsigned full = __ballot_sync(0xffffffffu, sa >= 0 && (sa & 15) == 0) & (unsigned)(run >> 1);
+    unsigned long long covered = full;
+    covered |= covered << 1;
+    covered |= covered << 2;
+    covered |= covered << 4;
+    covered |= covered << 8;
+    const T *src = static_cast<const T *>(is_v ? C.V : C.K) + h * (is_v ? C.v1 : C.s1) + ch;
+    const long long row = is_v ? C.v2 : C.s2;
+    Eight<T> x[4];
+    if (full >> 16) {
+        const int first = __ffs(full >> 16) - 1;
+        const int slot = __shfl_sync(0xffffffffu, sa, 16 + first);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            codes[q4_word<D>((((ch & 8) >> 1) + i) * 4 + ((t & 7) >> 1), ch >> 4) + byte] = (uint8_t)b[i];
-    } else {
-        pairs<false>(n, b);
-        uint8_t *w = codes + q4_word<D>((t & 7) * 4 + (ch >> 3 & 3), ch >> 5 << 1) + (t >> 3);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[2 * i] = (uint8_t)b[i];
+        for (int t = 0; t < 4; ++t) x[t].load(src + (i0 + first + 2 * j + (t & 1) + 8 * (t >> 1)) * row);
+        store_quad<T, D, G>(x, j, ch, is_v, page_tile(C, slot, h, q4_tile_bytes(D, G)));
     }
-    if (ch % G == 0)
-        *reinterpret_cast<unsigned short *>(tile + 2 * q4_codes(D) + (is_v ? q4_params(D, G) : 0) +
-                                            2 * (t * (D / G) + ch / G)) = p;
+    const unsigned there = __ballot_sync(0xffffffffu, sa >= 0) >> 16;
+    if ((there & ~(unsigned)(covered >> 16) & 0xFFFFu) == 0) return;
+    int slot[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int i = j + 4 * t;
+        slot[t] = __shfl_sync(0xffffffffu, sa, 16 + i);
+        if (covered >> (16 + i) & 1) slot[t] = -1;
+        x[t].zero();
+        if (slot[t] >= 0) x[t].load(src + (i0 + i) * row);
+    }
+    store_rows<T, D, G>(C, x, slot, h, ch, is_v);
 }
 
 // ---- reading back ----------------------------------------------------------------------------------
-__device__ __forceinline__ float value(uint32_t word, int bit, float s, float off) {
-    // 2^23 + n, minus 2^23 + k: exact
-    return (__uint_as_float((word >> bit & 15u) | 0x4B000000u) - off) * s;
-}
-
-template <typename T> __device__ __forceinline__ void store8(T *p, const float (&x)[8]) {
-    alignas(16) T v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = from_f<T>(x[e]);
-    reinterpret_cast<uint4 *>(p)[0] = reinterpret_cast<uint4 *>(v)[0];
-    if (sizeof(T) == 4) reinterpret_cast<uint4 *>(p)[1] = reinterpret_cast<uint4 *>(v)[sizeof(T) / 4];
-}
-
 template <typename T, int D, int G, bool PAGES>
 __global__ void __launch_bounds__(kQ4Threads) q4_unpack_kernel(Q4Cache C) {
     pg_wait_prior();
     pg_launch_dependents();
     constexpr int NG = D / G;
-    const int tiles = (C.rows + kQ4Tile - 1) / kQ4Tile;
-    const long long items = (long long)C.count * C.D.Hkv * tiles * D;
-    const long long step = (long long)gridDim.x * kQ4Threads;
-    for (long long i = (long long)blockIdx.x * kQ4Threads + threadIdx.x; i < items; i += step) {
-        int j, ch;
-        bool is_v;
-        const long long at = tile_of<D>(i, &j, &ch, &is_v), unit = pg_div(at, tiles);
-        const int tile = (int)(at - unit * tiles), s = (int)(unit / C.D.Hkv), h = (int)(unit - (long long)s * C.D.Hkv);
-        const int len = C.len ? pg_clamp(__ldg(C.len + s), 0, C.rows) : C.rows, t0 = tile * kQ4Tile;
-        if (t0 >= len) continue;
-        const uint8_t *src;
-        if (PAGES) {
-            const int page = pg_page(C.table + (size_t)s * C.width, t0, C.D.lgP, C.D.npages, C.err);
-            src = page_tile(C, (page << C.D.lgP) + (t0 & (C.D.P - 1)), h, q4_tile_bytes(D, G));
-        } else {
-            src = C.cache + ((size_t)unit * C.Q.ptiles + tile) * q4_tile_bytes(D, G);
+    int j, ch;
+    bool is_v;
+    const int tile = tile_of<D>(&j, &ch, &is_v), s = blockIdx.y, h = blockIdx.z, t0 = tile * kQ4Tile;
+    const int len = C.len ? pg_clamp(__ldg(C.len + s), 0, C.rows) : C.rows;
+    if (tile >= (len + kQ4Tile - 1) / kQ4Tile) return;
+    const uint8_t *src;
+    if (PAGES) {
+        const int page = pg_page(C.table + (size_t)s * C.width, t0, C.D.lgP, C.D.npages, C.err);
+        src = page_tile(C, (page << C.D.lgP) + (t0 & (C.D.P - 1)), h, q4_tile_bytes(D, G));
+    } else {
+        src = C.cache + (((size_t)s * C.D.Hkv + h) * C.Q.ptiles + tile) * q4_tile_bytes(D, G);
+    }
+    const uint8_t *codes = src + (is_v ? q4_codes(D) : 0);
+    const unsigned short *params = reinterpret_cast<const unsigned short *>(
+        src + 2 * q4_codes(D) + (is_v ? q4_params(D, G) : 0)) + ch / G;
+    // K: w[0], w[1] and w[2], w[3] of tokens 2 j and 2 j + 1 (with + 8); V: w[i] of channels 2 i, 2 i + 1
+    uint32_t w[4], p[4];
+    if (is_v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = __ldg(reinterpret_cast<const uint32_t *>(codes + q4_word<D>((((ch & 8) >> 1) + i) * 4 + j, ch >> 4)));
+    } else {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(
+                codes + q4_word<D>((2 * j + u) * 4 + (ch >> 3 & 3), ch >> 5 << 1)));
+            w[2 * u] = x.x;
+            w[2 * u + 1] = x.y;
         }
-        const uint8_t *codes = src + (is_v ? q4_codes(D) : 0);
-        const unsigned short *params = reinterpret_cast<const unsigned short *>(
-            src + 2 * q4_codes(D) + (is_v ? q4_params(D, G) : 0));
-        // w[t][i]: the byte of token t (in the order 2 j, 2 j + 1, 2 j + 8, 2 j + 9) of pair i, in its low 8 bits
-        uint32_t w[4][4];
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) p[t] = __ldg(params + (2 * j + (t & 1) + 8 * (t >> 1)) * NG);
+    Eight<T> out[4];  // of tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9
+    if constexpr (sizeof(T) == 2) {
         if (is_v) {
+            const Q4Codes<T> of0(p[0] | p[1] << 16), of1(p[2] | p[3] << 16);
+            uint32_t *o[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) o[t] = reinterpret_cast<uint32_t *>(out[t].w);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t x = __ldg(reinterpret_cast<const uint32_t *>(
-                    codes + q4_word<D>((((ch & 8) >> 1) + i) * 4 + j, ch >> 4)));
-                w[0][i] = x;
-                w[2][i] = x >> 8;
-                w[1][i] = x >> 16;
-                w[3][i] = x >> 24;
+                const uint32_t a = of0.low(w[i]), b = of0.high(w[i]), c = of1.low(w[i] >> 8), d = of1.high(w[i] >> 8);
+                o[0][i] = __byte_perm(a, b, 0x5410);
+                o[1][i] = __byte_perm(a, b, 0x7632);
+                o[2][i] = __byte_perm(c, d, 0x5410);
+                o[3][i] = __byte_perm(c, d, 0x7632);
             }
         } else {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(
-                    codes + q4_word<D>((2 * j + u) * 4 + (ch >> 3 & 3), ch >> 5 << 1)));
-                w[u][0] = x.x;
-                w[u + 2][0] = x.x >> 8;
-                w[u][1] = x.x >> 16;
-                w[u + 2][1] = x.x >> 24;
-                w[u][2] = x.y;
-                w[u + 2][2] = x.y >> 8;
-                w[u][3] = x.y >> 16;
-                w[u + 2][3] = x.y >> 24;
+            for (int t = 0; t < 4; ++t) {
+                const Q4Codes<T> of(p[t] * 0x10001u);
+                const uint32_t x = w[2 * (t & 1)] >> (t & 2 ? 8 : 0), y = w[2 * (t & 1) + 1] >> (t & 2 ? 8 : 0);
+                out[t].w[0] = make_uint4(of.low(x), of.high(x), of.low(y), of.high(y));
             }
         }
-        T *dst = static_cast<T *>(is_v ? C.Vo : C.Ko) + (is_v ? s * C.v0 + h * C.v1 : s * C.s0 + h * C.s1) + ch;
-        const long long row = is_v ? C.v2 : C.s2;
+    } else {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const int tok = 2 * j + (t & 1) + 8 * (t >> 1);
-            if (t0 + tok >= len) continue;
-            const uint32_t p = __ldg(params + tok * NG + ch / G);
-            const float step = __uint_as_float((p & 0xFFF0u) << 16);
-            const float off = 8388608.f + (float)(p & 15u);
-            float x[8];
-            float lo[4], hi[4];
+            const float step = __uint_as_float((p[t] & 0xFFF0u) << 16), off = 8388608.f + (float)(p[t] & 15u);
+            float *x = reinterpret_cast<float *>(out[t].w);
+            auto value = [&](uint32_t word, int bit) {  // 2^23 + n, less 2^23 + k: exact
+                return (__uint_as_float((word >> bit & 15u) | 0x4B000000u) - off) * step;
+            };
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                lo[i] = value(w[t][i], 0, step, off);
-                hi[i] = value(w[t][i], 4, step, off);
-            }
-            if (is_v) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[2 * i] = lo[i];
-                    x[2 * i + 1] = hi[i];
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[(i & 1) + 4 * (i >> 1)] = lo[i];
-                    x[(i & 1) + 4 * (i >> 1) + 2] = hi[i];
-                }
-            }
-            store8(dst + (t0 + tok) * row, x);
+            for (int e = 0; e < 8; ++e)
+                x[e] = is_v ? value(w[e >> 1], (t >> 1) * 8 + (t & 1) * 16 + (e & 1) * 4)
+                            : value(w[2 * (t & 1) + (e >> 2)], (t >> 1) * 8 + (e & 1) * 16 + (e & 2) * 2);
         }
+    }
+    T *dst = static_cast<T *>(is_v ? C.Vo : C.Ko) + (is_v ? s * C.v0 + h * C.v1 : s * C.s0 + h * C.s1) + ch;
+    const long long row = is_v ? C.v2 : C.s2;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int tok = t0 + 2 * j + (t & 1) + 8 * (t >> 1);
+        if (tok >= len) continue;
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(dst + tok * row)[i] = out[t].w[i];
     }
 }
 
@@ -370,41 +430,39 @@ template <typename F> cudaError_t by_sizes(const Q4Shape &Q, F f) {
     if (Q.d == 64) return Q.group == 32 ? f(Int<64>{}, Int<32>{}) : f(Int<64>{}, Int<64>{});
     return f(Int<32>{}, Int<32>{});
 }
-unsigned q4_blocks(long long items, int most) {
-    const long long blocks = (items + kQ4Threads - 1) / kQ4Threads;
-    return (unsigned)(blocks < most ? blocks : most);
-}
+// blocks of kQ4Threads / d tiles
+unsigned q4_blocks(long long tiles, int d) { return (unsigned)((tiles + kQ4Threads / d - 1) / (kQ4Threads / d)); }
 
 }  // namespace
 
 cudaError_t launch_q4_pack(const Q4Cache &C, cudaStream_t st) {
-    const long long items = (long long)C.count * C.D.Hkv * C.Q.ptiles * C.D.d;
+    const dim3 grid(q4_blocks(C.Q.ptiles, C.D.d), C.count, C.D.Hkv);
     return by_type(C.D.dtype, [&](auto t) {
         return by_sizes(C.Q, [&](auto d, auto g) {
-            return pg_launch(q4_pack_kernel<decltype(t), decltype(d)::value, decltype(g)::value>,
-                             q4_blocks(items, kPgSms * 64), kQ4Threads, 0, true, st, C);
+            return pg_launch(q4_pack_kernel<decltype(t), decltype(d)::value, decltype(g)::value>, grid, kQ4Threads, 0,
+                             true, st, C);
         });
     });
 }
 
 cudaError_t launch_q4_append(const Q4Cache &C, cudaStream_t st) {
-    const long long items = (long long)C.D.rows * C.D.Hkv * 2 * (C.D.d / 8);
+    const dim3 grid(q4_blocks((C.D.rows + 15) / 16, C.D.d), C.D.Hkv);
     return by_type(C.D.dtype, [&](auto t) {
         return by_sizes(C.Q, [&](auto d, auto g) {
-            return pg_launch(q4_append_kernel<decltype(t), decltype(d)::value, decltype(g)::value>,
-                             q4_blocks(items, 0x7fffffff), kQ4Threads, 0, true, st, C);
+            return pg_launch(q4_append_kernel<decltype(t), decltype(d)::value, decltype(g)::value>, grid, kQ4Threads, 0,
+                             true, st, C);
         });
     });
 }
 
 cudaError_t launch_q4_unpack(const Q4Cache &C, cudaStream_t st) {
-    const long long items = (long long)C.count * C.D.Hkv * ((C.rows + kQ4Tile - 1) / kQ4Tile) * C.D.d;
+    const dim3 grid(q4_blocks((C.rows + kQ4Tile - 1) / kQ4Tile, C.D.d), C.count, C.D.Hkv);
     return by_type(C.D.dtype, [&](auto t) {
         return by_sizes(C.Q, [&](auto d, auto g) {
             constexpr int D = decltype(d)::value, G = decltype(g)::value;
             auto kern = C.table ? q4_unpack_kernel<decltype(t), D, G, true>
                                 : q4_unpack_kernel<decltype(t), D, G, false>;
-            return pg_launch(kern, q4_blocks(items, kPgSms * 64), kQ4Threads, 0, true, st, C);
+            return pg_launch(kern, grid, kQ4Threads, 0, true, st, C);
         });
     });
 }
