@@ -287,6 +287,9 @@ struct PgShare {
     long long total, cpw;  // chunks in all, chunks per warp
     int q;                 // entities per thread
 };
+__device__ __forceinline__ long long pg_per_share(long long total, int shares, int longest) {
+    return max(max(1LL, pg_div(total + shares - 1, shares)), min(4LL, (longest + 15) / 16LL));
+}
 template <int THREADS, int SHARES = THREADS / 32, typename F>
 __device__ __forceinline__ PgShare pg_share(int n, int Hkv, long long *csum, int *usum,
                                             const PgOwn &W, F entity) {
@@ -341,8 +344,7 @@ __device__ __forceinline__ PgShare pg_share(int n, int Hkv, long long *csum, int
     PgShare s;
     s.total = csum[THREADS];
     s.q = q;
-    const int nw = gridDim.x * SHARES;
-    s.cpw = max(max(1LL, pg_div(s.total + nw - 1, nw)), min(4LL, (s_longest + 15) / 16LL));
+    s.cpw = pg_per_share(s.total, gridDim.x * SHARES, s_longest);
     if (blockIdx.x == 0) {
         cs = csum[threadIdx.x];
         us = usum[threadIdx.x];

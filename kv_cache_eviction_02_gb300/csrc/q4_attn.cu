@@ -110,27 +110,60 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
     if (D_.np == 0) pg_wait_prior();  // first kernel of its call (else the prompts' has waited)
     pg_launch_dependents();
 
-    const int e0 = F32 || D_.line ? 0 : D_.S;  // the line's first entity
-    const PgShare sh = pg_share<THREADS, 1>(D_.S + D_.R - e0, D_.Hkv, csum, usum, W, [&](int e, int *cr, int *nb) {
+    const int e0 = F32 || D_.line ? 0 : D_.S, ents = D_.S + D_.R - e0;  // the line's first entity, and how many
+    auto entity = [&](int e, int *cr, int *nb) {
         int len, first, nq, rows;
         pg_unit_entity<F32>(D_, A, e + e0, &len, &first, &nq, &rows, cr, nb);
-    });
-    long long X0 = blockIdx.x * sh.cpw;
-    int n = 0;  // tiles of this warp
-    {
+    };
+    PgShare sh{};
+    long long X0, x = 0;
+    int n = 0, e = 0, unit = 0;  // tiles of this warp; where they begin: entity, tiles into it, units before it
+    auto mine = [&]() {
+        X0 = blockIdx.x * sh.cpw;
         const long long all = min(sh.total - X0, sh.cpw);  // of the CTA
-        if (all > 0) {
-            const long long from = all * warp / WARPS;
-            n = (int)(all * (warp + 1) / WARPS - from);
-            X0 += from;
+        if (all <= 0) return;
+        const long long from = pg_div(all * warp, WARPS);
+        n = (int)(pg_div(all * (warp + 1), WARPS) - from);
+        X0 += from;
+    };
+    if (ents <= 32) {  // every warp by itself, an entity per lane
+        int cr = 0, nb = 0;
+        if (lane < ents) entity(lane, &cr, &nb);
+        const int us = nb * D_.Hkv;
+        const long long cs = (long long)cr * us;
+        long long c = cs;
+        int u = us;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, c, o);
+            const int z = __shfl_up_sync(0xffffffffu, u, o);
+            if (lane >= o) {
+                c += y;
+                u += z;
+            }
         }
-    }
-    if (n > 0) {
-        int unit;  // the index of its first unit
-        PgCursor<F32> cc;
-        long long x;
-        int e;
+        const int longest = __reduce_max_sync(0xffffffffu, nb > 0 ? cr : 0);
+        sh.total = __shfl_sync(0xffffffffu, c, 31);
+        sh.cpw = pg_per_share(sh.total, gridDim.x, longest);
+        if (blockIdx.x == 0 && warp == 0) {
+            if (lane < ents) {
+                W.base[lane] = c - cs;
+                W.unit[lane] = u - us;
+            }
+            if (lane == 0) *W.cpw = sh.cpw;
+        }
+        mine();
+        e = __popc(__ballot_sync(0xffffffffu, c <= X0)) & 31;
+        x = X0 - __shfl_sync(0xffffffffu, c - cs, e);
+        unit = __shfl_sync(0xffffffffu, u - us, e);
+    } else {
+        sh = pg_share<THREADS, 1>(ents, D_.Hkv, csum, usum, W, entity);
+        mine();
         pg_share_find<THREADS>(csum, usum, sh, X0, &e, &x, &unit);
+    }
+    __syncthreads();  // s_abort and the pieces' marks are set
+    if (n > 0) {
+        PgCursor<F32> cc;
         cc.enter(D_, A, e + e0);
         while (x >= (long long)cc.cr * cc.nb * D_.Hkv) {
             x -= (long long)cc.cr * cc.nb * D_.Hkv;
@@ -147,63 +180,62 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
         uint8_t *ring = smem + warp * L::WARP;
         uint64_t *bar = bars[warp];
         volatile int *abort_flag = &s_abort;
-        const float k1 = kLog2e * rsqrtf((float)D);
-        uint32_t qf[NT][NS][KW][2];       // B operand of S^T: query row lane / 4 of each block
+        // ---- queries of a unit ----
+        constexpr int QW = F32 ? 2 : 1;
+        uint4 raw[NT][D / 32][QW];        // this lane's channels 32 c + 8 j .. of query row lane / 4 of each block
+        uint32_t qf[NT][NS][KW][2];       // B operand of S^T
         uint32_t zq[NT][2];               // minus the sums of q over groups 2 (j & 1), + 1
         float fc[NT][2];                  // from the products to log2 units, for this lane's columns 2 j, + 1
         float o[NT][KW][4], z[NT][4], m[NT][2], l[NT][2];
-        int see[NT][2], see_least = 0, rows, row0;
+        int see[NT][2], see_least = 0, rows, row0;  // tokens that columns see; the tiles that all of them see whole
+        const float k1 = kLog2e * rsqrtf((float)D);
         uint32_t zmask[NG], rmask[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             zmask[g] = (j & 1) == g >> 1 ? (g & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
             rmask[g] = lane >> 2 == g ? ~0u : 0u;
         }
-        auto begin = [&]() {  // of a unit, or of this warp's part of one
+        auto ask_q = [&]() {
             rows = cc.rows;
             row0 = cc.rb * RB;
-            see_least = 0x7fffffff;
 #pragma unroll
             for (int b = 0; b < NT; ++b) {
                 const int rr = row0 + 8 * b + (lane >> 2), t = rr < rows ? rr / D_.g : 0;
                 const size_t at = (cc.first + t) * A.q_row +
                                   (size_t)(cc.kh * D_.g + (rr < rows ? rr - t * D_.g : 0)) * D + j * 8;
-                float v[D / 4], most = 0.f;
+                const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(A.q) + at * (F32 ? 4 : 2));
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
-                    if (F32) {
-                        const float *p = static_cast<const float *>(A.q) + at + 32 * c;
-                        if (rr < rows) {
-                            x0 = __ldg(reinterpret_cast<const uint4 *>(p));
-                            x1 = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
-                        }
-                        v[8 * c] = __uint_as_float(x0.x);
-                        v[8 * c + 1] = __uint_as_float(x0.y);
-                        v[8 * c + 2] = __uint_as_float(x0.z);
-                        v[8 * c + 3] = __uint_as_float(x0.w);
-                        v[8 * c + 4] = __uint_as_float(x1.x);
-                        v[8 * c + 5] = __uint_as_float(x1.y);
-                        v[8 * c + 6] = __uint_as_float(x1.z);
-                        v[8 * c + 7] = __uint_as_float(x1.w);
-                    } else {
-                        if (rr < rows)
-                            x0 = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __half *>(A.q) + at + 32 * c));
-                        const uint32_t y[4] = {x0.x, x0.y, x0.z, x0.w};
+                for (int c = 0; c < D / 32; ++c)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (MODE == kLnF16) {
-                                const float2 f = unpack(y[e]);
-                                v[8 * c + 2 * e] = f.x;
-                                v[8 * c + 2 * e + 1] = f.y;
-                            } else {
-                                v[8 * c + 2 * e] = __uint_as_float(y[e] << 16);
-                                v[8 * c + 2 * e + 1] = __uint_as_float(y[e] & 0xFFFF0000u);
-                            }
-                        }
+                    for (int i = 0; i < QW; ++i) {
+                        raw[b][c][i] = make_uint4(0, 0, 0, 0);
+                        if (rr < rows) raw[b][c][i] = __ldg(p + c * (F32 ? 8 : 4) + i);
                     }
+            }
+        };
+        auto begin = [&]() {  // of a unit, or of this warp's part of one, when its queries are there
+            see_least = 0x7fffffff;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[8 * c + e]));
+            for (int b = 0; b < NT; ++b) {
+                const uint32_t *w = reinterpret_cast<const uint32_t *>(raw[b]);
+                auto value = [&](int i) {
+                    if (F32) return __uint_as_float(w[i]);
+                    if (MODE == kLnF16) {
+                        const float2 f = unpack(w[i >> 1]);
+                        return i & 1 ? f.y : f.x;
+                    }
+                    return __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+                };
+                float most = 0.f;
+                if (F32) {
+#pragma unroll
+                    for (int i = 0; i < D / 4; ++i) most = fmaxf(most, fabsf(value(i)));
+                } else {  // magnitudes as whole numbers, two at a time
+                    uint32_t x = 0;
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) x = __vmaxu2(x, w[i] & 0x7FFF7FFFu);
+                    x = max(x >> 16, x & 0xFFFFu);
+                    most = MODE == kLnF16 ? unpack(x).x : __uint_as_float(x << 16);
                 }
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
@@ -212,43 +244,42 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
                 const float back = k1 * __uint_as_float((KC ? ex - 7 : ex + 17) << 23);  // 1 / up, with 2^24 for K's codes
 #pragma unroll
                 for (int e = 0; e < 2; ++e) fc[b][e] = __shfl_sync(0xffffffffu, back, (2 * j + e) * 4);
-                float sum[NG];
 #pragma unroll
-                for (int g = 0; g < NG; ++g) sum[g] = 0.f;
-#pragma unroll
-                for (int k = 0; k < KW; ++k)  // channels 16 k + 8 j .. of which 4 are this word's
+                for (int k = 0; k < KW; ++k)  // 4 channels of this word's
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        float a = v[4 * k + 2 * h] * up, c = v[4 * k + 2 * h + 1] * up;
-                        const float f = h ? 0.0625f : 1.f;  // (the second pair's codes stand 2^4 higher)
-                        a *= f;
-                        c *= f;
+                        const float f = h ? up * 0.0625f : up;  // (the second pair's codes stand 2^4 higher)
+                        float a = value(4 * k + 2 * h) * f, c = value(4 * k + 2 * h + 1) * f;
 #pragma unroll
                         for (int i = 0; i < NS; ++i) {
                             const uint32_t y = pack(a, c);
                             qf[b][i][k][h] = y;
                             const float2 r = unpack(y);
-                            sum[16 * k / G] += (r.x + r.y) * (h ? 16.f : 1.f);
                             a -= r.x;
                             c -= r.y;
                         }
                     }
+                if (!KC) {  // sums over groups: a product with ones (and 2^4 for the second pairs)
+                    float sum[NG];
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
-                    sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+                    for (int g = 0; g < NG; ++g) {
+                        float c[4];
+#pragma unroll
+                        for (int k = g * G / 16; k < (g + 1) * G / 16; ++k) {
+                            if (k == g * G / 16) mma0(c, 0x3C003C00u, 0x3C003C00u, 0x4C004C00u, 0x4C004C00u, qf[b][0][k][0], qf[b][0][k][1]);
+                            else mma(c, 0x3C003C00u, 0x3C003C00u, 0x4C004C00u, 0x4C004C00u, qf[b][0][k][0], qf[b][0][k][1]);
+                        }
+                        // column lane / 4, which lanes with j = lane / 8 hold
+                        const float s0 = __shfl_sync(0xffffffffu, c[0], lane >> 3), s1 = __shfl_sync(0xffffffffu, c[1], lane >> 3);
+                        sum[g] = -(lane & 4 ? s1 : s0);
+                    }
+                    const float a = NG > 2 && (j & 1) ? sum[NG > 2 ? 2 : 0] : (j & 1 ? 0.f : sum[0]);
+                    const float c = NG > 2 && (j & 1) ? sum[NG > 2 ? 3 : 0] : (j & 1 || NG == 1 ? 0.f : sum[NG > 1 ? 1 : 0]);
+                    const uint32_t y = pack(a, c);
+                    const float2 r = unpack(y);
+                    zq[b][0] = j < 2 ? y : 0u;
+                    zq[b][1] = j < 2 ? pack(a - r.x, c - r.y) : 0u;
                 }
-                float a = -sum[0], c = NG > 1 ? -sum[NG > 1 ? 1 : 0] : 0.f;
-                if (j & 1) {
-                    a = NG > 2 ? -sum[NG > 2 ? 2 : 0] : 0.f;
-                    c = NG > 2 ? -sum[NG > 2 ? 3 : 0] : 0.f;
-                }
-                const uint32_t y0 = pack(a, c);
-                const float2 r0 = unpack(y0);
-                const uint32_t y1 = pack(a - r0.x, c - r0.y);
-                const float2 r1 = unpack(y1);
-                zq[b][0] = j < 2 ? y0 : (F32 ? pack(a - r0.x - r1.x, c - r0.y - r1.y) : 0u);
-                zq[b][1] = j < 2 ? y1 : 0u;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int qr = row0 + 8 * b + j * 2 + e;
@@ -264,52 +295,68 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[b][k][e] = 0.f;
             }
-            see_least = __reduce_min_sync(0xffffffffu, see_least);
+            see_least = max(__reduce_min_sync(0xffffffffu, see_least), 0) / kQ4Tile;
         };
-        // Where a stage's pages are is asked a stage before it is loaded: the table's answer (a trip to L2) is not
-        // waited for.
+        // ---- tiles on their way ----
+        // A stage is a pair of tiles, the even one first, or one where a piece begins or ends between them. A request's
+        // pages are asked for 32 at a time, a lane each, and 32 ahead of those in use: the table's answer (a trip to L2)
+        // is not waited for.
         const int tpp = D_.lgP - 4, tmask = (1 << tpp) - 1;  // tiles per page: log2, less one
-        auto stage_of = [&](const PgCursor<F32> &c, int left) { return min(min(kLnStage, left), c.cr - c.c); };
-        auto step = [&](PgCursor<F32> &c, int t) {  // to the stage behind one of t tiles
-            c.c += t - 1;
-            c.next(D_, A);
+        const uint32_t page_bytes = ((uint32_t)D_.Hkv << tpp) * TB;
+        auto stage_of = [&](int c, int end) { return min(kLnStage - (c & 1), end - c); };
+        int fill = 0, togo = n, end = min(ca.cr, ca.c + n);  // of the piece that is being loaded
+        const uint8_t *base;
+        int pages = 0, ahead = 0, page0 = 0;  // this lane's page of the 32 from page0 on, and of the next 32
+        auto ask_pages = [&](int from) {
+            const int p = from + lane;
+            if (p > (ca.cr - 1) >> tpp) return 0;
+            return __ldg(A.table + (size_t)(ca.e - D_.S) * D_.maxp + p);
         };
-        int fill = 0, togo = n, page[2];  // of the next stage to load
-        auto where = [&]() {
-            page[0] = page[1] = 0;
-            if (ca.e < D_.S) return;
-            const int32_t *row = A.table + (size_t)(ca.e - D_.S) * D_.maxp;
-            page[0] = __ldg(row + (ca.c >> tpp));
-            page[1] = __ldg(row + (min(ca.c + 1, ca.cr - 1) >> tpp));
+        auto enter = [&]() {  // the piece to load
+            if (ca.e < D_.S) {
+                base = static_cast<const uint8_t *>(A.Kp) + ((size_t)ca.e * D_.Hkv + ca.kh) * ptiles * TB;
+            } else {
+                base = static_cast<const uint8_t *>(A.K) + ((size_t)ca.kh << tpp) * TB;
+                page0 = (ca.c >> tpp) & ~31;
+                pages = ask_pages(page0);
+                ahead = ask_pages(page0 + 32);
+            }
         };
         auto load = [&]() {
-            const int t = stage_of(ca, togo);
-            const uint8_t *src[2];
-            const bool prompt = ca.e < D_.S;
-            if (prompt) {
-                src[0] = static_cast<const uint8_t *>(A.Kp) + (((size_t)ca.e * D_.Hkv + ca.kh) * ptiles + ca.c) * TB;
-                src[1] = src[0] + TB;
+            const int t = stage_of(ca.c, end);
+            const uint8_t *src = base, *src1 = nullptr;
+            if (ca.e < D_.S) {
+                src += (size_t)ca.c * TB;
             } else {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    src[i] = static_cast<const uint8_t *>(A.K) +
-                             ((((size_t)pg_page_id(page[i], D_.npages, A.err) * D_.Hkv + ca.kh) << tpp) +
-                              ((ca.c + i) & tmask)) * TB;
+                if ((ca.c >> tpp) - page0 == 32) {
+                    page0 += 32;
+                    pages = ahead;
+                    ahead = ask_pages(page0 + 32);
+                }
+                auto page_at = [&](int c) {
+                    return base + (size_t)pg_page_id(__shfl_sync(0xffffffffu, pages, (c >> tpp) & 31), D_.npages, A.err) *
+                                      page_bytes;
+                };
+                src = page_at(ca.c) + (ca.c & tmask) * TB;
+                if (tmask == 0 && t == 2) src1 = page_at(ca.c + 1);
             }
             if (tc::elect_one()) {
                 tc::mbar_expect_tx(&bar[fill], t * TB);
-                const bool whole = src[1] == src[0] + TB || t == 1;
-                q4_bulk_load(ring + fill * SB, src[0], whole ? t * TB : TB, &bar[fill]);
-                if (!whole) q4_bulk_load(ring + fill * SB + TB, src[1], TB, &bar[fill]);
+                q4_bulk_load(ring + fill * SB, src, src1 ? TB : t * TB, &bar[fill]);
+                if (src1) q4_bulk_load(ring + fill * SB + TB, src1, TB, &bar[fill]);
             }
             if (++fill == NST) fill = 0;
+            ca.c += t;
             togo -= t;
-            if (togo > 0) {
-                step(ca, t);
-                where();
+            if (ca.c == end && togo > 0) {
+                --ca.c;
+                ca.next(D_, A);
+                end = min(ca.cr, togo);
+                enter();
             }
         };
-        where();
+        ask_q();
+        enter();
 #pragma unroll 1
         for (int i = 0; i < NST - 1 && togo > 0; ++i) load();
         begin();
@@ -322,7 +369,7 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
 #pragma unroll 1
         while (left > 0) {
             if (togo > 0) load();
-            const int nt = stage_of(cc, left);
+            const int nt = stage_of(cc.c, min(cc.cr, cc.c + left));
             if (!tc::mbar_wait_warp(&bar[slot], phase, abort_flag, A.err)) break;
             uint32_t tile = ring_at + slot * SB;
             if (++slot == NST) {
@@ -527,7 +574,7 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
                 }
             };
             // tiles that all rows see whole, then the others
-            const int whole = min(nt, see_least / kQ4Tile - cc.c);
+            const int whole = min(nt, see_least - cc.c);
             if (PAIR && whole == 2) {
                 work(std::integral_constant<int, PAIR ? 2 : 1>{}, std::false_type{});
             } else {
@@ -595,12 +642,13 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
                 ++unit;
             }
             __syncwarp();  // the stage's readers are done: the next issue may overwrite it
-            if (left > 0) {
-                step(cc, nt);
-                if (cc.c == 0) {
-                    starts = 0;
-                    begin();
-                }
+            cc.c += nt;
+            if (left > 0 && cc.c == cc.cr) {
+                --cc.c;
+                cc.next(D_, A);
+                starts = 0;
+                ask_q();
+                begin();
             }
         }
         if (s_abort) {  // copies still in flight land before the block ends
