@@ -124,6 +124,7 @@ bool pg_dims(const KvePgShape *sh, PgDims *D, const char **why) {
     D->max_new = sh->max_new < sh->n_rows ? sh->max_new : sh->n_rows;
     D->dtype = sh->dtype;
     D->unit_rows = D->dtype != KVE_F32 && (long long)D->max_new * D->g <= 8 ? 8 : 16;
+    D->pad = 0;
     D->few_rows = kPgFewRows;
     D->few_scores = kPgFewScores;
     pg_split(D);
@@ -473,7 +474,7 @@ template <bool F32> struct PgFound {
         // pieces of a unit: query row rr of entity e
         auto pieces = [&](int e, int rr, int chunks, int blocks, long long *at_row, int *count) {
             const int lg = pg_unit_rows(D) == 16 ? 4 : 3, u = kh * blocks + (rr >> lg);
-            const long long c = A.own.base[e] + (long long)u * chunks, cpw = *A.own.cpw;
+            const long long c = A.own.base[e] + (long long)u * (chunks + D.pad) + D.pad, cpw = *A.own.cpw;
             const long long w0 = pg_div(c, cpw), w1 = chunks > 0 ? pg_div(c + chunks - 1, cpw) : w0 - 1;
             const long long at = A.own.unit[e] + u + w0;
             // as many as there are places (all, when the row starts are sums of lengths)

@@ -23,6 +23,7 @@ struct PgDims {
     bool prompt_own;           // the prompt's kernel does the own rows too (split np)
     int few_rows, few_scores;  // pg_on_tc
     int unit_rows;             // pg_unit_rows
+    int pad;                   // chunks that a unit counts for beside its own (its set-up; a cache in 4 bits)
     // rows behind one prompt, when no request packs more than max_new
     __host__ __device__ long long group_rows() const {
         return (long long)F * max_new < rows ? (long long)F * max_new : rows;
@@ -292,7 +293,7 @@ __device__ __forceinline__ long long pg_per_share(long long total, int shares, i
 }
 template <int THREADS, int SHARES = THREADS / 32, typename F>
 __device__ __forceinline__ PgShare pg_share(int n, int Hkv, long long *csum, int *usum,
-                                            const PgOwn &W, F entity) {
+                                            const PgOwn &W, F entity, int pad = 0) {
     const int lane = threadIdx.x & 31, q = (n + THREADS - 1) / THREADS;
     const int a = min(n, (int)threadIdx.x * q), z = min(n, a + q);
     long long cs = 0;
@@ -300,7 +301,7 @@ __device__ __forceinline__ PgShare pg_share(int n, int Hkv, long long *csum, int
     for (int e = a; e < z; ++e) {
         int cr, nb;
         entity(e, &cr, &nb);
-        cs += (long long)cr * nb * Hkv;
+        cs += (long long)(cr + pad) * nb * Hkv;
         us += nb * Hkv;
         if (nb > 0) longest = max(longest, cr);
     }
@@ -353,7 +354,7 @@ __device__ __forceinline__ PgShare pg_share(int n, int Hkv, long long *csum, int
             entity(e, &cr, &nb);
             W.base[e] = cs;
             W.unit[e] = us;
-            cs += (long long)cr * nb * Hkv;
+            cs += (long long)(cr + pad) * nb * Hkv;
             us += nb * Hkv;
         }
         if (threadIdx.x == 0) *W.cpw = s.cpw;

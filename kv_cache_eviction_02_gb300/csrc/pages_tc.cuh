@@ -1,7 +1,7 @@
 // The kernel of pages_tc.cu on tcgen05, whose K and V come from 16-bit arrays (G = 0) or from a cache in 4 bits in
 // groups of G channels (q4.cuh). What differs then: a raw tile arrives as it lies (bulk copies of 64 tokens), and
-// warps turn its codes into the operands that TMA would have brought (with one row tile per CTA four more warps, with
-// two, which leave it twice the time, the three that are neither the products' nor a softmax's): n - k from 128 + n (bf16) or 1024 +
+// warps turn its codes into the operands that TMA would have brought (all that are neither the products' nor a softmax's:
+// three, with one row tile per CTA four more less the one that sends for the tiles): n - k from 128 + n (bf16) or 1024 +
 // n (fp16), exactly, times the step, which is exact too, since s m has 8 significant bits. K's words hold 8
 // channels of a token, a 16-byte store; V's hold tokens side by side, and stmatrix turns them, which leaves the
 // 8 even channels of every 16 before the 8 odd ones: the epilogue puts O's columns back in order.
@@ -46,10 +46,10 @@ template <> __device__ __forceinline__ uint32_t pt_pack<__half>(float a, float b
 template <int D, int QT, int G> struct PtLayout {
     static constexpr int KB = D / 64;  // 128-byte column blocks of a row
     static constexpr uint32_t TILE = KB * 16384;
-    static constexpr int SLOTS = G ? (D == 128 ? (QT == 2 ? 4 : 5) : 8)
+    static constexpr int SLOTS = G ? (D == 128 ? 4 : 8)
                                    : (D == 128 ? (QT == 2 ? 5 : 6) : (QT == 2 ? 11 : 12));
     static constexpr uint32_t RING = QT * TILE, RAW = RING + SLOTS * TILE;
-    static constexpr int RAWS = G ? 3 : 0, HALF = G ? 4 * q4_tile_bytes(D, G ? G : 32) : 0;
+    static constexpr int RAWS = G ? (QT == 1 || D == 64 ? 6 : 3) : 0, HALF = G ? 4 * q4_tile_bytes(D, G ? G : 32) : 0;
     static constexpr uint32_t BAR = (RAW + RAWS * HALF + 127) / 128 * 128;
     static constexpr int NBAR = 1 + 2 * SLOTS + 9 + 2 * RAWS;
     static constexpr size_t SMEM = BAR + 512 + 1024;
@@ -61,7 +61,7 @@ struct PtDesc {
     uint64_t q, k, v;  // of row tile 0 and of ring place 0 as K and as V
 };
 template <int QT, int G> constexpr int pt_threads() { return (4 + 4 * QT + (G && QT == 1 ? 4 : 0)) * 32; }
-template <int QT> constexpr int pt_makers() { return QT == 1 ? 4 : 3; }  // warps that make operands
+template <int QT> constexpr int pt_makers() { return QT == 1 ? 6 : 3; }  // warps that make operands
 
 struct PtArgs {
     PgDims D;
@@ -608,7 +608,7 @@ __device__ __noinline__ void pt_make_of(const PtArgs &A, uint64_t *bars, uint8_t
             ok = tc::mbar_wait_warp(&B.raw_full[place], (h / L::RAWS) & 1, abort_flag, err);
             if (!ok) break;
 #pragma unroll 1
-            for (int i = (part + MAKERS * 4 - h * 4 % MAKERS) % MAKERS; i < 4; i += MAKERS) {
+            for (int i = (part + MAKERS - (2 * c + half) * 4 % MAKERS) % MAKERS; i < 4; i += MAKERS) {
                 const uint32_t from = base + L::RAW + place * L::HALF + i * q4_tile_bytes(DR, G);
                 const int row0 = half * 64 + i * 16;
                 if (c & 1) pt_v_tile<T, DR, G>(from, to, row0, n - (c >> 1) * 128 - row0, lane);
@@ -833,9 +833,9 @@ __global__ void __launch_bounds__(pt_threads<QT, G>(), 1)
                 tc::mma_commit(B.drain);
                 tc::mbar_drain(B.drain, 0);
             }
-        } else if (G != 0 && (QT == 1 ? warp >= 8 : warp == 2 || warp == 3)) {
+        } else if (G != 0 && (warp == 2 || warp == 3 || (QT == 1 && warp >= 8))) {
             if constexpr (G != 0)
-                pt_make<T, D, QT, G, OWN, false>(A, bars, sm, QT == 1 ? warp & 3 : warp - 1, lane, s, kh, t0, t1,
+                pt_make<T, D, QT, G, OWN, false>(A, bars, sm, QT == 2 ? warp - 1 : (warp < 4 ? warp - 2 : warp - 6), lane, s, kh, t0, t1,
                                                  abort_flag);
         } else if (warp >= 4) {
             const int t = (warp - 4) >> 2;

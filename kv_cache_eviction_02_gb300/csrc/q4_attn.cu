@@ -31,6 +31,10 @@ constexpr float kLnUp = 7.f, kLnGrow = 15.f, kLnLeastStep = 0x1p-32f;
 // codes (for fp32 K's too) are made normal numbers n - k, by one subtraction from 1024 + n.
 enum { kLnBf16, kLnF16, kLnF32 };
 
+// A unit's set-up (its queries, its pages' numbers, a first tile from memory, its result) takes a warp as long as some
+// tiles: so many that it counts for in the line, before its own.
+constexpr int kLnPad = 3;
+
 constexpr int kLnStage = 2;  // tiles per ring place: at most, of one unit
 // One CTA per SM, of as many warps as its registers hold, and a ring of what shared memory has room for.
 template <int D, int G, int NT, int MODE> struct Ln {
@@ -130,7 +134,7 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
         int cr = 0, nb = 0;
         if (lane < ents) entity(lane, &cr, &nb);
         const int us = nb * D_.Hkv;
-        const long long cs = (long long)cr * us;
+        const long long cs = (long long)(cr + kLnPad) * us;
         long long c = cs;
         int u = us;
 #pragma unroll
@@ -157,7 +161,7 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
         x = X0 - __shfl_sync(0xffffffffu, c - cs, e);
         unit = __shfl_sync(0xffffffffu, u - us, e);
     } else {
-        sh = pg_share<THREADS, 1>(ents, D_.Hkv, csum, usum, W, entity);
+        sh = pg_share<THREADS, 1>(ents, D_.Hkv, csum, usum, W, entity, kLnPad);
         mine();
         pg_share_find<THREADS>(csum, usum, sh, X0, &e, &x, &unit);
     }
@@ -165,16 +169,23 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
     if (n > 0) {
         PgCursor<F32> cc;
         cc.enter(D_, A, e + e0);
-        while (x >= (long long)cc.cr * cc.nb * D_.Hkv) {
-            x -= (long long)cc.cr * cc.nb * D_.Hkv;
+        auto tiles = [&]() { return (long long)(cc.cr + kLnPad) * cc.nb * D_.Hkv; };
+        while (x >= tiles()) {
+            x -= tiles();
             unit += cc.nb * D_.Hkv;
             cc.enter(D_, A, cc.e + 1);
         }
-        const int u = (int)pg_div(x, cc.cr);
-        cc.c = (int)(x - (long long)u * cc.cr);
+        const int u = (int)pg_div(x, cc.cr + kLnPad);
+        cc.c = (int)(x - (long long)u * (cc.cr + kLnPad)) - kLnPad;
         cc.kh = u / cc.nb;
         cc.rb = u - cc.kh * cc.nb;
         unit += u;
+        if (cc.c < 0) {  // the share begins in the unit's set-up
+            n += cc.c;
+            cc.c = 0;
+        }
+
+        if (n > 0) {
         PgCursor<F32> ca = cc;  // runs ahead: the tiles to load
 
         uint8_t *ring = smem + warp * L::WARP;
@@ -348,7 +359,7 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
             if (++fill == NST) fill = 0;
             ca.c += t;
             togo -= t;
-            if (ca.c == end && togo > 0) {
+            if (ca.c == end && (togo -= kLnPad) > 0) {
                 --ca.c;
                 ca.next(D_, A);
                 end = min(ca.cr, togo);
@@ -584,7 +595,7 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
                     else work(std::integral_constant<int, 1>{}, std::true_type{});
             }
             left -= nt;
-            const bool ends = left == 0 || cc.c + nt == cc.cr;
+            const bool last = left == 0 || (cc.c + nt == cc.cr && left <= kLnPad), ends = last || cc.c + nt == cc.cr;
             // The zero codes' sums leave the codes' every few tiles: both grow with all weights, their difference only
             // as the values do, and the tensor cores cut the bits off that a large sum has no room for.
             if (!VC && (ends || (left & 2))) {
@@ -609,10 +620,10 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
                 // one that does not hold all of its unit waits for the other warps' pieces: a warp's last one where its
                 // ring was, which is empty now, one before it, its first, behind the ring
                 const bool open = starts > 0 || cc.c + nt < cc.cr;
-                uint8_t *to = left == 0 ? ring : ring + NST * SB;
+                uint8_t *to = last ? ring : ring + NST * SB;
                 if (open && lane == 0) {
-                    piece_unit[2 * warp + (left == 0)] = unit;
-                    piece_rows[2 * warp + (left == 0)] = min(RB, rows - row0);
+                    piece_unit[2 * warp + last] = unit;
+                    piece_rows[2 * warp + last] = min(RB, rows - row0);
                 }
 #pragma unroll
                 for (int b = 0; b < NT; ++b)
@@ -643,7 +654,7 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
             }
             __syncwarp();  // the stage's readers are done: the next issue may overwrite it
             cc.c += nt;
-            if (left > 0 && cc.c == cc.cr) {
+            if (cc.c == cc.cr && (left -= kLnPad) > 0) {
                 --cc.c;
                 cc.next(D_, A);
                 starts = 0;
@@ -656,6 +667,7 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
                 tc::mbar_drain(&bar[k], 0);
                 tc::mbar_drain(&bar[k], 1);
             }
+        }
         }
     }
     // pieces of one unit stand behind one another
@@ -698,7 +710,8 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
 // bytes), which the kernel of pages_tc.cu then takes as they are: the operands are made once instead of once per
 // one or two row tiles, on an SM whose issue slots the softmax of two row tiles needs.
 constexpr long long kQ4WideMost = 1LL << 32;
-constexpr int kQ4LineRows = 32, kQ4FewRows = 32, kQ4FewScores = 12288;
+// us, by lines and on tcgen05 (32/8 heads of d 128, bf16): @
+constexpr int kQ4LineRows = 16, kQ4FewRows = 32, kQ4FewScores = 32768, kQ4FewUnits = 128;
 
 int ln_ctas(const PgDims &D) {
     const int rb = pg_unit_rows(D);
@@ -714,11 +727,9 @@ cudaError_t go(const PgDims &D_, const Q4Shape &Q, const PgAttn &A, cudaStream_t
     using L = Ln<D, G, NT, MODE>;
     return pg_launch(q4_line_kernel<D, G, NT, MODE>, ln_ctas(D_), L::THREADS, L::SMEM, true, st, D_, A, A.own, Q.ptiles);
 }
-template <int D, int G> cudaError_t by_rows(const PgDims &D_, const Q4Shape &Q, const PgAttn &A, cudaStream_t st) {
+template <int D, int G> cudaError_t by_type(const PgDims &D_, const Q4Shape &Q, const PgAttn &A, cudaStream_t st) {
     if (D_.dtype == KVE_F32) return go<D, G, 2, kLnF32>(D_, Q, A, st);
-    const bool one = pg_unit_rows(D_) == 8;
-    if (D_.dtype == KVE_BF16) return one ? go<D, G, 1, kLnBf16>(D_, Q, A, st) : go<D, G, 2, kLnBf16>(D_, Q, A, st);
-    return one ? go<D, G, 1, kLnF16>(D_, Q, A, st) : go<D, G, 2, kLnF16>(D_, Q, A, st);
+    return D_.dtype == KVE_BF16 ? go<D, G, 1, kLnBf16>(D_, Q, A, st) : go<D, G, 1, kLnF16>(D_, Q, A, st);
 }
 
 }  // namespace
@@ -737,9 +748,10 @@ bool q4_dims(const KvePgShape *sh, int group, PgDims *D, Q4Shape *Q, const char 
     D->np = D->ns = 0;
     D->own_sms = kPgSms;
     D->line = D->n > 0;
+    D->pad = kLnPad;
     if (D->dtype == KVE_F32) return true;
     D->few_rows = kQ4FewRows;
-    D->few_scores = kQ4FewScores;
+    D->few_scores = D->R * D->Hkv >= kQ4FewUnits ? kQ4FewScores : 0x7fffffff;
     auto ctas = [](const PgDims &D, bool own) {  // per KV head, of a split: launched, and those that hold rows
         const long long of = own ? D.R : D.S;
         const long long per = (long long)pg_tile_rows(D) * pg_pairs(D, own ? D.max_new : D.group_rows());
@@ -755,7 +767,7 @@ bool q4_dims(const KvePgShape *sh, int group, PgDims *D, Q4Shape *Q, const char 
         if (D->Hkv * c.first * D->np < kPgShare) D->own_sms = (int)(kPgSms - D->Hkv * c.first * D->np);
     }
     if (pg_many_new(*D)) pg_tiles_split(D->Hkv * ctas(*D, true).second, D->cap(), &D->ns, &D->ssplit);
-    if ((D->line ? D->group_rows() : D->max_new) * D->g > 8) D->unit_rows = 16;
+    D->unit_rows = 8;
     return true;
 }
 
@@ -792,10 +804,10 @@ PgWorkspace q4_ws_layout(const PgDims &D, const Q4Shape &Q) {
 
 cudaError_t launch_q4_lines(const PgDims &D, const Q4Shape &Q, const PgAttn &A, cudaStream_t st) {
     if (Q.d == 128)
-        return Q.group == 32 ? by_rows<128, 32>(D, Q, A, st)
-                             : (Q.group == 64 ? by_rows<128, 64>(D, Q, A, st) : by_rows<128, 128>(D, Q, A, st));
-    if (Q.d == 64) return Q.group == 32 ? by_rows<64, 32>(D, Q, A, st) : by_rows<64, 64>(D, Q, A, st);
-    return by_rows<32, 32>(D, Q, A, st);
+        return Q.group == 32 ? by_type<128, 32>(D, Q, A, st)
+                             : (Q.group == 64 ? by_type<128, 64>(D, Q, A, st) : by_type<128, 128>(D, Q, A, st));
+    if (Q.d == 64) return Q.group == 32 ? by_type<64, 32>(D, Q, A, st) : by_type<64, 64>(D, Q, A, st);
+    return by_type<32, 32>(D, Q, A, st);
 }
 
 }  // namespace kve
