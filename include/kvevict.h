@@ -485,12 +485,16 @@ size_t q4_workspace_size(const KvePgShape *shape, int group);
 
 /* pg_attention with K and V held in 4 bits: the same rows see the same rows, with prefix for K_prefix and V_prefix and
  * pages for K_pages and V_pages (prefix may be NULL where n_prefix is 0). Scores, maxima, sums and results
- * before the last rounding are fp32. Products with the codes are exact but for these roundings: 16-bit queries are
- * off by at most 2^-32 of their row's largest entry (fp32 ones by 2^-22 of themselves), sums of q that go with zero
- * codes by 2^-22 (fp32: 2^-33); 16-bit types round each unnormalised weight times its step once to 16 bits
- * before it meets V's codes (half a step; fp32: 2^-22). Weights times steps below 2^-31 of the largest are lost.
- * Requirements as in pg_attention; q and steps are below 2^89 and the scores q.k too. A NaN that a row sees in K makes
- * its output NaN, one in V the channels of its group. */
+ * before the last rounding are fp32. What is rounded to fewer bits: 16-bit types, each unnormalised weight (or weight
+ * times step) once to the type, or to fp16, before it meets V (half a step; fp32 takes two fp16 numbers, 2^-22); queries
+ * of few rows, carried as fp16 below their row's largest entry, off by at most 2^-28 of it (fp32: two fp16
+ * numbers). Sums of products with codes are cut at 2^-17 of their terms (bf16), 2^-20 (fp16, fp32). Weights below 2^-31
+ * of the largest are lost.
+ * Prompts of 16-bit types behind more than one row tile of 128 query rows are read back into the workspace, one
+ * layer's n_prompts * n_kv_heads * n_prefix * d_head values of K and V, if that is 4 GiB at most.
+ * Requirements as in pg_attention; q, steps and scores are below 2^89. A row that sees a NaN in K is NaN, one that
+ * sees a NaN in V is NaN in that group's channels and may be in its head's others; other rows of a prompt's requests,
+ * or of the same request, that share a tile of query rows with it may be too. */
 int q4_attention(const KvePgShape *shape, int group, const void *q, long long q_row_stride,
                  const void *prefix, const int32_t *prefix_len, const void *pages,
                  const int32_t *block_table, const int32_t *len, const int32_t *q_start,

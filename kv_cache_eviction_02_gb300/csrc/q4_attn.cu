@@ -750,6 +750,7 @@ bool q4_dims(const KvePgShape *sh, int group, PgDims *D, Q4Shape *Q, const char 
     D->line = D->n > 0;
     D->pad = kLnPad;
     if (D->dtype == KVE_F32) return true;
+    D->unit_rows = 8;
     D->few_rows = kQ4FewRows;
     D->few_scores = D->R * D->Hkv >= kQ4FewUnits ? kQ4FewScores : 0x7fffffff;
     auto ctas = [](const PgDims &D, bool own) {  // per KV head, of a split: launched, and those that hold rows
@@ -758,7 +759,7 @@ bool q4_dims(const KvePgShape *sh, int group, PgDims *D, Q4Shape *Q, const char 
         const long long most = of * pg_tc_blocks(D, own), all = D.rows / per + of;
         return std::make_pair(most, most < all ? most : all);
     };
-    if (D->n > 0 && D->group_rows() * D->g > kQ4LineRows) {
+    if (D->n > 0 && D->group_rows() * D->g > kQ4LineRows && !pg_short_prompts(*D)) {
         D->line = false;
         const long long bytes = 4LL * D->S * D->Hkv * D->n * D->d;  // K and V
         Q->wide = D->group_rows() > pg_tile_rows(*D) && bytes <= kQ4WideMost;
@@ -767,7 +768,6 @@ bool q4_dims(const KvePgShape *sh, int group, PgDims *D, Q4Shape *Q, const char 
         if (D->Hkv * c.first * D->np < kPgShare) D->own_sms = (int)(kPgSms - D->Hkv * c.first * D->np);
     }
     if (pg_many_new(*D)) pg_tiles_split(D->Hkv * ctas(*D, true).second, D->cap(), &D->ns, &D->ssplit);
-    D->unit_rows = 8;
     return true;
 }
 
