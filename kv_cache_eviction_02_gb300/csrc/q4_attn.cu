@@ -8,13 +8,21 @@
 // a score is a product per group, times s in fp32, and the terms of the zero codes are products too: A holds k_g of
 // the 16 tokens, B the sums of q (as two fp16 numbers, off by 2^-22; fp32 three), or the same weights p s as the codes'.
 // Queries are carried as fp16 after their row's largest entry is brought to 2^7 .. 2^8 (bf16 and fp16 entries keep all
-// their bits down to 2^-17 of the largest, smaller ones are off by 2^-32 of it; fp32 ones are two fp16
+// their bits down to 2^-17 of the largest, smaller ones are off by 2^-28 of it; fp32 ones are two fp16
 // numbers). Weights p s are fp32 numbers rounded once to fp16, half a step (fp32: two fp16 numbers).
 //
 // Work is dealt out as in pages_own.cu: units (request or prompt, KV head, 8 or 16 query rows) and their tiles of 16
 // tokens in one line, equal shares for all CTAs (one per SM) and in them for their warps, a ring of tiles per warp that
 // runs on across units. A tile is one contiguous block: one bulk copy by one lane. Pieces of a unit that several
 // warps of a CTA have seen are joined in shared memory, so a CTA hands on one partial result of a unit.
+//
+// One request behind 128K rows (32/8 heads of d 128, groups of 32, 151 MB): 43 us, of which the set-up until the first
+// product takes 3.5, the tiles 30 (5.0 TB/s), the join 8. 64 requests with caches of up to 16K rows (groups of 64, 572
+// MB): 124 us, 4.6 TB/s, 287 instructions a tile and warp, the logic unit busy for 0.52 of the time and a warp's own
+// dependent instructions most of the rest: 12 warps an SM are what the registers hold. What was measured and not
+// kept: 16 warps with spills (59 -> 60 us), codes made normal numbers for bf16 too (V's 43 -> 47 us, K's and V's 53),
+// units of 16 query rows (109 -> 121), shifts as multiplications (124 -> 136), the join in this kernel by tickets (43 ->
+// 69: waits on atomics, and few warps for the join).
 #include <type_traits>
 
 #include "q4.cuh"
@@ -32,7 +40,8 @@ constexpr float kLnUp = 7.f, kLnGrow = 15.f, kLnLeastStep = 0x1p-32f;
 enum { kLnBf16, kLnF16, kLnF32 };
 
 // A unit's set-up (its queries, its pages' numbers, a first tile from memory, its result) takes a warp as long as some
-// tiles: so many that it counts for in the line, before its own.
+// tiles: so many that it counts for in the line, before its own (4 requests of a few own rows behind 16K rows: without,
+// the one CTA with all the own rows ends 6 us after the others; 25.5 -> 20.0 us).
 constexpr int kLnPad = 3;
 
 constexpr int kLnStage = 2;  // tiles per ring place: at most, of one unit
@@ -704,13 +713,18 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
 }
 
 // ---- host ------------------------------------------------------------------------------------------
-// Prompts of 16-bit types with more query rows than this go to tcgen05, as do the own rows of a request with more than
-// kQ4FewRows and kQ4FewScores scores.
 // Prompts of more than one row tile are read back into 16-bit arrays of the workspace (one layer's, up to kQ4WideMost
 // bytes), which the kernel of pages_tc.cu then takes as they are: the operands are made once instead of once per
 // one or two row tiles, on an SM whose issue slots the softmax of two row tiles needs.
 constexpr long long kQ4WideMost = 1LL << 32;
-// us, by lines and on tcgen05 (32/8 heads of d 128, bf16): @
+// Prompts of 16-bit types with more than kQ4LineRows query rows go to tcgen05 (unless all there is to do is short), as
+// do the own rows of a request with more than kQ4FewRows query rows and kQ4FewScores scores where there are at least
+// kQ4FewUnits requests times KV heads: a line's warps read the codes once for every 8 query rows, the tensor cores for
+// 128, but a CTA takes its time whatever it holds. By lines and on tcgen05, us (32/8 heads of d 128, bf16): behind 16K
+// rows 16 query rows a head 20 and 31, 32 rows 54 and 31, 64 rows 98 and 34; behind 128K rows 32 rows 241 and 121, 128
+// rows 959 and 128; behind 256 rows 8 requests 11.8 and 18.1, 64 requests 18.0 and 18.2. Own rows of 64 requests, `new`
+// new rows: 10 and 392 rows 53 and 49, 16 and 1024 96 and 85, 32 and 512 108 and 82, 64 and 2048 398 and 263; of 8
+// requests: 16 and 1024 21 and 30, 64 and 2048 55 and 65, 16 and 4096 33 and 59.
 constexpr int kQ4LineRows = 16, kQ4FewRows = 32, kQ4FewScores = 32768, kQ4FewUnits = 128;
 
 int ln_ctas(const PgDims &D) {
