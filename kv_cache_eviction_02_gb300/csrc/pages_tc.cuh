@@ -559,7 +559,7 @@ __device__ __forceinline__ void pt_k_tile(uint32_t raw, uint32_t place, int row0
         }
 }
 // 16 tokens of V, of which the first `have` are there; the others' rows are zeros.
-template <typename T, int DR, int G>
+template <typename T, int DR, int G, bool WHOLE>
 __device__ __forceinline__ void pt_v_tile(uint32_t raw, uint32_t place, int row0, int have, int lane) {
     constexpr int NG = DR / G, PW = (NG + 1) / 2;
     const int j = lane & 3;
@@ -579,8 +579,11 @@ __device__ __forceinline__ void pt_v_tile(uint32_t raw, uint32_t place, int row0
 #pragma unroll
         for (int c = g * G / 16; c < (g + 1) * G / 16; ++c) {
             const uint32_t x = w[c], y = x >> 8;
-            const uint32_t v[4] = {of0.low(x) & there[0], of0.high(x) & there[0], of1.low(y) & there[1],
-                                   of1.high(y) & there[1]};
+            uint32_t v[4] = {of0.low(x), of0.high(x), of1.low(y), of1.high(y)};
+            if (!WHOLE) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] &= there[i >> 1];
+            }
             asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(
                              place + (c >> 2) * 16384 + tc::sw128_offset(row, (2 * c + (to & 1)) & 7)),
                          "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
@@ -615,8 +618,10 @@ __device__ __noinline__ void pt_make_of(const PtArgs &A, uint64_t *bars, uint8_t
             for (int i = (part + MAKERS - (2 * c + half) * 4 % MAKERS) % MAKERS; i < 4; i += MAKERS) {
                 const uint32_t from = base + L::RAW + place * L::HALF + i * q4_tile_bytes(DR, G);
                 const int row0 = half * 64 + i * 16;
-                if (c & 1) pt_v_tile<T, DR, G>(from, to, row0, n - (c >> 1) * 128 - row0, lane);
-                else pt_k_tile<T, DR, G>(from, to, row0, lane);
+                const int have = n - (c >> 1) * 128 - row0;
+                if (!(c & 1)) pt_k_tile<T, DR, G>(from, to, row0, lane);
+                else if (have >= 16) pt_v_tile<T, DR, G, true>(from, to, row0, have, lane);
+                else pt_v_tile<T, DR, G, false>(from, to, row0, have, lane);
             }
             if (c & 1) {
                 __syncwarp();

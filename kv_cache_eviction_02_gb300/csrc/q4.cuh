@@ -124,31 +124,25 @@ template <> struct Q4Codes<__nv_bfloat16> {
     __device__ __forceinline__ uint32_t high(uint32_t x) const { return of(x >> 4); }
 };
 template <> struct Q4Codes<__half> {
-    // a code at bits 4 to 7 of 64's mantissa is 64 + n; step = a e, a power of two apart: (64 + n) a - (64 + k) a has 11
-    // bits at most and only the last product can round
-    uint32_t a, c, e;
+    // a code at bits 4 to 7 of 64's mantissa is 64 + n; step = a e, a of four bits below 2 and e a power of two: (64 + n) a - (64 + k) a
+    // has 11 bits at most and only the product with e can round. zero: 0, or NaN where e is none
+    uint32_t a, c, e, zero;
+    __device__ __forceinline__ static __half2 h2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
+    __device__ __forceinline__ static uint32_t u(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
     __device__ __forceinline__ explicit Q4Codes(uint32_t p2) {
-        float f[2], g[2], z[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float s = __uint_as_float((i ? p2 : p2 << 16) & 0xFFF00000u);
-            const int ex = min(max((int)(__float_as_uint(s) >> 23), 103), 142);  // 2^-24 .. 2^15
-            g[i] = __uint_as_float(ex << 23);
-            f[i] = s * __uint_as_float((254 - ex) << 23);
-            z[i] = -64.f * f[i] - (float)(p2 >> (16 * i) & 15u) * f[i];
+        a = (p2 & 0x00700070u) << 3 | 0x3C003C00u;
+        const uint32_t e0 = p2 << 16 & 0x7F800000u, e1 = p2 & 0x7F800000u;
+        e = u(__floats2half2_rn(__uint_as_float(e0), __uint_as_float(e1)));
+        if (min(e0, e1) < 103u << 23) {  // powers of two below fp16's least, 2^-24: a takes the rest
+            const float f0 = __uint_as_float(min(e0, 103u << 23)) * 0x1p24f, f1 = __uint_as_float(min(e1, 103u << 23)) * 0x1p24f;
+            a = u(__hmul2(h2(a), __floats2half2_rn(f0, f1)));
+            e = u(__floats2half2_rn(__uint_as_float(max(e0, 103u << 23)), __uint_as_float(max(e1, 103u << 23))));
         }
-        const __half2 fa = __floats2half2_rn(f[0], f[1]), fe = __floats2half2_rn(g[0], g[1]);
-        const __half2 fz = __floats2half2_rn(z[0], z[1]);
-        a = *reinterpret_cast<const uint32_t *>(&fa);
-        e = *reinterpret_cast<const uint32_t *>(&fe);
-        c = *reinterpret_cast<const uint32_t *>(&fz);
+        c = u(__hmul2(h2((p2 << 4 & 0x00F000F0u) | 0xD400D400u), h2(a)));  // -(64 + k) a
+        zero = u(__hmul2(h2(e), h2(0u)));
     }
     __device__ __forceinline__ uint32_t high(uint32_t x) const {
-        const uint32_t y = (x & 0x00F000F0u) | 0x54005400u;
-        const __half2 v = __hmul2(__hfma2(*reinterpret_cast<const __half2 *>(&y), *reinterpret_cast<const __half2 *>(&a),
-                                          *reinterpret_cast<const __half2 *>(&c)),
-                                  *reinterpret_cast<const __half2 *>(&e));
-        return *reinterpret_cast<const uint32_t *>(&v);
+        return u(__hfma2(__hfma2(h2((x & 0x00F000F0u) | 0x54005400u), h2(a), h2(c)), h2(e), h2(zero)));
     }
     __device__ __forceinline__ uint32_t low(uint32_t x) const { return high(x << 4); }
 };
