@@ -450,6 +450,64 @@ def test_row_starts_that_are_no_sums_of_lengths_stay_in_bounds(case):
         assert out.intact() and z.intact() and ws.intact()
 
 
+@pytest.mark.parametrize("dtype,d,Hkv", [("bf16", 64, 4), ("f16", 128, 4)])
+def test_one_request_with_most_of_the_new_rows(dtype, d, Hkv):
+    """More row blocks than the launch has places for: a CTA takes several in turn."""
+    new = [1] * 31 + [400]
+    c = Q4Case(dtype, 32, 1, 4 * Hkv, Hkv, d, 0, 16, 200, 400, new=new, seed=21)
+    assert "q4_own" in stages(c)
+    c.check([0, 15, 30, 31, 32, 100, 158, 159, 160, 250, 430])
+
+
+def test_prompts_too_large_to_be_read_back():
+    """Above 4 GiB of 16-bit values two row tiles run on codes: as one tile of the same requests does."""
+    n, heads, d = 2 ** 20 + 5, 8, 128
+    gen = torch.Generator(device=DEV).manual_seed(0)
+    K, V = (torch.randn(1, heads, n, d, generator=gen, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    qkv = torch.randn(40, 48, d, generator=gen, device=DEV).bfloat16()
+    outs = []
+    for fan in (40, 20):
+        pb = api.Q4Problem(1, fan, 32, heads, d, n, 16, fan, 1, fan, 1, api.KVE_BF16, 32)
+        assert api.q4_workspace_size(pb) < 2 ** 32
+        c = api.Q4Cache(pb, 1, DEV)
+        c.pack(0, K, V)
+        c.plan(i32([1] * fan))
+        c.append(0, qkv[:fan, 32:40], qkv[:fan, 40:])
+        out, lse = torch.zeros(fan, 32, d, device=DEV).bfloat16(), torch.zeros(fan, 32, device=DEV)
+        c.attend(0, qkv[:fan, :32], out, lse)
+        api.kve_check_device()
+        outs.append((f64(out[:20]), f64(lse[:20])))
+        del c
+    (a, x), (b, y) = outs
+    # each rounds its weights (2^-8, of sums over a million tokens: their random walk) and its output (2^-8)
+    assert np.abs(a - b).max() <= 2.0 ** -7 * np.abs(b).max() and np.abs(x - y).max() < 1e-4
+    assert np.linalg.norm(a - b) <= 2.0 ** -7 * np.linalg.norm(b)
+
+
+def test_pages_beyond_32_bit_offsets():
+    """A pool of more than 4 GiB: the last pages are written, attended to and read back as the first ones are."""
+    pages, heads, d = 240_000, 8, 128
+    pb = api.Q4Problem(2, 1, 8, heads, d, 0, 16, pages, 3, 96, 40, api.KVE_BF16, 32)
+    assert pb.pool_bytes > 2 ** 32
+    pool = torch.zeros(pb.pool_bytes, dtype=torch.uint8, device=DEV)
+    table = i32([[0, 1, 2], [pages - 1, pages - 3, pages - 2]])
+    x = torch.randn(96, 2 * heads, d, device=DEV).bfloat16()
+    x[48:] = x[:48]
+    slots = (table.long().repeat_interleave(16, 1).flatten() * 16 + torch.arange(16, device=DEV).repeat(6)).int()
+    api.q4_append(pb, x[:, :heads], x[:, heads:], slots, pool)
+    back = [torch.zeros(2, heads, 48, d, device=DEV).bfloat16() for _ in range(2)]
+    api.q4_unpack(pb, pool, table, i32([48, 48]), *back)
+    pb1 = dataclasses.replace(pb, n_rows=2, max_new=1)
+    q = torch.randn(1, 8, d, device=DEV).bfloat16().expand(2, 8, d).contiguous()
+    out = torch.zeros(2, 8, d, device=DEV).bfloat16()
+    ws = torch.empty(api.q4_workspace_size(pb1), dtype=torch.uint8, device=DEV)
+    api.q4_attention(pb1, q, None, None, pool, table, i32([48, 48]), i32([0, 1, 2]), i32([0, 1]), out, None, ws)
+    api.kve_check_device()
+    assert all(torch.equal(b[0], b[1]) and b.abs().max() > 1 for b in back)
+    # (the two requests' tiles fall to other warps: their weights round apart)
+    assert (out[0] - out[1]).abs().max() <= 2.0 ** -7 * out.abs().max() and out.abs().max() > 0.01
+
+
 def test_the_most_requests():
     c = Q4Case("bf16", 4096, 1, 2, 1, 32, 0, 16, 2, 1, seed=16)
     rng = np.random.default_rng(2)
