@@ -6,7 +6,7 @@
 // nibble is the number n 2^-24 or n 2^-20. With a group's step and zero code taken out of the sums,
 //   q.k = sum over groups of s_g (q_g.n_g - k_g sum q_g),   o_c = sum over tokens of (p_t s_t,g) (n_t,c - k_t,g),
 // a score is a product per group, times s in fp32, and the terms of the zero codes are products too: A holds k_g of
-// the 16 tokens, B the sums of q (as two fp16 numbers, off by 2^-22; fp32 three), or the same weights p s as the codes'.
+// the 16 tokens, B the sums of q (as two fp16 numbers, off by 2^-22), or the same weights p s as the codes'.
 // Queries are carried as fp16 after their row's largest entry is brought to 2^7 .. 2^8 (bf16 and fp16 entries keep all
 // their bits down to 2^-17 of the largest, smaller ones are off by 2^-28 of it; fp32 ones are two fp16
 // numbers). Weights p s are fp32 numbers rounded once to fp16, half a step (fp32: two fp16 numbers).
@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
         pg_share_find<THREADS>(csum, usum, sh, X0, &e, &x, &unit);
     }
     __syncthreads();  // s_abort and the pieces' marks are set
+    PgCursor<F32> cc;
     if (n > 0) {
-        PgCursor<F32> cc;
         cc.enter(D_, A, e + e0);
         auto tiles = [&]() { return (long long)(cc.cr + kLnPad) * cc.nb * D_.Hkv; };
         while (x >= tiles()) {
@@ -193,8 +193,8 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
             n += cc.c;
             cc.c = 0;
         }
-
-        if (n > 0) {
+    }
+    if (n > 0) {
         PgCursor<F32> ca = cc;  // runs ahead: the tiles to load
 
         uint8_t *ring = smem + warp * L::WARP;
@@ -280,17 +280,20 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
                         }
                     }
                 if (!KC) {  // sums over groups: a product with ones (and 2^4 for the second pairs)
+                    constexpr uint32_t k1 = 0x3C003C00u, k16 = 0x4C004C00u;
                     float sum[NG];
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
                         float c[4];
 #pragma unroll
                         for (int k = g * G / 16; k < (g + 1) * G / 16; ++k) {
-                            if (k == g * G / 16) mma0(c, 0x3C003C00u, 0x3C003C00u, 0x4C004C00u, 0x4C004C00u, qf[b][0][k][0], qf[b][0][k][1]);
-                            else mma(c, 0x3C003C00u, 0x3C003C00u, 0x4C004C00u, 0x4C004C00u, qf[b][0][k][0], qf[b][0][k][1]);
+                            const uint32_t(&f)[2] = qf[b][0][k];
+                            if (k == g * G / 16) mma0(c, k1, k1, k16, k16, f[0], f[1]);
+                            else mma(c, k1, k1, k16, k16, f[0], f[1]);
                         }
                         // column lane / 4, which lanes with j = lane / 8 hold
-                        const float s0 = __shfl_sync(0xffffffffu, c[0], lane >> 3), s1 = __shfl_sync(0xffffffffu, c[1], lane >> 3);
+                        const float s0 = __shfl_sync(0xffffffffu, c[0], lane >> 3);
+                        const float s1 = __shfl_sync(0xffffffffu, c[1], lane >> 3);
                         sum[g] = -(lane & 4 ? s1 : s0);
                     }
                     const float a = NG > 2 && (j & 1) ? sum[NG > 2 ? 2 : 0] : (j & 1 ? 0.f : sum[0]);
@@ -676,7 +679,6 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
                 tc::mbar_drain(&bar[k], 0);
                 tc::mbar_drain(&bar[k], 1);
             }
-        }
         }
     }
     // pieces of one unit stand behind one another

@@ -10,9 +10,10 @@
 // exact remainder x - s m.
 //
 // Bound by HBM: one layer's 128K prompt of bf16 (8 heads of d 128) packed and read back 226 us, 6.1 TB/s; four ragged
-// prompts of 32K read back 99 us, 6.4 TB/s. Each of four lanes works out one row's steps (each for itself: 289 us), and
-// values come back in 16-bit arithmetic, which is exact (in fp32: 122 -> 99 us). A thread takes 8 channels of the four tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9 of a tile, whose codes fill
-// whole words of K and of V: rows come in 16-byte loads and leave as full 32-byte sectors, no shared memory between.
+// prompts of 32K (fp16) read back 92 us, 6.8 TB/s. Each of four lanes works out one row's steps (each for itself: 289 us), and
+// values come back in 16-bit arithmetic, which is exact (in fp32: 122 us for the latter). A thread takes 8 channels of the four
+// tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9 of a tile, whose codes fill whole words of K and of V: rows come in 16-byte
+// loads and leave as full 32-byte sectors, no shared memory between.
 #include <type_traits>
 
 #include "q4.cuh"
@@ -281,7 +282,7 @@ __device__ __forceinline__ void store_rows(const Q4Cache &C, const Eight<T> (&x)
 // The threads of a tile (tile_of) take 16 rows that stand behind one another in the batch. Rows that fill a tile of the
 // cache (16 consecutive slots) are written as one by the threads of the 16 in which they begin, as whole words; other
 // rows byte by byte (64 prompts of up to 2000 rows, fp16, 8 heads of d 128, with their reading back: all of them byte by
-// byte 232 us, so 177).
+// byte 232 us, so 177; 131 with the steps and the way back as they are now).
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kQ4Threads) q4_append_kernel(Q4Cache C) {
     pg_wait_prior();
