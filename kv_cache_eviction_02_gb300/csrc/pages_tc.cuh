@@ -648,6 +648,13 @@ __device__ __forceinline__ void pt_make(const PtArgs &A, uint64_t *bars, uint8_t
     pt_make_of<T, D, D, QT, G, OWN, SENDS>(A, bars, sm, part, lane, s, kh, t0, t1, abort_flag);
 }
 
+// Tiles of 64 columns made for d_head 32 have 32 that nothing writes: zeros, of the ring that a round finds. (Q has zeros
+// there, but 0 times what an epilogue left may be NaN. A function of its own: inlined, it took registers.)
+__device__ __noinline__ void pt_clear(uint8_t *ring, uint32_t bytes) {
+    for (uint32_t i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16)
+        *reinterpret_cast<uint4 *>(ring + i) = make_uint4(0, 0, 0, 0);
+}
+
 // Warps: 0 TMA, 1 MMA, 2-3 own rows of short tables, then 4 softmax warps per row tile, with 4 bits
 // and one row tile then 4 that make operands.
 template <typename T, int D, int QT, int G, bool OWN>
@@ -676,11 +683,8 @@ __global__ void __launch_bounds__(pt_threads<QT, G>(), 1)
         tc::tma_prefetch_desc(&tm_q);
         *abort_flag = 0;
     }
-    if constexpr (G != 0 && D == 64) {  // the columns that d_head 32 does not have
-        if (A.D.d == 32)
-            for (uint32_t i = threadIdx.x * 16; i < L::SLOTS * L::TILE; i += blockDim.x * 16)
-                *reinterpret_cast<uint4 *>(sm + L::RING + i) = make_uint4(0, 0, 0, 0);
-    }
+    if constexpr (D == 64 && G == 32)
+        if (A.D.d == 32) pt_clear(sm + L::RING, L::SLOTS * L::TILE);
     if (!OWN) pg_wait_prior();  // (with OWN the call's first kernel has waited)
     pg_launch_dependents();
     // the row tiles of a (prompt or request, KV head, split) are adjacent: they meet in L2 on its K/V
@@ -869,6 +873,12 @@ __global__ void __launch_bounds__(pt_threads<QT, G>(), 1)
         if ((rt + A.nrt) * QT * per >= nrow) break;
         // another round (the fence waits for the stores of the one before, so not after the last): the ring's
         // plain reads and writes before the next TMA loads
+        if constexpr (D == 64 && G == 32) {
+            if (A.D.d == 32) {
+                __syncthreads();  // (the epilogues have read their rows)
+                pt_clear(sm + L::RING, L::SLOTS * L::TILE);
+            }
+        }
         tc::fence_proxy_async_smem();
         __syncthreads();
         tc::fence_after_sync();
