@@ -447,8 +447,9 @@ int pg_attention(const KvePgShape *shape, const void *q, long long q_row_stride,
  * d_head + 64 d_head / group bytes.
  *   prefix  [n_prompts][n_kv_heads][ceil(n_prefix / 16)] such blocks, q4_prefix_size() bytes
  *   pages   [n_pages][n_kv_heads][page_size / 16], q4_pages_size() bytes
- * Both are independent of shape->dtype but for F: an array written from one type may be read as another. They need no
- * initial values. */
+ * Both are independent of shape->dtype but for F: an array written from one type may be read as another. Values beyond that
+ * one's largest number (fp16's, with steps above 2^12) read back as infinities, and an attention call whose rows see
+ * one is free to take the number or the infinity in that channel. The arrays need no initial values. */
 
 /* Bytes of the arrays; 0 on invalid input, and for q4_prefix_size without a prompt. */
 size_t q4_prefix_size(const KvePgShape *shape, int group);

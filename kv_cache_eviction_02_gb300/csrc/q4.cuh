@@ -108,7 +108,8 @@ template <int NG> __device__ __forceinline__ void q4_params_of(uint32_t at, uint
 }
 
 // Codes as values of a 16-bit type, two at a time: p2 holds the parameters of the two, low() takes the nibbles at bits 0
-// and 16, high() those at bits 4 and 20. Exact, but for fp16 values below its normal numbers, which round once.
+// and 16, high() those at bits 4 and 20. Exact, but for fp16: values below its normal numbers round once, those above its
+// largest are infinities.
 template <typename T> struct Q4Codes;
 template <> struct Q4Codes<__nv_bfloat16> {
     uint32_t s, k;
@@ -133,10 +134,16 @@ template <> struct Q4Codes<__half> {
         a = (p2 & 0x00700070u) << 3 | 0x3C003C00u;
         const uint32_t e0 = p2 << 16 & 0x7F800000u, e1 = p2 & 0x7F800000u;
         e = u(__floats2half2_rn(__uint_as_float(e0), __uint_as_float(e1)));
-        if (min(e0, e1) < 103u << 23) {  // powers of two below fp16's least, 2^-24: a takes the rest
-            const float f0 = __uint_as_float(min(e0, 103u << 23)) * 0x1p24f, f1 = __uint_as_float(min(e1, 103u << 23)) * 0x1p24f;
-            a = u(__hmul2(h2(a), __floats2half2_rn(f0, f1)));
-            e = u(__floats2half2_rn(__uint_as_float(max(e0, 103u << 23)), __uint_as_float(max(e1, 103u << 23))));
+        // Powers of two that fp16 does not have: a takes what lies below its least, 2^-24, or, above its largest, 2^15, a
+        // factor of two, with which every code but 0 is an infinity (0 stays 0). NaN steps keep their infinite e.
+        constexpr uint32_t least = 103u << 23, most = 142u << 23, none = 255u << 23;
+        if (min(e0, e1) < least || max(e0, e1) > most) {
+            auto rest = [](uint32_t x) {
+                return x < least ? __uint_as_float(x) * 0x1p24f : (x > most ? 2.f : 1.f);
+            };
+            auto held = [](uint32_t x) { return __uint_as_float(x == none ? x : min(max(x, least), most)); };
+            a = u(__hmul2(h2(a), __floats2half2_rn(rest(e0), rest(e1))));
+            e = u(__floats2half2_rn(held(e0), held(e1)));
         }
         c = u(__hmul2(h2((p2 << 4 & 0x00F000F0u) | 0xD400D400u), h2(a)));  // -(64 + k) a
         zero = u(__hmul2(h2(e), h2(0u)));

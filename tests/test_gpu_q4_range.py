@@ -57,3 +57,58 @@ def test_rows_behind_a_refused_request(dtype, d):
     assert (np.abs(f64(out) - ref["out"])[rows] <= (2.5 * h * ref["terms"] + 2.0 ** -14)[rows]).all()
     assert (np.abs(f64(lse) - ref["lse"])[rows] <= 2.0 ** -14 * (1 + ref["mag"])[rows]).all()
     assert (out[2:302] == 3).all() and (lse[2:302] == 5).all()
+
+
+# ---- arrays read as another type -----------------------------------------------------------------------
+@pytest.mark.parametrize("d,group", [(128, 32), (64, 64), (32, 32)])
+@pytest.mark.parametrize("written,read", [("bf16", "f16"), ("f32", "f16"), ("f16", "bf16"), ("f16", "f32"),
+                                          ("bf16", "f32"), ("f32", "bf16")])
+def test_an_array_written_from_one_type_is_read_as_another(written, read, d, group):
+    """The values s m, rounded to the type that reads: zeros stay zeros whatever the step, what is above the largest number
+    becomes an infinity, and only groups that hold no number are NaN."""
+    n = 96
+    gen = torch.Generator(device=DEV).manual_seed(d)
+    x = torch.randn(1, 2, n, d, generator=gen, device=DEV)
+    power = torch.arange(n, device=DEV) - (48 if written != "f16" else 20)  # steps below and above all that fp16 has
+    x = x * torch.exp2(power.clamp(max=15 if written == "f16" else 47).float())[:, None]
+    x[..., ::3] = 0
+    x[:, 1, 5, 1] = float("nan")
+    x = x.to(DT[written])
+    pb = api.Q4Problem(1, 1, 2, 2, d, n, 16, 1, 1, 1, 1, KD[written], group)
+    other = api.Q4Problem(1, 1, 2, 2, d, n, 16, 1, 1, 1, 1, KD[read], group)
+    prefix = torch.zeros(pb.prefix_bytes, dtype=torch.uint8, device=DEV)
+    api.q4_pack(pb, x, -x, None, prefix)
+    out = [torch.full((1, 2, n, d), 7.0, device=DEV, dtype=DT[read]) for _ in range(2)]
+    api.q4_unpack(other, prefix, None, None, *out)
+    api.kve_check_device()
+    for y, o in zip((x, -x), out):
+        want = torch.from_numpy(held(y, group, written)[0]).to(DT[read])
+        got = o.cpu()
+        assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.nan_to_num(7.0), want.nan_to_num(7.0))
+        if read == "f16" and written != "f16":
+            assert want.isinf().any() and ((want == 0) & ~want.isnan()).any()
+
+
+@pytest.mark.parametrize("fan", [1, 8, 70])
+def test_zeros_of_large_groups_do_not_become_nan_in_attention(fan):
+    """V of steps of 2^18, written from bf16 and attended to as fp16: the channels that are 0 throughout are 0, by lines, on
+    tcgen05 from codes and read back first."""
+    n, d = 300, 64
+    gen = torch.Generator(device=DEV).manual_seed(fan)
+    K = torch.randn(1, 2, n, d, generator=gen, device=DEV)
+    V = torch.randn(1, 2, n, d, generator=gen, device=DEV)
+    V[..., :32] = 0
+    V[..., 3] = 15 * 2.0 ** 18
+    pw = api.Q4Problem(1, fan, 8, 2, d, n, 16, fan, 1, fan, 1, api.KVE_BF16, 32)
+    pb = api.Q4Problem(1, fan, 8, 2, d, n, 16, fan, 1, fan, 1, api.KVE_F16, 32)
+    c = api.Q4Cache(pb, 1, DEV)
+    api.q4_pack(pw, K.bfloat16(), V.bfloat16(), None, c.prefix[0])
+    c.plan(i32([1] * fan))
+    new = torch.randn(fan, 12, d, generator=gen, device=DEV).half()
+    new[..., :32] *= 0.125
+    c.append(0, new[:, 8:10], torch.zeros_like(new[:, 10:]))
+    out = torch.zeros(fan, 8, d, device=DEV).half()
+    c.attend(0, new[:, :8], out)
+    api.kve_check_device()
+    zero = [x for x in range(32) if x != 3]
+    assert (out[..., zero] == 0).all() and out[..., 32:].isfinite().all() and out[..., 32:].abs().max() > 0
