@@ -854,7 +854,7 @@ class Q4Cache:
         self.pb = pb
         self.prefix = torch.zeros(n_layers, pb.prefix_bytes, dtype=torch.uint8, device=dev)
         self.pages = torch.zeros(n_layers, pb.pool_bytes, dtype=torch.uint8, device=dev)
-        self.prefix_len = None  # int32 [n_prompts], set by pack
+        self.prefix_len = [None] * n_layers  # int32 [n_prompts] of each layer, set by pack
         self.block_table = torch.full((R, pb.max_pages), -1, dtype=i32, device=dev)
         self.free_pages = torch.arange(pb.n_pages, dtype=i32, device=dev)
         self.pool = torch.tensor([0, pb.n_pages, 0, 0], dtype=i32, device=dev)
@@ -866,10 +866,10 @@ class Q4Cache:
         self.workspace = torch.empty(size, dtype=torch.uint8, device=dev)
 
     def pack(self, layer, K, V, prefix_len=None, stream=None):
-        """Quantises the prompts of a layer. prefix_len (int32 [n_prompts], kept, not copied) holds for all
-        layers."""
+        """Quantises the prompts of a layer. prefix_len (int32 [n_prompts], kept, not copied; None: n_prefix rows each)
+        holds for this layer."""
         q4_pack(self.pb, K, V, prefix_len, self.prefix[layer], stream)
-        self.prefix_len = prefix_len
+        self.prefix_len[layer] = prefix_len
 
     def plan(self, new_len, stream=None):
         """Takes (or returns) pages for a step in which request r adds new_len[r] rows (int32)."""
@@ -881,13 +881,13 @@ class Q4Cache:
         q4_append(self.pb, K_new, V_new, self.slot_map, self.pages[layer], stream)
 
     def attend(self, layer, q, out, lse_out=None, stream=None):
-        q4_attention(self.pb, q, self.prefix[layer] if self.pb.n_prefix else None, self.prefix_len,
+        q4_attention(self.pb, q, self.prefix[layer] if self.pb.n_prefix else None, self.prefix_len[layer],
                      self.pages[layer], self.block_table, self.lens, self.q_start, self.row_req, out, lse_out,
                      self.workspace, stream)
 
     def unpack(self, layer, K_out, V_out, prompts=False, stream=None):
         if prompts:
-            q4_unpack(self.pb, self.prefix[layer], None, self.prefix_len, K_out, V_out, stream)
+            q4_unpack(self.pb, self.prefix[layer], None, self.prefix_len[layer], K_out, V_out, stream)
         else:
             q4_unpack(self.pb, self.pages[layer], self.block_table, self.lens, K_out, V_out, stream)
 

@@ -112,3 +112,35 @@ def test_zeros_of_large_groups_do_not_become_nan_in_attention(fan):
     api.kve_check_device()
     zero = [x for x in range(32) if x != 3]
     assert (out[..., zero] == 0).all() and out[..., 32:].isfinite().all() and out[..., 32:].abs().max() > 0
+
+
+# ---- layers of different lengths -----------------------------------------------------------------------
+def test_layers_of_one_cache_with_lengths_of_their_own():
+    """Each layer answers as a cache of its own would."""
+    n, fan, d = 60, 3, 64
+    pb = api.Q4Problem(2, fan, 8, 2, d, n, 16, 2 * fan, 1, 2 * fan, 1, api.KVE_BF16, 32)
+    gen = torch.Generator(device=DEV).manual_seed(0)
+    rows = [[torch.randn(2, 2, n, d, generator=gen, device=DEV).bfloat16() for _ in range(2)] for _ in range(3)]
+    lens = [i32([17, 60]), None, i32([0, 33])]
+    qkv = torch.randn(2 * fan, 12, d, generator=gen, device=DEV).bfloat16()
+
+    def answers(layers):
+        c = api.Q4Cache(pb, len(layers), DEV)
+        for at, x in enumerate(layers):
+            c.pack(at, *rows[x], lens[x])
+        c.plan(i32([1] * 2 * fan))
+        outs = []
+        for at in range(len(layers)):
+            out, back = torch.zeros(2 * fan, 8, d, device=DEV).bfloat16(), [torch.zeros_like(rows[0][0]) for _ in range(2)]
+            c.append(at, qkv[:, 8:10], qkv[:, 10:])
+            c.attend(at, qkv[:, :8], out)
+            c.unpack(at, *back, prompts=True)
+            outs.append((out, *back))
+        api.kve_check_device()
+        return outs
+
+    together = answers([0, 1, 2])
+    for x in range(3):
+        alone = answers([x])[0]
+        assert all(torch.equal(a, b) for a, b in zip(together[x], alone))
+    assert (together[0][1][0, :, 17:] == 0).all() and (together[1][1][:, :, n - 1] != 0).any()
