@@ -493,7 +493,7 @@ size_t q4_workspace_size(const KvePgShape *shape, int group);
  * of the largest are lost.
  * Prompts of 16-bit types behind more than one row tile of 128 query rows are read back into the workspace, one
  * layer's n_prompts * n_kv_heads * n_prefix * d_head values of K and V, if that is 4 GiB at most.
- * Requirements as in pg_attention; q, steps and scores are below 2^89. A row that sees a NaN in K is NaN, one that
+ * Requirements as in pg_attention; q, steps and scores are below 2^89. A row that sees a NaN in K is NaN, lse too, one that
  * sees a NaN in V is NaN in that group's channels and may be in its head's others; other rows of a prompt's requests,
  * or of the same request, that share a tile of query rows with it may be too. */
 int q4_attention(const KvePgShape *shape, int group, const void *q, long long q_row_stride,

@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(128) pg_join_kernel(PgDims D_, PgAttn A) {
     else
 #pragma unroll
         for (int e = 0; e < E; ++e) dst[e] = out[e];
-    if (A.lse && lane == 0) A.lse[row] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    if (A.lse && lane == 0) A.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 // The same for many rows of d_head 32 and 64: a warp joins four heads of a row (2 or 4 at a time, 4 columns a
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(128) pg_join_many_kernel(PgDims D_, PgAttn A) 
         T *dst = static_cast<T *>(A.out) + row * D + col;
         if (sizeof(out) == 16) *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<uint4 *>(out);
         else *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<uint2 *>(out);
-        if (A.lse && col == 0) A.lse[row] = L[i] > 0.f ? (M[i] + log2f(L[i])) * kLn2 : -INFINITY;
+        if (A.lse && col == 0) A.lse[row] = L[i] == 0.f ? -INFINITY : (M[i] + log2f(L[i])) * kLn2;
     }
 }
 

@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kMmThreads, NT == 1 ? 3 : 2)
                         dst[16 * j] = from_f<T>(o[b][j][e] * inv);
                         dst[16 * j + 8] = from_f<T>(o[b][j][e + 2] * inv);
                     }
-                    if (A.lse && lane < 4) A.lse[row] = x > 0.f ? (m[b][e] + log2f(x)) * kLn2 : -INFINITY;
+                    if (A.lse && lane < 4) A.lse[row] = x == 0.f ? -INFINITY : (m[b][e] + log2f(x)) * kLn2;
                 }
         }
         if (s_abort) {  // copies still in flight land before the block ends

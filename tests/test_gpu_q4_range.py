@@ -144,3 +144,29 @@ def test_layers_of_one_cache_with_lengths_of_their_own():
         alone = answers([x])[0]
         assert all(torch.equal(a, b) for a, b in zip(together[x], alone))
     assert (together[0][1][0, :, 17:] == 0).all() and (together[1][1][:, :, n - 1] != 0).any()
+
+
+# ---- rows that hold no number --------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,fan,n", [("bf16", 1, 100), ("f32", 1, 100), ("f16", 1, 0), ("bf16", 8, 300), ("f16", 70, 300),
+                                         ("f32", 20, 300)])
+def test_a_row_that_sees_a_nan_in_k_has_no_log_sum_either(dtype, fan, n):
+    """-inf would say that there was nothing to see. By lines, on tcgen05 from codes and read back first."""
+    c = Q4Case(dtype, 2, fan, 8, 2, 64, n, 16, 20, 1, seed=12)
+    good, z = c.run()
+    if n:
+        c.Kp[1, 0, 40, 3] = float("nan")
+        api.q4_pack(c.pb, c.Kp, c.Vp, None, c.prefix)
+        bad = range(fan, 2 * fan)
+    else:
+        slot = int(c.table[1, 0]) * 16
+        x = torch.full((1, 2, 64), float("inf"), device=DEV, dtype=DT[dtype])
+        x[:, 1] = 1
+        api.q4_append(api.Q4Problem(2, fan, 8, 2, 64, 0, 16, c.pb.n_pages, c.pb.max_pages, 1, 1, KD[dtype], 32), x,
+                      torch.ones_like(x), i32([slot]), c.pages)
+        bad = [1]
+    out, lse = c.run()
+    bad = list(bad)
+    assert torch.isnan(out[bad][:, :4]).all() and torch.isnan(lse[bad][:, :4]).all()
+    assert torch.isfinite(lse[:c.rows][:, 4:]).all() and torch.isfinite(out[:c.rows][:, 4:]).all()
+    rest = [i for i in range(fan) if i not in bad]
+    assert torch.equal(lse[rest], z[rest]) and torch.equal(out[rest], good[rest])
