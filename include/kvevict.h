@@ -487,10 +487,11 @@ size_t q4_workspace_size(const KvePgShape *shape, int group);
 /* pg_attention with K and V held in 4 bits: the same rows see the same rows, with prefix for K_prefix and V_prefix and
  * pages for K_pages and V_pages (prefix may be NULL where n_prefix is 0). Scores, maxima, sums and results
  * before the last rounding are fp32. What is rounded to fewer bits: 16-bit types, each unnormalised weight (or weight
- * times step) once to the type, or to fp16, before it meets V (half a step; fp32 takes two fp16 numbers, 2^-22); queries
- * of few rows, carried as fp16 below their row's largest entry, off by at most 2^-28 of it (fp32: two fp16
- * numbers). Sums of products with codes are cut at 2^-17 of their terms (bf16), 2^-20 (fp16, fp32). Weights below 2^-31
- * of the largest are lost.
+ * times step) once to the type, or to fp16, before it meets V (half a step, or 2^-20 of the largest of its row and group;
+ * fp32 takes two fp16 numbers, 2^-22); queries of few rows, carried as fp16 below their row's largest entry,
+ * off by at most 2^-28 of it (fp32: two fp16 numbers). Sums of products with codes are cut at 2^-17 of their terms
+ * (bf16), 2^-20 (fp16, fp32). Weights times steps below 2^-80 of the row's largest, or of steps below 2^-80, may be lost.
+ * Few rows behind a V whose groups have steps more than 2^12 (fp32 2^10) apart in one row take up to twice as long.
  * Prompts of 16-bit types behind more than one row tile of 128 query rows are read back into the workspace, one
  * layer's n_prompts * n_kv_heads * n_prefix * d_head values of K and V, if that is 4 GiB at most.
  * Requirements as in pg_attention; q, steps and scores are below 2^89. A row that sees a NaN in K is NaN, lse too, one that

@@ -16,9 +16,9 @@
 // runs on across units. A tile is one contiguous block: one bulk copy by one lane. Pieces of a unit that several
 // warps of a CTA have seen are joined in shared memory, so a CTA hands on one partial result of a unit.
 //
-// One request behind 128K rows (32/8 heads of d 128, groups of 32, 151 MB): 43 us, of which the set-up until the first
-// product takes 3.5, the tiles 30 (5.0 TB/s), the join 8. 64 requests with caches of up to 16K rows (groups of 64, 572
-// MB): 124 us, 4.6 TB/s, 287 instructions a tile and warp, the logic unit busy for 0.52 of the time and a warp's own
+// One request behind 128K rows (32/8 heads of d 128, groups of 32, 151 MB): 44.5 us, of which the set-up until the first
+// product takes 3.5, the tiles 32 (4.8 TB/s), the join 8. 64 requests with caches of up to 16K rows (groups of 64, 572
+// MB): 122 us, 4.7 TB/s, 287 instructions a tile and warp, the logic unit busy for 0.52 of the time and a warp's own
 // dependent instructions most of the rest: 12 warps an SM are what the registers hold. What was measured and not
 // kept: 16 warps with spills (59 -> 60 us), codes made normal numbers for bf16 too (V's 43 -> 47 us, K's and V's 53),
 // units of 16 query rows (109 -> 121), shifts as multiplications (124 -> 136), the join in this kernel by tickets (43 ->
@@ -30,9 +30,16 @@
 namespace kve {
 namespace {
 
-// Weights are carried up to 2^15 of the reference m, which is set 2^7 below the largest weight p s: of two pieces that
-// are joined, references may lie as far apart as steps do, so a step below 2^-32 does not raise it further.
-constexpr float kLnUp = 7.f, kLnGrow = 15.f, kLnLeastStep = 0x1p-32f;
+// Weights p s are fp16 numbers, carried up to 2^15 of a reference m that all groups of a row share: it is set 2^7 below
+// the largest, of the row's tokens and groups. That holds every group's bits as long as the steps of each token's groups
+// lie within 2^12 (fp32: 2^10) of one another and are not below 2^-32 less that, since no group's largest weight is then
+// further below: nothing above 2^-20 (2^-22) of it is lost. Tokens whose steps lie further apart raise m by their least
+// step only, as far as 2^-80 of the largest, so that their weights may be any fp32 numbers, and are brought to 2^7 .. 2^8
+// group by group, a tile at a time, and the products back into the sums (V's groups 2^20 apart: 64 caches 260 us for
+// 122, one request behind 128K 91 for 44.5). Groups of zeros would be such steps, on every token of a head that is
+// padded: those that a piece of a unit has only seen as zeros stay out of it (138 and 50 us). If one comes alive after
+// all, m may stand too high for it, and all further tiles of the piece take the longer way.
+constexpr float kLnUp = 7.f, kLnGrow = 15.f, kLnLeastStep = 0x1p-32f, kLnFar = 0x1p-80f, kLnZeroStep = 0x1p-126f;
 
 // The tensor cores cut the sums' bits at 2^-24 of the largest product's exponent, which for a number as it stands in the
 // cache counts as 2^-14: to 2^-17 of a product of V's. That is enough for outputs of bf16 (2^-9). For fp16 and fp32 V's
@@ -88,6 +95,11 @@ __device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b) {
     const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&v);
 }
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float y;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
 __device__ __forceinline__ float lg2_approx(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -107,6 +119,8 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
     constexpr int NST = L::NST, TB = L::TB, SB = L::SB, RB = L::RB, WARPS = L::WARPS, THREADS = L::THREADS;
     constexpr bool F32 = MODE == kLnF32, KC = F32, VC = MODE != kLnBf16;  // codes less their zero codes, of K and of V
     constexpr int NG = D / G, KW = D / 16, PW = (NG + 1) / 2, NS = F32 ? 2 : 1;
+    constexpr float kApart = F32 ? 0x1p10f : 0x1p12f;  // how far steps lie apart at most
+    constexpr int kFresh = 1 << NG;
     constexpr bool PAIR = NT == 1;  // two tiles at once: one alone leaves the warps waiting for its products
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
@@ -209,6 +223,7 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
         float o[NT][KW][4], z[NT][4], m[NT][2], l[NT][2];
         int see[NT][2], see_least = 0, rows, row0;  // tokens that columns see; the tiles that all of them see whole
         const float k1 = kLog2e * rsqrtf((float)D);
+        int dead;  // groups of V that were zeros so far, kFresh before the first tile, -1: more of them than are now
         uint32_t zmask[NG], rmask[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -235,6 +250,7 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
         };
         auto begin = [&]() {  // of a unit, or of this warp's part of one, when its queries are there
             see_least = 0x7fffffff;
+            dead = kFresh;
 #pragma unroll
             for (int b = 0; b < NT; ++b) {
                 const uint32_t *w = reinterpret_cast<const uint32_t *>(raw[b]);
@@ -400,9 +416,10 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
                 phase ^= 1;
             }
             int tok = cc.c * kQ4Tile + (lane >> 2);
+            // false: nothing done, since steps lie apart, which a masked tile alone takes
             auto work = [&](auto tiles, auto masked) {
                 constexpr int TT = decltype(tiles)::value;
-                constexpr bool MASK = decltype(masked)::value;
+                constexpr bool MASK = decltype(masked)::value, ALONE = MASK && TT == 1;
                 // scores: 16 tokens x 8 query rows per tile and block, a group at a time
                 float s[TT][NT][4];
                 {
@@ -472,27 +489,33 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
                     }
                 }
                 uint32_t vw[TT][KW], vp[TT][2][PW];
-                float sv[TT][2][NG], least[TT][2];
+                float sv[TT][2][NG], least[TT][2], far = 0.f;
 #pragma unroll
                 for (int i = 0; i < TT; ++i) {
                     q4_words<D>(tile + i * TB + codes_at + q4_codes(D), vw[i]);
                     q4_params_of<NG>(tile + i * TB + param_at + q4_params(D, G), vp[i][0]);
                     q4_params_of<NG>(tile + i * TB + param_at + q4_params(D, G) + 16 * NG, vp[i][1]);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < 2; ++h) {  // (groups that hold no number are left out)
                         steps_of<NG>(vp[i][h], sv[i][h]);
-                        least[i][h] = kLnLeastStep;
-#pragma unroll
-                        for (int g = 0; g < NG; ++g) least[i][h] = fmaxf(least[i][h], sv[i][h][g]);
-                        least[i][h] = lg2_approx(least[i][h]);
+                        float hi = kLnLeastStep, lo = sv[i][h][0];
+                        if constexpr (NG == 4) {
+                            hi = tc::max3(tc::max3(hi, sv[i][h][0], sv[i][h][1]), sv[i][h][2], sv[i][h][3]);
+                            lo = fminf(min3(lo, sv[i][h][1], sv[i][h][2]), sv[i][h][3]);
+                        } else if constexpr (NG == 2) {
+                            hi = tc::max3(hi, sv[i][h][0], sv[i][h][1]);
+                            lo = fminf(lo, sv[i][h][1]);
+                        } else {
+                            hi = fmaxf(hi, lo);
+                        }
+                        far = fmaxf(far, fmaf(-kApart, lo, hi));
+                        least[i][h] = lg2_approx(hi);
                     }
                 }
-                bool grow = false;
-                float mt[NT][2];
 #pragma unroll
                 for (int b = 0; b < NT; ++b)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
                         for (int i = 0; i < TT; ++i) {
                             s[i][b][e] *= fc[b][e];
@@ -501,12 +524,66 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
                                 if (tok + 16 * i >= see[b][e]) s[i][b][e] = -INFINITY;
                                 if (tok + 16 * i + 8 >= see[b][e]) s[i][b][e + 2] = -INFINITY;
                             }
-                            const float x = fmaxf(s[i][b][e] + least[i][0], s[i][b][e + 2] + least[i][1]);
-                            mt[b][e] = i == 0 ? x : fmaxf(mt[b][e], x);
                         }
-                        grow = grow || mt[b][e] > m[b][e] + kLnGrow;
-                    }
-                if (__any_sync(0xffffffffu, grow)) {
+                float mt[NT][2];
+                auto grows = [&]() {
+                    bool grow = false;
+#pragma unroll
+                    for (int b = 0; b < NT; ++b)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                            for (int i = 0; i < TT; ++i) {
+                                const float x = fmaxf(s[i][b][e] + least[i][0], s[i][b][e + 2] + least[i][1]);
+                                mt[b][e] = i == 0 ? x : fmaxf(mt[b][e], x);
+                            }
+                            grow = grow || mt[b][e] > m[b][e] + kLnGrow;
+                        }
+                    return grow;
+                };
+                bool grow = grows(), apart = far > 0.f;
+                grow = __any_sync(0xffffffffu, grow || apart || dead != 0);
+                if (grow && (__any_sync(0xffffffffu, apart) || dead != 0)) {
+                    // again, without tokens that nobody sees and groups that are none
+                    bool seen[TT][2];
+                    uint32_t some = 0;  // groups that are not zero
+#pragma unroll
+                    for (int i = 0; i < TT; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            seen[i][h] = !MASK;
+                            if (MASK)
+#pragma unroll
+                                for (int b = 0; b < NT; ++b)
+                                    seen[i][h] = seen[i][h] || tok + 16 * i + 8 * h < max(see[b][0], see[b][1]);
+#pragma unroll
+                            for (int g = 0; g < NG; ++g)
+                                if (seen[i][h] && !(sv[i][h][g] <= kLnZeroStep)) some |= 1u << g;
+                        }
+                    some = __reduce_or_sync(0xffffffffu, some);
+                    int now = dead == kFresh ? (int)(~some & (kFresh - 1)) : dead;
+                    if (now > 0 && (now & some)) now = -1;
+                    apart = now < 0;
+#pragma unroll
+                    for (int i = 0; i < TT; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float hi = kLnLeastStep, lo = INFINITY;
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) {
+                                hi = seen[i][h] ? fmaxf(hi, sv[i][h][g]) : hi;
+                                lo = now > 0 && (now >> g & 1) ? lo : fminf(lo, sv[i][h][g]);
+                            }
+                            const bool x = seen[i][h] && lo * kApart < hi;
+                            apart = apart || x;
+                            least[i][h] = lg2_approx(x ? fmaxf(fmaxf(lo, hi * kLnFar), kLnFar) : hi);
+                        }
+                    apart = __any_sync(0xffffffffu, apart);
+                    if (!ALONE && apart) return false;
+                    dead = now;
+                    grow = __any_sync(0xffffffffu, grows());
+                }
+                if (grow) {
 #pragma unroll
                     for (int b = 0; b < NT; ++b)
 #pragma unroll
@@ -541,6 +618,81 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
                 for (int i = 0; i < TT; ++i) {
                     v0[i] = transpose8(NG == 4 && (j & 1) ? vp[i][0][PW - 1] : vp[i][0][0]) & kLow;
                     v1[i] = transpose8(NG == 4 && (j & 1) ? vp[i][1][PW - 1] : vp[i][1][0]) & kLow;
+                }
+                auto v_operand = [&](int i, int k, uint32_t k0, uint32_t k1, uint32_t(&a)[4]) {
+                    const uint32_t x = vw[i][k], h = x >> 8;
+                    a[0] = x & kLow;
+                    a[1] = x & kHigh;
+                    a[2] = h & kLow;
+                    a[3] = h & kHigh;
+                    if (VC) {
+                        a[0] = minus(a[0] | k1024, k0 | k1024);
+                        a[1] = minus(a[1] | k1024, k0 << 4 | k1024);
+                        a[2] = minus(a[2] | k1024, k1 | k1024);
+                        a[3] = minus(a[3] | k1024, k1 << 4 | k1024);
+                    }
+                };
+                if (ALONE && apart) {
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        const uint32_t k0 = VC ? __shfl_sync(0xffffffffu, v0[0], g * 4 + j) : 0u;
+                        const uint32_t k1 = VC ? __shfl_sync(0xffffffffu, v1[0], g * 4 + j) : 0u;
+                        uint32_t pf[NT][NS][2];
+                        float down[NT][2], zero[NT][2];
+#pragma unroll
+                        for (int b = 0; b < NT; ++b) {
+                            float a[4], up[2];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                a[e] = tok + 8 * (e >> 1) >= see[b][e & 1] ? 0.f : s[0][b][e] * sv[0][e >> 1][g];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float x = fmaxf(a[e], a[e + 2]);
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                                const uint32_t ex = min(max(__float_as_uint(x) >> 23, 8u), 254u);
+                                up[e] = __uint_as_float((261 - ex) << 23);  // 2^(7 - exponent)
+                                down[b][e] = __uint_as_float((ex - 7) << 23);
+                            }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float x = a[2 * h] * up[0], y = a[2 * h + 1] * up[1];
+#pragma unroll
+                                for (int n = 0; n < NS; ++n) {
+                                    const uint32_t w = pack(x, y);
+                                    pf[b][n][h] = transpose8(w);
+                                    const float2 r = unpack(w);
+                                    x -= r.x;
+                                    y -= r.y;
+                                }
+                            }
+                            zero[b][0] = zero[b][1] = 0.f;
+                            if (!VC) {
+                                float c[4];
+                                mma0(c, v0[0] & rmask[g], 0u, v1[0] & rmask[g], 0u, pf[b][0][0], pf[b][0][1]);
+                                zero[b][0] = __shfl_sync(0xffffffffu, c[0], g * 4 + j);
+                                zero[b][1] = __shfl_sync(0xffffffffu, c[1], g * 4 + j);
+                            }
+                        }
+#pragma unroll
+                        for (int k = g * G / 16; k < (g + 1) * G / 16; ++k) {
+                            uint32_t a[4];
+                            v_operand(0, k, k0, k1, a);
+#pragma unroll
+                            for (int b = 0; b < NT; ++b) {
+                                float c[4];
+                                mma0(c, a[0], a[1], a[2], a[3], pf[b][0][0], pf[b][0][1]);
+                                if (NS == 2) mma(c, a[0], a[1], a[2], a[3], pf[b][NS - 1][0], pf[b][NS - 1][1]);
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    o[b][k][e] = fmaf(c[e] - zero[b][e], down[b][e], o[b][k][e]);
+                                    o[b][k][e + 2] = fmaf(fmaf(-16.f, zero[b][e], c[e + 2]), down[b][e], o[b][k][e + 2]);
+                                }
+                            }
+                        }
+                    }
+                    return true;
                 }
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
@@ -580,31 +732,25 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
                     for (int i = 0; i < TT; ++i)
 #pragma unroll
                         for (int k = g * G / 16; k < (g + 1) * G / 16; ++k) {
-                            const uint32_t x = vw[i][k], h = x >> 8;
-                            uint32_t a0 = x & kLow, a1 = x & kHigh, a2 = h & kLow, a3 = h & kHigh;
-                            if (VC) {
-                                a0 = minus(a0 | k1024, k0[i] | k1024);
-                                a1 = minus(a1 | k1024, k0[i] << 4 | k1024);
-                                a2 = minus(a2 | k1024, k1[i] | k1024);
-                                a3 = minus(a3 | k1024, k1[i] << 4 | k1024);
-                            }
+                            uint32_t a[4];
+                            v_operand(i, k, VC ? k0[i] : 0u, VC ? k1[i] : 0u, a);
 #pragma unroll
                             for (int b = 0; b < NT; ++b)
 #pragma unroll
                                 for (int y = 0; y < NS; ++y)
-                                    mma(o[b][k], a0, a1, a2, a3, pf[i][b][y][0], pf[i][b][y][1]);
+                                    mma(o[b][k], a[0], a[1], a[2], a[3], pf[i][b][y][0], pf[i][b][y][1]);
                         }
                 }
+                return true;
             };
             // tiles that all rows see whole, then the others
             const int whole = min(nt, see_least - cc.c);
-            if (PAIR && whole == 2) {
-                work(std::integral_constant<int, PAIR ? 2 : 1>{}, std::false_type{});
-            } else {
+            using One = std::integral_constant<int, 1>;
+            using Two = std::integral_constant<int, PAIR ? 2 : 1>;
+            if (!(PAIR && whole == 2 && work(Two{}, std::false_type{}))) {
 #pragma unroll 1
                 for (int i = 0; i < nt; ++i, tile += TB, tok += kQ4Tile)
-                    if (!PAIR && i < whole) work(std::integral_constant<int, 1>{}, std::false_type{});
-                    else work(std::integral_constant<int, 1>{}, std::true_type{});
+                    if (PAIR || i >= whole || !work(One{}, std::false_type{})) work(One{}, std::true_type{});
             }
             left -= nt;
             const bool last = left == 0 || (cc.c + nt == cc.cr && left <= kLnPad), ends = last || cc.c + nt == cc.cr;

@@ -170,3 +170,88 @@ def test_a_row_that_sees_a_nan_in_k_has_no_log_sum_either(dtype, fan, n):
     assert torch.isfinite(lse[:c.rows][:, 4:]).all() and torch.isfinite(out[:c.rows][:, 4:]).all()
     rest = [i for i in range(fan) if i not in bad]
     assert torch.equal(lse[rest], z[rest]) and torch.equal(out[rest], good[rest])
+
+
+# ---- groups of very different steps --------------------------------------------------------------------
+def refill(c):
+    """What Q4Case's pages and prompts hold, from its K and V as they are now."""
+    page = c.pb.page_size
+    slots = [int(c.table[r, j // page]) * page + j % page for r in range(len(c.lens)) for j in range(c.lens[r])]
+    at = torch.tensor(slots, device=DEV)
+    pb = api.Q4Problem(1, 1, c.pb.n_kv_heads, c.pb.n_kv_heads, c.pb.d_head, 0, page, c.pb.n_pages, c.pb.max_pages,
+                       len(slots), len(slots), c.pb.dtype, c.group)
+    api.q4_append(pb, c.K[at // page, :, at % page].contiguous(), c.V[at // page, :, at % page].contiguous(), i32(slots),
+                  c.pages)
+    if c.pb.n_prefix:
+        api.q4_pack(c.pb, c.Kp.contiguous(), c.Vp.contiguous(), c.plen, c.prefix)
+    api.kve_check_device()
+    return c
+
+
+def scaled(c, power):
+    """V's channels times 2^power, a number per group."""
+    f = torch.exp2(torch.tensor(power, device=DEV, dtype=torch.float64).repeat_interleave(c.group))
+    c.V, c.Vp = ((x.double() * f).to(x.dtype) for x in (c.V, c.Vp))
+    return refill(c)
+
+
+POWERS = [("bf16", 32, [0, -28, -60, 20]), ("f32", 32, [-34, 0, 12, -70]), ("f16", 32, [12, -9, 0, -8]),
+          ("bf16", 64, [-64, 0]), ("f16", 64, [-10, 12]), ("f32", 64, [0, -30]), ("bf16", 128, [-64]), ("f32", 128, [-66]),
+          ("bf16", 32, [-90] * 4), ("f32", 32, [-85] * 4), ("bf16", 32, [40, -35, 40, -35])]
+
+
+@pytest.mark.parametrize("fan,new_hi", [(1, 1), (2, 3), (6, 1)])
+@pytest.mark.parametrize("dtype,group,power", POWERS, ids=str)
+def test_every_group_of_v_keeps_its_own_bits(dtype, group, power, fan, new_hi):
+    """A group's output does not go by the size of its row's other groups, nor by V's size as a whole."""
+    scaled(Q4Case(dtype, 2, fan, 4, 2, 128, 200, 16, 50, new_hi, group=group, ragged=True, seed=22), power).check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_groups_that_change_their_size_from_token_to_token(dtype, d):
+    """Sizes of every group and token for itself, over 2^40 (fp16 2^20), rows without any at all and a NaN that nobody
+    sees among them."""
+    c = Q4Case(dtype, 1, 2, 4, 1, d, 150, 16, 90, 4, ragged=False, seed=23)
+    gen = torch.Generator(device=DEV).manual_seed(d)
+    lo, hi = (-14, 6) if dtype == "f16" else (-30, 10)
+    for name in ("V", "Vp"):
+        x = getattr(c, name)
+        e = torch.randint(lo, hi, x.shape[:-1] + (d // 32,), generator=gen, device=DEV)
+        e = e.masked_fill(torch.rand(e.shape, generator=gen, device=DEV) < 0.1, -999).double()
+        setattr(c, name, (x.double() * torch.exp2(e).repeat_interleave(32, -1)).to(x.dtype))
+    refill(c).check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_small_v_behind_one_that_is_large_in_another_group(dtype):
+    """The first tokens weigh in one group 2^50 times what the later ones do, in the others as much."""
+    c = Q4Case(dtype, 1, 1, 4, 1, 128, 400, 16, 60, 1, seed=24)
+    c.Vp[:, :, :20, 32:64] = (c.Vp[:, :, :20, 32:64].double() * 2.0 ** 50).to(DT[dtype])
+    refill(c).check()
+    c.Vp[:, :, 100:110, 96:] = (c.Vp[:, :, 100:110, 96:].double() * 2.0 ** 70).to(DT[dtype])
+    refill(c).check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_channels_that_are_not_used(dtype):
+    """A head of 96 channels in 128: the last group is 0 throughout, and stays it."""
+    c = Q4Case(dtype, 1, 2, 4, 1, 128, 200, 16, 60, 2, seed=25)
+    for x in (c.V, c.Vp):
+        x[..., 96:] = torch.where(x[..., 96:].isnan(), x[..., 96:], 0)
+    out, _ = refill(c).check()
+    assert (out[:c.rows, :, 96:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("d,group", [(128, 32), (128, 64), (64, 32), (64, 64)])
+def test_groups_that_are_zero_at_first(dtype, d, group):
+    """The last group is zero for some tokens, then small, then as the others; others are zero for a while, too."""
+    for late, size in ((16, -20), (7, -9), (130, 0)):
+        c = Q4Case(dtype, 1, 1, 4, 1, d, 200, 16, 90, 3, seed=26)
+        for x in (c.V, c.Vp):
+            x[..., -group:] *= 2.0 ** size
+        c.Vp[:, :, :late, -group:] = 0
+        c.Vp[:, :, late + 20:late + 30, :group] = 0
+        c.Vp[:, :, 180:, -group:] *= 2.0 ** -size
+        refill(c).check()
