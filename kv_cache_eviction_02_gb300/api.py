@@ -752,6 +752,11 @@ def _q4_rows(t, name, pb, count, rows, dev):
     return t.data_ptr(), s0, s1, s2
 
 
+def _q4_alike(ks, vs, pb, count, rows):
+    """Whether K's and V's strides agree, but for dimensions of one entry, where they are never used."""
+    return all(n == 1 or a == b for n, a, b in zip((count, pb.n_kv_heads, rows), ks, vs))
+
+
 def q4_pack(pb: Q4Problem, K, V, prefix_len, prefix, stream=None):
     """Quantises prompts K, V [n_prompts][n_kv_heads][>= n_prefix][d_head] (a layer's slice of a larger cache, or
     what lorekv_select_compact leaves; the same strides for both) into prefix (uint8, pb.prefix_bytes). prefix_len
@@ -762,7 +767,7 @@ def q4_pack(pb: Q4Problem, K, V, prefix_len, prefix, stream=None):
         return _check(status)
     k, *ks = _q4_rows(K, "K", pb, pb.n_prompts, pb.n_prefix, dev)
     v, *vs = _q4_rows(V, "V", pb, pb.n_prompts, pb.n_prefix, dev)
-    if ks != vs:
+    if not _q4_alike(ks, vs, pb, pb.n_prompts, pb.n_prefix):
         raise ValueError("V: the strides differ from K's")
     _check(lib().q4_pack(pb.c_shape, pb.group, k, v, *ks,
                          _pg(prefix_len, "prefix_len", torch.int32, pb.n_prompts, dev),
@@ -800,7 +805,7 @@ def q4_unpack(pb: Q4Problem, cache, block_table, lens, K_out, V_out, stream=None
         most = min(most, K_out.shape[2])
     k, *ks = _q4_rows(K_out, "K_out", pb, count, most, dev)
     v, *vs = _q4_rows(V_out, "V_out", pb, count, most, dev)
-    if ks != vs:
+    if not _q4_alike(ks, vs, pb, count, most):
         raise ValueError("V_out: the strides differ from K_out's")
     _check(lib().q4_unpack(
         pb.c_shape, pb.group, _pg(cache, "cache", torch.uint8, pb.pool_bytes if paged else pb.prefix_bytes, dev),

@@ -123,6 +123,11 @@ struct Args {
         for (int k = 0; k < 3; ++k) s[k] = x->stride(k);
         return x->data_ptr();
     }
+    // K's and V's strides agree, but for dimensions of one entry, where they are never used
+    bool alike(const long long (&s)[3], const long long (&t)[3], long long count, long long rows) const {
+        return ok && (count == 1 || s[0] == t[0]) && (shape->n_kv_heads == 1 || s[1] == t[1]) &&
+               (rows == 1 || s[2] == t[2]);
+    }
     long long requests() const { return ok ? (long long)shape->n_prompts * shape->fan : 0; }
     long long pool() const {
         return ok ? (long long)shape->n_pages * shape->n_kv_heads * shape->page_size * shape->d_head : 0;
@@ -206,7 +211,7 @@ PyObject *pack4(Args &a) {
     a.ok = a.ok && n > 0;
     const long long S = a.ok ? a.shape->n_prompts : 0;
     const void *K = a.cache_rows(1, S, &n, n, s), *V = a.cache_rows(2, S, &n, n, t);
-    a.ok = a.ok && s[0] == t[0] && s[1] == t[1] && s[2] == t[2];
+    a.ok = a.alike(s, t, S, n);
     const int32_t *len = a.ints(3, S, true);
     void *prefix = a.array(4, at::kByte, a.bytes(g, false));
     return result(a, [&] { return g_q4_pack(a.shape, g, K, V, s[0], s[1], s[2], len, prefix, a.stream); });
@@ -233,7 +238,7 @@ PyObject *unpack4(Args &a) {
     void *K = a.cache_rows(4, count, &n, most, s);
     a.ok = a.ok && n > 0;
     void *V = a.cache_rows(5, count, &n, most, t);
-    a.ok = a.ok && s[0] == t[0] && s[1] == t[1] && s[2] == t[2];
+    a.ok = a.alike(s, t, count, n);
     return result(a, [&] {
         return g_q4_unpack(a.shape, g, cache, table, len, (int)n, K, V, s[0], s[1], s[2], a.stream);
     });

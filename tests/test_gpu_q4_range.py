@@ -64,7 +64,7 @@ def test_rows_behind_a_refused_request(dtype, d):
 @pytest.mark.parametrize("written,read", [("bf16", "f16"), ("f32", "f16"), ("f16", "bf16"), ("f16", "f32"),
                                           ("bf16", "f32"), ("f32", "bf16")])
 def test_an_array_written_from_one_type_is_read_as_another(written, read, d, group):
-    """The values s m, rounded to the type that reads: zeros stay zeros whatever the step, what is above the largest number
+    """The values s m, rounded to the type that reads: zeros stay zeros whatever the step, what is above its largest number
     becomes an infinity, and only groups that hold no number are NaN."""
     n = 96
     gen = torch.Generator(device=DEV).manual_seed(d)
@@ -255,3 +255,26 @@ def test_groups_that_are_zero_at_first(dtype, d, group):
         c.Vp[:, :, late + 20:late + 30, :group] = 0
         c.Vp[:, :, 180:, -group:] *= 2.0 ** -size
         refill(c).check()
+
+
+# ---- strides ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("native", [True, False])
+def test_strides_of_dimensions_of_one_entry_do_not_matter(native, monkeypatch):
+    """One prompt, one KV head or one row: K and V may come from arrays of different widths."""
+    if not native:
+        monkeypatch.setattr(api, "_native", api._NoBinding)
+    for S, H, n in ((1, 2, 40), (2, 1, 40), (1, 1, 40), (2, 2, 1), (1, 1, 1)):
+        d = 64
+        K = torch.randn(S, H, n, d, device=DEV).bfloat16()
+        V = torch.randn(S, H, n, d, device=DEV).bfloat16()
+        apart = [7 * H * n * d if S == 1 else H * n * d, 3 * n * d if H == 1 else n * d, 5 * d if n == 1 else d, 1]
+        W = V.as_strided(V.shape, apart)
+        pb = api.Q4Problem(S, 1, H, H, d, n, 16, 1, 1, 1, 1, api.KVE_BF16, 32)
+        prefix = [torch.zeros(pb.prefix_bytes, dtype=torch.uint8, device=DEV) for _ in range(2)]
+        api.q4_pack(pb, K, V, None, prefix[0])
+        api.q4_pack(pb, K, W, None, prefix[1])
+        assert torch.equal(*prefix)
+        a, b = torch.zeros_like(K), torch.zeros_like(V)
+        api.q4_unpack(pb, prefix[0], None, None, a, b.as_strided(V.shape, apart))
+        api.kve_check_device()
+        assert all(torch.equal(y, torch.from_numpy(held(x, 32, "bf16")[0]).to(DEV).bfloat16()) for x, y in ((K, a), (V, b)))
