@@ -1,8 +1,10 @@
-"""Q4Cache without a GPU: what it hands to the calls."""
+"""Cache in 4 bits without a GPU: what Q4Cache hands to the calls, and values of the oracle worked out by hand."""
+import numpy as np
 import pytest
 import torch
 
 from kv_cache_eviction_02_gb300 import _build, api
+from oracle import cache4
 
 
 @pytest.fixture
@@ -37,3 +39,12 @@ def test_every_layer_keeps_its_own_lengths(calls):
     c.pack(0, K, K, other)  # after another eviction
     c.attend(0, None, None)
     assert calls[-1][1][3] is other
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_a_group_of_ones_beside_one_that_holds_no_number(dtype):
+    """1 / 15 lies between the numbers of four bits 8 / 128 and 9 / 128; 128 / 9 is nearest to 14."""
+    x = np.ones((2, 32))
+    x[0, 5] = np.inf
+    v, s = cache4.hold(x, 32, cache4.LARGEST[dtype])
+    assert np.isnan(v[0]).all() and (v[1] == 14 * 9 / 128).all() and (s[1] == 9 / 128).all()
