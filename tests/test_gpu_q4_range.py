@@ -147,8 +147,8 @@ def test_layers_of_one_cache_with_lengths_of_their_own():
 
 
 # ---- rows that hold no number --------------------------------------------------------------------------
-@pytest.mark.parametrize("dtype,fan,n", [("bf16", 1, 100), ("f32", 1, 100), ("f16", 1, 0), ("bf16", 8, 300), ("f16", 70, 300),
-                                         ("f32", 20, 300)])
+@pytest.mark.parametrize("dtype,fan,n", [("bf16", 1, 100), ("f32", 1, 100), ("f16", 1, 0), ("bf16", 8, 300),
+                                         ("f16", 70, 300), ("f32", 20, 300)])
 def test_a_row_that_sees_a_nan_in_k_has_no_log_sum_either(dtype, fan, n):
     """-inf would say that there was nothing to see. By lines, on tcgen05 from codes and read back first."""
     c = Q4Case(dtype, 2, fan, 8, 2, 64, n, 16, 20, 1, seed=12)
@@ -255,6 +255,61 @@ def test_groups_that_are_zero_at_first(dtype, d, group):
         c.Vp[:, :, late + 20:late + 30, :group] = 0
         c.Vp[:, :, 180:, -group:] *= 2.0 ** -size
         refill(c).check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_largest_steps_beside_the_smallest(dtype):
+    """Near 2^89 and near 2^-90 in one row: all finite, the large group within its bound; and beside zeros."""
+    for power in ([83, -90, 83, 0], [83, -9999, 83, 83]):
+        c = Q4Case(dtype, 1, 2, 4, 1, 128, 120, 16, 40, 2, seed=27)
+        scaled(c, power)
+        out, lse = c.run()
+        (V, _), (K, _) = held(c.V, 32, dtype), held(c.K, 32, dtype)
+        (Vp, _), (Kp, _) = held(c.Vp, 32, dtype), held(c.Kp, 32, dtype)
+        ref = sp.pg_attention(f64(c.q), Kp, Vp, c.np_plen, K, V, np.where(c.table > 2 ** 30, 0, c.table), c.lens, c.q_start,
+                              c.F)
+        got, h = f64(out)[:c.rows], torch.finfo(DT[dtype]).eps / 2
+        assert np.isfinite(got).all() and np.isfinite(f64(lse)[:c.rows]).all()
+        # weights and output round (h each), codes and zero codes to 2^-12 of a step, of which a term is one at least
+        big = [i for i in range(128) if power[i // 32] == 83]
+        tol = 2.5 * h * ref["terms"] + 2.0 ** -12 * ref["terms"].max(-1, keepdims=True)
+        assert (np.abs(got - ref["out"][:c.rows]) <= tol[:c.rows])[..., big].all()
+        assert (np.abs(f64(lse) - ref["lse"])[:c.rows] <= 2.0 ** -12 * (1 + ref["mag"])[:c.rows]).all()
+
+
+@pytest.mark.parametrize("dtype,fan,n,new,path", [("bf16", 8, 300, 1, "q4_prompt"), ("f16", 70, 300, 1, "q4_prompt"),
+                                                  ("bf16", 70, 0, 24, "q4_own"), ("f32", 5, 40, 3, "q4_lines")])
+def test_captured_calls_of_every_path_replay_on_other_rows(dtype, fan, n, new, path):
+    """Captured once, replayed with other queries, lengths and prompts: as the same calls one by one."""
+    c = Q4Case(dtype, 1, fan, 8, 2, 64, n, 16, 600 if new > 20 else 40, new, seed=28)
+    assert path in stages(c)
+    q, out, lse = c.q.contiguous(), torch.zeros(c.shape, device=DEV, dtype=DT[dtype]), torch.zeros(c.shape[:2], device=DEV)
+    plen = i32([n]) if n else None
+    args = (c.prefix, plen, c.pages, i32(c.table), i32(c.lens), i32(c.q_start), i32(c.row_req), out, lse, c.ws)
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        api.q4_attention(c.pb, q, *args)
+    st.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        api.q4_attention(c.pb, q, *args)
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    for step in range(3):
+        q.copy_(torch.randn(c.shape, generator=gen, device=DEV))
+        if n:
+            plen.fill_(n - 37 * step)
+            api.q4_pack(c.pb, torch.randn(1, 2, n, 64, generator=gen, device=DEV).to(DT[dtype]),
+                        torch.randn(1, 2, n, 64, generator=gen, device=DEV).to(DT[dtype]), None, c.prefix)
+        out.fill_(3.0)
+        api.q4_attention(c.pb, q, *args)
+        want = out.clone(), lse.clone()
+        out.fill_(3.0)
+        lse.fill_(5.0)
+        c.ws.fill_(0xFF)
+        g.replay()
+        api.kve_check_device()
+        assert torch.equal(out, want[0]) and torch.equal(lse[:c.rows], want[1][:c.rows])
+        assert (lse[c.rows:] == 5).all()
 
 
 # ---- strides ---------------------------------------------------------------------------------------------
