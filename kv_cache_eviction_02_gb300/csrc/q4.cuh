@@ -137,7 +137,8 @@ template <> struct Q4Codes<__half> {
         // Powers of two that fp16 does not have: a takes what lies below its least, 2^-24, or, above its largest, 2^15, a
         // factor of two, with which every code but 0 is an infinity (0 stays 0). NaN steps keep their infinite e.
         constexpr uint32_t least = 103u << 23, most = 142u << 23, none = 255u << 23;
-        if (min(e0, e1) < least || max(e0, e1) > most) {
+        constexpr uint32_t span = ((most - least) >> 16) * 0x10001u;  // (a borrow leaves the half that it comes from outside)
+        if (__vmaxu2((p2 & 0x7F807F80u) - (least >> 16) * 0x10001u, span) != span) {
             auto rest = [](uint32_t x) {
                 return x < least ? __uint_as_float(x) * 0x1p24f : (x > most ? 2.f : 1.f);
             };
