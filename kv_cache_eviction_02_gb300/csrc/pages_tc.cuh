@@ -541,22 +541,26 @@ __device__ __forceinline__ void pt_k_tile(uint32_t raw, uint32_t place, int row0
     q4_words<DR>(raw + q4_lane<DR>(lane), w);
 #pragma unroll
     for (int h = 0; h < 2; ++h) q4_params_of<NG>(raw + 2 * q4_codes(DR) + (r + 8 * h) * 2 * NG, p[h]);
+    auto make = [&](auto check) {
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
+        for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const Q4Codes<T> of(__byte_perm(p[h][g >> 1], 0, g & 1 ? 0x3232 : 0x1010));
-            const int row = row0 + r + 8 * h;
+            for (int h = 0; h < 2; ++h) {
+                const Q4Codes<T> of(__byte_perm(p[h][g >> 1], 0, g & 1 ? 0x3232 : 0x1010), check);
+                const int row = row0 + r + 8 * h;
 #pragma unroll
-            for (int c = g * G / 32; c < (g + 1) * G / 32; ++c) {
-                const uint32_t x = w[2 * c] >> (8 * h), y = w[2 * c + 1] >> (8 * h);
-                const uint32_t v[4] = {of.low(x), of.high(x), of.low(y), of.high(y)};
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
-                                 place + (c >> 1) * 16384 + tc::sw128_offset(row, (c & 1) * 4 + j)),
-                             "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                             : "memory");
+                for (int c = g * G / 32; c < (g + 1) * G / 32; ++c) {
+                    const uint32_t x = w[2 * c] >> (8 * h), y = w[2 * c + 1] >> (8 * h);
+                    const uint32_t v[4] = {of.low(x), of.high(x), of.low(y), of.high(y)};
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                     place + (c >> 1) * 16384 + tc::sw128_offset(row, (c & 1) * 4 + j)),
+                                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                                 : "memory");
+                }
             }
-        }
+    };
+    if (q4_any_far<T, NG>(p)) make(std::true_type{});
+    else make(std::false_type{});
 }
 // 16 tokens of V, of which the first `have` are there; the others' rows are zeros.
 template <typename T, int DR, int G, bool WHOLE>
@@ -572,24 +576,28 @@ __device__ __forceinline__ void pt_v_tile(uint32_t raw, uint32_t place, int row0
     for (int h = 0; h < 2; ++h)
         there[h] = (2 * j + 8 * h < have ? 0xFFFFu : 0u) | (2 * j + 8 * h + 1 < have ? 0xFFFF0000u : 0u);
     const int to = lane >> 3, row = row0 + (to >> 1) * 8 + (lane & 7);
+    auto make = [&](auto check) {
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        const Q4Codes<T> of0(__byte_perm(p[0][g >> 1], p[1][g >> 1], g & 1 ? 0x7632 : 0x5410));
-        const Q4Codes<T> of1(__byte_perm(p[2][g >> 1], p[3][g >> 1], g & 1 ? 0x7632 : 0x5410));
+        for (int g = 0; g < NG; ++g) {
+            const Q4Codes<T> of0(__byte_perm(p[0][g >> 1], p[1][g >> 1], g & 1 ? 0x7632 : 0x5410), check);
+            const Q4Codes<T> of1(__byte_perm(p[2][g >> 1], p[3][g >> 1], g & 1 ? 0x7632 : 0x5410), check);
 #pragma unroll
-        for (int c = g * G / 16; c < (g + 1) * G / 16; ++c) {
-            const uint32_t x = w[c], y = x >> 8;
-            uint32_t v[4] = {of0.low(x), of0.high(x), of1.low(y), of1.high(y)};
-            if (!WHOLE) {
+            for (int c = g * G / 16; c < (g + 1) * G / 16; ++c) {
+                const uint32_t x = w[c], y = x >> 8;
+                uint32_t v[4] = {of0.low(x), of0.high(x), of1.low(y), of1.high(y)};
+                if (!WHOLE) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] &= there[i >> 1];
+                    for (int i = 0; i < 4; ++i) v[i] &= there[i >> 1];
+                }
+                asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(
+                                 place + (c >> 2) * 16384 + tc::sw128_offset(row, (2 * c + (to & 1)) & 7)),
+                             "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                             : "memory");
             }
-            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(
-                             place + (c >> 2) * 16384 + tc::sw128_offset(row, (2 * c + (to & 1)) & 7)),
-                         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                         : "memory");
         }
-    }
+    };
+    if (q4_any_far<T, NG>(p)) make(std::true_type{});
+    else make(std::false_type{});
 }
 // K and V of ntl tiles of 128 tokens (n tokens there): K of both halves, then V. The makers take turns at the 16-token
 // tiles; one of them may also be the one that sends for the raw halves.

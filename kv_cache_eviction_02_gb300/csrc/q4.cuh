@@ -19,6 +19,8 @@
 // A lane's words lie in pieces of 16 bytes (8 with d_head 32), lane after lane.
 #pragma once
 
+#include <type_traits>
+
 #include "pages_ptx.cuh"
 
 namespace kve {
@@ -113,7 +115,7 @@ template <int NG> __device__ __forceinline__ void q4_params_of(uint32_t at, uint
 template <typename T> struct Q4Codes;
 template <> struct Q4Codes<__nv_bfloat16> {
     uint32_t s, k;
-    __device__ __forceinline__ explicit Q4Codes(uint32_t p2) : s(p2 & 0xFFF0FFF0u), k((p2 & 0x000F000Fu) | 0x43004300u) {}
+    __device__ __forceinline__ explicit Q4Codes(uint32_t p2, bool = true) : s(p2 & 0xFFF0FFF0u), k((p2 & 0x000F000Fu) | 0x43004300u) {}
     __device__ __forceinline__ uint32_t of(uint32_t low_nibbles) const {
         const uint32_t x = (low_nibbles & 0x000F000Fu) | 0x43004300u;  // 128 + n
         const __nv_bfloat162 v = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x),
@@ -130,29 +132,50 @@ template <> struct Q4Codes<__half> {
     uint32_t a, c, e, zero;
     __device__ __forceinline__ static __half2 h2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
     __device__ __forceinline__ static uint32_t u(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
-    __device__ __forceinline__ explicit Q4Codes(uint32_t p2) {
+    // Whether fp16 does not have the power of two of a parameter, least .. most, in either half of the words of which
+    // y is the maximum of beyond(word).
+    static constexpr uint32_t kLeast = 103u << 23, kMost = 142u << 23, kNone = 255u << 23;  // 2^-24, 2^15; NaN's
+    __device__ __forceinline__ static uint32_t beyond(uint32_t p2) {  // (a borrow leaves its half far outside)
+        return (p2 & 0x7F807F80u) - (kLeast >> 16) * 0x10001u;
+    }
+    __device__ __forceinline__ static bool far(uint32_t y) {
+        constexpr uint32_t span = ((kMost - kLeast) >> 16) * 0x10001u;
+        return __vmaxu2(y, span) != span;
+    }
+    // check: the parameters may be such ones
+    __device__ __forceinline__ explicit Q4Codes(uint32_t p2, bool check = true) {
         a = (p2 & 0x00700070u) << 3 | 0x3C003C00u;
         const uint32_t e0 = p2 << 16 & 0x7F800000u, e1 = p2 & 0x7F800000u;
         e = u(__floats2half2_rn(__uint_as_float(e0), __uint_as_float(e1)));
-        // Powers of two that fp16 does not have: a takes what lies below its least, 2^-24, or, above its largest, 2^15, a
-        // factor of two, with which every code but 0 is an infinity (0 stays 0). NaN steps keep their infinite e.
-        constexpr uint32_t least = 103u << 23, most = 142u << 23, none = 255u << 23;
-        constexpr uint32_t span = ((most - least) >> 16) * 0x10001u;  // (a borrow leaves the half that it comes from outside)
-        if (__vmaxu2((p2 & 0x7F807F80u) - (least >> 16) * 0x10001u, span) != span) {
-            auto rest = [](uint32_t x) {
-                return x < least ? __uint_as_float(x) * 0x1p24f : (x > most ? 2.f : 1.f);
-            };
-            auto held = [](uint32_t x) { return __uint_as_float(x == none ? x : min(max(x, least), most)); };
+        // a takes what lies below the least power of two or, above the largest, a factor of two, with which every code
+        // but 0 is an infinity (0 stays 0). NaN steps keep their infinite e.
+        if (check && far(beyond(p2))) {
+            auto rest = [](uint32_t x) { return x < kLeast ? __uint_as_float(x) * 0x1p24f : (x > kMost ? 2.f : 1.f); };
+            auto held = [](uint32_t x) { return __uint_as_float(x == kNone ? x : min(max(x, kLeast), kMost)); };
             a = u(__hmul2(h2(a), __floats2half2_rn(rest(e0), rest(e1))));
             e = u(__floats2half2_rn(held(e0), held(e1)));
         }
         c = u(__hmul2(h2((p2 << 4 & 0x00F000F0u) | 0xD400D400u), h2(a)));  // -(64 + k) a
-        zero = u(__hmul2(h2(e), h2(0u)));
+        zero = check ? u(__hmul2(h2(e), h2(0u))) : 0u;
     }
     __device__ __forceinline__ uint32_t high(uint32_t x) const {
         return u(__hfma2(__hfma2(h2((x & 0x00F000F0u) | 0x54005400u), h2(a), h2(c)), h2(e), h2(zero)));
     }
     __device__ __forceinline__ uint32_t low(uint32_t x) const { return high(x << 4); }
 };
+
+// The same of all parameters of N tokens, NG each: whether Q4Codes have to look at them one by one. All lanes call.
+template <typename T, int NG, int N> __device__ __forceinline__ bool q4_any_far(const uint32_t (&p)[N][(NG + 1) / 2]) {
+    if constexpr (std::is_same<T, __half>::value) {
+        uint32_t y = 0;
+#pragma unroll
+        for (int t = 0; t < N; t += NG == 1 ? 2 : 1)
+#pragma unroll
+            for (int i = 0; i < (NG + 1) / 2; ++i)
+                y = __vmaxu2(y, Q4Codes<T>::beyond(NG == 1 ? __byte_perm(p[t][0], p[(t + 1) % N][0], 0x5410) : p[t][i]));
+        return __any_sync(0xffffffffu, Q4Codes<T>::far(y));
+    }
+    return false;
+}
 
 }  // namespace kve
