@@ -493,7 +493,9 @@ size_t q4_workspace_size(const KvePgShape *shape, int group);
  * (bf16), 2^-20 (fp16, fp32). Weights times steps below 2^-80 of the row's largest, or of steps below 2^-80, may be lost.
  * Few rows behind a V whose groups have steps more than 2^12 (fp32 2^10) apart in one row take up to twice as long.
  * Prompts of 16-bit types behind more than one row tile of 128 query rows are read back into the workspace, one
- * layer's n_prompts * n_kv_heads * n_prefix * d_head values of K and V, if that is 4 GiB at most.
+ * layer's n_prompts * n_kv_heads * n_prefix * d_head values of K and V, if that is 4 GiB at most. Behind prompts of
+ * many thousand rows more than 16 query rows per KV head (of 16-bit types) take longer than pg_attention over 16-bit
+ * arrays does.
  * Requirements as in pg_attention; q, steps and scores are below 2^89. A row that sees a NaN in K is NaN, lse too, one that
  * sees a NaN in V is NaN in that group's channels and may be in its head's others; other rows of a prompt's requests,
  * or of the same request, that share a tile of query rows with it may be too. */

@@ -6,7 +6,7 @@
 // channels of a token, a 16-byte store; V's hold tokens side by side, and stmatrix turns them, which leaves the
 // 8 even channels of every 16 before the 8 odd ones: the epilogue puts O's columns back in order.
 //
-// One row tile behind 128K rows (8 KV heads, groups of 32): bf16 133 us, fp16 158, 2.4 to 2.9 us a tile of 128 tokens, which
+// One row tile behind 128K rows (8 KV heads, groups of 32): bf16 133 us, fp16 156, 2.4 to 2.9 us a tile of 128 tokens, which
 // the makers bound (without their work 81 us): a warp takes 2200 cycles for 16 tokens' K and V. More makers (4 -> 6) or raw halves (3 -> 6) changed
 // nothing; makers in functions of their own did, which leaves the softmax its registers (two row tiles: 384 -> 233 us).
 #pragma once

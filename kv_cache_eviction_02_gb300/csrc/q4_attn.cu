@@ -18,7 +18,7 @@
 //
 // One request behind 128K rows (32/8 heads of d 128, groups of 32, 151 MB): 44.5 us, of which the set-up until the first
 // product takes 3.5, the tiles 32 (4.8 TB/s), the join 8. 64 requests with caches of up to 16K rows (groups of 64, 572
-// MB): 122 us, 4.7 TB/s, 287 instructions a tile and warp, the logic unit busy for 0.52 of the time and a warp's own
+// MB): 122 us, 4.7 TB/s, 295 instructions a tile and warp, the logic unit busy for 0.54 of the time and a warp's own
 // dependent instructions most of the rest: 12 warps an SM are what the registers hold. What was measured and not
 // kept: 16 warps with spills (59 -> 60 us), codes made normal numbers for bf16 too (V's 43 -> 47 us, K's and V's 53),
 // units of 16 query rows (109 -> 121), shifts as multiplications (124 -> 136), the join in this kernel by tickets (43 ->

@@ -10,7 +10,7 @@
 // exact remainder x - s m.
 //
 // Bound by HBM: one layer's 128K prompt of bf16 (8 heads of d 128) packed and read back 226 us, 6.1 TB/s; four ragged
-// prompts of 32K (fp16) read back 92 us, 6.8 TB/s. Each of four lanes works out one row's steps (each for itself: 289 us), and
+// prompts of 32K (fp16) read back 93.5 us, 6.7 TB/s. Each of four lanes works out one row's steps (each for itself: 289 us), and
 // values come back in 16-bit arithmetic, which is exact (in fp32: 122 us for the latter). A thread takes 8 channels of the four
 // tokens 2 j, 2 j + 1, 2 j + 8, 2 j + 9 of a tile, whose codes fill whole words of K and of V: rows come in 16-byte
 // loads and leave as full 32-byte sectors, no shared memory between.
