@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
         float o[NT][KW][4], z[NT][4], m[NT][2], l[NT][2];
         int see[NT][2], see_least = 0, rows, row0;  // tokens that columns see; the tiles that all of them see whole
         const float k1 = kLog2e * rsqrtf((float)D);
-        int dead;  // groups of V that were zeros so far, kFresh before the first tile, -1: more of them than are now
+        int dead;  // groups of V that were zeros in all tiles so far; kFresh: before the first, -1: one came alive
         uint32_t zmask[NG], rmask[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(Ln<D, G, NT, MODE>::THREADS, 1)
                 bool grow = grows(), apart = far > 0.f;
                 grow = __any_sync(0xffffffffu, grow || apart || dead != 0);
                 if (grow && (__any_sync(0xffffffffu, apart) || dead != 0)) {
-                    // again, without tokens that nobody sees and groups that are none
+                    // again, without tokens that nobody sees and dead groups
                     bool seen[TT][2];
                     uint32_t some = 0;  // groups that are not zero
 #pragma unroll
